@@ -43,6 +43,9 @@ RG_ERR_SINGULAR = 9
 RG_FLAG_SYNC = 1
 RG_FLAG_HOST = 2
 RG_FLAG_TRANS_B = 4
+RG_FLAG_TILE_B = 8
+RG_TYPE_F32, RG_TYPE_F16, RG_TYPE_BF16 = 0, 1, 2
+RG_F8_ROWS, RG_F8_COLUMNS, RG_F8_BOTH, RG_F8_TILES = 0, 1, 2, 3
 RG_OP_I64, RG_OP_LIMBS, RG_OP_ENCLOSE, RG_OP_STAGE, RG_OP_ENCLOSE_F32 = 0, 1, 2, 3, 4
 RG_OP_INTERVAL, RG_OP_INTERVAL_F32 = 5, 6
 RG_PROBE_MMA_S8, RG_PROBE_TCGEN05_F16, RG_PROBE_TCGEN05_E4M3 = 0, 1, 2
@@ -59,7 +62,8 @@ EXPORTED = (
     "rg_workspace_layout_batched", "enclose_gemm_f32", "enclose_gemm_f32_batched", "interval_gemm_f64",
     "interval_gemm_f32", "interval_gemm_f64_batched", "interval_gemm_f32_batched", "rg_solve_i64",
     "rg_solution_free", "rg_rational_reconstruct", "rg_big_gcd", "rg_set_crt_mode", "rg_set_stage_events",
-    "rg_probe_mma_rate", "rg_big_mulmod",
+    "rg_probe_mma_rate", "rg_big_mulmod", "quantize_f8", "scaled_gemm_f8",
+    "moe_layer_f8", "moe_layer_f8_ws_bytes",
 )
 
 
@@ -166,6 +170,14 @@ def library():
             lib.rg_probe_mma_rate.restype = ci
             lib.res_gemm_i64_noalloc.argtypes = [vp, vp, vp, i64, i64, i64, ci, cu, vp]
             lib.res_gemm_i64_noalloc.restype = ci
+            lib.quantize_f8.argtypes = [vp, ci, i64, i64, i64, ci, vp, i64, vp, vp, i64, vp, cu, vp]
+            lib.quantize_f8.restype = ci
+            lib.scaled_gemm_f8.argtypes = [vp, i64, vp, vp, i64, vp, vp, ci, i64, i64, i64, i64, cu, vp, sz, vp]
+            lib.scaled_gemm_f8.restype = ci
+            lib.moe_layer_f8.argtypes = [vp, ci, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ci, ci, cu, vp, sz, vp]
+            lib.moe_layer_f8.restype = ci
+            lib.moe_layer_f8_ws_bytes.argtypes = [i64, i64, i64, i64, ci]
+            lib.moe_layer_f8_ws_bytes.restype = sz
             lib.rg_noalloc_scratch_bytes.argtypes = []
             lib.rg_noalloc_scratch_bytes.restype = sz
             _lib = lib
@@ -691,3 +703,6 @@ def rational_reconstruct(x: int, m: int, nbits: int, dbits: int):
     _check(rc, "rg_rational_reconstruct")
     return _limbs_to_int(list(num)), _limbs_to_int(list(den))
 
+
+# 8-bit block-scaled operators (quantisation, products, linear and expert layers)
+from .f8 import linear_f8, linear_f8_backward, moe_layer_f8, quantize_f8, scaled_gemm_f8  # noqa: E402,F401

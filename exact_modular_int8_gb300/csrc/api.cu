@@ -17,7 +17,7 @@
 namespace {
 using namespace rg;
 
-constexpr size_t kPlanBytes = 4096;
+constexpr size_t kPlanBytes = kCallBlockBytes;
 // One residue plane of A and B (fp16) from which the int64 split writes the
 // previous call's plane count instead of the most an int64 product can need:
 // below it the saved writes are worth less than the fix-up pass's launch.
@@ -421,6 +421,12 @@ int run(int op, const void* A, const void* A2, int la, const void* B, const void
 }
 
 }  // namespace
+
+namespace rg {
+int finish_call(void* ws, cudaStream_t s, unsigned flags) { return finish(ws, s, flags); }
+int take_fault() { return g_fault.exchange(0); }
+unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
+}  // namespace rg
 
 extern "C" {
 

@@ -8,6 +8,15 @@
 
 namespace rg {
 
+// What every entry point keeps at the start of its workspace: the plan block
+// (status and diagnostics) and words that outlive a call.
+constexpr size_t kCallBlockBytes = 4096;
+// The end of a call on workspace `ws`: with RG_FLAG_SYNC, synchronises `s` and
+// returns the device status.
+int finish_call(void* ws, cudaStream_t s, unsigned flags);
+int take_fault();                       // the injected fault, once (rg_inject_fault)
+unsigned long long wait_limit_ns();     // rg_set_wait_limit_ns
+
 // Copies the constant tables to the current device once.
 cudaError_t upload_tables();
 

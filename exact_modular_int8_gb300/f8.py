@@ -1,0 +1,221 @@
+"""8-bit block-scaled operators: quantisation, matrix product, linear layer, mixture-of-experts layer.
+
+The format: E4M3 values (``torch.float8_e4m3fn``) with one float32 scale for every 128 values along the
+contraction, or for every 128 x 128 tile of a weight matrix; an entry stands for value * scale.  Argument
+marshalling only, as in the rest of the binding: every step runs in the library's kernels on the current
+stream.  Quantised matrices are views whose rows start on 16-byte boundaries, which is what the product
+reads; operands from elsewhere that do not are copied into such rows first.
+
+With sync=False a call only enqueues its work, and errors found on the device are read with status().
+"""
+from __future__ import annotations
+
+import functools
+
+import torch
+
+from . import (RG_ERR_ARG, RG_ERR_RANGE, RG_F8_BOTH, RG_F8_COLUMNS, RG_F8_ROWS, RG_F8_TILES, RG_FLAG_SYNC,
+               RG_FLAG_TILE_B, RG_FLAG_TRANS_B, RG_TYPE_BF16, RG_TYPE_F16, RG_TYPE_F32, ResGemmError, _check, _on,
+               _output, library, workspace)
+
+BLOCK = 128
+F8 = torch.float8_e4m3fn
+_TYPES = {torch.float32: RG_TYPE_F32, torch.float16: RG_TYPE_F16, torch.bfloat16: RG_TYPE_BF16}
+_FORMS = {"rows": RG_F8_ROWS, "columns": RG_F8_COLUMNS, "both": RG_F8_BOTH, "tiles": RG_F8_TILES}
+_WS_BYTES = 4096
+
+
+def _blocks(x: int) -> int:
+    return (x + BLOCK - 1) // BLOCK
+
+
+def _device(where: str, *ts):
+    dev = ts[0].device
+    if dev.type != "cuda" or any(t.device != dev for t in ts):
+        raise ValueError(f"{where}: tensors on one CUDA device expected")
+    return dev
+
+
+def _empty_rows(m: int, k: int, device) -> torch.Tensor:
+    """[m, k] E4M3 with rows on 16-byte boundaries."""
+    ld = (k + 15) & ~15
+    q = torch.empty((m, ld), dtype=F8, device=device)
+    return q if ld == k else q[:, :k]
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """The row stride of a matrix whose rows are contiguous, else 0 (a stride is immaterial with one row)."""
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        return 0
+    if t.shape[0] <= 1:
+        return max(t.shape[1], 1)
+    return t.stride(0) if t.stride(0) >= t.shape[1] else 0
+
+
+def _aligned_rows(q: torch.Tensor):
+    """(matrix, row stride) with rows on 16-byte boundaries, copied only where they are not."""
+    ld = _row_stride(q)
+    if q.shape[0] <= 1:
+        ld = (ld + 15) & ~15
+    if not ld or ld % 16 or q.data_ptr() % 16:
+        c = _empty_rows(q.shape[0], q.shape[1], q.device)
+        c.view(torch.uint8).copy_(q.view(torch.uint8))
+        return c, (q.shape[1] + 15) & ~15
+    return q, ld
+
+
+def quantize_f8(X: torch.Tensor, form: str = "rows", sync: bool = True):
+    """E4M3 values and float32 scales of a float32, float16 or bfloat16 matrix X [M, K].
+
+    form "rows":    Q [M, K], S [M, ceil(K/128)]: blocks of 128 along each row
+         "columns": Q [K, M], S [K, ceil(M/128)]: the same of X.T
+         "both":    (Q, S, Qt, St), the two of them from one read of X
+         "tiles":   Q [M, K], S [ceil(M/128), ceil(K/128)]: 128 x 128 tiles
+    Per block, a = max |x| (at least 2^-60), S = a / 448, Q = 448 x / a to the nearest E4M3 value, ties to
+    even; an inf or NaN makes its whole block NaN."""
+    if form not in _FORMS:
+        raise ValueError(f"quantize_f8: form must be one of {', '.join(_FORMS)}")
+    if X.dim() != 2 or X.dtype not in _TYPES:
+        raise ValueError("quantize_f8: X [M, K] float32, float16 or bfloat16 expected")
+    dev = _device("quantize_f8", X)
+    M, K = X.shape
+    ldx = _row_stride(X)
+    if not ldx:
+        X = X.contiguous()
+        ldx = K
+    q = s = qt = st = None
+    ldq = ldqt = 0
+    if form != "columns":
+        q = _empty_rows(M, K, dev)
+        ldq = (K + 15) & ~15
+        s = torch.empty((_blocks(M) if form == "tiles" else M, _blocks(K)), dtype=torch.float32, device=dev)
+    if form in ("columns", "both"):
+        qt = _empty_rows(K, M, dev)
+        ldqt = (M + 15) & ~15
+        st = torch.empty((K, _blocks(M)), dtype=torch.float32, device=dev)
+    with _on(dev):
+        rc = library().quantize_f8(X.data_ptr(), _TYPES[X.dtype], ldx, M, K, _FORMS[form],
+                                   q.data_ptr() if q is not None else None, ldq,
+                                   s.data_ptr() if s is not None else None,
+                                   qt.data_ptr() if qt is not None else None, ldqt,
+                                   st.data_ptr() if st is not None else None, RG_FLAG_SYNC if sync else 0,
+                                   torch.cuda.current_stream(dev).cuda_stream)
+    _check(rc, "quantize_f8")
+    if form == "both":
+        return q, s, qt, st
+    return (qt, st) if form == "columns" else (q, s)
+
+
+def scaled_gemm_f8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Tensor,
+                   out_dtype: torch.dtype = torch.bfloat16, transb: bool = False, sync: bool = True, out=None,
+                   ws: torch.Tensor | None = None) -> torch.Tensor:
+    """C = A @ B for block-scaled operands; with transb, B is given as [N, K] and C = A @ B.T.
+
+    A [M, K] E4M3 with SA [M, ceil(K/128)].  B's scales are per 128 x 128 tile of B or per 128 values along
+    the contraction, told apart by shape: transb SB [ceil(N/128), ceil(K/128)] or [N, ceil(K/128)], else
+    [ceil(K/128), ceil(N/128)] or [ceil(K/128), N] (N = 1 is either).  Products per block on the tensor
+    cores, scales and sums in float32, one rounding to out_dtype (float32, float16 or bfloat16)."""
+    if A.dim() != 2 or B.dim() != 2 or A.dtype != F8 or B.dtype != F8:
+        raise ValueError("scaled_gemm_f8: A [M, K] and B [K, N] (transb: [N, K]) float8_e4m3fn expected")
+    M, K = A.shape
+    N, Kb = B.shape if transb else (B.shape[1], B.shape[0])
+    if K != Kb:
+        raise ValueError("scaled_gemm_f8: A and B differ in K")
+    if out_dtype not in _TYPES:
+        raise ValueError("scaled_gemm_f8: out_dtype float32, float16 or bfloat16 expected")
+    kb, nb = _blocks(K), _blocks(N)
+    tile, row = ((nb, kb), (N, kb)) if transb else ((kb, nb), (kb, N))
+    if SA.dtype != torch.float32 or SB.dtype != torch.float32 or tuple(SA.shape) != (M, kb) or \
+            tuple(SB.shape) not in (tile, row):
+        raise ValueError(f"scaled_gemm_f8: float32 scales SA {(M, kb)} and SB {tile} or {row} expected")
+    dev = _device("scaled_gemm_f8", A, SA, B, SB)
+    flags = (RG_FLAG_SYNC if sync else 0) | (RG_FLAG_TRANS_B if transb else 0)
+    flags |= RG_FLAG_TILE_B if tuple(SB.shape) == tile else 0
+    A, lda = _aligned_rows(A)
+    B, ldb = _aligned_rows(B)
+    SA, SB = SA.contiguous(), SB.contiguous()
+    C = _output(out, (M, N), out_dtype, A, False, "scaled_gemm_f8")
+    with _on(dev):
+        w = ws if ws is not None else workspace(_WS_BYTES, dev)
+        rc = library().scaled_gemm_f8(A.data_ptr(), lda, SA.data_ptr(), B.data_ptr(), ldb, SB.data_ptr(),
+                                      C.data_ptr(), _TYPES[out_dtype], N, M, N, K, flags, w.data_ptr(), w.numel(),
+                                      torch.cuda.current_stream(dev).cuda_stream)
+    _check(rc, "scaled_gemm_f8")
+    return C
+
+
+def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True):
+    """(Y, saved): Y = X W^T with X [M, K] quantised along K and the weights W [N, K] in 128 x 128 tiles, in X's
+    dtype.  `saved` is what linear_f8_backward needs (X quantised along M and the quantised weights)."""
+    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
+        raise ValueError("linear_f8: X [M, K] and W [N, K] expected")
+    _device("linear_f8", X, W)
+    qx, sx, qxt, sxt = quantize_f8(X, "both", sync=False)
+    qw, sw = quantize_f8(W, "tiles", sync=False)
+    Y = scaled_gemm_f8(qx, sx, qw, sw, out_dtype=X.dtype, transb=True, sync=sync)
+    return Y, (qxt, sxt, qw, sw)
+
+
+def linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: torch.dtype = torch.float32):
+    """(dX, dW) of linear_f8 for the output's gradient dY [M, N]: dX = dY W with dY quantised along N, in dY's
+    dtype, and dW = dY^T X with both quantised along M, in dw_dtype."""
+    qxt, sxt, qw, sw = saved
+    if dY.dim() != 2 or dY.shape != (qxt.shape[1], qw.shape[0]):
+        raise ValueError("linear_f8_backward: dY must have the output's shape")
+    _device("linear_f8_backward", dY, qxt)
+    qd, sd, qdt, sdt = quantize_f8(dY, "both", sync=False)
+    dX = scaled_gemm_f8(qd, sd, qw, sw, out_dtype=dY.dtype, sync=False)
+    dW = scaled_gemm_f8(qdt, sdt, qxt, sxt, out_dtype=dw_dtype, transb=True, sync=sync)
+    return dX, dW
+
+
+MOE_MAX_TOKENS = 64
+
+
+@functools.lru_cache(maxsize=512)
+def _moe_ws_bytes(T, H, I, E, top_k) -> int:  # noqa: E741
+    return int(library().moe_layer_f8_ws_bytes(T, H, I, E, top_k))
+
+
+def moe_layer_f8(X: torch.Tensor, WR: torch.Tensor, W13: torch.Tensor, S13: torch.Tensor, W2: torch.Tensor,
+                 S2: torch.Tensor, top_k: int, renorm: bool = True, sync: bool = True, out=None,
+                 ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Y [T, H]: a mixture-of-experts layer with 8-bit expert weights for at most 64 tokens X [T, H] (float16 or
+    bfloat16): softmax router WR [E, H] (X's dtype), the top_k experts of each token (ties: the lower index),
+    their SwiGLU outputs summed with the router's probabilities, divided by the taken ones' sum if renorm.
+
+    W13 [E, 2I, H] E4M3 holds each expert's gate rows, then its up rows, with S13 [E, ceil(2I/128),
+    ceil(H/128)]; W2 [E, H, I] with S2 [E, ceil(H/128), ceil(I/128)]: per expert what quantize_f8(W, "tiles")
+    gives.  H and I are multiples of 16."""
+    if X.dim() != 2 or X.dtype not in (torch.float16, torch.bfloat16) or WR.dtype != X.dtype:
+        raise ValueError("moe_layer_f8: X [T, H] and WR [E, H] of one dtype, float16 or bfloat16, expected")
+    if W13.dtype != F8 or W2.dtype != F8 or S13.dtype != torch.float32 or S2.dtype != torch.float32:
+        raise ValueError("moe_layer_f8: float8_e4m3fn weights with float32 scales expected")
+    T, H = X.shape
+    if W2.dim() != 3 or W2.shape[1] != H:
+        raise ValueError("moe_layer_f8: W2 [E, H, I] expected")
+    E, I = W2.shape[0], W2.shape[2]  # noqa: E741
+    if tuple(WR.shape) != (E, H) or tuple(W13.shape) != (E, 2 * I, H):
+        raise ValueError("moe_layer_f8: WR [E, H] and W13 [E, 2I, H] expected")
+    if tuple(S13.shape) != (E, _blocks(2 * I), _blocks(H)) or tuple(S2.shape) != (E, _blocks(H), _blocks(I)):
+        raise ValueError("moe_layer_f8: one scale per 128 x 128 tile expected")
+    dev = _device("moe_layer_f8", X, WR, W13, S13, W2, S2)
+    X, WR, W13, S13, W2, S2 = (_start16(t) for t in (X, WR, W13, S13, W2, S2))
+    Y = _output(out, (T, H), X.dtype, X, False, "moe_layer_f8")
+    need = _moe_ws_bytes(T, H, I, E, int(top_k))
+    if not need:
+        raise ResGemmError(RG_ERR_RANGE if T > MOE_MAX_TOKENS else RG_ERR_ARG, "moe_layer_f8")
+    with _on(dev):
+        w = ws if ws is not None else workspace(need, dev)
+        rc = library().moe_layer_f8(X.data_ptr(), _TYPES[X.dtype], WR.data_ptr(), W13.data_ptr(), S13.data_ptr(),
+                                    W2.data_ptr(), S2.data_ptr(), Y.data_ptr(), T, H, I, E, int(top_k), int(renorm),
+                                    RG_FLAG_SYNC if sync else 0, w.data_ptr(), w.numel(),
+                                    torch.cuda.current_stream(dev).cuda_stream)
+    _check(rc, "moe_layer_f8")
+    return Y
+
+
+def _start16(t: torch.Tensor) -> torch.Tensor:
+    """Contiguous, starting on a 16-byte boundary."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()

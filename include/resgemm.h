@@ -73,6 +73,13 @@ extern "C" {
 #define RG_FLAG_TRANS_B 4u /* B is given transposed: [N][K] (limbs [N][K][lb]); the product is A * B^T,
                               without a transposed copy ("enclosure-gemm", Usage: mm_enclose_nt) */
 
+#define RG_FLAG_TILE_B 8u /* scaled_gemm_f8: B carries one scale per 128 x 128 tile (weights) */
+
+/* Element types of the 8-bit operators' 16- and 32-bit tensors. */
+#define RG_TYPE_F32 0
+#define RG_TYPE_F16 1
+#define RG_TYPE_BF16 2
+
 /* Operations, for rg_workspace_bytes() and rg_workspace_layout(). */
 #define RG_OP_I64 0
 #define RG_OP_LIMBS 1
@@ -412,6 +419,88 @@ int rg_big_gcd(const uint64_t* a, int al, const uint64_t* b, int bl, uint64_t* g
  */
 int rg_big_mulmod(const uint64_t* a, int al, const uint64_t* b, int bl, const uint64_t* m, int ml, uint64_t* r,
                   int rl);
+
+/* ------------------------------------------------------------------------
+ * 8-bit block-scaled operators.  Beside the exact products, the products a
+ * language model trains and serves with: E4M3 values (1 sign, 4 exponent, 3
+ * significand bits, no inf, largest 448) with one fp32 scale for every 128
+ * values along the contraction, or for every 128 x 128 tile of a weight
+ * matrix.  An entry stands for value * scale.  Device pointers only
+ * (RG_FLAG_HOST is not taken); row strides (ld*) count entries.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Quantises X [M][ldx] (M x K entries of x_type RG_TYPE_*).  For each block, a
+ * = max |x| (at least 2^-60), scale = a / 448, value = 448 x / a rounded to the
+ * nearest E4M3 value, ties to even.  A block holding an inf or NaN gets that
+ * as its scale, and all of it stands for NaN.
+ *   RG_F8_ROWS     blocks of 128 along each row: Q [M][ldq], S [M][ceil(K/128)]
+ *   RG_F8_COLUMNS  blocks of 128 along each column, stored transposed:
+ *                  QT [K][ldqt], ST [K][ceil(M/128)]
+ *   RG_F8_BOTH     both of these from one read of X
+ *   RG_F8_TILES    128 x 128 tiles: Q [M][ldq], S [ceil(M/128)][ceil(K/128)]
+ * The last block of a row or column may be shorter.  Pointers a form does not
+ * write may be null.  Rows of Q (QT) that start on 16-byte boundaries suit
+ * scaled_gemm_f8 and are written faster.  No workspace.
+ * Errors: RG_ERR_ARG (sizes above 2^30, strides shorter than the rows, null
+ * pointers, unknown type or form), RG_ERR_CUDA.
+ */
+#define RG_F8_ROWS 0
+#define RG_F8_COLUMNS 1
+#define RG_F8_BOTH 2
+#define RG_F8_TILES 3
+int quantize_f8(const void* X, int x_type, int64_t ldx, int64_t M, int64_t K, int form, uint8_t* Q, int64_t ldq,
+                float* S, uint8_t* QT, int64_t ldqt, float* ST, unsigned flags, void* stream);
+
+/*
+ * C [M][ldc] = A * B for block-scaled operands, in c_type (RG_TYPE_*).
+ * A [M][lda] with SA [M][ceil(K/128)].  B [K][ldb], or [N][ldb] with
+ * RG_FLAG_TRANS_B.  B's scales, contiguous:
+ *                       RG_FLAG_TILE_B                   without
+ *   RG_FLAG_TRANS_B     [ceil(N/128)][ceil(K/128)]       [N][ceil(K/128)]
+ *   without             [ceil(K/128)][ceil(N/128)]       [ceil(K/128)][N]
+ * Each 128-block's product is formed on the tensor cores, scaled in fp32 and
+ * summed in fp32, in an order fixed by the shape (equal calls give equal
+ * bits); C is rounded once.  NaN and inf scales propagate.  K = 0 gives 0.
+ * A and B start on 16-byte boundaries and lda, ldb are multiples of 16.
+ * ws: RG_F8_WS_BYTES bytes, 256-byte aligned (status and diagnostics).
+ * Errors: RG_ERR_ARG (also sizes above 2^30), RG_ERR_WORKSPACE, RG_ERR_CUDA,
+ * RG_ERR_TIMEOUT.
+ */
+#define RG_F8_WS_BYTES 4096
+int scaled_gemm_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t* B, int64_t ldb, const float* SB,
+                   void* C, int c_type, int64_t ldc, int64_t M, int64_t N, int64_t K, unsigned flags, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (decoding):
+ *   p = softmax(X WR^T) over the E experts; each token takes the top_k
+ *   largest (equal ones: the lower index), with weights p or, with renorm,
+ *   p over the sum of the taken ones;
+ *   Y = sum of weight * (silu(X G^T) * (X U^T)) D^T over its experts,
+ * silu(a) = a / (1 + exp(-a)).  X [T][H], WR [E][H] and Y [T][H] are x_type
+ * (RG_TYPE_F16 or RG_TYPE_BF16).  W13 [E][2I][H] holds G in its first I rows
+ * and U in the others, W2 [E][H][I] holds D, both E4M3 with one scale per 128 x
+ * 128 tile of an expert's matrix: S13 [E][ceil(2I/128)][ceil(H/128)],
+ * S2 [E][ceil(H/128)][ceil(I/128)].  All contiguous, starting on 16-byte
+ * boundaries; H and I are multiples of 16.  Sums, softmax and the gated
+ * product are fp32 (the latter rounded to 11 bits as an operand of the last
+ * product); Y is rounded once, and equal calls give equal bits.  An inf or NaN
+ * in a token makes that token's whole row NaN.
+ * ws: moe_layer_f8_ws_bytes() bytes, 256-byte aligned; that function returns 0
+ * for invalid sizes.
+ * Errors: RG_ERR_RANGE (T > RG_MOE_MAX_TOKENS: use quantize_f8 and
+ * scaled_gemm_f8 per expert), RG_ERR_ARG, RG_ERR_WORKSPACE, RG_ERR_CUDA,
+ * RG_ERR_TIMEOUT.
+ */
+#define RG_MOE_MAX_TOKENS 64
+#define RG_MOE_MAX_EXPERTS 512
+#define RG_MOE_MAX_TOP_K 16
+#define RG_MOE_MAX_WIDTH 65536
+size_t moe_layer_f8_ws_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int top_k);
+int moe_layer_f8(const void* X, int x_type, const void* WR, const uint8_t* W13, const float* S13, const uint8_t* W2,
+                 const float* S2, void* Y, int64_t T, int64_t H, int64_t I, int64_t E, int top_k, int renorm,
+                 unsigned flags, void* ws, size_t ws_bytes, void* stream);
 
 /* Reconstruction of the results.  Mode 0 (the default): one-limb results
  * (res_gemm_i64, res_gemm_limbs with lc = 1) of at most 12 primes (every
