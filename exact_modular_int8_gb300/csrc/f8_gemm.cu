@@ -10,8 +10,9 @@
 // the block's row), beside the MMAs of the next block: two accumulators
 // alternate.
 //
-// Warp roles: warp 0 TMA producer, warp 1 tensor memory and MMA issue, warps
-// 2..9 epilogue.  Every wait is bounded as in the residue product.
+// Warp roles: warp 0 TMA producer, warp 1 tensor memory and MMA issue, warps 2
+// and 3 copy the scales to shared memory, warps 4..11 epilogue.  Every wait is
+// bounded as in the residue product.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -20,6 +21,7 @@
 #include <mutex>
 
 #include "f8_kernels.h"
+#include "rg_kernels.h"
 #include "rg_tc.cuh"
 
 namespace rg {
@@ -27,7 +29,7 @@ namespace {
 
 constexpr int BK = 128;  // values of k per block and pipeline stage: one 128-byte swizzle row
 constexpr int EPI_WARPS = 8;
-constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int NUM_THREADS = 128 + 32 * EPI_WARPS;
 constexpr int SLAB = 128 * BK;  // 128 rows (or columns) of one stage
 
 // Instruction descriptor, kind::f8f6f4: D f32, A and B E4M3, A K-major.
@@ -69,10 +71,130 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   return v;
 }
 
+// ---------------------------------------------------------------------------
+// Scales.  Two warps copy the CTA's scales to shared memory, KC blocks of 128
+// at a time and two such chunks deep, so that the epilogue reads them there:
+// sa[KC][128 rows], sb[KC][NC columns] (or one value per 128 columns).  The
+// scales lie with the blocks of a row next to each other (or B's columns, for
+// an untransposed B), so a warp's copy instruction covers a few short runs of
+// consecutive words; loading them a row to a lane in the epilogue itself took
+// three times as long as all its other work.
+// ---------------------------------------------------------------------------
+constexpr int KC = 8;
+constexpr int SCALE_BUFS = 2;
+template <int NC>
+struct ScaleChunk {
+  float a[KC][128 + 4];  // rows padded: the copies of one instruction fall into different banks
+  float b[KC][NC + 4];
+};
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrive on the barrier once this thread's copies have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Blocks kb0 .. kb0 + KC - 1 (at most kb_end) of rows [m0, m0 + 128) and columns
+// [n0, n0 + NC), by the 64 threads t.  Entries past the matrix repeat its last.
+template <int NC, bool TILE_B>
+__device__ __forceinline__ void load_scales(const Params& gp, ScaleChunk<NC>& c, int m0, int n0, int kb0, int kb_end,
+                                            int t) {
+  const int kbi = t & (KC - 1), kb = min(kb0 + kbi, kb_end - 1);
+#pragma unroll 4
+  for (int r = t >> 3; r < 128; r += 8)
+    cp_async4(smem_u32(&c.a[kbi][r]), gp.SA + (long long)min(m0 + r, gp.M - 1) * gp.KB + kb);
+  if constexpr (TILE_B) {
+    if (t < KC * (NC / 128)) {
+      const int h = t >> 3;
+      cp_async4(smem_u32(&c.b[kbi][h]),
+                gp.SB + (long long)min(n0 / 128 + h, (gp.N - 1) / 128) * gp.sb_n + kb * gp.sb_k);
+    }
+  } else if (gp.sb_k == 1) {
+#pragma unroll 4
+    for (int n = t >> 3; n < NC; n += 8)
+      cp_async4(smem_u32(&c.b[kbi][n]), gp.SB + (long long)min(n0 + n, gp.N - 1) * gp.sb_n + kb);
+  } else {
+    for (int q = 0; q < KC; ++q)
+      for (int n = t; n < NC; n += 64)
+        cp_async4(smem_u32(&c.b[q][n]),
+                  gp.SB + (long long)min(n0 + n, gp.N - 1) * gp.sb_n + (long long)min(kb0 + q, kb_end - 1) * gp.sb_k);
+  }
+}
+
 __device__ __forceinline__ void store_out(void* C, long long at, int type, float v) {
   if (type == RG_TYPE_F32) static_cast<float*>(C)[at] = v;
   else if (type == RG_TYPE_F16) static_cast<__half*>(C)[at] = __float2half_rn(v);
   else static_cast<__nv_bfloat16*>(C)[at] = __float2bfloat16_rn(v);
+}
+
+// Pairs of fp32 (fma.rn.f32x2: two multiply-adds per instruction).
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Arrive on a barrier of another CTA of the cluster without releasing memory:
+// it only reports tensor-memory reads, ordered by the tcgen05 fence before it.
+// (A release at cluster scope drains the warp's memory operations; it took 1100
+// of the 2500 cycles that a 128-block then cost.)
+__device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar_cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
+}
+
+// Adds a block's product, read from tensor memory 32 columns at a time, to this
+// lane's sums of COLS columns: acc += p * s (TILE_B) or acc += (p * s) * sb[column].
+// `release` runs once the last read is complete.
+template <int COLS, bool TILE_B, typename F>
+__device__ __forceinline__ void add_block(uint64_t (&acc)[COLS / 2], uint32_t taddr, float s, const float* sb,
+                                          F&& release) {
+  const uint64_t s2 = pack2(s, s);
+#pragma unroll
+  for (int h = 0; h < COLS / 32; ++h) {
+    uint32_t r[32];
+    tmem_ld32(taddr + 32 * h, r);
+    tmem_wait_ld();
+    pin32(r);
+    if (h == COLS / 32 - 1) release();
+    if constexpr (TILE_B) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[16 * h + i] = fma2(pack2u(r[2 * i], r[2 * i + 1]), s2, acc[16 * h + i]);
+    } else {
+      const ulonglong2* sv = reinterpret_cast<const ulonglong2*>(sb + 32 * h);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const ulonglong2 v = sv[i];
+        uint64_t* a = &acc[16 * h + 2 * i];
+        a[0] = fma2(mul2(pack2u(r[4 * i], r[4 * i + 1]), s2), (uint64_t)v.x, a[0]);
+        a[1] = fma2(mul2(pack2u(r[4 * i + 2], r[4 * i + 3]), s2), (uint64_t)v.y, a[1]);
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -84,7 +206,7 @@ constexpr int STAGES1 = 6;
 constexpr int STAGE1_BYTES = 2 * SLAB;
 constexpr int PART_LD = BN1 + 4;  // floats per row of a CTA's partial tile, kept where the stages were
 static_assert(128 * PART_LD * 4 <= STAGES1 * STAGE1_BYTES, "partial tile");
-constexpr int SCALE1_BYTES = EPI_WARPS * 2 * 64 * 4;
+constexpr int SCALE1_BYTES = SCALE_BUFS * (int)sizeof(ScaleChunk<BN1>);
 constexpr int SMEM1_BYTES = 1024 + STAGES1 * STAGE1_BYTES + SCALE1_BYTES + 256;
 static_assert(SMEM1_BYTES <= 232448, "shared memory");
 
@@ -95,14 +217,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stage_base = smem;
-  float* scale_base = reinterpret_cast<float*>(smem + STAGES1 * STAGE1_BYTES);
+  ScaleChunk<BN1>* scales = reinterpret_cast<ScaleChunk<BN1>*>(smem + STAGES1 * STAGE1_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES1 * STAGE1_BYTES + SCALE1_BYTES);
   uint64_t* full = bars;
   uint64_t* empty = bars + STAGES1;
   uint64_t* tfull = bars + 2 * STAGES1;
   uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tfull + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 5);
+  uint64_t* sfull = tfull + 4;
+  uint64_t* sempty = sfull + SCALE_BUFS;
+  uint64_t* drain = sempty + SCALE_BUFS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -120,6 +244,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&tfull[b]), 1);
       mbar_init(smem_u32(&tempty[b]), EPI_WARPS);
+    }
+    for (int b = 0; b < SCALE_BUFS; ++b) {
+      mbar_init(smem_u32(&sfull[b]), 64);
+      mbar_init(smem_u32(&sempty[b]), EPI_WARPS);
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -210,69 +338,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         wait_bounded(smem_u32(drain), 0, drain_ctl, 0);
       }
     }
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ scales
+    int c = 0;
+    for (int kb = kb_lo; kb < kb_hi; kb += KC, ++c) {
+      const int b = c & 1;
+      if (!wait_bounded(smem_u32(&sempty[b]), ((c >> 1) & 1u) ^ 1u, ctl, 25)) break;
+      load_scales<BN1, TILE_B>(gp, scales[b], tm * 128, tn * BN1, kb, kb_hi, threadIdx.x - 64);
+      cp_async_arrive(smem_u32(&sfull[b]));
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ------------------------------------------------------------ epilogue
     const int q4 = warp & 3;  // tensor-memory lane quarter this warp may access
     const int row = q4 * 32 + lane;
-    const int col0 = ((warp - 2) >> 2) * 64;
-    const int m = min(tm * 128 + row, gp.M - 1);
-    const float* sa = gp.SA + (long long)m * gp.KB;
-    float* sbuf = scale_base + (warp - 2) * 128;
-    const float* sb0;  // this lane's scales of B: columns lane, lane + 32 of the warp's 64 (or the tile's one)
-    const float* sb1;
-    if constexpr (TILE_B) {
-      sb0 = gp.SB + (long long)tn * gp.sb_n;  // a tile's 128 columns are one block
-      sb1 = sb0;
-    } else {
-      const int n = tn * BN1 + col0 + lane;
-      sb0 = gp.SB + (long long)min(n, gp.N - 1) * gp.sb_n;
-      sb1 = gp.SB + (long long)min(n + 32, gp.N - 1) * gp.sb_n;
-    }
-    float acc[64];
+    const int col0 = ((warp - 4) >> 2) * 64;
+    uint64_t acc[32];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < 32; ++i) acc[i] = 0;
     uint32_t it = 0;
     bool ok = true;
     for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
       const uint32_t b = it & 1u, aph = (it >> 1) & 1u;
-      float s = __ldg(sa + kb);
-      if constexpr (TILE_B) {
-        s *= __ldg(sb0 + kb * gp.sb_k);
-      } else {
-        sbuf[b * 64 + lane] = __ldg(sb0 + kb * gp.sb_k);
-        sbuf[b * 64 + 32 + lane] = __ldg(sb1 + kb * gp.sb_k);
-      }
-      ok = __all_sync(0xFFFFFFFFu, wait_bounded(smem_u32(&tfull[b]), aph, ctl, 24));
+      const int c = (int)it / KC, kbi = (int)it % KC;
+      const ScaleChunk<BN1>& sc = scales[c & 1];
+      ok = kbi != 0 || wait_bounded(smem_u32(&sfull[c & 1]), (c >> 1) & 1u, ctl, 26);
+      ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded(smem_u32(&tfull[b]), aph, ctl, 24));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q4 * 32) << 16) + b * BN1 + col0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t r[32];
-        tmem_ld32(taddr + 32 * h, r);
-        tmem_wait_ld();
-        pin32(r);
-        if (h == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&tempty[b]));
-        }
-        if constexpr (TILE_B) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[32 * h + i] = __fmaf_rn(__uint_as_float(r[i]), s, acc[32 * h + i]);
-        } else {
-          const float4* sv = reinterpret_cast<const float4*>(sbuf + b * 64 + 32 * h);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 v = sv[i];
-            const float w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int e = 4 * i + j;
-              acc[32 * h + e] = __fmaf_rn(__uint_as_float(r[e]), s * w[j], acc[32 * h + e]);
-            }
-          }
-        }
+      float s = sc.a[kbi][row];
+      if constexpr (TILE_B) s *= sc.b[kbi][0];
+      add_block<64, TILE_B>(acc, tmem_base + ((uint32_t)(q4 * 32) << 16) + b * BN1 + col0, s, &sc.b[kbi][col0], [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(smem_u32(&tempty[b]));
+      });
+      if (kbi == KC - 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sempty[c & 1]));
       }
     }
     // the stages are idle once the last block's product is complete; the
@@ -280,9 +383,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (ok) {
       float* part = reinterpret_cast<float*>(stage_base) + row * PART_LD + col0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        *reinterpret_cast<float4*>(part + 4 * i) =
-            make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+      for (int i = 0; i < 16; ++i) {
+        const float2 lo = unpack2(acc[2 * i]), hi = unpack2(acc[2 * i + 1]);
+        *reinterpret_cast<float4*>(part + 4 * i) = make_float4(lo.x, lo.y, hi.x, hi.y);
+      }
     }
   }
 
@@ -319,6 +423,305 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
+// Tiles of 256 x 256 on CTA pairs (cta_group::2), persistent.  Each CTA holds
+// 128 rows of A and 128 columns of B per stage and receives its own 128 rows
+// of the accumulator; its eight epilogue warps each keep 32 rows x 128 columns
+// of fp32 sums in registers (128 of them a lane).  The block is launched with
+// 168 registers a thread; the first warpgroup (producer, MMA issue, scales)
+// gives up 96 of them and the two epilogue warpgroups take 48 more each:
+// 72 + 2 * 216 = 3 * 168.
+// ---------------------------------------------------------------------------
+constexpr int BN2 = 256;
+constexpr int STAGES2 = 5;
+constexpr int STAGE2_BYTES = 2 * SLAB;
+constexpr int OUT_ROW = 128 + 16;  // bytes of a staged output row, padded against bank conflicts
+constexpr int OUT_WARP = 32 * OUT_ROW;
+constexpr int SCALE2_BYTES = SCALE_BUFS * (int)sizeof(ScaleChunk<BN2>);
+constexpr int SMEM2_BYTES = 1024 + STAGES2 * STAGE2_BYTES + EPI_WARPS * OUT_WARP + SCALE2_BYTES + 256;
+static_assert(SMEM2_BYTES <= 232448, "shared memory");
+
+__device__ __forceinline__ void umma_f8_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+          d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster_addr,
+                                                 int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// This warp's 32 rows x 128 columns of sums (a lane holds a row) to C, through
+// the warp's staging buffer 128 bytes of each row at a time, so that the global
+// stores are whole 128-byte row segments.
+template <int ES>  // bytes per entry of C
+__device__ __forceinline__ void store_rows(const Params& gp, const uint64_t (&acc)[64], uint8_t* stage, int row0,
+                                           int col0, int lane) {
+  constexpr int COLS = 128 / ES;
+  const int rows = min(32, gp.M - row0);
+#pragma unroll
+  for (int c = 0; c < 128 / COLS; ++c) {
+    uint4* mine = reinterpret_cast<uint4*>(stage + lane * OUT_ROW);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // 16 bytes
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (ES == 4) {
+          const float2 f = unpack2(acc[c * (COLS / 2) + 2 * i + (j >> 1)]);
+          w[j] = __float_as_uint(j & 1 ? f.y : f.x);
+        } else {
+          const float2 f = unpack2(acc[c * (COLS / 2) + 4 * i + j]);
+          if (gp.out_type == RG_TYPE_F16) {
+            const __half2 h = __floats2half2_rn(f.x, f.y);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+          } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+      }
+      mine[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    const int cc = col0 + c * COLS;
+    const int cols = min(COLS, gp.N - cc);
+    uint8_t* out = static_cast<uint8_t*>(gp.C) + ((long long)row0 * gp.ldc + cc) * ES;
+    if (cols == COLS && gp.vec_c) {
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += 4) {
+        const int r = r0 + (lane >> 3), j = lane & 7;
+        if (r < rows)
+          *reinterpret_cast<uint4*>(out + (long long)r * gp.ldc * ES + 16 * j) =
+              *reinterpret_cast<const uint4*>(stage + r * OUT_ROW + 16 * j);
+      }
+    } else {
+      for (int r = 0; r < rows; ++r)
+        for (int j = lane; j < cols; j += 32) {
+          if constexpr (ES == 4)
+            reinterpret_cast<uint32_t*>(out + (long long)r * gp.ldc * ES)[j] =
+                reinterpret_cast<const uint32_t*>(stage + r * OUT_ROW)[j];
+          else
+            reinterpret_cast<uint16_t*>(out + (long long)r * gp.ldc * ES)[j] =
+                reinterpret_cast<const uint16_t*>(stage + r * OUT_ROW)[j];
+        }
+    }
+    __syncwarp();
+  }
+}
+
+template <bool B_KMAJOR, bool TILE_B>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    f8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ Params gp, DevPlan* plan) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t rank = cluster_rank();
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* stage_base = smem;
+  uint8_t* out_base = smem + STAGES2 * STAGE2_BYTES;
+  ScaleChunk<BN2>* scales = reinterpret_cast<ScaleChunk<BN2>*>(out_base + EPI_WARPS * OUT_WARP);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(out_base + EPI_WARPS * OUT_WARP + SCALE2_BYTES);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + STAGES2;
+  uint64_t* tfull = bars + 2 * STAGES2;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* sfull = tfull + 4;
+  uint64_t* sempty = sfull + SCALE_BUFS;
+  uint64_t* drain = sempty + SCALE_BUFS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Ctl ctl{abort_flag, &plan->status, &plan->timeout_where, gp.wait_ns};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES2; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&tfull[b]), 1);
+      mbar_init(smem_u32(&tempty[b]), 2 * EPI_WARPS);  // the epilogue warps of both CTAs
+    }
+    for (int b = 0; b < SCALE_BUFS; ++b) {
+      mbar_init(smem_u32(&sfull[b]), 64);
+      mbar_init(smem_u32(&sempty[b]), EPI_WARPS);
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {  // one warp in each CTA allocates for the pair
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"((uint32_t)(2 * BN2)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers of both CTAs are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  wait_for_predecessor();
+  const int total = gp.mt * gp.nt;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer (both CTAs)
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = cid; t < total && ok; t += ncl) {
+        const int tn = t / gp.mt, tm = t - tn * gp.mt;
+        for (int kb = 0; kb < gp.KB; ++kb) {
+          if (!wait_bounded_cluster(smem_u32(&empty[stage]), phase ^ 1u, ctl, 31)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb_local = smem_u32(&full[stage]);
+          if (rank == 0) mbar_arrive_expect_tx(fb_local, 2 * STAGE2_BYTES);
+          const uint32_t fb = mapa_shared(fb_local, 0);
+          const uint32_t a_dst = smem_u32(stage_base + stage * STAGE2_BYTES);
+          const int n0 = tn * BN2 + (int)rank * 128;
+          tma_load_2d_pair(a_dst, &tmA, fb, kb * BK, tm * 256 + (int)rank * 128);
+          if constexpr (B_KMAJOR) tma_load_2d_pair(a_dst + SLAB, &tmB, fb, kb * BK, n0);
+          else tma_load_2d_pair(a_dst + SLAB, &tmB, fb, n0, kb * BK);
+          if (++stage == STAGES2) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    if (warp == 1 && lane == 0 && rank == 0) {
+      // ---------------------------------------------------------- MMA issuer (first CTA)
+      int stage = 0;
+      uint32_t phase = 0, it = 0;
+      bool ok = true;
+      for (int t = cid; t < total && ok; t += ncl) {
+        for (int kb = 0; kb < gp.KB; ++kb, ++it) {
+          const uint32_t b = it & 1u, aph = (it >> 1) & 1u;
+          if (!wait_bounded_cluster(smem_u32(&tempty[b]), aph ^ 1u, ctl, 32) ||
+              !wait_bounded_cluster(smem_u32(&full[stage]), phase, ctl, 33)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(stage_base + stage * STAGE2_BYTES);
+          const uint64_t adesc = sw128_desc(a_addr, 16, 1024);
+          const uint64_t bdesc =
+              B_KMAJOR ? sw128_desc(a_addr + SLAB, 16, 1024) : sw128_desc(a_addr + SLAB, SLAB, 1024);
+          constexpr uint32_t b_step = B_KMAJOR ? 2 : 256;
+          constexpr uint32_t idesc = idesc_f8(256, BN2, B_KMAJOR);
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            umma_f8_pair(tmem_base + b * BN2, adesc + (uint64_t)(2 * kk), bdesc + (uint64_t)(b_step * kk), idesc,
+                         kk > 0);
+          umma_commit_pair(smem_u32(&empty[stage]));
+          if (!(gp.fault == 1 && it == 0)) umma_commit_pair(smem_u32(&tfull[b]));
+          if (++stage == STAGES2) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && it > 0) {  // all issued MMAs must finish before the memory is freed
+        Ctl drain_ctl = ctl;
+        volatile int never = 0;
+        drain_ctl.abort = &never;
+        umma_commit_pair_local(smem_u32(drain));
+        wait_bounded(smem_u32(drain), 0, drain_ctl, 0);
+      }
+    }
+    if (warp >= 2) {
+      // ---------------------------------------------------------- scales (both CTAs)
+      int c = 0;
+      bool ok = true;
+      for (int t = cid; t < total && ok; t += ncl) {
+        const int tn = t / gp.mt, tm = t - tn * gp.mt;
+        for (int kb = 0; kb < gp.KB && ok; kb += KC, ++c) {
+          const int b = c & 1;
+          ok = wait_bounded(smem_u32(&sempty[b]), ((c >> 1) & 1u) ^ 1u, ctl, 35);
+          if (!ok) break;
+          load_scales<BN2, TILE_B>(gp, scales[b], tm * 256 + (int)rank * 128, tn * BN2, kb, gp.KB, threadIdx.x - 64);
+          cp_async_arrive(smem_u32(&sfull[b]));
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int q4 = warp & 3, ew = warp - 4;
+    const int half = ew >> 2;  // this warp's 128 of the 256 columns
+    uint8_t* stage = out_base + ew * OUT_WARP;
+    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
+    const uint32_t lane_addr = tmem_base + ((uint32_t)(q4 * 32) << 16) + half * 128;
+    uint32_t it = 0;
+    int chunk = 0;
+    bool ok = true;
+    for (int t = cid; t < total && ok; t += ncl) {
+      const int tn = t / gp.mt, tm = t - tn * gp.mt;
+      const int row0 = tm * 256 + (int)rank * 128 + q4 * 32, col0 = tn * BN2 + half * 128;
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      for (int kb = 0; kb < gp.KB; ++kb, ++it) {
+        const uint32_t b = it & 1u, aph = (it >> 1) & 1u;
+        const int kbi = kb % KC;
+        const ScaleChunk<BN2>& sc = scales[chunk & 1];
+        ok = kbi != 0 || wait_bounded(smem_u32(&sfull[chunk & 1]), (chunk >> 1) & 1u, ctl, 36);
+        ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded_cluster(smem_u32(&tfull[b]), aph, ctl, 34));
+        if (!ok) break;
+        tc_fence_after();
+        float s = sc.a[kbi][q4 * 32 + lane];
+        if constexpr (TILE_B) s *= sc.b[kbi][half];
+        add_block<128, TILE_B>(acc, lane_addr + b * BN2, s, &sc.b[kbi][half * 128], [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_relaxed_cluster(tempty_leader[b]);
+        });
+        if (kbi == KC - 1 || kb == gp.KB - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sempty[chunk & 1]));
+          ++chunk;
+        }
+      }
+      if (ok && row0 < gp.M && col0 < gp.N) {
+        if (gp.out_type == RG_TYPE_F32) store_rows<4>(gp, acc, stage, row0, col0, lane);
+        else store_rows<2>(gp, acc, stage, row0, col0, lane);
+      }
+    }
+  }
+
+  __syncwarp();  // whole warps again before the abort check and the barriers below
+  if (*abort_flag) {
+    // an aborted role may leave copies in flight that signal either CTA:
+    // give them time to land before the pair leaves
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 200000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  allow_dependents();
+  cluster_sync();  // neither CTA frees the pair's memory while the other still uses it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"((uint32_t)(2 * BN2)));
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
 bool make_map_2d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t stride_bytes, uint32_t b0,
@@ -334,12 +737,31 @@ bool make_map_2d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uin
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaLaunchConfig_t cluster_config(dim3 grid, int threads, int smem, cudaStream_t st, int cluster, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
 using TileKernel = void (*)(const CUtensorMap, const CUtensorMap, const Params, int, DevPlan*);
 constexpr TileKernel kTileKernels[2][2] = {{f8_gemm_tile_kernel<false, false>, f8_gemm_tile_kernel<false, true>},
                                            {f8_gemm_tile_kernel<true, false>, f8_gemm_tile_kernel<true, true>}};
 
+using PairKernel = void (*)(const CUtensorMap, const CUtensorMap, const Params, DevPlan*);
+constexpr PairKernel kPairKernels[2][2] = {{f8_gemm_pair_kernel<false, false>, f8_gemm_pair_kernel<false, true>},
+                                           {f8_gemm_pair_kernel<true, false>, f8_gemm_pair_kernel<true, true>}};
+
 struct F8Device {
-  int sms = 0;
+  int sms = 0, max_pairs = 0;
 };
 cudaError_t f8_device(int dev, F8Device& out) {
   static std::mutex mu;
@@ -356,6 +778,20 @@ cudaError_t f8_device(int dev, F8Device& out) {
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     if (sms < 2) return cudaErrorInvalidDevice;
+    for (auto& row : kPairKernels)
+      for (auto k : row) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM2_BYTES);
+        if (e != cudaSuccess) return e;
+      }
+    // not every SM can be paired within its GPC
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(sms & ~1)), NUM_THREADS, SMEM2_BYTES, nullptr, 2, attr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kPairKernels[1][1], &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();  // the query's own failure is not the call's
+      n = sms / 2;
+    }
+    d.max_pairs = n;
     d.sms = sms;
   }
   out = d;
@@ -395,21 +831,20 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
       !(a.b_kmajor ? make_map_2d(&mb, a.B, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.ldb, BK, 128)
                    : make_map_2d(&mb, a.B, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.ldb, 128, BK)))
     return cudaErrorInvalidValue;
+  cudaLaunchAttribute attr[1];
+  const int variant = gemm_variant();
+  const long long tiles2 = ((a.M + 255) / 256) * ((a.N + BN2 - 1) / BN2);
+  if (variant == 2 || (variant == 0 && tiles2 >= fd.max_pairs)) {
+    p.mt = (int)((a.M + 255) / 256);
+    p.nt = (int)((a.N + BN2 - 1) / BN2);
+    const long long clusters = tiles2 < fd.max_pairs ? tiles2 : fd.max_pairs;
+    cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(2 * clusters)), NUM_THREADS, SMEM2_BYTES, st, 2, attr);
+    return cudaLaunchKernelEx(&cfg, kPairKernels[a.b_kmajor][a.tile_b], ma, mb, p, plan);
+  }
   const long long tiles = (long long)p.mt * p.nt;
   int S = 1;
   while (S < 8 && tiles * S * 2 <= fd.sms && p.KB >= 4 * S) S *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * S));
-  cfg.blockDim = dim3(NUM_THREADS);
-  cfg.dynamicSmemBytes = SMEM1_BYTES;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)S;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(tiles * S)), NUM_THREADS, SMEM1_BYTES, st, S, attr);
   return cudaLaunchKernelEx(&cfg, kTileKernels[a.b_kmajor][a.tile_b], ma, mb, p, S, plan);
 }
 

@@ -976,6 +976,8 @@ cudaError_t launch_gemm(const void* RA, long long lda, const void* RB, long long
   return e != cudaSuccess ? e : slice_sum();
 }
 
+int gemm_variant() { return g_gemm_variant.load(); }
+
 int gemm_max_splits(long long gemm_batch, long long M, long long N, long long K) {
   const long long nkc = (K + (long long)KC_BLOCKS * BK - 1) / ((long long)KC_BLOCKS * BK);
   // tiles with a single prime, of the larger (CTA-pair) kind; 160 bounds the

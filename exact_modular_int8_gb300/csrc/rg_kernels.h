@@ -16,6 +16,7 @@ constexpr size_t kCallBlockBytes = 4096;
 int finish_call(void* ws, cudaStream_t s, unsigned flags);
 int take_fault();                       // the injected fault, once (rg_inject_fault)
 unsigned long long wait_limit_ns();     // rg_set_wait_limit_ns
+int gemm_variant();                     // rg_set_gemm_variant
 
 // Copies the constant tables to the current device once.
 cudaError_t upload_tables();

@@ -554,9 +554,9 @@ void rg_inject_fault(int kind);
  * RG_ERR_ARG for another n or a null handle. */
 int rg_set_stage_events(void* const* events, int n);
 
-/* Test hook: which tensor-core kernel runs the per-prime stage.  0 = choose
- * by shape (the CTA-pair kernel when M > 128), 1 = single-CTA kernel,
- * 2 = CTA-pair kernel.  Returns the previous choice, or -1 for an invalid
+/* Test hook: which tensor-core kernel runs the per-prime stage and
+ * scaled_gemm_f8.  0 = choose by shape (per-prime stage: the CTA-pair kernel
+ * when M > 128), 1 = single-CTA kernel, 2 = CTA-pair kernel.  Returns the previous choice, or -1 for an invalid
  * value.  Not thread-safe; for tests and measurements only. */
 int rg_set_gemm_variant(int variant);
 

@@ -16,7 +16,7 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_util import rg  # noqa: F401
+from gpu_util import rg, variant  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -215,6 +215,15 @@ def test_product_many_tiles(rg, m, n, k, transb, tile):  # noqa: F811
     check_product(rg, m, n, k, transb, tile, torch.float32, seed=70)
 
 
+@pytest.mark.parametrize("transb,tile", [(True, True), (True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("m,n,k,out", [(1, 1, 1, torch.float32), (130, 260, 1000, torch.float32),
+                                       (257, 513, 200, torch.bfloat16), (520, 392, 2100, torch.float32),
+                                       (300, 200, 640, torch.float16)])
+def test_product_kernels(rg, variant, m, n, k, out, transb, tile):  # noqa: F811
+    """Both tensor-core kernels, whatever the shape would choose."""
+    check_product(rg, m, n, k, transb, tile, out, seed=90)
+
+
 def test_product_long_k(rg):  # noqa: F811
     check_product(rg, 40, 50, 70001, True, False, torch.float32, seed=80)
     check_product(rg, 3, 200, 70001, True, True, torch.float32, seed=81)
@@ -280,7 +289,7 @@ def test_product_out_and_repeats(rg):  # noqa: F811
     assert torch.equal(other, first)
 
 
-def test_product_timeout_is_reported(rg):  # noqa: F811
+def test_product_timeout_is_reported(rg, variant):  # noqa: F811
     """A product whose tensor-core stage never reports its first block ends with a time-out, and the next is sound."""
     lib = rg.library()
     A, _ = random_f8(512, 512, 1)
