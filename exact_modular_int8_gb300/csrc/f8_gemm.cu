@@ -10,9 +10,10 @@
 // the block's row), beside the MMAs of the next block: two accumulators
 // alternate.
 //
-// Warp roles: warp 0 TMA producer, warp 1 tensor memory and MMA issue, warps 2
-// and 3 copy the scales to shared memory, warps 4..11 epilogue.  Every wait is
-// bounded as in the residue product.
+// Warp roles: warp 0 TMA producer, warps 1 (and 2, in the pair kernel) tensor
+// memory and MMA issue, the rest of the first four copy the scales to shared
+// memory, warps 4..11 epilogue.  Every wait is bounded as in the residue
+// product.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -58,6 +59,29 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t adesc, uint64_t bde
       : "memory");
 }
 
+// One thread of a converged warp.  The issuing warps run their loops whole and
+// elect a thread for the MMAs alone: their descriptors then stay in uniform
+// registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// Waits for a phase of both barriers; by whole warps (the answer is the same for all lanes).
+__device__ __forceinline__ bool wait_both(uint32_t bar0, uint32_t par0, uint32_t bar1, uint32_t par1, const Ctl& ctl,
+                                          int where) {
+  const bool r0 = mbar_try_wait(bar0, par0), r1 = mbar_try_wait(bar1, par1);  // the two round trips overlap
+  bool ok = true;
+  if (!r0) ok = wait_bounded(bar0, par0, ctl, where);
+  if (!r1 && ok) ok = wait_bounded(bar1, par1, ctl, where + 1);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// Shared-memory matrix descriptor, 64-byte swizzle.  lbo/sbo in bytes.
+__device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (sw128_desc(saddr, lbo, sbo) & ~((uint64_t)7 << 61)) | (uint64_t)4 << 61;
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
@@ -72,7 +96,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 }
 
 // ---------------------------------------------------------------------------
-// Scales.  Two warps copy the CTA's scales to shared memory, KC blocks of 128
+// Scales.  One or two warps copy the CTA's scales to shared memory, KC blocks of 128
 // at a time and two such chunks deep, so that the epilogue reads them there:
 // sa[KC][128 rows], sb[KC][NC columns] (or one value per 128 columns).  The
 // scales lie with the blocks of a row next to each other (or B's columns, for
@@ -97,13 +121,13 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 
 // Blocks kb0 .. kb0 + KC - 1 (at most kb_end) of rows [m0, m0 + 128) and columns
-// [n0, n0 + NC), by the 64 threads t.  Entries past the matrix repeat its last.
-template <int NC, bool TILE_B>
+// [n0, n0 + NC), by NT threads t.  Entries past the matrix repeat its last.
+template <int NC, bool TILE_B, int NT>
 __device__ __forceinline__ void load_scales(const Params& gp, ScaleChunk<NC>& c, int m0, int n0, int kb0, int kb_end,
                                             int t) {
   const int kbi = t & (KC - 1), kb = min(kb0 + kbi, kb_end - 1);
 #pragma unroll 4
-  for (int r = t >> 3; r < 128; r += 8)
+  for (int r = t >> 3; r < 128; r += NT / 8)
     cp_async4(smem_u32(&c.a[kbi][r]), gp.SA + (long long)min(m0 + r, gp.M - 1) * gp.KB + kb);
   if constexpr (TILE_B) {
     if (t < KC * (NC / 128)) {
@@ -113,11 +137,11 @@ __device__ __forceinline__ void load_scales(const Params& gp, ScaleChunk<NC>& c,
     }
   } else if (gp.sb_k == 1) {
 #pragma unroll 4
-    for (int n = t >> 3; n < NC; n += 8)
+    for (int n = t >> 3; n < NC; n += NT / 8)
       cp_async4(smem_u32(&c.b[kbi][n]), gp.SB + (long long)min(n0 + n, gp.N - 1) * gp.sb_n + kb);
   } else {
     for (int q = 0; q < KC; ++q)
-      for (int n = t; n < NC; n += 64)
+      for (int n = t; n < NC; n += NT)
         cp_async4(smem_u32(&c.b[q][n]),
                   gp.SB + (long long)min(n0 + n, gp.N - 1) * gp.sb_n + (long long)min(kb0 + q, kb_end - 1) * gp.sb_k);
   }
@@ -167,32 +191,58 @@ __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar_cluster
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
 }
 
-// Adds a block's product, read from tensor memory 32 columns at a time, to this
-// lane's sums of COLS columns: acc += p * s (TILE_B) or acc += (p * s) * sb[column].
-// `release` runs once the last read is complete.
+// Adds 32 columns of a block's product to a lane's sums: acc += p * s (TILE_B) or
+// acc += (p * s) * sb[column].
+template <bool TILE_B>
+__device__ __forceinline__ void add32(uint64_t* acc, const uint32_t (&c)[32], uint64_t s2, const ulonglong2* sb) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t p0 = pack2u(c[4 * i], c[4 * i + 1]), p1 = pack2u(c[4 * i + 2], c[4 * i + 3]);
+    if constexpr (TILE_B) {
+      acc[2 * i] = fma2(p0, s2, acc[2 * i]);
+      acc[2 * i + 1] = fma2(p1, s2, acc[2 * i + 1]);
+    } else {
+      acc[2 * i] = fma2(mul2(p0, s2), (uint64_t)sb[i].x, acc[2 * i]);
+      acc[2 * i + 1] = fma2(mul2(p1, s2), (uint64_t)sb[i].y, acc[2 * i + 1]);
+    }
+  }
+}
+
+// Adds a block's product, read from tensor memory, to this lane's sums of COLS
+// columns.  `release` runs once the last read is complete.  With one scale for
+// all columns 64 of them are read at a time, so that the release comes earlier;
+// with one each, their 32 scales take the other registers.
 template <int COLS, bool TILE_B, typename F>
 __device__ __forceinline__ void add_block(uint64_t (&acc)[COLS / 2], uint32_t taddr, float s, const float* sb,
                                           F&& release) {
   const uint64_t s2 = pack2(s, s);
+  if constexpr (TILE_B && COLS >= 64) {
 #pragma unroll
-  for (int h = 0; h < COLS / 32; ++h) {
-    uint32_t r[32];
-    tmem_ld32(taddr + 32 * h, r);
-    tmem_wait_ld();
-    pin32(r);
-    if (h == COLS / 32 - 1) release();
-    if constexpr (TILE_B) {
+    for (int h = 0; h < COLS / 64; ++h) {
+      uint32_t c[32], d[32];
+      tmem_ld32(taddr + 64 * h, c);
+      tmem_ld32(taddr + 64 * h + 32, d);
+      tmem_wait_ld();
+      pin32(c);
+      pin32(d);
+      if (h == COLS / 64 - 1) release();
+      add32<true>(&acc[32 * h], c, s2, nullptr);
+      add32<true>(&acc[32 * h + 16], d, s2, nullptr);
+    }
+  } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[16 * h + i] = fma2(pack2u(r[2 * i], r[2 * i + 1]), s2, acc[16 * h + i]);
-    } else {
-      const ulonglong2* sv = reinterpret_cast<const ulonglong2*>(sb + 32 * h);
+    for (int h = 0; h < COLS / 32; ++h) {
+      uint32_t c[32];
+      tmem_ld32(taddr + 32 * h, c);
+      tmem_wait_ld();
+      pin32(c);
+      if (h == COLS / 32 - 1) release();
+      ulonglong2 w[8];
+      if constexpr (!TILE_B) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const ulonglong2 v = sv[i];
-        uint64_t* a = &acc[16 * h + 2 * i];
-        a[0] = fma2(mul2(pack2u(r[4 * i], r[4 * i + 1]), s2), (uint64_t)v.x, a[0]);
-        a[1] = fma2(mul2(pack2u(r[4 * i + 2], r[4 * i + 3]), s2), (uint64_t)v.y, a[1]);
+        for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const ulonglong2*>(sb + 32 * h)[i];
       }
+      add32<TILE_B>(&acc[16 * h], c, s2, w);
     }
   }
 }
@@ -344,7 +394,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int kb = kb_lo; kb < kb_hi; kb += KC, ++c) {
       const int b = c & 1;
       if (!wait_bounded(smem_u32(&sempty[b]), ((c >> 1) & 1u) ^ 1u, ctl, 25)) break;
-      load_scales<BN1, TILE_B>(gp, scales[b], tm * 128, tn * BN1, kb, kb_hi, threadIdx.x - 64);
+      load_scales<BN1, TILE_B, 64>(gp, scales[b], tm * 128, tn * BN1, kb, kb_hi, threadIdx.x - 64);
       cp_async_arrive(smem_u32(&sfull[b]));
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -352,10 +402,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------ epilogue
     const int q4 = warp & 3;  // tensor-memory lane quarter this warp may access
     const int row = q4 * 32 + lane;
-    const int col0 = ((warp - 4) >> 2) * 64;
-    uint64_t acc[32];
+    constexpr int WC = BN1 * 4 / EPI_WARPS;  // columns per warp
+    const int col0 = ((warp - 4) >> 2) * WC;
+    uint64_t acc[WC / 2];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) acc[i] = 0;
+    for (int i = 0; i < WC / 2; ++i) acc[i] = 0;
     uint32_t it = 0;
     bool ok = true;
     for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
@@ -368,7 +419,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after();
       float s = sc.a[kbi][row];
       if constexpr (TILE_B) s *= sc.b[kbi][0];
-      add_block<64, TILE_B>(acc, tmem_base + ((uint32_t)(q4 * 32) << 16) + b * BN1 + col0, s, &sc.b[kbi][col0], [&] {
+      add_block<WC, TILE_B>(acc, tmem_base + ((uint32_t)(q4 * 32) << 16) + b * BN1 + col0, s, &sc.b[kbi][col0], [&] {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_relaxed(smem_u32(&tempty[b]));
@@ -383,7 +434,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (ok) {
       float* part = reinterpret_cast<float*>(stage_base) + row * PART_LD + col0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < WC / 4; ++i) {
         const float2 lo = unpack2(acc[2 * i]), hi = unpack2(acc[2 * i + 1]);
         *reinterpret_cast<float4*>(part + 4 * i) = make_float4(lo.x, lo.y, hi.x, hi.y);
       }
@@ -426,16 +477,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // Tiles of 256 x 256 on CTA pairs (cta_group::2), persistent.  Each CTA holds
 // 128 rows of A and 128 columns of B per stage and receives its own 128 rows
 // of the accumulator; its eight epilogue warps each keep 32 rows x 128 columns
-// of fp32 sums in registers (128 of them a lane).  The block is launched with
-// 168 registers a thread; the first warpgroup (producer, MMA issue, scales)
-// gives up 96 of them and the two epilogue warpgroups take 48 more each:
-// 72 + 2 * 216 = 3 * 168.
+// of fp32 sums in registers (128 of them a lane).
+//
+// The tile's two column halves are separate MMAs (M = 256, N = 128, each CTA
+// holding 64 of the 128 columns), issued by a warp each, into two alternating
+// accumulators of their own.  A block's product, its read-back and the way back
+// through the barriers is a chain of about 1300 cycles with whole 256-column
+// MMAs, of which only two are in flight; the halves' chains are shorter and
+// interleave.
+//
+// The block is launched with 168 registers a thread; the first warpgroup
+// (producer, MMA issue, scales) gives up 112 of them and the two epilogue
+// warpgroups take 56 more each: 56 + 2 * 224 = 3 * 168.
 // ---------------------------------------------------------------------------
 constexpr int BN2 = 256;
 constexpr int STAGES2 = 5;
 constexpr int STAGE2_BYTES = 2 * SLAB;
-constexpr int OUT_ROW = 128 + 16;  // bytes of a staged output row, padded against bank conflicts
-constexpr int OUT_WARP = 32 * OUT_ROW;
+constexpr int HALF_SLAB = SLAB / 2;  // a CTA's 64 columns of one half
+constexpr int PAIR_COLS = BN2 * 4 / EPI_WARPS;  // columns per epilogue warp
+constexpr int OUT_BUF = 32 * 64;  // 64 bytes of each of a warp's rows
+constexpr int OUT_WARP = 2 * OUT_BUF;
 constexpr int SCALE2_BYTES = SCALE_BUFS * (int)sizeof(ScaleChunk<BN2>);
 constexpr int SMEM2_BYTES = 1024 + STAGES2 * STAGE2_BYTES + EPI_WARPS * OUT_WARP + SCALE2_BYTES + 256;
 static_assert(SMEM2_BYTES <= 232448, "shared memory");
@@ -457,19 +518,26 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// This warp's 32 rows x 128 columns of sums (a lane holds a row) to C, through
-// the warp's staging buffer 128 bytes of each row at a time, so that the global
-// stores are whole 128-byte row segments.
+// This warp's 32 rows x 128 columns of sums (a lane holds a row) to C, 64 bytes
+// of each row at a time through two alternating staging buffers (16-byte chunks
+// swizzled as the TMA's 64-byte mode has them).  Where C's rows start on
+// 16-byte boundaries a TMA store takes each buffer away and cuts it to the
+// matrix; else the warp writes it entry by entry.
 template <int ES>  // bytes per entry of C
-__device__ __forceinline__ void store_rows(const Params& gp, const uint64_t (&acc)[64], uint8_t* stage, int row0,
-                                           int col0, int lane) {
-  constexpr int COLS = 128 / ES;
+__device__ __forceinline__ void store_rows(const Params& gp, const CUtensorMap* tmC,
+                                           const uint64_t (&acc)[PAIR_COLS / 2], uint8_t* stage, int row0, int col0,
+                                           int lane) {
+  constexpr int COLS = 64 / ES;
   const int rows = min(32, gp.M - row0);
 #pragma unroll
-  for (int c = 0; c < 128 / COLS; ++c) {
-    uint4* mine = reinterpret_cast<uint4*>(stage + lane * OUT_ROW);
+  for (int c = 0; c < PAIR_COLS / COLS; ++c) {
+    uint8_t* buf = stage + (c & 1) * OUT_BUF;
+    if (gp.vec_c) {  // the store that used this buffer before has read it
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {  // 16 bytes
+    for (int i = 0; i < 4; ++i) {  // 16 bytes
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -487,39 +555,42 @@ __device__ __forceinline__ void store_rows(const Params& gp, const uint64_t (&ac
           }
         }
       }
-      mine[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __syncwarp();
     const int cc = col0 + c * COLS;
-    const int cols = min(COLS, gp.N - cc);
-    uint8_t* out = static_cast<uint8_t*>(gp.C) + ((long long)row0 * gp.ldc + cc) * ES;
-    if (cols == COLS && gp.vec_c) {
-#pragma unroll
-      for (int r0 = 0; r0 < 32; r0 += 4) {
-        const int r = r0 + (lane >> 3), j = lane & 7;
-        if (r < rows)
-          *reinterpret_cast<uint4*>(out + (long long)r * gp.ldc * ES + 16 * j) =
-              *reinterpret_cast<const uint4*>(stage + r * OUT_ROW + 16 * j);
+    if (gp.vec_c) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (cc < gp.N)
+          asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                           reinterpret_cast<uint64_t>(tmC)),
+                       "r"(smem_u32(buf)), "r"(cc), "r"(row0)
+                       : "memory");
+        bulk_commit();
       }
     } else {
+      __syncwarp();
+      const int cols = min(COLS, gp.N - cc);
+      uint8_t* out = static_cast<uint8_t*>(gp.C) + ((long long)row0 * gp.ldc + cc) * ES;
       for (int r = 0; r < rows; ++r)
         for (int j = lane; j < cols; j += 32) {
+          const int at = j * ES;
+          const uint8_t* src = buf + r * 64 + (((at >> 4) ^ ((r >> 1) & 3)) << 4) + (at & 15);
           if constexpr (ES == 4)
-            reinterpret_cast<uint32_t*>(out + (long long)r * gp.ldc * ES)[j] =
-                reinterpret_cast<const uint32_t*>(stage + r * OUT_ROW)[j];
+            reinterpret_cast<uint32_t*>(out + (long long)r * gp.ldc * ES)[j] = *reinterpret_cast<const uint32_t*>(src);
           else
-            reinterpret_cast<uint16_t*>(out + (long long)r * gp.ldc * ES)[j] =
-                reinterpret_cast<const uint16_t*>(stage + r * OUT_ROW)[j];
+            reinterpret_cast<uint16_t*>(out + (long long)r * gp.ldc * ES)[j] = *reinterpret_cast<const uint16_t*>(src);
         }
+      __syncwarp();
     }
-    __syncwarp();
   }
 }
 
 template <bool B_KMAJOR, bool TILE_B>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     f8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                        const __grid_constant__ Params gp, DevPlan* plan) {
+                        const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Params gp, DevPlan* plan) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t rank = cluster_rank();
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
@@ -529,13 +600,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   ScaleChunk<BN2>* scales = reinterpret_cast<ScaleChunk<BN2>*>(out_base + EPI_WARPS * OUT_WARP);
   uint64_t* bars = reinterpret_cast<uint64_t*>(out_base + EPI_WARPS * OUT_WARP + SCALE2_BYTES);
   uint64_t* full = bars;
-  uint64_t* empty = bars + STAGES2;
-  uint64_t* tfull = bars + 2 * STAGES2;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* sfull = tfull + 4;
+  uint64_t* done = bars + STAGES2;         // by half * STAGES2 + stage: the half's MMAs of the stage are complete
+  uint64_t* tempty = bars + 3 * STAGES2;  // by half * 2 + accumulator
+  uint64_t* sfull = tempty + 4;
   uint64_t* sempty = sfull + SCALE_BUFS;
-  uint64_t* drain = sempty + SCALE_BUFS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = sempty + SCALE_BUFS;  // by half
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -544,17 +614,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES2; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(smem_u32(&done[s]), 1);
+      mbar_init(smem_u32(&done[STAGES2 + s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&tfull[b]), 1);
-      mbar_init(smem_u32(&tempty[b]), 2 * EPI_WARPS);  // the epilogue warps of both CTAs
-    }
+    for (int b = 0; b < 4; ++b) mbar_init(smem_u32(&tempty[b]), EPI_WARPS);  // the half's warps of both CTAs
     for (int b = 0; b < SCALE_BUFS; ++b) {
-      mbar_init(smem_u32(&sfull[b]), 64);
+      mbar_init(smem_u32(&sfull[b]), 32);
       mbar_init(smem_u32(&sempty[b]), EPI_WARPS);
     }
-    mbar_init(smem_u32(drain), 1);
+    for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&drain[h]), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_tmap(&tmA);
@@ -573,7 +641,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int total = gp.mt * gp.nt;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- producer (both CTAs)
       int stage = 0;
@@ -582,7 +650,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int t = cid; t < total && ok; t += ncl) {
         const int tn = t / gp.mt, tm = t - tn * gp.mt;
         for (int kb = 0; kb < gp.KB; ++kb) {
-          if (!wait_bounded_cluster(smem_u32(&empty[stage]), phase ^ 1u, ctl, 31)) {
+          if (!wait_bounded(smem_u32(&done[stage]), phase ^ 1u, ctl, 31) ||
+              !wait_bounded(smem_u32(&done[STAGES2 + stage]), phase ^ 1u, ctl, 31)) {
             ok = false;
             break;
           }
@@ -590,10 +659,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (rank == 0) mbar_arrive_expect_tx(fb_local, 2 * STAGE2_BYTES);
           const uint32_t fb = mapa_shared(fb_local, 0);
           const uint32_t a_dst = smem_u32(stage_base + stage * STAGE2_BYTES);
-          const int n0 = tn * BN2 + (int)rank * 128;
           tma_load_2d_pair(a_dst, &tmA, fb, kb * BK, tm * 256 + (int)rank * 128);
-          if constexpr (B_KMAJOR) tma_load_2d_pair(a_dst + SLAB, &tmB, fb, kb * BK, n0);
-          else tma_load_2d_pair(a_dst + SLAB, &tmB, fb, n0, kb * BK);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t b_dst = a_dst + SLAB + h * HALF_SLAB;
+            const int n0 = tn * BN2 + h * 128 + (int)rank * 64;
+            if constexpr (B_KMAJOR) tma_load_2d_pair(b_dst, &tmB, fb, kb * BK, n0);
+            else tma_load_2d_pair(b_dst, &tmB, fb, n0, kb * BK);
+          }
           if (++stage == STAGES2) {
             stage = 0;
             phase ^= 1u;
@@ -601,32 +674,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
     }
-    if (warp == 1 && lane == 0 && rank == 0) {
-      // ---------------------------------------------------------- MMA issuer (first CTA)
+    if ((warp == 1 || warp == 2) && rank == 0) {
+      // ---------------------------------------------------------- MMA issuers (first CTA), one warp per half
+      const int half = __shfl_sync(0xFFFFFFFFu, warp - 1, 0);
+      const uint32_t a_addr = smem_u32(stage_base), b_addr = a_addr + SLAB + half * HALF_SLAB;
+      const uint64_t adesc0 = sw128_desc(a_addr, 16, 1024);
+      // N-major: 64 columns are one 64-byte swizzle row per k, eight k to a group of 512 bytes
+      const uint64_t bdesc0 = B_KMAJOR ? sw128_desc(b_addr, 16, 1024) : sw64_desc(b_addr, HALF_SLAB, 512);
+      constexpr uint32_t b_step = B_KMAJOR ? 2 : 128;  // 32 k: 32 bytes along a row, or 32 rows of 64 bytes
+      constexpr uint32_t idesc = idesc_f8(256, 128, B_KMAJOR);
       int stage = 0;
       uint32_t phase = 0, it = 0;
       bool ok = true;
       for (int t = cid; t < total && ok; t += ncl) {
         for (int kb = 0; kb < gp.KB; ++kb, ++it) {
           const uint32_t b = it & 1u, aph = (it >> 1) & 1u;
-          if (!wait_bounded_cluster(smem_u32(&tempty[b]), aph ^ 1u, ctl, 32) ||
-              !wait_bounded_cluster(smem_u32(&full[stage]), phase, ctl, 33)) {
-            ok = false;
-            break;
-          }
+          ok = wait_both(smem_u32(&tempty[half * 2 + b]), aph ^ 1u, smem_u32(&full[stage]), phase, ctl, 32);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(stage_base + stage * STAGE2_BYTES);
-          const uint64_t adesc = sw128_desc(a_addr, 16, 1024);
-          const uint64_t bdesc =
-              B_KMAJOR ? sw128_desc(a_addr + SLAB, 16, 1024) : sw128_desc(a_addr + SLAB, SLAB, 1024);
-          constexpr uint32_t b_step = B_KMAJOR ? 2 : 256;
-          constexpr uint32_t idesc = idesc_f8(256, BN2, B_KMAJOR);
+          const uint64_t off = (uint64_t)(stage * (STAGE2_BYTES >> 4));
+          const uint32_t d = tmem_base + (half * 2 + b) * 128;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            umma_f8_pair(tmem_base + b * BN2, adesc + (uint64_t)(2 * kk), bdesc + (uint64_t)(b_step * kk), idesc,
-                         kk > 0);
-          umma_commit_pair(smem_u32(&empty[stage]));
-          if (!(gp.fault == 1 && it == 0)) umma_commit_pair(smem_u32(&tfull[b]));
+            for (int kk = 0; kk < BK / 32; ++kk)
+              umma_f8_pair(d, adesc0 + off + (uint64_t)(2 * kk), bdesc0 + off + (uint64_t)(b_step * kk), idesc, kk > 0);
+            if (!(gp.fault == 1 && it == 0)) umma_commit_pair(smem_u32(&done[half * STAGES2 + stage]));
+          }
+          __syncwarp();
           if (++stage == STAGES2) {
             stage = 0;
             phase ^= 1u;
@@ -637,11 +711,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         Ctl drain_ctl = ctl;
         volatile int never = 0;
         drain_ctl.abort = &never;
-        umma_commit_pair_local(smem_u32(drain));
-        wait_bounded(smem_u32(drain), 0, drain_ctl, 0);
+        if (elect_one()) umma_commit_pair_local(smem_u32(&drain[half]));
+        __syncwarp();
+        wait_bounded(smem_u32(&drain[half]), 0, drain_ctl, 0);
       }
     }
-    if (warp >= 2) {
+    if (warp == 3) {
       // ---------------------------------------------------------- scales (both CTAs)
       int c = 0;
       bool ok = true;
@@ -651,7 +726,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const int b = c & 1;
           ok = wait_bounded(smem_u32(&sempty[b]), ((c >> 1) & 1u) ^ 1u, ctl, 35);
           if (!ok) break;
-          load_scales<BN2, TILE_B>(gp, scales[b], tm * 256 + (int)rank * 128, tn * BN2, kb, gp.KB, threadIdx.x - 64);
+          load_scales<BN2, TILE_B, 32>(gp, scales[b], tm * 256 + (int)rank * 128, tn * BN2, kb, gp.KB, lane);
           cp_async_arrive(smem_u32(&sfull[b]));
         }
       }
@@ -659,32 +734,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue (both CTAs)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q4 = warp & 3, ew = warp - 4;
-    const int half = ew >> 2;  // this warp's 128 of the 256 columns
+    const int half = ew / (EPI_WARPS / 2);
+    const int col = (ew >> 2) * PAIR_COLS;  // of the tile
     uint8_t* stage = out_base + ew * OUT_WARP;
-    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
-    const uint32_t lane_addr = tmem_base + ((uint32_t)(q4 * 32) << 16) + half * 128;
-    uint32_t it = 0;
-    int chunk = 0;
+    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[half * 2]), 0),
+                                       mapa_shared(smem_u32(&tempty[half * 2 + 1]), 0)};
+    const uint32_t lane_addr = tmem_base + ((uint32_t)(q4 * 32) << 16) + half * 256 + (col & 127);
+    uint32_t it = 0, phase = 0;
+    int chunk = 0, st = 0;  // pipeline stage
     bool ok = true;
     for (int t = cid; t < total && ok; t += ncl) {
       const int tn = t / gp.mt, tm = t - tn * gp.mt;
-      const int row0 = tm * 256 + (int)rank * 128 + q4 * 32, col0 = tn * BN2 + half * 128;
-      uint64_t acc[64];
+      const int row0 = tm * 256 + (int)rank * 128 + q4 * 32, col0 = tn * BN2 + col;
+      uint64_t acc[PAIR_COLS / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
+      for (int i = 0; i < PAIR_COLS / 2; ++i) acc[i] = 0;
       for (int kb = 0; kb < gp.KB; ++kb, ++it) {
-        const uint32_t b = it & 1u, aph = (it >> 1) & 1u;
+        const uint32_t b = it & 1u;
         const int kbi = kb % KC;
         const ScaleChunk<BN2>& sc = scales[chunk & 1];
         ok = kbi != 0 || wait_bounded(smem_u32(&sfull[chunk & 1]), (chunk >> 1) & 1u, ctl, 36);
-        ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded_cluster(smem_u32(&tfull[b]), aph, ctl, 34));
+        ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded(smem_u32(&done[half * STAGES2 + st]), phase, ctl, 34));
+        if (++st == STAGES2) {
+          st = 0;
+          phase ^= 1u;
+        }
         if (!ok) break;
         tc_fence_after();
         float s = sc.a[kbi][q4 * 32 + lane];
         if constexpr (TILE_B) s *= sc.b[kbi][half];
-        add_block<128, TILE_B>(acc, lane_addr + b * BN2, s, &sc.b[kbi][half * 128], [&] {
+        add_block<PAIR_COLS, TILE_B>(acc, lane_addr + b * 128, s, &sc.b[kbi][col], [&] {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_relaxed_cluster(tempty_leader[b]);
@@ -696,10 +777,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if (ok && row0 < gp.M && col0 < gp.N) {
-        if (gp.out_type == RG_TYPE_F32) store_rows<4>(gp, acc, stage, row0, col0, lane);
-        else store_rows<2>(gp, acc, stage, row0, col0, lane);
+        if (gp.out_type == RG_TYPE_F32) store_rows<4>(gp, &tmC, acc, stage, row0, col0, lane);
+        else store_rows<2>(gp, &tmC, acc, stage, row0, col0, lane);
       }
     }
+    bulk_wait0();
   }
 
   __syncwarp();  // whole warps again before the abort check and the barriers below
@@ -725,15 +807,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // Host side
 // ---------------------------------------------------------------------------
 bool make_map_2d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t stride_bytes, uint32_t b0,
-                 uint32_t b1) {
+                 uint32_t b1, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,
+                 CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {d0, d1};
   cuuint64_t strides[1] = {stride_bytes};
   cuuint32_t box[2] = {b0, b1};
   cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -756,7 +839,7 @@ using TileKernel = void (*)(const CUtensorMap, const CUtensorMap, const Params, 
 constexpr TileKernel kTileKernels[2][2] = {{f8_gemm_tile_kernel<false, false>, f8_gemm_tile_kernel<false, true>},
                                            {f8_gemm_tile_kernel<true, false>, f8_gemm_tile_kernel<true, true>}};
 
-using PairKernel = void (*)(const CUtensorMap, const CUtensorMap, const Params, DevPlan*);
+using PairKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const Params, DevPlan*);
 constexpr PairKernel kPairKernels[2][2] = {{f8_gemm_pair_kernel<false, false>, f8_gemm_pair_kernel<false, true>},
                                            {f8_gemm_pair_kernel<true, false>, f8_gemm_pair_kernel<true, true>}};
 
@@ -826,20 +909,28 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
   p.vec_c = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc * es % 16 == 0;
   p.fault = fault;
   p.wait_ns = wait_ns;
-  CUtensorMap ma, mb;
-  if (!make_map_2d(&ma, a.A, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.lda, BK, 128) ||
-      !(a.b_kmajor ? make_map_2d(&mb, a.B, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.ldb, BK, 128)
-                   : make_map_2d(&mb, a.B, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.ldb, 128, BK)))
-    return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
   const int variant = gemm_variant();
   const long long tiles2 = ((a.M + 255) / 256) * ((a.N + BN2 - 1) / BN2);
-  if (variant == 2 || (variant == 0 && tiles2 >= fd.max_pairs)) {
+  const bool pair = variant == 2 || (variant == 0 && tiles2 >= fd.max_pairs);
+  const uint32_t b_cols = pair ? 64 : 128;  // columns of B per copy
+  CUtensorMap ma, mb;
+  if (!make_map_2d(&ma, a.A, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.lda, BK, 128) ||
+      !(a.b_kmajor ? make_map_2d(&mb, a.B, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.ldb, BK, b_cols)
+                   : make_map_2d(&mb, a.B, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.ldb, b_cols, BK,
+                                 pair ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)))
+    return cudaErrorInvalidValue;
+  if (pair) {
     p.mt = (int)((a.M + 255) / 256);
     p.nt = (int)((a.N + BN2 - 1) / BN2);
     const long long clusters = tiles2 < fd.max_pairs ? tiles2 : fd.max_pairs;
     cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(2 * clusters)), NUM_THREADS, SMEM2_BYTES, st, 2, attr);
-    return cudaLaunchKernelEx(&cfg, kPairKernels[a.b_kmajor][a.tile_b], ma, mb, p, plan);
+    CUtensorMap mc = {};
+    if (p.vec_c && !make_map_2d(&mc, a.C, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.ldc * es, 64 / es, 32,
+                                CU_TENSOR_MAP_SWIZZLE_64B,
+                                es == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16))
+      return cudaErrorInvalidValue;
+    return cudaLaunchKernelEx(&cfg, kPairKernels[a.b_kmajor][a.tile_b], ma, mb, mc, p, plan);
   }
   const long long tiles = (long long)p.mt * p.nt;
   int S = 1;
