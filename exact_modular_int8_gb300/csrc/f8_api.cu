@@ -89,10 +89,13 @@ int moe_layer_f8(const void* X, int x_type, const void* WR, const uint8_t* W13, 
             !aligned16(W13, 0) || !aligned16(W2, 0) || !aligned16(Y, 0)))
     return RG_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(ws, 0, sizeof(DevPlan), st) != cudaSuccess) return RG_ERR_CUDA;
   if (T) {
     const MoeArgs a{X, WR, W13, S13, W2, S2, Y, T, H, I, E, top_k, x_type, renorm != 0};
-    if (launch_moe_f8(a, static_cast<uint8_t*>(ws) + kCallBlockBytes, st) != cudaSuccess) return RG_ERR_CUDA;
+    if (launch_moe_f8(a, static_cast<DevPlan*>(ws), static_cast<uint8_t*>(ws) + kCallBlockBytes, st,
+                      wait_limit_ns()) != cudaSuccess)
+      return RG_ERR_CUDA;
+  } else if (cudaMemsetAsync(ws, 0, sizeof(DevPlan), st) != cudaSuccess) {
+    return RG_ERR_CUDA;
   }
   return finish_call(ws, st, flags);
 }

@@ -56,6 +56,7 @@ struct MoeArgs {
   bool renorm;
 };
 size_t moe_f8_scratch_bytes(long long T, long long H, long long I, long long E, long long top_k);
-cudaError_t launch_moe_f8(const MoeArgs& a, void* scratch, cudaStream_t st);
+cudaError_t launch_moe_f8(const MoeArgs& a, DevPlan* plan, void* scratch, cudaStream_t st,
+                          unsigned long long wait_ns);
 
 }  // namespace rg

@@ -38,6 +38,11 @@ constexpr int kMaxT = RG_MOE_MAX_TOKENS;
 constexpr int kMaxK = RG_MOE_MAX_TOP_K;
 constexpr int kMaxE = RG_MOE_MAX_EXPERTS;
 constexpr int kSlots = kMaxT * kMaxK;
+constexpr int kMaxNT = 4;            // column tiles of eight tokens per pass over the weights
+constexpr int kRing = 6;             // weight pieces (16 rows x 128 k) per warp, on their way or in use
+constexpr int kPiece = 16 * 128;
+constexpr int kColsBytes = 76 * 1024;  // the tokens' operand of one expert
+constexpr int kRedLd = 8 * kMaxNT + 4;
 
 struct MoeWs {
   float* logits;     // [T][E]
@@ -45,6 +50,7 @@ struct MoeWs {
   float* x_inv;      // [T] 2^-n
   float* h;          // [T * top_k][I]
   uint32_t* h_max;   // [T * top_k] largest |h|, as bits
+  unsigned* arrived;  // CTAs that have reached the grid's barriers
   float* part;       // [T * top_k][H] the experts' outputs
 };
 
@@ -59,6 +65,10 @@ struct MoeParams {
   int T, H, I, E, top_k;
   int type;  // of X, WR and Y
   int renorm;
+  int ks_up, ks_down;    // warps that split k in the two products
+  int cap_up, cap_down;  // tokens per pass
+  unsigned long long wait_ns;
+  DevPlan* plan;
   MoeWs w;
 };
 
@@ -82,38 +92,102 @@ __device__ __forceinline__ float2 pow2_scale(uint32_t max_bits) {
 }
 
 // ---------------------------------------------------------------------------
-// Phase 1: router logits, scaled fp16 copies of the tokens
+// Kernel 1: router logits (16 experts x 8 tokens per block, its warps splitting
+// k; the products of 16-bit entries are exact in the MMA's fp32), scaled fp16
+// copies of the tokens, and the words that kernel 2 starts from.
 // ---------------------------------------------------------------------------
 template <typename T>
-__device__ void router_phase(const MoeParams& p, int cta, int ctas) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ void mma_t(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1);
+template <>
+__device__ __forceinline__ void mma_t<__half>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma_t<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                     uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) moe_router_kernel(MoeParams p) {
+  __shared__ float red[kWarps][16][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const T* X = static_cast<const T*>(p.X);
-  const T* WR = static_cast<const T*>(p.WR);
-  for (int i = cta * kWarps + warp; i < p.T * (p.E + 1); i += ctas * kWarps) {
-    const int t = i / (p.E + 1), e = i - t * (p.E + 1);
+  const int te = (p.E + 15) / 16, tt = (p.T + 7) / 8;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.plan->status = 0;
+    p.plan->timeout_where = 0;
+    *p.w.arrived = 0;
+  }
+  if ((int)blockIdx.x >= te * tt) {  // one token: its largest entry, then the scaled copy
+    const int t = (int)blockIdx.x - te * tt;
     const T* x = X + (long long)t * p.H;
-    if (e < p.E) {
-      const T* w = WR + (long long)e * p.H;
-      float s = 0.0f;
-      for (int k = lane * 8; k < p.H; k += 256) {  // H is a multiple of 16
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k)), b = __ldg(reinterpret_cast<const uint4*>(w + k));
-        const T* av = reinterpret_cast<const T*>(&a);
-        const T* bv = reinterpret_cast<const T*>(&b);
+    uint32_t m = 0;
+    for (int k = threadIdx.x * 8; k < p.H; k += kThreads * 8) {  // H is a multiple of 16
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k));
+      const T* v = reinterpret_cast<const T*>(&a);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(to_f(av[j]), to_f(bv[j]), s);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      if (lane == 0) p.w.logits[t * p.E + e] = s;
-    } else {
-      uint32_t m = 0;
-      for (int k = lane; k < p.H; k += 32) m = max(m, __float_as_uint(to_f(x[k])) & 0x7FFFFFFFu);
-      m = __reduce_max_sync(0xFFFFFFFFu, m);
-      const float2 sc = pow2_scale(m);
-      for (int k = lane; k < p.H; k += 32) p.w.xs[(long long)t * p.H + k] = __float2half_rn(to_f(x[k]) * sc.x);
-      if (lane == 0) p.w.x_inv[t] = sc.y;
-      for (int j = lane; j < p.top_k; j += 32) p.w.h_max[t * p.top_k + j] = 0;
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(to_f(v[j])) & 0x7FFFFFFFu);
     }
+    uint32_t* wmax = reinterpret_cast<uint32_t*>(red);
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (lane == 0) wmax[warp] = m;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) m = max(m, wmax[w]);
+    const float2 sc = pow2_scale(m);
+    for (int k = threadIdx.x * 8; k < p.H; k += kThreads * 8) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k));
+      const T* v = reinterpret_cast<const T*>(&a);
+      uint4 o;
+      uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half2 h = __floats2half2_rn(to_f(v[2 * j]) * sc.x, to_f(v[2 * j + 1]) * sc.x);
+        ow[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(p.w.xs + (long long)t * p.H + k) = o;
+    }
+    if (threadIdx.x == 0) p.w.x_inv[t] = sc.y;
+    if ((int)threadIdx.x < p.top_k) p.w.h_max[t * p.top_k + threadIdx.x] = 0;
+    return;
+  }
+  const int e0 = (int)(blockIdx.x % te) * 16, t0 = (int)(blockIdx.x / te) * 8;
+  const T* WR = static_cast<const T*>(p.WR);
+  // rows past the last repeat it; their results are dropped
+  const T* wa = WR + (long long)min(e0 + g, p.E - 1) * p.H;
+  const T* wb = WR + (long long)min(e0 + g + 8, p.E - 1) * p.H;
+  const T* xb = X + (long long)min(t0 + g, p.T - 1) * p.H;
+  float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int k = warp * 32 + t4 * 8; k - t4 * 8 < p.H; k += kWarps * 32) {
+    uint4 a = make_uint4(0, 0, 0, 0), b = a, x = a;
+    if (k < p.H) {
+      a = __ldg(reinterpret_cast<const uint4*>(wa + k));
+      b = __ldg(reinterpret_cast<const uint4*>(wb + k));
+      x = __ldg(reinterpret_cast<const uint4*>(xb + k));
+    }
+    mma_t<T>(c, a.x, b.x, a.y, b.y, x.x, x.y);
+    mma_t<T>(c, a.z, b.z, a.w, b.w, x.z, x.w);
+  }
+  red[warp][g][2 * t4] = c[0];
+  red[warp][g][2 * t4 + 1] = c[1];
+  red[warp][g + 8][2 * t4] = c[2];
+  red[warp][g + 8][2 * t4 + 1] = c[3];
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    const int e = threadIdx.x & 15, t = threadIdx.x >> 4;
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += red[w][e][t];
+    if (e0 + e < p.E && t0 + t < p.T) p.w.logits[(t0 + t) * p.E + e0 + e] = s;
   }
 }
 
@@ -126,9 +200,11 @@ struct Routing {
   short order[kSlots];           // slots, grouped by expert
   short start[kMaxE + 1];        // of each expert's group
   short active[kMaxE];           // experts with tokens
-  short fill[kMaxE];
+  int fill[kMaxE];
   int counts[kMaxE];
+  int units[kMaxE + 1];          // of a product phase: first unit of each active expert
   int num_active;
+  int go;                        // the grid's barrier was passed
 };
 
 // Order of floats as unsigned integers; NaN sorts by its bits (the softmax
@@ -138,6 +214,7 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+template <int PER>  // E <= 32 PER
 __device__ void form_routing(const MoeParams& p, Routing& r) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
@@ -145,7 +222,6 @@ __device__ void form_routing(const MoeParams& p, Routing& r) {
     r.fill[e] = 0;
   }
   __syncthreads();
-  constexpr int PER = (kMaxE + 31) / 32;
   for (int t = warp; t < p.T; t += kWarps) {
     const float* lg = p.w.logits + t * p.E;
     float v[PER];
@@ -233,218 +309,342 @@ __device__ void form_routing(const MoeParams& p, Routing& r) {
     }
   }
   __syncthreads();
-  // slots in their own order within each expert's group
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
-    if (r.counts[e] == 0) continue;
-    int at = r.start[e];
-    for (int s = 0; s < p.T * p.top_k; ++s)
-      if (r.expert[s] == e) r.order[at++] = (short)s;
+  // Slots in their own order within each expert's group, 32 at a time.  The
+  // order has to be the same in every CTA: passes over an expert take tokens by it.
+  if (warp == 0) {
+    for (int s0 = 0; s0 < p.T * p.top_k; s0 += 32) {
+      const int s = s0 + lane;
+      const bool live = s < p.T * p.top_k;
+      const int e = live ? r.expert[s] : -1;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      const int base = live ? r.start[e] + r.fill[e] : 0;
+      __syncwarp();
+      if (live) {
+        r.order[base + before] = (short)s;
+        if (before == 0) r.fill[e] += __popc(same);
+      }
+      __syncwarp();
+    }
   }
   __syncthreads();
 }
 
+// All CTAs of the (cooperative) grid, bounded in time.
+__device__ bool grid_barrier(const MoeParams& p, Routing& r, unsigned target) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(p.w.arrived, 1u);
+    unsigned long long t0 = 0;
+    int ok = 1;
+    for (uint32_t i = 1;; ++i) {
+      unsigned n;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(n) : "l"(p.w.arrived) : "memory");
+      if (n >= target) break;
+      if ((i & 63u) == 0) {
+        unsigned long long now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (!t0) t0 = now;
+        if (now - t0 > p.wait_ns) {
+          ok = 0;
+          atomicCAS(&p.plan->status, 0, RG_ERR_TIMEOUT);
+          atomicCAS(&p.plan->timeout_where, 0, 41);
+          break;
+        }
+      }
+    }
+    r.go = ok;
+  }
+  __syncthreads();
+  return r.go != 0;
+}
+
 // ---------------------------------------------------------------------------
-// The product core: 16 weight rows times up to 8 NT columns over the 128-blocks
-// kb0, kb0 + step, ... of k.
+// The products.  A unit is 16 weight rows times the (up to cap) tokens of one
+// pass over an expert.  A group of ks warps works on a unit, each on every ks-th
+// 128-block of k, and the groups of all CTAs share the units out evenly, in
+// contiguous ranges per CTA, so that a CTA stages an expert's tokens in shared
+// memory once.  Every lane copies the weights it will use itself, kRing - 1
+// pieces ahead of their use and across units (cp.async, 2 KB a piece and warp:
+// 80 KB on their way per SM, where the latency times the bandwidth of this
+// memory needs about 45).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {  // the low 16 bits: two E4M3 values
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
   return h;
 }
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;  // zeros where there is nothing to read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 
-// Columns (tokens) of the second operand, 16 consecutive k at a time, as eight
-// fp16 pairs.
-struct HalfColumns {  // fp16 rows
-  const __half* base[8];
-  __device__ __forceinline__ void load(int nt, int k, bool live, uint32_t (&b)[8]) const {
-    uint4 u = make_uint4(0, 0, 0, 0), v = u;
-    if (live) {
-      u = __ldcg(reinterpret_cast<const uint4*>(base[nt] + k));
-      v = __ldcg(reinterpret_cast<const uint4*>(base[nt] + k) + 1);
-    }
-    b[0] = u.x; b[1] = u.y; b[2] = u.z; b[3] = u.w;
-    b[4] = v.x; b[5] = v.y; b[6] = v.z; b[7] = v.w;
-  }
-};
-struct FloatColumns {  // fp32 rows, scaled and rounded to fp16 here
-  const float* base[8];
-  float scale[8];
-  __device__ __forceinline__ void load(int nt, int k, bool live, uint32_t (&b)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (live) f = __ldcg(reinterpret_cast<const float4*>(base[nt] + k) + i);
-      const __half2 lo = __floats2half2_rn(f.x * scale[nt], f.y * scale[nt]);
-      const __half2 hi = __floats2half2_rn(f.z * scale[nt], f.w * scale[nt]);
-      b[2 * i] = *reinterpret_cast<const uint32_t*>(&lo);
-      b[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
-    }
-  }
-};
-
-// row_lo / row_hi: this lane's two weight rows (null: zeros), K long (a multiple
-// of 16); s_lo / s_hi: their scales along k.
-template <int NT, typename Cols>
-__device__ __forceinline__ void rows_product(const uint8_t* row_lo, const uint8_t* row_hi, const float* s_lo,
-                                             const float* s_hi, int K, int kb0, int step, const Cols& cols,
-                                             float (&tot)[NT][4]) {
-  const int t4 = threadIdx.x & 3;
-  const int nkb = (K + 127) / 128;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) tot[n][i] = 0.0f;
-  for (int kb = kb0; kb < nkb; kb += step) {
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int k = kb * 128 + half * 64 + t4 * 16;
-      const bool live = k < K;
-      uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-      if (live && row_lo) lo = __ldg(reinterpret_cast<const uint4*>(row_lo + k));
-      if (live && row_hi) hi = __ldg(reinterpret_cast<const uint4*>(row_hi + k));
-      const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-      uint32_t a[4][4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        a[j][0] = e4m3x2_to_h2(wl[j]);
-        a[j][1] = e4m3x2_to_h2(wh[j]);
-        a[j][2] = e4m3x2_to_h2(wl[j] >> 16);
-        a[j][3] = e4m3x2_to_h2(wh[j] >> 16);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        uint32_t b[8];
-        cols.load(n, k, live, b);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mma_f16(acc[n], a[j], b[2 * j], b[2 * j + 1]);
-      }
-    }
-    const float s0 = __ldg(s_lo + kb), s1 = __ldg(s_hi + kb);
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      tot[n][0] = fmaf(acc[n][0], s0, tot[n][0]);
-      tot[n][1] = fmaf(acc[n][1], s0, tot[n][1]);
-      tot[n][2] = fmaf(acc[n][2], s1, tot[n][2]);
-      tot[n][3] = fmaf(acc[n][3], s1, tot[n][3]);
-    }
-  }
-}
-
-constexpr int kRedLd = 8 * 8 + 4;  // columns of a warp's partial sums, padded
 struct Smem {
   Routing r;
-  float red[kWarps][16][kRedLd];
+  __align__(16) float red[2][kWarps][16][kRedLd];
+  __align__(16) uint8_t ring[kWarps][kRing][kPiece + 16];  // 16 rows x 128 k as the lanes copied them, two scales
+  __align__(16) uint8_t cols[kColsBytes];
 };
-
-// ---------------------------------------------------------------------------
-// Phase 2: h = silu(x G^T) * (x U^T), eight columns of h per unit (their eight
-// gate rows and eight up rows are one 16-row operand); warps split k.
-// ---------------------------------------------------------------------------
-template <int NT>
-__device__ void up_unit(const MoeParams& p, Smem& sm, int e, int r0, int first, int n_tok) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const Routing& r = sm.r;
-  HalfColumns cols;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int c = min(n * 8 + g, n_tok - 1);  // columns past the last repeat it and are not stored
-    cols.base[n] = p.w.xs + (long long)(r.order[first + c] / p.top_k) * p.H;
-  }
-  const int hb = (p.H + 127) / 128, ib = (2 * p.I + 127) / 128;
-  const uint8_t* W = p.W13 + (long long)e * 2 * p.I * p.H;
-  const float* S = p.S13 + (long long)e * ib * hb;
-  const int row = r0 + g;
-  float tot[NT][4];
-  rows_product<NT>(W + (long long)row * p.H, W + (long long)(p.I + row) * p.H, S + (long long)(row / 128) * hb,
-                   S + (long long)((p.I + row) / 128) * hb, p.H, warp, kWarps, cols, tot);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    *reinterpret_cast<float2*>(&sm.red[warp][g][n * 8 + 2 * t4]) = make_float2(tot[n][0], tot[n][1]);
-    *reinterpret_cast<float2*>(&sm.red[warp][g + 8][n * 8 + 2 * t4]) = make_float2(tot[n][2], tot[n][3]);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 8 * n_tok; i += kThreads) {
-    const int c = i >> 3, rr = i & 7;
-    float a = 0.0f, u = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      a += sm.red[w][rr][c];
-      u += sm.red[w][rr + 8][c];
-    }
-    const int slot = r.order[first + c];
-    const float inv = p.w.x_inv[slot / p.top_k];
-    a *= inv;
-    u *= inv;
-    const float h = a / (1.0f + expf(-a)) * u;
-    p.w.h[(long long)slot * p.I + r0 + rr] = h;
-    atomicMax(&p.w.h_max[slot], __float_as_uint(h) & 0x7FFFFFFFu);  // a maximum: the order does not matter
-  }
-  __syncthreads();
-}
-
-// ---------------------------------------------------------------------------
-// Phase 3: an expert's output for its tokens, 16 rows of D per unit.
-// ---------------------------------------------------------------------------
-template <int NT>
-__device__ void down_unit(const MoeParams& p, Smem& sm, int e, int r0, int first, int n_tok) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  const Routing& r = sm.r;
-  FloatColumns cols;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int slot = r.order[first + min(n * 8 + g, n_tok - 1)];
-    cols.base[n] = p.w.h + (long long)slot * p.I;
-    cols.scale[n] = pow2_scale(__ldcg(&p.w.h_max[slot])).x;
-  }
-  const int hb = (p.H + 127) / 128, ib = (p.I + 127) / 128;
-  const uint8_t* W = p.W2 + (long long)e * p.H * p.I + (long long)(r0 + g) * p.I;
-  const float* S = p.S2 + ((long long)e * hb + r0 / 128) * ib;
-  float tot[NT][4];
-  rows_product<NT>(W, W + 8LL * p.I, S, S, p.I, warp, kWarps, cols, tot);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    *reinterpret_cast<float2*>(&sm.red[warp][g][n * 8 + 2 * t4]) = make_float2(tot[n][0], tot[n][1]);
-    *reinterpret_cast<float2*>(&sm.red[warp][g + 8][n * 8 + 2 * t4]) = make_float2(tot[n][2], tot[n][3]);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 16 * n_tok; i += kThreads) {
-    const int c = i >> 4, rr = i & 15;
-    float y = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) y += sm.red[w][rr][c];
-    const int slot = r.order[first + c];
-    p.w.part[(long long)slot * p.H + r0 + rr] = y * pow2_scale(__ldcg(&p.w.h_max[slot])).y;
-  }
-  __syncthreads();
-}
+static_assert(sizeof(Smem) <= 232448, "shared memory");
+static_assert((RG_MOE_MAX_WIDTH + 127) / 128 * 256 + 16 <= kColsBytes, "one token of the widest layer");
 
 template <bool UP>
-__device__ void expert_phase(const MoeParams& p, Smem& sm, int cta, int ctas) {
-  const int groups = UP ? p.I / 8 : p.H / 16;
-  const int units = sm.r.num_active * groups;
-  for (int u = cta; u < units; u += ctas) {
-    const int a = u / groups, e = sm.r.active[a], r0 = (u - a * groups) * (UP ? 8 : 16);
-    const int first = sm.r.start[e], n = sm.r.counts[e];
-#define RG_MOE_UNIT(NT) (UP ? up_unit<NT>(p, sm, e, r0, first, n) : down_unit<NT>(p, sm, e, r0, first, n))
-    if (n <= 8) RG_MOE_UNIT(1);
-    else if (n <= 16) RG_MOE_UNIT(2);
-    else if (n <= 32) RG_MOE_UNIT(4);
-    else RG_MOE_UNIT(8);
-#undef RG_MOE_UNIT
+struct Phase {
+  const MoeParams& p;
+  Smem& sm;
+  const int warp, lane, g, t4;
+  const int K, nkb, ks, groups, group, kpart, rows_per_expert;
+  int u0, u1;            // this CTA's units
+  // the next piece to copy
+  int pu, pkb, pa;
+  const uint8_t* p_lo;
+  const uint8_t* p_hi;
+  const float* p_slo;
+  const float* p_shi;
+  int slot;              // ring slot of the next piece to use
+  int parity;            // of the reduction buffers
+
+  __device__ Phase(const MoeParams& pp, Smem& s)
+      : p(pp), sm(s), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2),
+        t4(threadIdx.x & 3), K(UP ? pp.H : pp.I), nkb((K + 127) / 128), ks(UP ? pp.ks_up : pp.ks_down),
+        groups(kWarps / ks), group((threadIdx.x >> 5) / ks), kpart((threadIdx.x >> 5) % ks),
+        rows_per_expert(UP ? pp.I / 8 : pp.H / 16), slot(0), parity(0) {}
+
+  __device__ int cap() const { return UP ? p.cap_up : p.cap_down; }
+
+  // Units of the active experts, and this CTA's range of them.
+  __device__ void plan_units(int cta, int ctas) {
+    Routing& r = sm.r;
+    __syncthreads();
+    if (warp == 0) {
+      int base = 0;
+      for (int a0 = 0; a0 < r.num_active; a0 += 32) {
+        const int a = a0 + lane;
+        const int n = a < r.num_active ? (r.counts[r.active[a]] + cap() - 1) / cap() * rows_per_expert : 0;
+        int s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xFFFFFFFFu, s, o);
+          if (lane >= o) s += v;
+        }
+        if (a < r.num_active) r.units[a] = base + s - n;
+        base += __shfl_sync(0xFFFFFFFFu, s, 31);
+      }
+      if (lane == 0) r.units[r.num_active] = base;
+    }
+    __syncthreads();
+    const long long total = r.units[r.num_active];
+    u0 = (int)(total * cta / ctas);
+    u1 = (int)(total * (cta + 1) / ctas);
+    pu = u0 + group;
+    pkb = kpart;
+    pa = 0;
+    if (pu < u1) point();
   }
-}
+
+  // The weight rows and scales of unit pu.
+  __device__ __forceinline__ void point() {
+    const Routing& r = sm.r;
+    while (pu >= r.units[pa + 1]) ++pa;
+    const int e = r.active[pa], rb = (pu - r.units[pa]) % rows_per_expert;
+    const int hb = (p.H + 127) / 128;
+    if constexpr (UP) {  // eight gate rows, eight up rows
+      const int ib = (2 * p.I + 127) / 128, row = rb * 8 + g;
+      p_lo = p.W13 + ((long long)e * 2 * p.I + row) * p.H;
+      p_hi = p_lo + (long long)p.I * p.H;
+      const float* s = p.S13 + (long long)e * ib * hb;
+      p_slo = s + (long long)(row / 128) * hb;
+      p_shi = s + (long long)((p.I + row) / 128) * hb;
+    } else {
+      const int ib = (p.I + 127) / 128, row = rb * 16 + g;
+      p_lo = p.W2 + ((long long)e * p.H + row) * p.I;
+      p_hi = p_lo + 8LL * p.I;
+      p_slo = p_shi = p.S2 + ((long long)e * hb + row / 128) * ib;
+    }
+  }
+
+  // Starts the copy of the next piece into ring slot s (an empty group at the end).
+  __device__ __forceinline__ void copy_next(int s) {
+    if (pu < u1) {
+      const uint32_t dst = su32(sm.ring[warp][s]) + lane * 16;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int k = pkb * 128 + half * 64 + t4 * 16;
+        const bool live = k < K;
+        copy16(dst + (2 * half) * 512, live ? p_lo + k : p_lo, live);
+        copy16(dst + (2 * half + 1) * 512, live ? p_hi + k : p_hi, live);
+      }
+      if (lane < 2) copy4(su32(sm.ring[warp][s]) + kPiece + lane * 4, (lane ? p_shi : p_slo) + pkb);
+      pkb += ks;
+      if (pkb >= nkb) {
+        pkb = kpart;
+        pu += groups;
+        if (pu < u1) point();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+
+  __device__ int stride() const { return nkb * 256 + 16; }  // bytes per staged token: conflict-free for the lanes' loads
+
+  // The operand of tokens [first, first + n) of the order: fp16, zeros past K.
+  __device__ void stage(int first, int n) {
+    const Routing& r = sm.r;
+    const int chunks = nkb * 16, st = stride();
+    for (int i = threadIdx.x; i < n * chunks; i += kThreads) {
+      const int c = i / chunks, k = (i - c * chunks) * 8, s = r.order[first + c];
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (k < K) {
+        if constexpr (UP) {
+          v = __ldcg(reinterpret_cast<const uint4*>(p.w.xs + (long long)(s / p.top_k) * K + k));
+        } else {
+          const float sc = pow2_scale(__ldcg(&p.w.h_max[s])).x;
+          const float4* h = reinterpret_cast<const float4*>(p.w.h + (long long)s * K + k);
+          const float4 a = __ldcg(h), b = __ldcg(h + 1);
+          const __half2 h0 = __floats2half2_rn(a.x * sc, a.y * sc), h1 = __floats2half2_rn(a.z * sc, a.w * sc);
+          const __half2 h2 = __floats2half2_rn(b.x * sc, b.y * sc), h3 = __floats2half2_rn(b.z * sc, b.w * sc);
+          v.x = *reinterpret_cast<const uint32_t*>(&h0);
+          v.y = *reinterpret_cast<const uint32_t*>(&h1);
+          v.z = *reinterpret_cast<const uint32_t*>(&h2);
+          v.w = *reinterpret_cast<const uint32_t*>(&h3);
+        }
+      }
+      *reinterpret_cast<uint4*>(sm.cols + c * st + k * 2) = v;
+    }
+  }
+
+  __device__ void store(int rb, int row, int first, int c, float lo, float hi) {
+    const int s = sm.r.order[first + c];
+    if constexpr (UP) {
+      const float inv = __ldcg(&p.w.x_inv[s / p.top_k]);
+      const float a = lo * inv, u = hi * inv;
+      const float h = a / (1.0f + expf(-a)) * u;
+      p.w.h[(long long)s * p.I + rb * 8 + row] = h;
+      atomicMax(&p.w.h_max[s], __float_as_uint(h) & 0x7FFFFFFFu);  // a maximum: the order does not matter
+    } else {
+      const float back = pow2_scale(__ldcg(&p.w.h_max[s])).y;
+      float* out = p.w.part + (long long)s * p.H + rb * 16 + row;
+      out[0] = lo * back;
+      out[8] = hi * back;
+    }
+  }
+
+  // One unit: row block rb of the pass over tokens [first, first + n).
+  template <int NT>
+  __device__ void unit(int rb, int first, int n) {
+    float tot[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) tot[i][0] = tot[i][1] = tot[i][2] = tot[i][3] = 0.0f;
+    // columns past the last repeat it and are not stored
+    uint32_t col[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) col[i] = su32(sm.cols) + min(i * 8 + g, n - 1) * stride() + t4 * 32;
+    for (int kb = kpart; kb < nkb; kb += ks) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+      __syncwarp();
+      const uint32_t piece = su32(sm.ring[warp][slot]);
+      float acc[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint4 lo = lds16(piece + lane * 16 + (2 * half) * 512), hi = lds16(piece + lane * 16 + (2 * half + 1) * 512);
+        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+        uint32_t a[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a[j][0] = e4m3x2_to_h2(wl[j]);
+          a[j][1] = e4m3x2_to_h2(wh[j]);
+          a[j][2] = e4m3x2_to_h2(wl[j] >> 16);
+          a[j][3] = e4m3x2_to_h2(wh[j] >> 16);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const uint32_t at = col[i] + kb * 256 + half * 128;
+          const uint4 x0 = lds16(at), x1 = lds16(at + 16);
+          mma_t<__half>(acc[i], a[0][0], a[0][1], a[0][2], a[0][3], x0.x, x0.y);
+          mma_t<__half>(acc[i], a[1][0], a[1][1], a[1][2], a[1][3], x0.z, x0.w);
+          mma_t<__half>(acc[i], a[2][0], a[2][1], a[2][2], a[2][3], x1.x, x1.y);
+          mma_t<__half>(acc[i], a[3][0], a[3][1], a[3][2], a[3][3], x1.z, x1.w);
+        }
+      }
+      const float s0 = *reinterpret_cast<const float*>(sm.ring[warp][slot] + kPiece);
+      const float s1 = *reinterpret_cast<const float*>(sm.ring[warp][slot] + kPiece + 4);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        tot[i][0] = fmaf(acc[i][0], s0, tot[i][0]);
+        tot[i][1] = fmaf(acc[i][1], s0, tot[i][1]);
+        tot[i][2] = fmaf(acc[i][2], s1, tot[i][2]);
+        tot[i][3] = fmaf(acc[i][3], s1, tot[i][3]);
+      }
+      __syncwarp();  // every lane has read this slot's scales before the slot before it is refilled
+      copy_next(slot == 0 ? kRing - 1 : slot - 1);
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+    }
+    if (ks == 1) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (i * 8 + 2 * t4 + j < n) store(rb, g, first, i * 8 + 2 * t4 + j, tot[i][j], tot[i][2 + j]);
+      return;
+    }
+    float(*red)[16][kRedLd] = sm.red[parity] + group * ks;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      *reinterpret_cast<float2*>(&red[kpart][g][i * 8 + 2 * t4]) = make_float2(tot[i][0], tot[i][1]);
+      *reinterpret_cast<float2*>(&red[kpart][g + 8][i * 8 + 2 * t4]) = make_float2(tot[i][2], tot[i][3]);
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ks * 32) : "memory");
+    for (int i = kpart * 32 + lane; i < 8 * n; i += ks * 32) {
+      const int c = i >> 3, row = i & 7;
+      float lo = 0.0f, hi = 0.0f;
+      for (int w = 0; w < ks; ++w) {
+        lo += red[w][row][c];
+        hi += red[w][row + 8][c];
+      }
+      store(rb, row, first, c, lo, hi);
+    }
+    parity ^= 1;  // the group meets again before this buffer is written the next time
+  }
+
+  template <typename F>
+  __device__ bool run(int cta, int ctas, F&& before_use) {
+    Routing& r = sm.r;
+    plan_units(cta, ctas);
+    slot = 0;
+    for (int s = 0; s < kRing - 1; ++s) copy_next(s);
+    if (!before_use()) return false;
+    int a = 0, mine = u0 + group;
+    for (int at = u0; at < u1;) {  // segments: the units of one pass over one expert
+      while (at >= r.units[a + 1]) ++a;
+      const int pass = (at - r.units[a]) / rows_per_expert, base = r.units[a] + pass * rows_per_expert;
+      const int end = min(base + rows_per_expert, u1);
+      const int e = r.active[a], first = r.start[e] + pass * cap(), n = min(r.counts[e] - pass * cap(), cap());
+      __syncthreads();
+      stage(first, n);
+      __syncthreads();
+      for (; mine < end; mine += groups) {
+        const int rb = mine - base;
+        if (n <= 8) unit<1>(rb, first, n);
+        else if (n <= 16) unit<2>(rb, first, n);
+        else unit<kMaxNT>(rb, first, n);
+      }
+      at = end;
+    }
+    return true;
+  }
+};
 
 // Phase 4: the weighted sum of each token's experts, in the order of their ranks.
 template <typename T>
@@ -463,19 +663,28 @@ __device__ void combine_phase(const MoeParams& p, const Routing& r, int cta, int
   }
 }
 
-__global__ void __launch_bounds__(kThreads) moe_phase_kernel(MoeParams p, int phase) {
+// Kernel 2 (cooperative, one CTA per SM): routing, the two products, the sum.
+__global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_constant__ MoeParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
-  if (phase == 0) {
-    if (p.type == RG_TYPE_F16) router_phase<__half>(p, blockIdx.x, gridDim.x);
-    else router_phase<__nv_bfloat16>(p, blockIdx.x, gridDim.x);
-    return;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  if (p.E <= 128) form_routing<4>(p, sm.r);
+  else form_routing<kMaxE / 32>(p, sm.r);
+  {
+    Phase<true> up(p, sm);
+    up.run(cta, ctas, [] { return true; });
   }
-  form_routing(p, sm.r);
-  if (phase == 1) expert_phase<true>(p, sm, blockIdx.x, gridDim.x);
-  else if (phase == 2) expert_phase<false>(p, sm, blockIdx.x, gridDim.x);
-  else if (p.type == RG_TYPE_F16) combine_phase<__half>(p, sm.r, blockIdx.x, gridDim.x);
-  else combine_phase<__nv_bfloat16>(p, sm.r, blockIdx.x, gridDim.x);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  bool ok;
+  {
+    // the second product's first weights are on their way while the grid meets
+    Phase<false> down(p, sm);
+    ok = down.run(cta, ctas, [&] { return grid_barrier(p, sm.r, (unsigned)ctas); });
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!ok || !grid_barrier(p, sm.r, 2u * (unsigned)ctas)) return;
+  if (p.type == RG_TYPE_F16) combine_phase<__half>(p, sm.r, cta, ctas);
+  else combine_phase<__nv_bfloat16>(p, sm.r, cta, ctas);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -495,6 +704,7 @@ size_t layout(long long T, long long H, long long I, long long E, long long top_
   m.x_inv = reinterpret_cast<float*>(take((size_t)T * 4));
   m.h = reinterpret_cast<float*>(take(slots * I * 4));
   m.h_max = reinterpret_cast<uint32_t*>(take(slots * 4));
+  m.arrived = reinterpret_cast<unsigned*>(take(4));
   m.part = reinterpret_cast<float*>(take(slots * H * 4));
   if (w) *w = m;
   return off;
@@ -506,23 +716,59 @@ size_t moe_f8_scratch_bytes(long long T, long long H, long long I, long long E, 
   return layout(T, H, I, E, top_k, nullptr, nullptr);
 }
 
-cudaError_t launch_moe_f8(const MoeArgs& a, void* scratch, cudaStream_t st) {
+// Warps that split k: as many (a power of two) as leave each two 128-blocks.
+// Fixed by the widths alone, so that a token's sums do not depend on what comes
+// with it.
+int k_split(long long K) {
+  const long long nkb = (K + 127) / 128;
+  int ks = 1;
+  while (ks < kWarps && nkb >= 4 * ks) ks *= 2;
+  return ks;
+}
+// Tokens per pass over an expert's weights: what fits beside the weights.
+int tokens_per_pass(long long K) {
+  const long long n = kColsBytes / ((K + 127) / 128 * 256 + 16);
+  return (int)(n >= 8 * kMaxNT ? 8 * kMaxNT : n >= 8 ? n / 8 * 8 : n);
+}
+
+cudaError_t launch_moe_f8(const MoeArgs& a, DevPlan* plan, void* scratch, cudaStream_t st,
+                          unsigned long long wait_ns) {
   MoeParams p{a.X, a.WR, a.W13, a.S13, a.W2, a.S2, a.Y, (int)a.T, (int)a.H, (int)a.I, (int)a.E, (int)a.top_k, a.type,
-              a.renorm ? 1 : 0, {}};
+              a.renorm ? 1 : 0, k_split(a.H), k_split(a.I), tokens_per_pass(a.H), tokens_per_pass(a.I), wait_ns, plan,
+              {}};
   layout(a.T, a.H, a.I, a.E, a.top_k, static_cast<uint8_t*>(scratch), &p.w);
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(moe_phase_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
-  });
-  if (attr != cudaSuccess) return attr;
-  const int grid = 304;
-  for (int phase = 0; phase < 4; ++phase) {
-    moe_phase_kernel<<<grid, kThreads, sizeof(Smem), st>>>(p, phase);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    static std::mutex mu;
+    static int known[64];
+    std::lock_guard<std::mutex> lock(mu);
+    if (!known[dev]) {
+      e = cudaFuncSetAttribute(moe_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+      if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+      if (e != cudaSuccess) return e;
+      known[dev] = sms;
+    }
+    sms = known[dev];
   }
-  return cudaSuccess;
+  const unsigned blocks = (unsigned)((p.E + 15) / 16 * ((p.T + 7) / 8) + p.T);
+  if (p.type == RG_TYPE_F16) moe_router_kernel<__half><<<blocks, kThreads, 0, st>>>(p);
+  else moe_router_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, moe_experts_kernel, p);
 }
 
 }  // namespace rg

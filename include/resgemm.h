@@ -496,7 +496,7 @@ int scaled_gemm_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t
 #define RG_MOE_MAX_TOKENS 64
 #define RG_MOE_MAX_EXPERTS 512
 #define RG_MOE_MAX_TOP_K 16
-#define RG_MOE_MAX_WIDTH 65536
+#define RG_MOE_MAX_WIDTH 32768
 size_t moe_layer_f8_ws_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int top_k);
 int moe_layer_f8(const void* X, int x_type, const void* WR, const uint8_t* W13, const float* S13, const uint8_t* W2,
                  const float* S2, void* Y, int64_t T, int64_t H, int64_t I, int64_t E, int top_k, int renorm,
