@@ -74,7 +74,7 @@ int scaled_gemm_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t
 
 size_t moe_layer_f8_ws_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int top_k) {
   if (!good_moe(T, H, I, E, top_k)) return 0;
-  return kCallBlockBytes + (T ? moe_f8_scratch_bytes(T, H, I, E, top_k) : 0);
+  return kCallBlockBytes + (T ? moe_f8_scratch_bytes(T, H, I, top_k) : 0);
 }
 
 int moe_layer_f8(const void* X, int x_type, const void* WR, const uint8_t* W13, const float* S13, const uint8_t* W2,

@@ -55,7 +55,7 @@ struct MoeArgs {
   int type;  // of X, WR and Y: RG_TYPE_F16 or RG_TYPE_BF16
   bool renorm;
 };
-size_t moe_f8_scratch_bytes(long long T, long long H, long long I, long long E, long long top_k);
+size_t moe_f8_scratch_bytes(long long T, long long H, long long I, long long top_k);
 cudaError_t launch_moe_f8(const MoeArgs& a, DevPlan* plan, void* scratch, cudaStream_t st,
                           unsigned long long wait_ns);
 

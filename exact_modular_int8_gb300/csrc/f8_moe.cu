@@ -32,20 +32,23 @@
 namespace rg {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kRouterWarps = 8;
+constexpr int kRouterThreads = 32 * kRouterWarps;
 constexpr int kMaxT = RG_MOE_MAX_TOKENS;
 constexpr int kMaxK = RG_MOE_MAX_TOP_K;
 constexpr int kMaxE = RG_MOE_MAX_EXPERTS;
 constexpr int kSlots = kMaxT * kMaxK;
 constexpr int kMaxNT = 4;            // column tiles of eight tokens per pass over the weights
-constexpr int kRing = 6;             // weight pieces (16 rows x 128 k) per warp, on their way or in use
+constexpr int kRing = 3;             // weight pieces (16 rows x 128 k) per warp, on their way or in use
 constexpr int kPiece = 16 * 128;
 constexpr int kColsBytes = 76 * 1024;  // the tokens' operand of one expert
 constexpr int kRedLd = 8 * kMaxNT + 4;
 
 struct MoeWs {
-  float* logits;     // [T][E]
+  float* gate;       // [T * top_k] weights, and
+  int* expert;       // experts, by slot = token * top_k + rank
   __half* xs;        // [T][H] x times 2^n
   float* x_inv;      // [T] 2^-n
   float* h;          // [T * top_k][I]
@@ -92,9 +95,12 @@ __device__ __forceinline__ float2 pow2_scale(uint32_t max_bits) {
 }
 
 // ---------------------------------------------------------------------------
-// Kernel 1: router logits (16 experts x 8 tokens per block, its warps splitting
-// k; the products of 16-bit entries are exact in the MMA's fp32), scaled fp16
-// copies of the tokens, and the words that kernel 2 starts from.
+// Kernel 1: the router.  A cluster of eight CTAs takes eight tokens: its CTAs
+// form the logits of a share of the experts each (tiles of 8 or 16 experts x 8
+// tokens, a CTA's warps splitting k; the products of 16-bit entries are exact in
+// the MMA's fp32), then one token's top-k each, reading the logits from each
+// other's shared memory.  It also makes the scaled fp16 copies of the tokens
+// and clears the words that kernel 2 starts from.
 // ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ void mma_t(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -116,34 +122,138 @@ __device__ __forceinline__ void mma_t<__nv_bfloat16>(float (&c)[4], uint32_t a0,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Order of floats as unsigned integers; NaN sorts by its bits (the softmax
+// makes every weight of such a token NaN whichever experts it takes).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// Softmax and top-k of one token by a warp; logit(e) gives its logits.
+template <int PER, typename F>  // E <= 32 PER
+__device__ __forceinline__ void choose(const MoeParams& p, int t, F&& logit) {
+  const int lane = threadIdx.x & 31;
+  float v[PER];
+  float mx = -INFINITY;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    v[i] = i * 32 + lane < p.E ? logit(i * 32 + lane) : -INFINITY;
+    mx = fmaxf(mx, v[i]);
+    nan |= v[i] != v[i];
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+  nan = __any_sync(0xFFFFFFFFu, nan);
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) sum += i * 32 + lane < p.E ? expf(v[i] - mx) : 0.0f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  uint32_t taken = 0;  // bit i: this lane's entry i is chosen
+  float mine = 0.0f, total = 0.0f;
+  int my_expert = 0;
+  for (int j = 0; j < p.top_k; ++j) {
+    uint32_t key = 0;
+    int at = 0;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const uint32_t k = order_key(v[i] + 0.0f);  // -0 ties with +0
+      if (i * 32 + lane < p.E && !(taken >> i & 1u) && (!any || k > key)) {
+        key = k;
+        at = i;
+        any = true;
+      }
+    }
+    // the largest key, then the lowest expert that has it
+    const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, any ? key : 0u);
+    const uint32_t cand = any && key == best ? (uint32_t)(at * 32 + lane) : 0xFFFFFFFFu;
+    const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, cand);
+    float pe = 0.0f;
+    if (cand == e) {
+      taken |= 1u << at;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i == at) pe = expf(v[i] - mx) / sum;
+    }
+    pe = __shfl_sync(0xFFFFFFFFu, pe, (int)(e & 31u));
+    total += pe;
+    if (lane == j) {
+      mine = pe;
+      my_expert = (int)e;
+    }
+  }
+  if (lane < p.top_k) {
+    const float w = p.renorm ? mine / total : mine;
+    p.w.gate[t * p.top_k + lane] = nan ? __int_as_float(0x7FC00000) : w;
+    p.w.expert[t * p.top_k + lane] = my_expert;
+    p.w.h_max[t * p.top_k + lane] = 0;
+  }
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) moe_router_kernel(MoeParams p) {
-  __shared__ float red[kWarps][16][8];
+__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kRouterThreads) moe_router_kernel(MoeParams p) {
+  __shared__ float red[kRouterWarps][16][8];
+  __shared__ float logits[8][kMaxE / 8];  // [token][16-expert (8-expert) tiles of this CTA]
+  __shared__ uint32_t wmax[kRouterWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const T* X = static_cast<const T*>(p.X);
-  const int te = (p.E + 15) / 16, tt = (p.T + 7) / 8;
+  const T* WR = static_cast<const T*>(p.WR);
+  const int rank = (int)(blockIdx.x & 7u), t0 = (int)(blockIdx.x >> 3) * 8;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     p.plan->status = 0;
     p.plan->timeout_where = 0;
     *p.w.arrived = 0;
   }
-  if ((int)blockIdx.x >= te * tt) {  // one token: its largest entry, then the scaled copy
-    const int t = (int)blockIdx.x - te * tt;
+  // logits of this CTA's tiles; rows past the last repeat it, and nothing reads their results
+  const int rows = p.E > 64 ? 16 : 8;  // experts per tile: all eight CTAs busy from 57 experts on
+  const T* xb = X + (long long)min(t0 + g, p.T - 1) * p.H;
+  for (int tile = rank, local = 0; tile * rows < p.E; tile += 8, ++local) {
+    const T* wa = WR + (long long)min(tile * rows + g, p.E - 1) * p.H;
+    const T* wb = WR + (long long)min(tile * rows + g + 8, p.E - 1) * p.H;
+    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int k = warp * 32 + t4 * 8; k - t4 * 8 < p.H; k += kRouterWarps * 32) {  // H is a multiple of 16
+      uint4 a = make_uint4(0, 0, 0, 0), b = a, x = a;
+      if (k < p.H) {
+        a = __ldg(reinterpret_cast<const uint4*>(wa + k));
+        if (rows == 16) b = __ldg(reinterpret_cast<const uint4*>(wb + k));
+        x = __ldg(reinterpret_cast<const uint4*>(xb + k));
+      }
+      mma_t<T>(c, a.x, b.x, a.y, b.y, x.x, x.y);
+      mma_t<T>(c, a.z, b.z, a.w, b.w, x.z, x.w);
+    }
+    red[warp][g][2 * t4] = c[0];
+    red[warp][g][2 * t4 + 1] = c[1];
+    red[warp][g + 8][2 * t4] = c[2];
+    red[warp][g + 8][2 * t4 + 1] = c[3];
+    __syncthreads();
+    if ((int)threadIdx.x < 8 * rows) {
+      const int e = threadIdx.x % rows, t = threadIdx.x / rows;
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRouterWarps; ++w) s += red[w][e][t];
+      logits[t][local * rows + e] = s;
+    }
+    __syncthreads();
+  }
+  const int t = t0 + rank;
+  if (t < p.T) {  // this CTA's token: its largest entry, then the scaled copy
     const T* x = X + (long long)t * p.H;
     uint32_t m = 0;
-    for (int k = threadIdx.x * 8; k < p.H; k += kThreads * 8) {  // H is a multiple of 16
+    for (int k = threadIdx.x * 8; k < p.H; k += kRouterThreads * 8) {
       const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k));
       const T* v = reinterpret_cast<const T*>(&a);
 #pragma unroll
       for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(to_f(v[j])) & 0x7FFFFFFFu);
     }
-    uint32_t* wmax = reinterpret_cast<uint32_t*>(red);
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if (lane == 0) wmax[warp] = m;
     __syncthreads();
-    for (int w = 0; w < kWarps; ++w) m = max(m, wmax[w]);
+    for (int w = 0; w < kRouterWarps; ++w) m = max(m, wmax[w]);
     const float2 sc = pow2_scale(m);
-    for (int k = threadIdx.x * 8; k < p.H; k += kThreads * 8) {
+    for (int k = threadIdx.x * 8; k < p.H; k += kRouterThreads * 8) {
       const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k));
       const T* v = reinterpret_cast<const T*>(&a);
       uint4 o;
@@ -156,46 +266,29 @@ __global__ void __launch_bounds__(kThreads) moe_router_kernel(MoeParams p) {
       *reinterpret_cast<uint4*>(p.w.xs + (long long)t * p.H + k) = o;
     }
     if (threadIdx.x == 0) p.w.x_inv[t] = sc.y;
-    if ((int)threadIdx.x < p.top_k) p.w.h_max[t * p.top_k + threadIdx.x] = 0;
-    return;
   }
-  const int e0 = (int)(blockIdx.x % te) * 16, t0 = (int)(blockIdx.x / te) * 8;
-  const T* WR = static_cast<const T*>(p.WR);
-  // rows past the last repeat it; their results are dropped
-  const T* wa = WR + (long long)min(e0 + g, p.E - 1) * p.H;
-  const T* wb = WR + (long long)min(e0 + g + 8, p.E - 1) * p.H;
-  const T* xb = X + (long long)min(t0 + g, p.T - 1) * p.H;
-  float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int k = warp * 32 + t4 * 8; k - t4 * 8 < p.H; k += kWarps * 32) {
-    uint4 a = make_uint4(0, 0, 0, 0), b = a, x = a;
-    if (k < p.H) {
-      a = __ldg(reinterpret_cast<const uint4*>(wa + k));
-      b = __ldg(reinterpret_cast<const uint4*>(wb + k));
-      x = __ldg(reinterpret_cast<const uint4*>(xb + k));
-    }
-    mma_t<T>(c, a.x, b.x, a.y, b.y, x.x, x.y);
-    mma_t<T>(c, a.z, b.z, a.w, b.w, x.z, x.w);
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (t < p.T && warp == 0) {
+    auto logit = [&](int e) {
+      const int tile = e / rows;
+      const uint32_t at = (uint32_t)__cvta_generic_to_shared(&logits[rank][(tile >> 3) * rows + e % rows]);
+      uint32_t remote;
+      float v;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(tile & 7));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote));
+      return v;
+    };
+    if (p.E <= 128) choose<4>(p, t, logit);
+    else choose<kMaxE / 32>(p, t, logit);
   }
-  red[warp][g][2 * t4] = c[0];
-  red[warp][g][2 * t4 + 1] = c[1];
-  red[warp][g + 8][2 * t4] = c[2];
-  red[warp][g + 8][2 * t4 + 1] = c[3];
-  __syncthreads();
-  if (threadIdx.x < 128) {
-    const int e = threadIdx.x & 15, t = threadIdx.x >> 4;
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += red[w][e][t];
-    if (e0 + e < p.E && t0 + t < p.T) p.w.logits[(t0 + t) * p.E + e0 + e] = s;
-  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
-// Top-k and the tokens' order by expert, formed by every CTA for itself
+// Kernel 2.  The tokens' order by expert, formed by every CTA for itself.
 // ---------------------------------------------------------------------------
 struct Routing {
-  float gate[kSlots];            // by slot = token * top_k + j
+  float gate[kSlots];            // by slot = token * top_k + rank
   short expert[kSlots];
   short order[kSlots];           // slots, grouped by expert
   short start[kMaxE + 1];        // of each expert's group
@@ -207,14 +300,6 @@ struct Routing {
   int go;                        // the grid's barrier was passed
 };
 
-// Order of floats as unsigned integers; NaN sorts by its bits (the softmax
-// makes every weight of such a token NaN whichever experts it takes).
-__device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t b = __float_as_uint(v);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-
-template <int PER>  // E <= 32 PER
 __device__ void form_routing(const MoeParams& p, Routing& r) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
@@ -222,67 +307,11 @@ __device__ void form_routing(const MoeParams& p, Routing& r) {
     r.fill[e] = 0;
   }
   __syncthreads();
-  for (int t = warp; t < p.T; t += kWarps) {
-    const float* lg = p.w.logits + t * p.E;
-    float v[PER];
-    float mx = -INFINITY;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      v[i] = i * 32 + lane < p.E ? __ldcg(lg + i * 32 + lane) : -INFINITY;
-      mx = fmaxf(mx, v[i]);
-      nan |= v[i] != v[i];
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-    nan = __any_sync(0xFFFFFFFFu, nan);
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) sum += i * 32 + lane < p.E ? expf(v[i] - mx) : 0.0f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    uint32_t taken = 0;  // bit i: this lane's entry i is chosen
-    float mine = 0.0f, total = 0.0f;
-    int my_expert = 0;
-    for (int j = 0; j < p.top_k; ++j) {
-      uint32_t key = 0;
-      int at = 0;
-      bool any = false;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const uint32_t k = order_key(v[i] + 0.0f);  // -0 ties with +0
-        if (i * 32 + lane < p.E && !(taken >> i & 1u) && (!any || k > key)) {
-          key = k;
-          at = i;
-          any = true;
-        }
-      }
-      // the largest key, then the lowest expert that has it
-      const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, any ? key : 0u);
-      const uint32_t cand = any && key == best ? (uint32_t)(at * 32 + lane) : 0xFFFFFFFFu;
-      const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, cand);
-      float pe = 0.0f;
-      if (cand == e) {
-        taken |= 1u << at;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-          if (i == at) pe = expf(v[i] - mx) / sum;
-      }
-      pe = __shfl_sync(0xFFFFFFFFu, pe, (int)(e & 31u));
-      total += pe;
-      if (lane == j) {
-        mine = pe;
-        my_expert = (int)e;
-      }
-    }
-    if (lane < p.top_k) {
-      float g = p.renorm ? mine / total : mine;
-      if (nan) g = __int_as_float(0x7FC00000);
-      const int slot = t * p.top_k + lane;
-      r.gate[slot] = g;
-      r.expert[slot] = (short)my_expert;
-      atomicAdd(&r.counts[my_expert], 1);
-    }
+  for (int s = threadIdx.x; s < p.T * p.top_k; s += kThreads) {
+    const int e = __ldg(p.w.expert + s);
+    r.gate[s] = __ldg(p.w.gate + s);
+    r.expert[s] = (short)e;
+    atomicAdd(&r.counts[e], 1);
   }
   __syncthreads();
   if (warp == 0) {  // exclusive sums of the counts, and the experts that have any
@@ -307,21 +336,19 @@ __device__ void form_routing(const MoeParams& p, Routing& r) {
       r.start[p.E] = (short)base;
       r.num_active = nact;
     }
-  }
-  __syncthreads();
-  // Slots in their own order within each expert's group, 32 at a time.  The
-  // order has to be the same in every CTA: passes over an expert take tokens by it.
-  if (warp == 0) {
+    __syncwarp();
+    // Slots in their own order within each expert's group, 32 at a time.  The
+    // order has to be the same in every CTA: passes over an expert take tokens by it.
     for (int s0 = 0; s0 < p.T * p.top_k; s0 += 32) {
       const int s = s0 + lane;
       const bool live = s < p.T * p.top_k;
       const int e = live ? r.expert[s] : -1;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
       const int before = __popc(same & ((1u << lane) - 1u));
-      const int base = live ? r.start[e] + r.fill[e] : 0;
+      const int at = live ? r.start[e] + r.fill[e] : 0;
       __syncwarp();
       if (live) {
-        r.order[base + before] = (short)s;
+        r.order[at + before] = (short)s;
         if (before == 0) r.fill[e] += __popc(same);
       }
       __syncwarp();
@@ -367,7 +394,7 @@ __device__ bool grid_barrier(const MoeParams& p, Routing& r, unsigned target) {
 // contiguous ranges per CTA, so that a CTA stages an expert's tokens in shared
 // memory once.  Every lane copies the weights it will use itself, kRing - 1
 // pieces ahead of their use and across units (cp.async, 2 KB a piece and warp:
-// 80 KB on their way per SM, where the latency times the bandwidth of this
+// 64 KB on their way per SM, where the latency times the bandwidth of this
 // memory needs about 45).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {  // the low 16 bits: two E4M3 values
@@ -391,7 +418,8 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 
 struct Smem {
   Routing r;
-  __align__(16) float red[2][kWarps][16][kRedLd];
+  __align__(16) float red[kWarps][16][kRedLd];
+  float col_scale[8 * kMaxNT];   // of the staged columns: takes a sum back from the operand's power of two
   __align__(16) uint8_t ring[kWarps][kRing][kPiece + 16];  // 16 rows x 128 k as the lanes copied them, two scales
   __align__(16) uint8_t cols[kColsBytes];
 };
@@ -412,7 +440,7 @@ struct Phase {
   const float* p_slo;
   const float* p_shi;
   int slot;              // ring slot of the next piece to use
-  int parity;            // of the reduction buffers
+  int parity;            // half of the reduction buffer
 
   __device__ Phase(const MoeParams& pp, Smem& s)
       : p(pp), sm(s), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2),
@@ -501,6 +529,10 @@ struct Phase {
   __device__ void stage(int first, int n) {
     const Routing& r = sm.r;
     const int chunks = nkb * 16, st = stride();
+    if ((int)threadIdx.x < n) {
+      const int s = r.order[first + threadIdx.x];
+      sm.col_scale[threadIdx.x] = UP ? __ldcg(&p.w.x_inv[s / p.top_k]) : pow2_scale(__ldcg(&p.w.h_max[s])).y;
+    }
     for (int i = threadIdx.x; i < n * chunks; i += kThreads) {
       const int c = i / chunks, k = (i - c * chunks) * 8, s = r.order[first + c];
       uint4 v = make_uint4(0, 0, 0, 0);
@@ -526,13 +558,12 @@ struct Phase {
   __device__ void store(int rb, int row, int first, int c, float lo, float hi) {
     const int s = sm.r.order[first + c];
     if constexpr (UP) {
-      const float inv = __ldcg(&p.w.x_inv[s / p.top_k]);
-      const float a = lo * inv, u = hi * inv;
+      const float a = lo * sm.col_scale[c], u = hi * sm.col_scale[c];
       const float h = a / (1.0f + expf(-a)) * u;
       p.w.h[(long long)s * p.I + rb * 8 + row] = h;
       atomicMax(&p.w.h_max[s], __float_as_uint(h) & 0x7FFFFFFFu);  // a maximum: the order does not matter
     } else {
-      const float back = pow2_scale(__ldcg(&p.w.h_max[s])).y;
+      const float back = sm.col_scale[c];
       float* out = p.w.part + (long long)s * p.H + rb * 16 + row;
       out[0] = lo * back;
       out[8] = hi * back;
@@ -553,9 +584,12 @@ struct Phase {
       asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
       __syncwarp();
       const uint32_t piece = su32(sm.ring[warp][slot]);
-      float acc[NT][4];
+      float acc[NT][4], odd[NT][4];  // two chains of MMAs, even and odd k groups
 #pragma unroll
-      for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+      for (int i = 0; i < NT; ++i) {
+        acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+        odd[i][0] = odd[i][1] = odd[i][2] = odd[i][3] = 0.0f;
+      }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const uint4 lo = lds16(piece + lane * 16 + (2 * half) * 512), hi = lds16(piece + lane * 16 + (2 * half + 1) * 512);
@@ -573,19 +607,19 @@ struct Phase {
           const uint32_t at = col[i] + kb * 256 + half * 128;
           const uint4 x0 = lds16(at), x1 = lds16(at + 16);
           mma_t<__half>(acc[i], a[0][0], a[0][1], a[0][2], a[0][3], x0.x, x0.y);
-          mma_t<__half>(acc[i], a[1][0], a[1][1], a[1][2], a[1][3], x0.z, x0.w);
+          mma_t<__half>(odd[i], a[1][0], a[1][1], a[1][2], a[1][3], x0.z, x0.w);
           mma_t<__half>(acc[i], a[2][0], a[2][1], a[2][2], a[2][3], x1.x, x1.y);
-          mma_t<__half>(acc[i], a[3][0], a[3][1], a[3][2], a[3][3], x1.z, x1.w);
+          mma_t<__half>(odd[i], a[3][0], a[3][1], a[3][2], a[3][3], x1.z, x1.w);
         }
       }
       const float s0 = *reinterpret_cast<const float*>(sm.ring[warp][slot] + kPiece);
       const float s1 = *reinterpret_cast<const float*>(sm.ring[warp][slot] + kPiece + 4);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        tot[i][0] = fmaf(acc[i][0], s0, tot[i][0]);
-        tot[i][1] = fmaf(acc[i][1], s0, tot[i][1]);
-        tot[i][2] = fmaf(acc[i][2], s1, tot[i][2]);
-        tot[i][3] = fmaf(acc[i][3], s1, tot[i][3]);
+        tot[i][0] = fmaf(acc[i][0] + odd[i][0], s0, tot[i][0]);
+        tot[i][1] = fmaf(acc[i][1] + odd[i][1], s0, tot[i][1]);
+        tot[i][2] = fmaf(acc[i][2] + odd[i][2], s1, tot[i][2]);
+        tot[i][3] = fmaf(acc[i][3] + odd[i][3], s1, tot[i][3]);
       }
       __syncwarp();  // every lane has read this slot's scales before the slot before it is refilled
       copy_next(slot == 0 ? kRing - 1 : slot - 1);
@@ -599,23 +633,28 @@ struct Phase {
           if (i * 8 + 2 * t4 + j < n) store(rb, g, first, i * 8 + 2 * t4 + j, tot[i][j], tot[i][2 + j]);
       return;
     }
-    float(*red)[16][kRedLd] = sm.red[parity] + group * ks;
+    // up to 16 columns: units alternate between the buffer's halves, so that one
+    // meeting of the group per unit is enough
+    constexpr bool kHalves = NT <= kMaxNT / 2;
+    const int off = kHalves ? parity * (8 * kMaxNT / 2) : 0;
+    float(*red)[16][kRedLd] = sm.red + group * ks;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      *reinterpret_cast<float2*>(&red[kpart][g][i * 8 + 2 * t4]) = make_float2(tot[i][0], tot[i][1]);
-      *reinterpret_cast<float2*>(&red[kpart][g + 8][i * 8 + 2 * t4]) = make_float2(tot[i][2], tot[i][3]);
+      *reinterpret_cast<float2*>(&red[kpart][g][off + i * 8 + 2 * t4]) = make_float2(tot[i][0], tot[i][1]);
+      *reinterpret_cast<float2*>(&red[kpart][g + 8][off + i * 8 + 2 * t4]) = make_float2(tot[i][2], tot[i][3]);
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ks * 32) : "memory");
     for (int i = kpart * 32 + lane; i < 8 * n; i += ks * 32) {
       const int c = i >> 3, row = i & 7;
       float lo = 0.0f, hi = 0.0f;
       for (int w = 0; w < ks; ++w) {
-        lo += red[w][row][c];
-        hi += red[w][row + 8][c];
+        lo += red[w][row][off + c];
+        hi += red[w][row + 8][off + c];
       }
       store(rb, row, first, c, lo, hi);
     }
-    parity ^= 1;  // the group meets again before this buffer is written the next time
+    if constexpr (kHalves) parity ^= 1;
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ks * 32) : "memory");
   }
 
   template <typename F>
@@ -668,8 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
   extern __shared__ __align__(16) uint8_t raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int cta = blockIdx.x, ctas = gridDim.x;
-  if (p.E <= 128) form_routing<4>(p, sm.r);
-  else form_routing<kMaxE / 32>(p, sm.r);
+  form_routing(p, sm.r);
   {
     Phase<true> up(p, sm);
     up.run(cta, ctas, [] { return true; });
@@ -690,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Workspace after the call block; base may be null (sizes only).
-size_t layout(long long T, long long H, long long I, long long E, long long top_k, uint8_t* base, MoeWs* w) {
+size_t layout(long long T, long long H, long long I, long long top_k, uint8_t* base, MoeWs* w) {
   size_t off = 0;
   auto take = [&](size_t bytes) {
     uint8_t* q = base ? base + off : nullptr;
@@ -699,7 +737,8 @@ size_t layout(long long T, long long H, long long I, long long E, long long top_
   };
   const size_t slots = (size_t)(T * top_k);
   MoeWs m;
-  m.logits = reinterpret_cast<float*>(take((size_t)T * E * 4));
+  m.gate = reinterpret_cast<float*>(take(slots * 4));
+  m.expert = reinterpret_cast<int*>(take(slots * 4));
   m.xs = reinterpret_cast<__half*>(take((size_t)T * H * 2));
   m.x_inv = reinterpret_cast<float*>(take((size_t)T * 4));
   m.h = reinterpret_cast<float*>(take(slots * I * 4));
@@ -712,8 +751,8 @@ size_t layout(long long T, long long H, long long I, long long E, long long top_
 
 }  // namespace
 
-size_t moe_f8_scratch_bytes(long long T, long long H, long long I, long long E, long long top_k) {
-  return layout(T, H, I, E, top_k, nullptr, nullptr);
+size_t moe_f8_scratch_bytes(long long T, long long H, long long I, long long top_k) {
+  return layout(T, H, I, top_k, nullptr, nullptr);
 }
 
 // Warps that split k: as many (a power of two) as leave each two 128-blocks.
@@ -722,7 +761,7 @@ size_t moe_f8_scratch_bytes(long long T, long long H, long long I, long long E, 
 int k_split(long long K) {
   const long long nkb = (K + 127) / 128;
   int ks = 1;
-  while (ks < kWarps && nkb >= 4 * ks) ks *= 2;
+  while (ks < 8 && nkb >= 4 * ks) ks *= 2;
   return ks;
 }
 // Tokens per pass over an expert's weights: what fits beside the weights.
@@ -736,7 +775,7 @@ cudaError_t launch_moe_f8(const MoeArgs& a, DevPlan* plan, void* scratch, cudaSt
   MoeParams p{a.X, a.WR, a.W13, a.S13, a.W2, a.S2, a.Y, (int)a.T, (int)a.H, (int)a.I, (int)a.E, (int)a.top_k, a.type,
               a.renorm ? 1 : 0, k_split(a.H), k_split(a.I), tokens_per_pass(a.H), tokens_per_pass(a.I), wait_ns, plan,
               {}};
-  layout(a.T, a.H, a.I, a.E, a.top_k, static_cast<uint8_t*>(scratch), &p.w);
+  layout(a.T, a.H, a.I, a.top_k, static_cast<uint8_t*>(scratch), &p.w);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -753,9 +792,9 @@ cudaError_t launch_moe_f8(const MoeArgs& a, DevPlan* plan, void* scratch, cudaSt
     }
     sms = known[dev];
   }
-  const unsigned blocks = (unsigned)((p.E + 15) / 16 * ((p.T + 7) / 8) + p.T);
-  if (p.type == RG_TYPE_F16) moe_router_kernel<__half><<<blocks, kThreads, 0, st>>>(p);
-  else moe_router_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(p);
+  const unsigned blocks = 8u * (unsigned)((p.T + 7) / 8);
+  if (p.type == RG_TYPE_F16) moe_router_kernel<__half><<<blocks, kRouterThreads, 0, st>>>(p);
+  else moe_router_kernel<__nv_bfloat16><<<blocks, kRouterThreads, 0, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
