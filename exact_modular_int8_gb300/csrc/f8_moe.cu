@@ -24,6 +24,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -41,10 +42,10 @@ constexpr int kMaxK = RG_MOE_MAX_TOP_K;
 constexpr int kMaxE = RG_MOE_MAX_EXPERTS;
 constexpr int kSlots = kMaxT * kMaxK;
 constexpr int kMaxNT = 4;            // column tiles of eight tokens per pass over the weights
-constexpr int kRing = 3;             // weight pieces (16 rows x 128 k) per warp, on their way or in use
-constexpr int kPiece = 16 * 128;
-constexpr int kColsBytes = 76 * 1024;  // the tokens' operand of one expert
-constexpr int kRedLd = 8 * kMaxNT + 4;
+constexpr int kMinRing = 3, kMaxRing = 8;  // weight pieces (16 rows x 128 k) per warp, on their way or in use
+constexpr int kPiece = 16 * 128 + 16;      // and the two scales of its rows
+constexpr int kMaxStride = 32;             // words between two slots' maxima
+constexpr int kSmemBytes = 231424;         // all of an SM's
 
 struct MoeWs {
   float* gate;       // [T * top_k] weights, and
@@ -52,7 +53,7 @@ struct MoeWs {
   __half* xs;        // [T][H] x times 2^n
   float* x_inv;      // [T] 2^-n
   float* h;          // [T * top_k][I]
-  uint32_t* h_max;   // [T * top_k] largest |h|, as bits
+  uint32_t* h_max;   // [T * top_k][kMaxStride] largest |h|, as bits, in the first word
   unsigned* arrived;  // CTAs that have reached the grid's barriers
   float* part;       // [T * top_k][H] the experts' outputs
 };
@@ -70,6 +71,9 @@ struct MoeParams {
   int renorm;
   int ks_up, ks_down;    // warps that split k in the two products
   int cap_up, cap_down;  // tokens per pass
+  int ring;              // pieces per warp
+  int red_ld;            // columns of the warps' partial sums, padded
+  int red_off, cols_off, ring_off;  // shared memory beyond struct Smem
   unsigned long long wait_ns;
   DevPlan* plan;
   MoeWs w;
@@ -188,7 +192,7 @@ __device__ __forceinline__ void choose(const MoeParams& p, int t, F&& logit) {
     const float w = p.renorm ? mine / total : mine;
     p.w.gate[t * p.top_k + lane] = nan ? __int_as_float(0x7FC00000) : w;
     p.w.expert[t * p.top_k + lane] = my_expert;
-    p.w.h_max[t * p.top_k + lane] = 0;
+    p.w.h_max[(t * p.top_k + lane) * kMaxStride] = 0;
   }
 }
 
@@ -288,12 +292,11 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kRouterThreads) moe_
 // Kernel 2.  The tokens' order by expert, formed by every CTA for itself.
 // ---------------------------------------------------------------------------
 struct Routing {
-  float gate[kSlots];            // by slot = token * top_k + rank
-  short expert[kSlots];
+  short expert[kSlots];          // by slot = token * top_k + rank
   short order[kSlots];           // slots, grouped by expert
   short start[kMaxE + 1];        // of each expert's group
   short active[kMaxE];           // experts with tokens
-  int fill[kMaxE];
+  short fill[kMaxE];
   int counts[kMaxE];
   int units[kMaxE + 1];          // of a product phase: first unit of each active expert
   int num_active;
@@ -309,7 +312,6 @@ __device__ void form_routing(const MoeParams& p, Routing& r) {
   __syncthreads();
   for (int s = threadIdx.x; s < p.T * p.top_k; s += kThreads) {
     const int e = __ldg(p.w.expert + s);
-    r.gate[s] = __ldg(p.w.gate + s);
     r.expert[s] = (short)e;
     atomicAdd(&r.counts[e], 1);
   }
@@ -349,7 +351,7 @@ __device__ void form_routing(const MoeParams& p, Routing& r) {
       __syncwarp();
       if (live) {
         r.order[at + before] = (short)s;
-        if (before == 0) r.fill[e] += __popc(same);
+        if (before == 0) r.fill[e] += (short)__popc(same);
       }
       __syncwarp();
     }
@@ -392,10 +394,10 @@ __device__ bool grid_barrier(const MoeParams& p, Routing& r, unsigned target) {
 // pass over an expert.  A group of ks warps works on a unit, each on every ks-th
 // 128-block of k, and the groups of all CTAs share the units out evenly, in
 // contiguous ranges per CTA, so that a CTA stages an expert's tokens in shared
-// memory once.  Every lane copies the weights it will use itself, kRing - 1
-// pieces ahead of their use and across units (cp.async, 2 KB a piece and warp:
-// 64 KB on their way per SM, where the latency times the bandwidth of this
-// memory needs about 45).
+// memory once.  Every warp copies the weights it will use itself, ring - 1
+// pieces ahead of their use and across units (cp.async, 2 KB a piece and warp: at
+// least 64 KB on their way per SM, where the latency times the bandwidth of
+// this memory needs about 45).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t two) {  // the low 16 bits: two E4M3 values
   uint32_t h;
@@ -416,15 +418,17 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   return v;
 }
 
+// Shared memory: this, then the warps' partial sums, the staged tokens and the
+// rings of weight pieces, laid out by the host for the call's shape.
 struct Smem {
   Routing r;
-  __align__(16) float red[kWarps][16][kRedLd];
   float col_scale[8 * kMaxNT];   // of the staged columns: takes a sum back from the operand's power of two
-  __align__(16) uint8_t ring[kWarps][kRing][kPiece + 16];  // 16 rows x 128 k as the lanes copied them, two scales
-  __align__(16) uint8_t cols[kColsBytes];
 };
-static_assert(sizeof(Smem) <= 232448, "shared memory");
-static_assert((RG_MOE_MAX_WIDTH + 127) / 128 * 256 + 16 <= kColsBytes, "one token of the widest layer");
+constexpr int kFixedBytes = ((int)sizeof(Smem) + 127) / 128 * 128;
+// the widest layer: three pieces per warp, one column tile, one token
+static_assert(kFixedBytes + kWarps * 16 * 20 * 4 + kWarps * kMinRing * kPiece + (RG_MOE_MAX_WIDTH / 128) * 256 + 16 <=
+                  kSmemBytes,
+              "shared memory");
 
 template <bool UP>
 struct Phase {
@@ -434,19 +438,25 @@ struct Phase {
   const int K, nkb, ks, groups, group, kpart, rows_per_expert;
   int u0, u1;            // this CTA's units
   // the next piece to copy
-  int pu, pkb, pa;
+  int pu, pkb, pa, prb, pend;  // unit, 128-block, active expert, its row block, its last unit + 1
+  const uint8_t* pw;
+  const float* ps;
   const uint8_t* p_lo;
   const uint8_t* p_hi;
-  const float* p_slo;
-  const float* p_shi;
-  int slot;              // ring slot of the next piece to use
+  const float* p_s;      // the even lanes' (gate, or all) or the odd lanes' (up) row scales
+  uint8_t* const cols;   // staged tokens
+  float* const red;      // [warps][16][red_ld]
+  const uint32_t ring;   // this warp's pieces
+  int slot;              // the next piece to use
   int parity;            // half of the reduction buffer
 
-  __device__ Phase(const MoeParams& pp, Smem& s)
+  __device__ Phase(const MoeParams& pp, Smem& s, uint8_t* base)
       : p(pp), sm(s), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), g((threadIdx.x & 31) >> 2),
         t4(threadIdx.x & 3), K(UP ? pp.H : pp.I), nkb((K + 127) / 128), ks(UP ? pp.ks_up : pp.ks_down),
         groups(kWarps / ks), group((threadIdx.x >> 5) / ks), kpart((threadIdx.x >> 5) % ks),
-        rows_per_expert(UP ? pp.I / 8 : pp.H / 16), slot(0), parity(0) {}
+        rows_per_expert(UP ? pp.I / 8 : pp.H / 16),
+        cols(base + pp.cols_off), red(reinterpret_cast<float*>(base + pp.red_off)),
+        ring(su32(base + pp.ring_off) + (threadIdx.x >> 5) * pp.ring * kPiece), slot(0), parity(0) {}
 
   __device__ int cap() const { return UP ? p.cap_up : p.cap_down; }
 
@@ -477,50 +487,87 @@ struct Phase {
     pu = u0 + group;
     pkb = kpart;
     pa = 0;
-    if (pu < u1) point();
+    if (pu < u1) point_expert();
   }
 
-  // The weight rows and scales of unit pu.
-  __device__ __forceinline__ void point() {
+  // The expert of unit pu: its weights and scales, and pu's row block.
+  __device__ __forceinline__ void point_expert() {
     const Routing& r = sm.r;
     while (pu >= r.units[pa + 1]) ++pa;
-    const int e = r.active[pa], rb = (pu - r.units[pa]) % rows_per_expert;
-    const int hb = (p.H + 127) / 128;
-    if constexpr (UP) {  // eight gate rows, eight up rows
-      const int ib = (2 * p.I + 127) / 128, row = rb * 8 + g;
-      p_lo = p.W13 + ((long long)e * 2 * p.I + row) * p.H;
-      p_hi = p_lo + (long long)p.I * p.H;
-      const float* s = p.S13 + (long long)e * ib * hb;
-      p_slo = s + (long long)(row / 128) * hb;
-      p_shi = s + (long long)((p.I + row) / 128) * hb;
+    const int e = r.active[pa], hb = (p.H + 127) / 128;
+    prb = (pu - r.units[pa]) % rows_per_expert;
+    pend = r.units[pa + 1];
+    if constexpr (UP) {
+      pw = p.W13 + ((long long)e * 2 * p.I + (lane >> 3)) * p.H;
+      ps = p.S13 + (long long)e * ((2 * p.I + 127) / 128) * hb;
     } else {
-      const int ib = (p.I + 127) / 128, row = rb * 16 + g;
-      p_lo = p.W2 + ((long long)e * p.H + row) * p.I;
-      p_hi = p_lo + 8LL * p.I;
-      p_slo = p_shi = p.S2 + ((long long)e * hb + row / 128) * ib;
+      pw = p.W2 + ((long long)e * p.H + (lane >> 3)) * p.I;
+      ps = p.S2 + (long long)e * hb * nkb;
+    }
+    point();
+  }
+  // Row block prb's weights and scales.  A lane copies 16 bytes of rows lane / 8 +
+  // 4 j of the 16 (whole 128-byte lines per eight lanes); the even lanes' scales
+  // are the gate's (or all rows'), the odd lanes' the up rows'.
+  __device__ __forceinline__ void point() {
+    if constexpr (UP) {  // eight gate rows, eight up rows
+      p_lo = pw + (long long)(prb * 8) * K;
+      p_hi = p_lo + (long long)p.I * K;
+      p_s = ps + (((lane & 1) * p.I + prb * 8) >> 7) * nkb;
+    } else {
+      p_lo = pw + (long long)(prb * 16) * K;
+      p_hi = p_lo + 8LL * K;
+      p_s = ps + (prb >> 3) * nkb;
+    }
+  }
+  __device__ __forceinline__ void next_unit() {
+    pu += groups;
+    if (pu >= u1) return;
+    if (pu >= pend) {
+      point_expert();
+    } else {
+      prb += groups;
+      while (prb >= rows_per_expert) prb -= rows_per_expert;  // the next pass over the same expert
+      point();
     }
   }
 
-  // Starts the copy of the next piece into ring slot s (an empty group at the end).
+  // Starts the copy of the next piece into ring slot s (an empty group at the
+  // end).  Row r's 16-byte chunk c lies at r * 128 + (c ^ 4 (r & 1)) * 16, which
+  // the MMA lanes read without bank conflicts.
   __device__ __forceinline__ void copy_next(int s) {
     if (pu < u1) {
-      const uint32_t dst = su32(sm.ring[warp][s]) + lane * 16;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int k = pkb * 128 + half * 64 + t4 * 16;
-        const bool live = k < K;
-        copy16(dst + (2 * half) * 512, live ? p_lo + k : p_lo, live);
-        copy16(dst + (2 * half + 1) * 512, live ? p_hi + k : p_hi, live);
-      }
-      if (lane < 2) copy4(su32(sm.ring[warp][s]) + kPiece + lane * 4, (lane ? p_shi : p_slo) + pkb);
+      const uint32_t at = ring + s * kPiece;
+      const int c = lane & 7, k = pkb * 128 + c * 16;
+      const bool live = k < K;
+      const uint32_t dst = at + (lane >> 3) * 128 + ((c ^ ((lane >> 3) & 1) << 2) << 4);
+      const long long down4 = 4LL * K;
+      const uint8_t* lo = live ? p_lo + k : p_lo;
+      const uint8_t* hi = live ? p_hi + k : p_hi;
+      copy16(dst, lo, live);
+      copy16(dst + 4 * 128, lo + down4, live);
+      copy16(dst + 8 * 128, hi, live);
+      copy16(dst + 12 * 128, hi + down4, live);
+      if (lane < 2) copy4(at + 16 * 128 + lane * 4, p_s + pkb);
       pkb += ks;
       if (pkb >= nkb) {
         pkb = kpart;
-        pu += groups;
-        if (pu < u1) point();
+        next_unit();
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+
+  // All but the newest ring - 2 copies of this lane have landed.
+  __device__ __forceinline__ void wait_oldest() {
+    switch (p.ring) {
+      case 3: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+      case 4: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+      case 5: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+      case 6: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+      case 7: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+      default: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    }
   }
 
   __device__ int stride() const { return nkb * 256 + 16; }  // bytes per staged token: conflict-free for the lanes' loads
@@ -531,7 +578,7 @@ struct Phase {
     const int chunks = nkb * 16, st = stride();
     if ((int)threadIdx.x < n) {
       const int s = r.order[first + threadIdx.x];
-      sm.col_scale[threadIdx.x] = UP ? __ldcg(&p.w.x_inv[s / p.top_k]) : pow2_scale(__ldcg(&p.w.h_max[s])).y;
+      sm.col_scale[threadIdx.x] = UP ? __ldcg(&p.w.x_inv[s / p.top_k]) : pow2_scale(__ldcg(&p.w.h_max[s * kMaxStride])).y;
     }
     for (int i = threadIdx.x; i < n * chunks; i += kThreads) {
       const int c = i / chunks, k = (i - c * chunks) * 8, s = r.order[first + c];
@@ -540,7 +587,7 @@ struct Phase {
         if constexpr (UP) {
           v = __ldcg(reinterpret_cast<const uint4*>(p.w.xs + (long long)(s / p.top_k) * K + k));
         } else {
-          const float sc = pow2_scale(__ldcg(&p.w.h_max[s])).x;
+          const float sc = pow2_scale(__ldcg(&p.w.h_max[s * kMaxStride])).x;
           const float4* h = reinterpret_cast<const float4*>(p.w.h + (long long)s * K + k);
           const float4 a = __ldcg(h), b = __ldcg(h + 1);
           const __half2 h0 = __floats2half2_rn(a.x * sc, a.y * sc), h1 = __floats2half2_rn(a.z * sc, a.w * sc);
@@ -551,18 +598,30 @@ struct Phase {
           v.w = *reinterpret_cast<const uint32_t*>(&h3);
         }
       }
-      *reinterpret_cast<uint4*>(sm.cols + c * st + k * 2) = v;
+      *reinterpret_cast<uint4*>(cols + c * st + k * 2) = v;
     }
   }
 
-  __device__ void store(int rb, int row, int first, int c, float lo, float hi) {
-    const int s = sm.r.order[first + c];
+  // Column c's sums of row pair `row` of row block rb, by whole warps; the lanes
+  // that differ in the bits of `lanes` hold the rows of one column.
+  __device__ __forceinline__ void store(int rb, int row, int first, int c, bool live, float lo, float hi, int lanes) {
+    const int s = live ? sm.r.order[first + c] : 0;
     if constexpr (UP) {
-      const float a = lo * sm.col_scale[c], u = hi * sm.col_scale[c];
-      const float h = a / (1.0f + expf(-a)) * u;
-      p.w.h[(long long)s * p.I + rb * 8 + row] = h;
-      atomicMax(&p.w.h_max[s], __float_as_uint(h) & 0x7FFFFFFFu);  // a maximum: the order does not matter
-    } else {
+      uint32_t m = 0;
+      if (live) {
+        const float a = lo * sm.col_scale[c], u = hi * sm.col_scale[c];
+        const float h = a / (1.0f + expf(-a)) * u;
+        p.w.h[(long long)s * p.I + rb * 8 + row] = h;
+        m = __float_as_uint(h) & 0x7FFFFFFFu;
+      }
+      // one maximum per column (their order does not matter), each slot's in a
+      // sector of its own: a maximum per entry into adjacent words kept one L2
+      // slice busy for longer than all the weights took
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, lanes));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2 * lanes));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4 * lanes));
+      if (live && row == 0) atomicMax(&p.w.h_max[s * kMaxStride], m);
+    } else if (live) {
       const float back = sm.col_scale[c];
       float* out = p.w.part + (long long)s * p.H + rb * 16 + row;
       out[0] = lo * back;
@@ -579,11 +638,11 @@ struct Phase {
     // columns past the last repeat it and are not stored
     uint32_t col[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) col[i] = su32(sm.cols) + min(i * 8 + g, n - 1) * stride() + t4 * 32;
+    for (int i = 0; i < NT; ++i) col[i] = su32(cols) + min(i * 8 + g, n - 1) * stride() + t4 * 32;
     for (int kb = kpart; kb < nkb; kb += ks) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+      wait_oldest();
       __syncwarp();
-      const uint32_t piece = su32(sm.ring[warp][slot]);
+      const uint32_t piece = ring + slot * kPiece;
       float acc[NT][4], odd[NT][4];  // two chains of MMAs, even and odd k groups
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
@@ -592,7 +651,8 @@ struct Phase {
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const uint4 lo = lds16(piece + lane * 16 + (2 * half) * 512), hi = lds16(piece + lane * 16 + (2 * half + 1) * 512);
+        const uint32_t at = piece + g * 128 + (((half * 4 + t4) ^ (g & 1) << 2) << 4);
+        const uint4 lo = lds16(at), hi = lds16(at + 8 * 128);
         const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
         uint32_t a[4][4];
 #pragma unroll
@@ -604,16 +664,16 @@ struct Phase {
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const uint32_t at = col[i] + kb * 256 + half * 128;
-          const uint4 x0 = lds16(at), x1 = lds16(at + 16);
+          const uint32_t xa = col[i] + kb * 256 + half * 128;
+          const uint4 x0 = lds16(xa), x1 = lds16(xa + 16);
           mma_t<__half>(acc[i], a[0][0], a[0][1], a[0][2], a[0][3], x0.x, x0.y);
           mma_t<__half>(odd[i], a[1][0], a[1][1], a[1][2], a[1][3], x0.z, x0.w);
           mma_t<__half>(acc[i], a[2][0], a[2][1], a[2][2], a[2][3], x1.x, x1.y);
           mma_t<__half>(odd[i], a[3][0], a[3][1], a[3][2], a[3][3], x1.z, x1.w);
         }
       }
-      const float s0 = *reinterpret_cast<const float*>(sm.ring[warp][slot] + kPiece);
-      const float s1 = *reinterpret_cast<const float*>(sm.ring[warp][slot] + kPiece + 4);
+      float s0, s1;
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(s0), "=f"(s1) : "r"(piece + 16 * 128) : "memory");
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         tot[i][0] = fmaf(acc[i][0] + odd[i][0], s0, tot[i][0]);
@@ -621,37 +681,41 @@ struct Phase {
         tot[i][2] = fmaf(acc[i][2] + odd[i][2], s1, tot[i][2]);
         tot[i][3] = fmaf(acc[i][3] + odd[i][3], s1, tot[i][3]);
       }
-      __syncwarp();  // every lane has read this slot's scales before the slot before it is refilled
-      copy_next(slot == 0 ? kRing - 1 : slot - 1);
-      slot = slot + 1 == kRing ? 0 : slot + 1;
+      // the slot before this one: all lanes have read it since they met above
+      copy_next(slot == 0 ? p.ring - 1 : slot - 1);
+      slot = slot + 1 == p.ring ? 0 : slot + 1;
     }
     if (ks == 1) {
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-          if (i * 8 + 2 * t4 + j < n) store(rb, g, first, i * 8 + 2 * t4 + j, tot[i][j], tot[i][2 + j]);
+        {
+          const int c = i * 8 + 2 * t4 + j;
+          store(rb, g, first, c, c < n, tot[i][j], tot[i][2 + j], 4);
+        }
       return;
     }
-    // up to 16 columns: units alternate between the buffer's halves, so that one
-    // meeting of the group per unit is enough
+    // up to 16 columns: units alternate between two halves of the buffer, so that
+    // one meeting of the group per unit is enough
     constexpr bool kHalves = NT <= kMaxNT / 2;
-    const int off = kHalves ? parity * (8 * kMaxNT / 2) : 0;
-    float(*red)[16][kRedLd] = sm.red + group * ks;
+    const int ld = p.red_ld;
+    float* part = red + (size_t)group * ks * 16 * ld + (kHalves ? parity * (8 * NT) : 0);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      *reinterpret_cast<float2*>(&red[kpart][g][off + i * 8 + 2 * t4]) = make_float2(tot[i][0], tot[i][1]);
-      *reinterpret_cast<float2*>(&red[kpart][g + 8][off + i * 8 + 2 * t4]) = make_float2(tot[i][2], tot[i][3]);
+      *reinterpret_cast<float2*>(&part[(kpart * 16 + g) * ld + i * 8 + 2 * t4]) = make_float2(tot[i][0], tot[i][1]);
+      *reinterpret_cast<float2*>(&part[(kpart * 16 + g + 8) * ld + i * 8 + 2 * t4]) = make_float2(tot[i][2], tot[i][3]);
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ks * 32) : "memory");
-    for (int i = kpart * 32 + lane; i < 8 * n; i += ks * 32) {
-      const int c = i >> 3, row = i & 7;
+    for (int c0 = kpart * 4; c0 < n; c0 += ks * 4) {  // four columns of eight row pairs per warp
+      const int c = c0 + (lane >> 3), row = lane & 7;
       float lo = 0.0f, hi = 0.0f;
-      for (int w = 0; w < ks; ++w) {
-        lo += red[w][row][off + c];
-        hi += red[w][row + 8][off + c];
-      }
-      store(rb, row, first, c, lo, hi);
+      if (c < n)
+        for (int w = 0; w < ks; ++w) {
+          lo += part[(w * 16 + row) * ld + c];
+          hi += part[(w * 16 + row + 8) * ld + c];
+        }
+      store(rb, row, first, c, c < n, lo, hi, 1);
     }
     if constexpr (kHalves) parity ^= 1;
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ks * 32) : "memory");
@@ -662,7 +726,7 @@ struct Phase {
     Routing& r = sm.r;
     plan_units(cta, ctas);
     slot = 0;
-    for (int s = 0; s < kRing - 1; ++s) copy_next(s);
+    for (int s = 0; s < p.ring - 1; ++s) copy_next(s);
     if (!before_use()) return false;
     int a = 0, mine = u0 + group;
     for (int at = u0; at < u1;) {  // segments: the units of one pass over one expert
@@ -687,14 +751,14 @@ struct Phase {
 
 // Phase 4: the weighted sum of each token's experts, in the order of their ranks.
 template <typename T>
-__device__ void combine_phase(const MoeParams& p, const Routing& r, int cta, int ctas) {
+__device__ void combine_phase(const MoeParams& p, int cta, int ctas) {
   T* Y = static_cast<T*>(p.Y);
   for (long long i = (long long)cta * kThreads + threadIdx.x; i < (long long)p.T * p.H; i += (long long)ctas * kThreads) {
     const int t = (int)(i / p.H), c = (int)(i - (long long)t * p.H);
     float y = 0.0f;
     for (int j = 0; j < p.top_k; ++j) {
       const int slot = t * p.top_k + j;
-      y = fmaf(r.gate[slot], __ldcg(&p.w.part[(long long)slot * p.H + c]), y);
+      y = fmaf(__ldg(&p.w.gate[slot]), __ldcg(&p.w.part[(long long)slot * p.H + c]), y);
     }
     T o;
     from_f(y, o);
@@ -704,25 +768,25 @@ __device__ void combine_phase(const MoeParams& p, const Routing& r, int cta, int
 
 // Kernel 2 (cooperative, one CTA per SM): routing, the two products, the sum.
 __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_constant__ MoeParams p) {
-  extern __shared__ __align__(16) uint8_t raw[];
+  extern __shared__ __align__(128) uint8_t raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int cta = blockIdx.x, ctas = gridDim.x;
   form_routing(p, sm.r);
   {
-    Phase<true> up(p, sm);
+    Phase<true> up(p, sm, raw);
     up.run(cta, ctas, [] { return true; });
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   bool ok;
   {
     // the second product's first weights are on their way while the grid meets
-    Phase<false> down(p, sm);
+    Phase<false> down(p, sm, raw);
     ok = down.run(cta, ctas, [&] { return grid_barrier(p, sm.r, (unsigned)ctas); });
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (!ok || !grid_barrier(p, sm.r, 2u * (unsigned)ctas)) return;
-  if (p.type == RG_TYPE_F16) combine_phase<__half>(p, sm.r, cta, ctas);
-  else combine_phase<__nv_bfloat16>(p, sm.r, cta, ctas);
+  if (p.type == RG_TYPE_F16) combine_phase<__half>(p, cta, ctas);
+  else combine_phase<__nv_bfloat16>(p, cta, ctas);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -742,7 +806,7 @@ size_t layout(long long T, long long H, long long I, long long top_k, uint8_t* b
   m.xs = reinterpret_cast<__half*>(take((size_t)T * H * 2));
   m.x_inv = reinterpret_cast<float*>(take((size_t)T * 4));
   m.h = reinterpret_cast<float*>(take(slots * I * 4));
-  m.h_max = reinterpret_cast<uint32_t*>(take(slots * 4));
+  m.h_max = reinterpret_cast<uint32_t*>(take(slots * 4 * kMaxStride));
   m.arrived = reinterpret_cast<unsigned*>(take(4));
   m.part = reinterpret_cast<float*>(take(slots * H * 4));
   if (w) *w = m;
@@ -755,26 +819,52 @@ size_t moe_f8_scratch_bytes(long long T, long long H, long long I, long long top
   return layout(T, H, I, top_k, nullptr, nullptr);
 }
 
-// Warps that split k: as many (a power of two) as leave each two 128-blocks.
-// Fixed by the widths alone, so that a token's sums do not depend on what comes
-// with it.
+// Warps that split k: as many (a power of two) as leave each eight 128-blocks
+// (with two, the work around a unit took as long as the unit).  Fixed by the
+// widths alone, so that a token's sums do not depend on what comes with it.
 int k_split(long long K) {
   const long long nkb = (K + 127) / 128;
   int ks = 1;
-  while (ks < 8 && nkb >= 4 * ks) ks *= 2;
+  while (ks < 8 && nkb >= 16 * ks) ks *= 2;
   return ks;
 }
-// Tokens per pass over an expert's weights: what fits beside the weights.
-int tokens_per_pass(long long K) {
-  const long long n = kColsBytes / ((K + 127) / 128 * 256 + 16);
-  return (int)(n >= 8 * kMaxNT ? 8 * kMaxNT : n >= 8 ? n / 8 * 8 : n);
+// The call's shared memory: room for the tokens that nearly every expert gets
+// in one pass (the mean of even routing and two deviations), at least three
+// pieces per warp, and what is left to deeper rings.
+void plan_smem(MoeParams& p) {
+  const int bytes_up = (p.H + 127) / 128 * 256 + 16, bytes_down = (p.I + 127) / 128 * 256 + 16;
+  const int wide = bytes_up > bytes_down ? bytes_up : bytes_down, ring1 = kWarps * kPiece;
+  const double mean = (double)p.T * p.top_k / p.E;
+  int tokens = (int)std::ceil(mean + 2.0 * std::sqrt(mean));
+  if (tokens > 8) tokens = (tokens + 7) / 8 * 8;
+  if (tokens > 8 * kMaxNT) tokens = 8 * kMaxNT;
+  if (tokens > p.T) tokens = p.T;
+  // one or two column tiles: two halves (see unit())
+  auto tiles = [](int n) { return n <= 8 ? 1 : n <= 16 ? 2 : kMaxNT; };
+  auto ld = [&](int n) { return (tiles(n) < kMaxNT ? 16 * tiles(n) : 8 * kMaxNT) + 4; };
+  auto room_for = [&](int n) { return kSmemBytes - kFixedBytes - kMinRing * ring1 - kWarps * 16 * 4 * ld(n); };
+  while (tokens * wide > room_for(tokens)) tokens = tokens > 8 ? (tokens - 1) / 8 * 8 : tokens - 1;
+  int room = room_for(tokens) - tokens * wide;
+  p.ring = kMinRing;
+  for (; p.ring < kMaxRing && room >= ring1; ++p.ring) room -= ring1;
+  auto fit = [&](int bytes) {
+    int n = (tokens * wide + room) / bytes;
+    if (n > 8) n = n / 8 * 8;
+    return n > 8 * tiles(tokens) ? 8 * tiles(tokens) : n;
+  };
+  p.cap_up = fit(bytes_up);
+  p.cap_down = fit(bytes_down);
+  p.red_ld = ld(tokens);
+  p.red_off = kFixedBytes;
+  p.cols_off = p.red_off + kWarps * 16 * 4 * p.red_ld;
+  p.ring_off = kSmemBytes - p.ring * ring1;
 }
 
 cudaError_t launch_moe_f8(const MoeArgs& a, DevPlan* plan, void* scratch, cudaStream_t st,
                           unsigned long long wait_ns) {
   MoeParams p{a.X, a.WR, a.W13, a.S13, a.W2, a.S2, a.Y, (int)a.T, (int)a.H, (int)a.I, (int)a.E, (int)a.top_k, a.type,
-              a.renorm ? 1 : 0, k_split(a.H), k_split(a.I), tokens_per_pass(a.H), tokens_per_pass(a.I), wait_ns, plan,
-              {}};
+              a.renorm ? 1 : 0, k_split(a.H), k_split(a.I), 0, 0, 0, 0, 0, 0, 0, wait_ns, plan, {}};
+  plan_smem(p);
   layout(a.T, a.H, a.I, a.top_k, static_cast<uint8_t*>(scratch), &p.w);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -785,7 +875,7 @@ cudaError_t launch_moe_f8(const MoeArgs& a, DevPlan* plan, void* scratch, cudaSt
     static int known[64];
     std::lock_guard<std::mutex> lock(mu);
     if (!known[dev]) {
-      e = cudaFuncSetAttribute(moe_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+      e = cudaFuncSetAttribute(moe_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
       if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
       if (e != cudaSuccess) return e;
       known[dev] = sms;
@@ -800,7 +890,7 @@ cudaError_t launch_moe_f8(const MoeArgs& a, DevPlan* plan, void* scratch, cudaSt
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = sizeof(Smem);
+  cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
