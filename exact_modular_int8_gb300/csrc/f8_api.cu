@@ -61,10 +61,11 @@ int scaled_gemm_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t
       return RG_ERR_ARG;
     if (blocks128(M) * blocks128(N) > INT_MAX / 8) return RG_ERR_ARG;
   }
-  if (cudaMemsetAsync(plan, 0, sizeof(DevPlan), st) != cudaSuccess) return RG_ERR_CUDA;
-  if (M && N && !K) {  // an empty sum
-    if (cudaMemset2DAsync(C, (size_t)ldc * es, 0, (size_t)N * es, (size_t)M, st) != cudaSuccess) return RG_ERR_CUDA;
-  } else if (M && N) {
+  if (!(M && N && K)) {  // an empty sum, or nothing at all (the kernels clear the status themselves)
+    if (cudaMemsetAsync(plan, 0, sizeof(DevPlan), st) != cudaSuccess) return RG_ERR_CUDA;
+    if (M && N && cudaMemset2DAsync(C, (size_t)ldc * es, 0, (size_t)N * es, (size_t)M, st) != cudaSuccess)
+      return RG_ERR_CUDA;
+  } else {
     const long long kb = blocks128(K), nb = tile_b ? blocks128(N) : N;
     F8GemmArgs a{A, B, SA, SB, C, lda, ldb, ldc, transb ? kb : 1, transb ? 1 : nb, M, N, K, c_type, transb, tile_b};
     if (launch_f8_gemm(a, plan, st, take_fault(), wait_limit_ns()) != cudaSuccess) return RG_ERR_CUDA;

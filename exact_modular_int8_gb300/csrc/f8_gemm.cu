@@ -59,6 +59,16 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t adesc, uint64_t bde
       : "memory");
 }
 
+// The call's status, in place of a memset before the kernel: by the grid's first
+// thread as it starts, a time limit (which no wait can have used up yet) before
+// any CTA could write to it.
+__device__ __forceinline__ void clear_status(DevPlan* plan) {
+  if (blockIdx.x == 0) {
+    plan->status = 0;
+    plan->timeout_where = 0;
+  }
+}
+
 // One thread of a converged warp.  The issuing warps run their loops whole and
 // elect a thread for the MMAs alone: their descriptors then stay in uniform
 // registers.
@@ -89,9 +99,12 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -270,10 +283,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   ScaleChunk<BN1>* scales = reinterpret_cast<ScaleChunk<BN1>*>(smem + STAGES1 * STAGE1_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES1 * STAGE1_BYTES + SCALE1_BYTES);
   uint64_t* full = bars;
-  uint64_t* empty = bars + STAGES1;
-  uint64_t* tfull = bars + 2 * STAGES1;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* sfull = tfull + 4;
+  uint64_t* done = bars + STAGES1;        // the stage's MMAs are complete
+  uint64_t* tempty = bars + 2 * STAGES1;  // by accumulator
+  uint64_t* sfull = tempty + 2;
   uint64_t* sempty = sfull + SCALE_BUFS;
   uint64_t* drain = sempty + SCALE_BUFS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -287,14 +299,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   Ctl ctl{abort_flag, &plan->status, &plan->timeout_where, gp.wait_ns};
 
   if (threadIdx.x == 0) {
+    clear_status(plan);
     for (int s = 0; s < STAGES1; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(smem_u32(&done[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&tfull[b]), 1);
-      mbar_init(smem_u32(&tempty[b]), EPI_WARPS);
-    }
+    for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&tempty[b]), EPI_WARPS);
     for (int b = 0; b < SCALE_BUFS; ++b) {
       mbar_init(smem_u32(&sfull[b]), 64);
       mbar_init(smem_u32(&sempty[b]), EPI_WARPS);
@@ -325,7 +335,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t issued_phase[STAGES1] = {};
       bool ok = true;
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
-        if (!wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, ctl, 21)) {
+        if (!wait_bounded(smem_u32(&done[stage]), phase ^ 1u, ctl, 21)) {
           ok = false;
           break;
         }
@@ -352,41 +362,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, it = 0;
-      bool ok = true;
-      for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
-        const uint32_t b = it & 1u, aph = (it >> 1) & 1u;
-        if (!wait_bounded(smem_u32(&tempty[b]), aph ^ 1u, ctl, 22) ||
-            !wait_bounded(smem_u32(&full[stage]), phase, ctl, 23)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t a_addr = smem_u32(stage_base + stage * STAGE1_BYTES);
-        const uint64_t adesc = sw128_desc(a_addr, 16, 1024);
-        const uint64_t bdesc =
-            B_KMAJOR ? sw128_desc(a_addr + SLAB, 16, 1024) : sw128_desc(a_addr + SLAB, SLAB, 1024);
-        constexpr uint32_t b_step = B_KMAJOR ? 2 : 256;  // 32 k: 32 bytes along a row, or 32 rows of 128 bytes
-        constexpr uint32_t idesc = idesc_f8(128, BN1, B_KMAJOR);
+    const uint32_t a_addr = smem_u32(stage_base), b_addr = a_addr + SLAB;
+    const uint64_t adesc0 = sw128_desc(a_addr, 16, 1024);
+    const uint64_t bdesc0 = B_KMAJOR ? sw128_desc(b_addr, 16, 1024) : sw128_desc(b_addr, SLAB, 1024);
+    constexpr uint32_t b_step = B_KMAJOR ? 2 : 256;  // 32 k: 32 bytes along a row, or 32 rows of 128 bytes
+    constexpr uint32_t idesc = idesc_f8(128, BN1, B_KMAJOR);
+    int stage = 0;
+    uint32_t phase = 0, it = 0;
+    bool ok = true;
+    for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
+      const uint32_t b = it & 1u, aph = (it >> 1) & 1u;
+      ok = wait_both(smem_u32(&tempty[b]), aph ^ 1u, smem_u32(&full[stage]), phase, ctl, 22);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t off = (uint64_t)(stage * (STAGE1_BYTES >> 4));
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < BK / 32; ++kk)
-          umma_f8(tmem_base + b * BN1, adesc + (uint64_t)(2 * kk), bdesc + (uint64_t)(b_step * kk), idesc, kk > 0);
-        umma_commit(smem_u32(&empty[stage]));
-        if (!(gp.fault == 1 && it == 0)) umma_commit(smem_u32(&tfull[b]));
-        if (++stage == STAGES1) {
-          stage = 0;
-          phase ^= 1u;
-        }
+          umma_f8(tmem_base + b * BN1, adesc0 + off + (uint64_t)(2 * kk), bdesc0 + off + (uint64_t)(b_step * kk), idesc,
+                  kk > 0);
+        if (!(gp.fault == 1 && it == 0)) umma_commit(smem_u32(&done[stage]));
       }
-      if (!ok && it > 0) {  // all issued MMAs must finish before the memory is freed
-        Ctl drain_ctl = ctl;
-        volatile int never = 0;
-        drain_ctl.abort = &never;
-        umma_commit(smem_u32(drain));
-        wait_bounded(smem_u32(drain), 0, drain_ctl, 0);
+      __syncwarp();
+      if (++stage == STAGES1) {
+        stage = 0;
+        phase ^= 1u;
       }
+    }
+    if (!ok && it > 0) {  // all issued MMAs must finish before the memory is freed
+      Ctl drain_ctl = ctl;
+      volatile int never = 0;
+      drain_ctl.abort = &never;
+      if (elect_one()) umma_commit(smem_u32(drain));
+      __syncwarp();
+      wait_bounded(smem_u32(drain), 0, drain_ctl, 0);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------ scales
@@ -407,14 +416,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint64_t acc[WC / 2];
 #pragma unroll
     for (int i = 0; i < WC / 2; ++i) acc[i] = 0;
-    uint32_t it = 0;
+    uint32_t it = 0, phase = 0;
+    int st = 0;  // pipeline stage
     bool ok = true;
     for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
-      const uint32_t b = it & 1u, aph = (it >> 1) & 1u;
+      const uint32_t b = it & 1u;
       const int c = (int)it / KC, kbi = (int)it % KC;
       const ScaleChunk<BN1>& sc = scales[c & 1];
       ok = kbi != 0 || wait_bounded(smem_u32(&sfull[c & 1]), (c >> 1) & 1u, ctl, 26);
-      ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded(smem_u32(&tfull[b]), aph, ctl, 24));
+      ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded(smem_u32(&done[st]), phase, ctl, 24));
+      if (++st == STAGES1) {
+        st = 0;
+        phase ^= 1u;
+      }
       if (!ok) break;
       tc_fence_after();
       float s = sc.a[kbi][row];
@@ -454,18 +468,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (!*abort_flag) {
     const int rows = min(128, gp.M - tm * 128), cols = min(BN1, gp.N - tn * BN1);
     const uint32_t base = smem_u32(stage_base);
-    for (int r = rank + S * warp; r < rows; r += S * (NUM_THREADS / 32)) {
-      const long long out = (long long)(tm * 128 + r) * gp.ldc + (long long)tn * BN1;
-      for (int c = lane; c < cols; c += 32) {
-        const uint32_t at = base + (uint32_t)(r * PART_LD + c) * 4;
-        float v;
-        if (S == 1) {
-          v = reinterpret_cast<const float*>(stage_base)[r * PART_LD + c];
+    const int c = 4 * lane;  // this lane's columns
+    for (int r = rank + S * warp; r < rows && c < cols; r += S * (NUM_THREADS / 32)) {
+      const uint32_t at = base + (uint32_t)(r * PART_LD + c) * 4;
+      float4 v = ld_cluster4(mapa_shared(at, 0));
+#pragma unroll 4
+      for (int k = 1; k < S; ++k) {
+        const float4 u = ld_cluster4(mapa_shared(at, (uint32_t)k));
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+      }
+      const long long out = (long long)(tm * 128 + r) * gp.ldc + (long long)tn * BN1 + c;
+      if (gp.vec_c && c + 4 <= cols) {
+        if (gp.out_type == RG_TYPE_F32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(gp.C) + out) = v;
         } else {
-          v = ld_cluster(mapa_shared(at, 0));
-          for (int k = 1; k < S; ++k) v += ld_cluster(mapa_shared(at, (uint32_t)k));
+          uint2 w;
+          if (gp.out_type == RG_TYPE_F16) {
+            const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+            w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+          } else {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+            w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+          }
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(gp.C) + out) = w;
         }
-        store_out(gp.C, out + c, gp.out_type, v);
+      } else {
+        const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c + q < cols) store_out(gp.C, out + q, gp.out_type, e[q]);
       }
     }
   }
@@ -612,6 +646,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   Ctl ctl{abort_flag, &plan->status, &plan->timeout_where, gp.wait_ns};
 
   if (threadIdx.x == 0) {
+    clear_status(plan);
     for (int s = 0; s < STAGES2; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&done[s]), 1);
@@ -885,6 +920,13 @@ cudaError_t f8_device(int dev, F8Device& out) {
 
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, int fault,
                            unsigned long long wait_ns) {
+  const int variant = gemm_variant();
+  // Few rows: up to 16 the warp-level kernel is faster at every size measured
+  // (8192 x 4096: 9.3 us for one row, 11.7 for 16, against 14.5 with padded tiles);
+  // from 17 to 32 while B is small enough for latency to count (24 rows: 2.7
+  // against 6.4 us at 1024 x 1024, 17.8 against 14.3 at 8192 x 4096).
+  if (variant == 0 && a.b_kmajor && (a.M <= 16 || (a.M <= kSkinnyRows && a.N * a.K <= (1LL << 24))))
+    return launch_f8_skinny(a, plan, st);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -910,9 +952,12 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
   p.fault = fault;
   p.wait_ns = wait_ns;
   cudaLaunchAttribute attr[1];
-  const int variant = gemm_variant();
   const long long tiles2 = ((a.M + 255) / 256) * ((a.N + BN2 - 1) / BN2);
-  const bool pair = variant == 2 || (variant == 0 && tiles2 >= fd.max_pairs);
+  // Tiles of 128 x 128 while one wave of CTAs holds them all, split along K where
+  // that leaves SMs idle; beyond that the pair kernel's tiles.  (4096 columns, K =
+  // 4096: 512 rows, 128 tiles, 15.2 against the pairs' 20.6 us; 768 rows, 192
+  // tiles, 27.8 against 20.9 us.)
+  const bool pair = variant == 2 || (variant == 0 && (long long)p.mt * p.nt > fd.sms);
   const uint32_t b_cols = pair ? 64 : 128;  // columns of B per copy
   CUtensorMap ma, mb;
   if (!make_map_2d(&ma, a.A, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.lda, BK, 128) ||

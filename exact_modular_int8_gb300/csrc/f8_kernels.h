@@ -42,6 +42,10 @@ struct F8GemmArgs {
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, int fault,
                            unsigned long long wait_ns);
 
+// The same for M <= kSkinnyRows and a transposed B.
+constexpr int kSkinnyRows = 32;
+cudaError_t launch_f8_skinny(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st);
+
 // Mixture-of-experts layer of T <= RG_MOE_MAX_TOKENS tokens (moe_layer_f8).
 struct MoeArgs {
   const void* X;        // [T][H]

@@ -15,8 +15,8 @@ import functools
 import torch
 
 from . import (RG_ERR_ARG, RG_ERR_RANGE, RG_F8_BOTH, RG_F8_COLUMNS, RG_F8_ROWS, RG_F8_TILES, RG_FLAG_SYNC,
-               RG_FLAG_TILE_B, RG_FLAG_TRANS_B, RG_TYPE_BF16, RG_TYPE_F16, RG_TYPE_F32, ResGemmError, _check, _on,
-               _output, library, workspace)
+               RG_FLAG_TILE_B, RG_FLAG_TRANS_B, RG_TYPE_BF16, RG_TYPE_F16, RG_TYPE_F32, ResGemmError, _check, _output,
+               _ws_cache, library, workspace)
 
 BLOCK = 128
 F8 = torch.float8_e4m3fn
@@ -29,11 +29,32 @@ def _blocks(x: int) -> int:
     return (x + BLOCK - 1) // BLOCK
 
 
-def _device(where: str, *ts):
-    dev = ts[0].device
-    if dev.type != "cuda" or any(t.device != dev for t in ts):
-        raise ValueError(f"{where}: tensors on one CUDA device expected")
-    return dev
+def _device_index(where: str, *ts) -> int:
+    """The index of the CUDA device that holds all of the tensors."""
+    idx = ts[0].get_device()
+    for t in ts:
+        if t.get_device() != idx or idx < 0:
+            raise ValueError(f"{where}: tensors on one CUDA device expected")
+    return idx
+
+
+def _launch(idx: int, where: str, f, *args):
+    """The library call f(*args, current stream of device idx) with that device current.  (The raw handle and
+    the plain device check take 0.2 us; torch.cuda's Stream object and device context take ten times that.)"""
+    stream = torch._C._cuda_getCurrentRawStream(idx)
+    if torch._C._cuda_getDevice() == idx:
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(idx):
+            rc = f(*args, stream)
+    if rc:
+        _check(rc, where)
+
+
+def _scratch(nbytes: int, idx: int) -> torch.Tensor:
+    """The cached workspace of the device's current stream (see workspace())."""
+    w = _ws_cache.get((idx, torch._C._cuda_getCurrentRawStream(idx)))
+    return w if w is not None and w.numel() >= nbytes else workspace(nbytes, torch.device("cuda", idx))
 
 
 def _empty_rows(m: int, k: int, device) -> torch.Tensor:
@@ -45,11 +66,12 @@ def _empty_rows(m: int, k: int, device) -> torch.Tensor:
 
 def _row_stride(t: torch.Tensor) -> int:
     """The row stride of a matrix whose rows are contiguous, else 0 (a stride is immaterial with one row)."""
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    (m, k), (s0, s1) = t.shape, t.stride()
+    if s1 != 1 and k > 1:
         return 0
-    if t.shape[0] <= 1:
-        return max(t.shape[1], 1)
-    return t.stride(0) if t.stride(0) >= t.shape[1] else 0
+    if m <= 1:
+        return k or 1
+    return s0 if s0 >= k else 0
 
 
 def _aligned_rows(q: torch.Tensor):
@@ -57,7 +79,7 @@ def _aligned_rows(q: torch.Tensor):
     ld = _row_stride(q)
     if q.shape[0] <= 1:
         ld = (ld + 15) & ~15
-    if not ld or ld % 16 or q.data_ptr() % 16:
+    if not ld or ld & 15 or q.data_ptr() & 15:
         c = _empty_rows(q.shape[0], q.shape[1], q.device)
         c.view(torch.uint8).copy_(q.view(torch.uint8))
         return c, (q.shape[1] + 15) & ~15
@@ -73,37 +95,33 @@ def quantize_f8(X: torch.Tensor, form: str = "rows", sync: bool = True):
          "tiles":   Q [M, K], S [ceil(M/128), ceil(K/128)]: 128 x 128 tiles
     Per block, a = max |x| (at least 2^-60), S = a / 448, Q = 448 x / a to the nearest E4M3 value, ties to
     even; an inf or NaN makes its whole block NaN."""
-    if form not in _FORMS:
+    f = _FORMS.get(form)
+    if f is None:
         raise ValueError(f"quantize_f8: form must be one of {', '.join(_FORMS)}")
-    if X.dim() != 2 or X.dtype not in _TYPES:
+    t = _TYPES.get(X.dtype)
+    if t is None or X.dim() != 2:
         raise ValueError("quantize_f8: X [M, K] float32, float16 or bfloat16 expected")
-    dev = _device("quantize_f8", X)
+    idx = _device_index("quantize_f8", X)
     M, K = X.shape
     ldx = _row_stride(X)
     if not ldx:
         X = X.contiguous()
         ldx = K
-    q = s = qt = st = None
-    ldq = ldqt = 0
-    if form != "columns":
+    dev = X.device
+    q = s = qt = st = qp = sp = qtp = stp = None
+    if f != RG_F8_COLUMNS:
         q = _empty_rows(M, K, dev)
-        ldq = (K + 15) & ~15
-        s = torch.empty((_blocks(M) if form == "tiles" else M, _blocks(K)), dtype=torch.float32, device=dev)
-    if form in ("columns", "both"):
+        s = torch.empty((_blocks(M) if f == RG_F8_TILES else M, _blocks(K)), dtype=torch.float32, device=dev)
+        qp, sp = q.data_ptr(), s.data_ptr()
+    if f == RG_F8_COLUMNS or f == RG_F8_BOTH:
         qt = _empty_rows(K, M, dev)
-        ldqt = (M + 15) & ~15
         st = torch.empty((K, _blocks(M)), dtype=torch.float32, device=dev)
-    with _on(dev):
-        rc = library().quantize_f8(X.data_ptr(), _TYPES[X.dtype], ldx, M, K, _FORMS[form],
-                                   q.data_ptr() if q is not None else None, ldq,
-                                   s.data_ptr() if s is not None else None,
-                                   qt.data_ptr() if qt is not None else None, ldqt,
-                                   st.data_ptr() if st is not None else None, RG_FLAG_SYNC if sync else 0,
-                                   torch.cuda.current_stream(dev).cuda_stream)
-    _check(rc, "quantize_f8")
-    if form == "both":
+        qtp, stp = qt.data_ptr(), st.data_ptr()
+    _launch(idx, "quantize_f8", library().quantize_f8, X.data_ptr(), t, ldx, M, K, f, qp, (K + 15) & ~15, sp, qtp,
+            (M + 15) & ~15, stp, RG_FLAG_SYNC if sync else 0)
+    if f == RG_F8_BOTH:
         return q, s, qt, st
-    return (qt, st) if form == "columns" else (q, s)
+    return (qt, st) if f == RG_F8_COLUMNS else (q, s)
 
 
 def scaled_gemm_f8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Tensor,
@@ -121,26 +139,25 @@ def scaled_gemm_f8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch
     N, Kb = B.shape if transb else (B.shape[1], B.shape[0])
     if K != Kb:
         raise ValueError("scaled_gemm_f8: A and B differ in K")
-    if out_dtype not in _TYPES:
+    t = _TYPES.get(out_dtype)
+    if t is None:
         raise ValueError("scaled_gemm_f8: out_dtype float32, float16 or bfloat16 expected")
     kb, nb = _blocks(K), _blocks(N)
     tile, row = ((nb, kb), (N, kb)) if transb else ((kb, nb), (kb, N))
-    if SA.dtype != torch.float32 or SB.dtype != torch.float32 or tuple(SA.shape) != (M, kb) or \
-            tuple(SB.shape) not in (tile, row):
+    is_tile = SB.shape == tile
+    if SA.dtype != torch.float32 or SB.dtype != torch.float32 or SA.shape != (M, kb) or \
+            not (is_tile or SB.shape == row):
         raise ValueError(f"scaled_gemm_f8: float32 scales SA {(M, kb)} and SB {tile} or {row} expected")
-    dev = _device("scaled_gemm_f8", A, SA, B, SB)
-    flags = (RG_FLAG_SYNC if sync else 0) | (RG_FLAG_TRANS_B if transb else 0)
-    flags |= RG_FLAG_TILE_B if tuple(SB.shape) == tile else 0
+    idx = _device_index("scaled_gemm_f8", A, SA, B, SB)
+    flags = (RG_FLAG_SYNC if sync else 0) | (RG_FLAG_TRANS_B if transb else 0) | (RG_FLAG_TILE_B if is_tile else 0)
     A, lda = _aligned_rows(A)
     B, ldb = _aligned_rows(B)
     SA, SB = SA.contiguous(), SB.contiguous()
-    C = _output(out, (M, N), out_dtype, A, False, "scaled_gemm_f8")
-    with _on(dev):
-        w = ws if ws is not None else workspace(_WS_BYTES, dev)
-        rc = library().scaled_gemm_f8(A.data_ptr(), lda, SA.data_ptr(), B.data_ptr(), ldb, SB.data_ptr(),
-                                      C.data_ptr(), _TYPES[out_dtype], N, M, N, K, flags, w.data_ptr(), w.numel(),
-                                      torch.cuda.current_stream(dev).cuda_stream)
-    _check(rc, "scaled_gemm_f8")
+    C = torch.empty((M, N), dtype=out_dtype, device=A.device) if out is None else \
+        _output(out, (M, N), out_dtype, A, False, "scaled_gemm_f8")
+    w = ws if ws is not None else _scratch(_WS_BYTES, idx)
+    _launch(idx, "scaled_gemm_f8", library().scaled_gemm_f8, A.data_ptr(), lda, SA.data_ptr(), B.data_ptr(), ldb,
+            SB.data_ptr(), C.data_ptr(), t, N, M, N, K, flags, w.data_ptr(), w.numel())
     return C
 
 
@@ -149,7 +166,7 @@ def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True):
     dtype.  `saved` is what linear_f8_backward needs (X quantised along M and the quantised weights)."""
     if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
         raise ValueError("linear_f8: X [M, K] and W [N, K] expected")
-    _device("linear_f8", X, W)
+    _device_index("linear_f8", X, W)
     qx, sx, qxt, sxt = quantize_f8(X, "both", sync=False)
     qw, sw = quantize_f8(W, "tiles", sync=False)
     Y = scaled_gemm_f8(qx, sx, qw, sw, out_dtype=X.dtype, transb=True, sync=sync)
@@ -162,7 +179,7 @@ def linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: tor
     qxt, sxt, qw, sw = saved
     if dY.dim() != 2 or dY.shape != (qxt.shape[1], qw.shape[0]):
         raise ValueError("linear_f8_backward: dY must have the output's shape")
-    _device("linear_f8_backward", dY, qxt)
+    _device_index("linear_f8_backward", dY, qxt)
     qd, sd, qdt, sdt = quantize_f8(dY, "both", sync=False)
     dX = scaled_gemm_f8(qd, sd, qw, sw, out_dtype=dY.dtype, sync=False)
     dW = scaled_gemm_f8(qdt, sdt, qxt, sxt, out_dtype=dw_dtype, transb=True, sync=sync)
@@ -195,27 +212,25 @@ def moe_layer_f8(X: torch.Tensor, WR: torch.Tensor, W13: torch.Tensor, S13: torc
     if W2.dim() != 3 or W2.shape[1] != H:
         raise ValueError("moe_layer_f8: W2 [E, H, I] expected")
     E, I = W2.shape[0], W2.shape[2]  # noqa: E741
-    if tuple(WR.shape) != (E, H) or tuple(W13.shape) != (E, 2 * I, H):
+    if WR.shape != (E, H) or W13.shape != (E, 2 * I, H):
         raise ValueError("moe_layer_f8: WR [E, H] and W13 [E, 2I, H] expected")
-    if tuple(S13.shape) != (E, _blocks(2 * I), _blocks(H)) or tuple(S2.shape) != (E, _blocks(H), _blocks(I)):
+    if S13.shape != (E, _blocks(2 * I), _blocks(H)) or S2.shape != (E, _blocks(H), _blocks(I)):
         raise ValueError("moe_layer_f8: one scale per 128 x 128 tile expected")
-    dev = _device("moe_layer_f8", X, WR, W13, S13, W2, S2)
+    idx = _device_index("moe_layer_f8", X, WR, W13, S13, W2, S2)
     X, WR, W13, S13, W2, S2 = (_start16(t) for t in (X, WR, W13, S13, W2, S2))
-    Y = _output(out, (T, H), X.dtype, X, False, "moe_layer_f8")
+    Y = torch.empty((T, H), dtype=X.dtype, device=X.device) if out is None else \
+        _output(out, (T, H), X.dtype, X, False, "moe_layer_f8")
     need = _moe_ws_bytes(T, H, I, E, int(top_k))
     if not need:
         raise ResGemmError(RG_ERR_RANGE if T > MOE_MAX_TOKENS else RG_ERR_ARG, "moe_layer_f8")
-    with _on(dev):
-        w = ws if ws is not None else workspace(need, dev)
-        rc = library().moe_layer_f8(X.data_ptr(), _TYPES[X.dtype], WR.data_ptr(), W13.data_ptr(), S13.data_ptr(),
-                                    W2.data_ptr(), S2.data_ptr(), Y.data_ptr(), T, H, I, E, int(top_k), int(renorm),
-                                    RG_FLAG_SYNC if sync else 0, w.data_ptr(), w.numel(),
-                                    torch.cuda.current_stream(dev).cuda_stream)
-    _check(rc, "moe_layer_f8")
+    w = ws if ws is not None else _scratch(need, idx)
+    _launch(idx, "moe_layer_f8", library().moe_layer_f8, X.data_ptr(), _TYPES[X.dtype], WR.data_ptr(), W13.data_ptr(),
+            S13.data_ptr(), W2.data_ptr(), S2.data_ptr(), Y.data_ptr(), T, H, I, E, int(top_k), int(renorm),
+            RG_FLAG_SYNC if sync else 0, w.data_ptr(), w.numel())
     return Y
 
 
 def _start16(t: torch.Tensor) -> torch.Tensor:
     """Contiguous, starting on a 16-byte boundary."""
     t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+    return t if t.data_ptr() & 15 == 0 else t.clone()
