@@ -63,7 +63,8 @@ EXPORTED = (
     "interval_gemm_f32", "interval_gemm_f64_batched", "interval_gemm_f32_batched", "rg_solve_i64",
     "rg_solution_free", "rg_rational_reconstruct", "rg_big_gcd", "rg_set_crt_mode", "rg_set_stage_events",
     "rg_probe_mma_rate", "rg_big_mulmod", "quantize_f8", "scaled_gemm_f8",
-    "moe_layer_f8", "moe_layer_f8_ws_bytes",
+    "moe_layer_f8", "moe_layer_f8_ws_bytes", "linear_f8", "linear_f8_backward", "linear_f8_saved_bytes",
+    "linear_f8_ws_bytes",
 )
 
 
@@ -176,6 +177,13 @@ def library():
             lib.scaled_gemm_f8.restype = ci
             lib.moe_layer_f8.argtypes = [vp, ci, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, ci, ci, cu, vp, sz, vp]
             lib.moe_layer_f8.restype = ci
+            lib.linear_f8.argtypes = [vp, ci, i64, vp, ci, i64, vp, i64, i64, i64, vp, sz, cu, vp, sz, vp]
+            lib.linear_f8.restype = ci
+            lib.linear_f8_backward.argtypes = [vp, ci, i64, vp, sz, vp, vp, ci, i64, i64, i64, cu, vp, sz, vp]
+            lib.linear_f8_backward.restype = ci
+            for f in ("linear_f8_saved_bytes", "linear_f8_ws_bytes"):
+                getattr(lib, f).argtypes = [i64, i64, i64]
+                getattr(lib, f).restype = sz
             lib.moe_layer_f8_ws_bytes.argtypes = [i64, i64, i64, i64, ci]
             lib.moe_layer_f8_ws_bytes.restype = sz
             lib.rg_noalloc_scratch_bytes.argtypes = []

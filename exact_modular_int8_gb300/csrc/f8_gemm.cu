@@ -48,6 +48,7 @@ struct Params {
   int out_type;
   int vec_c;  // rows of C start on 16-byte boundaries
   int fault;
+  int keep_status;
   unsigned long long wait_ns;
 };
 
@@ -62,8 +63,8 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t adesc, uint64_t bde
 // The call's status, in place of a memset before the kernel: by the grid's first
 // thread as it starts, a time limit (which no wait can have used up yet) before
 // any CTA could write to it.
-__device__ __forceinline__ void clear_status(DevPlan* plan) {
-  if (blockIdx.x == 0) {
+__device__ __forceinline__ void clear_status(const Params& gp, DevPlan* plan) {
+  if (blockIdx.x == 0 && !gp.keep_status) {
     plan->status = 0;
     plan->timeout_where = 0;
   }
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   Ctl ctl{abort_flag, &plan->status, &plan->timeout_where, gp.wait_ns};
 
   if (threadIdx.x == 0) {
-    clear_status(plan);
+    clear_status(gp, plan);
     for (int s = 0; s < STAGES1; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&done[s]), 1);
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   Ctl ctl{abort_flag, &plan->status, &plan->timeout_where, gp.wait_ns};
 
   if (threadIdx.x == 0) {
-    clear_status(plan);
+    clear_status(gp, plan);
     for (int s = 0; s < STAGES2; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&done[s]), 1);
@@ -950,6 +951,7 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
   const int es = a.out_type == RG_TYPE_F32 ? 4 : 2;
   p.vec_c = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc * es % 16 == 0;
   p.fault = fault;
+  p.keep_status = a.keep_status;
   p.wait_ns = wait_ns;
   cudaLaunchAttribute attr[1];
   const long long tiles2 = ((a.M + 255) / 256) * ((a.N + BN2 - 1) / BN2);

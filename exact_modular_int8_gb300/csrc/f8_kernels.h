@@ -38,6 +38,7 @@ struct F8GemmArgs {
   long long M, N, K;
   int out_type;  // RG_TYPE_*
   bool b_kmajor, tile_b;
+  bool keep_status = false;  // an earlier product of the same call has cleared it
 };
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, int fault,
                            unsigned long long wait_ns);

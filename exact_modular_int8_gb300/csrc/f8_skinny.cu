@@ -37,6 +37,7 @@ struct SkinnyParams {
   int M, N, K, KB;
   int tiles;
   int out_type;
+  int keep_status;
   DevPlan* plan;
 };
 
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) f8_skinny_kernel(const __grid_consta
   using S = Shape<NT, MT>;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.plan->status = 0;  // no wait here that could fail
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !p.keep_status) p.plan->status = 0;  // no wait here that could fail
   const uint32_t ring = su32(smem) + 2 * S::kRed + warp * S::kRing * S::kPiece;
 
   // Copies of the next piece: 128-block pkb of tile pt.  Row r's 16-byte chunk c
@@ -247,7 +248,7 @@ cudaError_t launch(const SkinnyParams& p, bool tile_b, cudaStream_t st) {
 
 cudaError_t launch_f8_skinny(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st) {
   const SkinnyParams p{a.A, a.B, a.SA, a.SB, a.C, a.lda, a.ldb, a.ldc, a.sb_n, (int)a.M, (int)a.N, (int)a.K,
-                       (int)((a.K + 127) / 128), 0, a.out_type, plan};
+                       (int)((a.K + 127) / 128), 0, a.out_type, a.keep_status, plan};
   // with more than eight rows, two row tiles of B share a piece's rows of A
   if (a.M <= 8) return launch<1, 1>(p, a.tile_b, st);
   if (a.M <= 16) return launch<2, 2>(p, a.tile_b, st);

@@ -161,28 +161,59 @@ def scaled_gemm_f8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch
     return C
 
 
+@functools.lru_cache(maxsize=512)
+def _linear_bytes(M, N, K):
+    """(bytes kept between the passes, workspace bytes)."""
+    lib = library()
+    saved, need = int(lib.linear_f8_saved_bytes(M, N, K)), int(lib.linear_f8_ws_bytes(M, N, K))
+    if not saved or not need:
+        raise ResGemmError(RG_ERR_ARG, "linear_f8")
+    return saved, need
+
+
+def _rows_of(t: torch.Tensor):
+    """(matrix with contiguous rows, row stride), copied only where its rows are not."""
+    ld = _row_stride(t)
+    return (t, ld) if ld else (t.contiguous(), t.shape[1])
+
+
 def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True):
     """(Y, saved): Y = X W^T with X [M, K] quantised along K and the weights W [N, K] in 128 x 128 tiles, in X's
-    dtype.  `saved` is what linear_f8_backward needs (X quantised along M and the quantised weights)."""
-    if X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
-        raise ValueError("linear_f8: X [M, K] and W [N, K] expected")
-    _device_index("linear_f8", X, W)
-    qx, sx, qxt, sxt = quantize_f8(X, "both", sync=False)
-    qw, sw = quantize_f8(W, "tiles", sync=False)
-    Y = scaled_gemm_f8(qx, sx, qw, sw, out_dtype=X.dtype, transb=True, sync=sync)
-    return Y, (qxt, sxt, qw, sw)
+    dtype (both float32, float16 or bfloat16).  `saved` is what linear_f8_backward needs: one buffer with X
+    quantised along M and the quantised weights.  One library call; the same as quantize_f8(X, "both"),
+    quantize_f8(W, "tiles") and scaled_gemm_f8."""
+    tx, tw = _TYPES.get(X.dtype), _TYPES.get(W.dtype)
+    if tx is None or tw is None or X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
+        raise ValueError("linear_f8: X [M, K] and W [N, K] float32, float16 or bfloat16 expected")
+    idx = _device_index("linear_f8", X, W)
+    (M, K), N = X.shape, W.shape[0]
+    nsaved, need = _linear_bytes(M, N, K)
+    X, ldx = _rows_of(X)
+    W, ldw = _rows_of(W)
+    dev = X.device
+    Y = torch.empty((M, N), dtype=X.dtype, device=dev)
+    kept = torch.empty(nsaved, dtype=torch.uint8, device=dev)
+    w = _scratch(need, idx)
+    _launch(idx, "linear_f8", library().linear_f8, X.data_ptr(), tx, ldx, W.data_ptr(), tw, ldw, Y.data_ptr(), M, N, K,
+            kept.data_ptr(), nsaved, RG_FLAG_SYNC if sync else 0, w.data_ptr(), w.numel())
+    return Y, (kept, M, N, K)
 
 
 def linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: torch.dtype = torch.float32):
     """(dX, dW) of linear_f8 for the output's gradient dY [M, N]: dX = dY W with dY quantised along N, in dY's
     dtype, and dW = dY^T X with both quantised along M, in dw_dtype."""
-    qxt, sxt, qw, sw = saved
-    if dY.dim() != 2 or dY.shape != (qxt.shape[1], qw.shape[0]):
-        raise ValueError("linear_f8_backward: dY must have the output's shape")
-    _device_index("linear_f8_backward", dY, qxt)
-    qd, sd, qdt, sdt = quantize_f8(dY, "both", sync=False)
-    dX = scaled_gemm_f8(qd, sd, qw, sw, out_dtype=dY.dtype, sync=False)
-    dW = scaled_gemm_f8(qdt, sdt, qxt, sxt, out_dtype=dw_dtype, transb=True, sync=sync)
+    kept, M, N, K = saved
+    t, tw = _TYPES.get(dY.dtype), _TYPES.get(dw_dtype)
+    if t is None or tw is None or dY.shape != (M, N):
+        raise ValueError("linear_f8_backward: dY with the output's shape, float32, float16 or bfloat16, expected")
+    idx = _device_index("linear_f8_backward", dY, kept)
+    nsaved, need = _linear_bytes(M, N, K)
+    dY, lddy = _rows_of(dY)
+    dX = torch.empty((M, K), dtype=dY.dtype, device=dY.device)
+    dW = torch.empty((N, K), dtype=dw_dtype, device=dY.device)
+    w = _scratch(need, idx)
+    _launch(idx, "linear_f8_backward", library().linear_f8_backward, dY.data_ptr(), t, lddy, kept.data_ptr(), nsaved,
+            dX.data_ptr(), dW.data_ptr(), tw, M, N, K, RG_FLAG_SYNC if sync else 0, w.data_ptr(), w.numel())
     return dX, dW
 
 

@@ -473,6 +473,29 @@ int scaled_gemm_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t
                    size_t ws_bytes, void* stream);
 
 /*
+ * A linear layer's training step in this format.
+ *   forward   Y [M][N] (x_type) = X W^T, X [M][ldx] quantised along K, W [N][ldw]
+ *             (w_type) in 128 x 128 tiles
+ *   backward  dX [M][K] (dy_type) = dY W, dY [M][lddy] quantised along N, and
+ *             dW [N][K] (dw_type) = dY^T X, both quantised along M
+ * The forward call leaves X^T and W, quantised, in `saved`
+ * (linear_f8_saved_bytes() bytes, 256-byte aligned), which the backward call
+ * of the same sizes reads.  Each is what quantize_f8 and scaled_gemm_f8 give
+ * one after the other, to the bit.  ws: linear_f8_ws_bytes() bytes, 256-byte
+ * aligned; both functions return 0 for sizes the calls refuse.
+ * Errors: RG_ERR_ARG, RG_ERR_WORKSPACE (saved or ws too small), RG_ERR_CUDA,
+ * RG_ERR_TIMEOUT.
+ */
+size_t linear_f8_saved_bytes(int64_t M, int64_t N, int64_t K);
+size_t linear_f8_ws_bytes(int64_t M, int64_t N, int64_t K);
+int linear_f8(const void* X, int x_type, int64_t ldx, const void* W, int w_type, int64_t ldw, void* Y, int64_t M,
+              int64_t N, int64_t K, void* saved, size_t saved_bytes, unsigned flags, void* ws, size_t ws_bytes,
+              void* stream);
+int linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* saved, size_t saved_bytes, void* dX,
+                       void* dW, int dw_type, int64_t M, int64_t N, int64_t K, unsigned flags, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
  * A whole mixture-of-experts layer for a few tokens (decoding):
  *   p = softmax(X WR^T) over the E experts; each token takes the top_k
  *   largest (equal ones: the lower index), with weights p or, with renorm,

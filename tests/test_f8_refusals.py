@@ -51,6 +51,29 @@ def test_product_arguments(rg, mem):
     assert call(wsb=4095) == rg.RG_ERR_WORKSPACE
 
 
+def test_linear_arguments(rg, mem):
+    p, lib = mem[0], rg.library()
+    saved, need = lib.linear_f8_saved_bytes(4, 8, 16), lib.linear_f8_ws_bytes(4, 8, 16)
+    assert saved > 0 and need > 4096
+    for f in (lib.linear_f8_saved_bytes, lib.linear_f8_ws_bytes):
+        assert f(-1, 8, 16) == 0 and f(2**31, 8, 16) == 0 and f(2**30, 2**30, 16) == 0
+
+    def forward(X=p, xt=2, ldx=16, W=p, wt=0, ldw=16, Y=p, M=4, N=8, K=16, sv=p, svb=saved, ws=p, wsb=need):
+        return lib.linear_f8(X, xt, ldx, W, wt, ldw, Y, M, N, K, sv, svb, 0, ws, wsb, None)
+
+    def backward(dY=p, t=2, ld=8, sv=p, svb=saved, dX=p, dW=p, wt=0, M=4, N=8, K=16, ws=p, wsb=need):
+        return lib.linear_f8_backward(dY, t, ld, sv, svb, dX, dW, wt, M, N, K, 0, ws, wsb, None)
+
+    for bad in (dict(X=None), dict(W=None), dict(Y=None), dict(xt=3), dict(wt=-1), dict(ldx=15), dict(ldw=15),
+                dict(M=-1), dict(N=2**31), dict(sv=None), dict(sv=p + 16), dict(ws=None), dict(ws=p + 16)):
+        assert forward(**bad) == rg.RG_ERR_ARG, bad
+    for bad in (dict(dY=None), dict(dX=None), dict(dW=None), dict(t=3), dict(wt=3), dict(ld=7), dict(K=-1),
+                dict(sv=None), dict(sv=p + 128), dict(ws=None)):
+        assert backward(**bad) == rg.RG_ERR_ARG, bad
+    for f in (forward, backward):
+        assert f(wsb=need - 1) == rg.RG_ERR_WORKSPACE and f(svb=saved - 1) == rg.RG_ERR_WORKSPACE
+
+
 def test_expert_layer_arguments(rg, mem):
     p, lib = mem[0], rg.library()
 

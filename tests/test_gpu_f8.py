@@ -356,6 +356,45 @@ def test_linear_gradients(rg, m, n, k, dtype):  # noqa: F811
     assert abs((dW.double().cpu().numpy() * v).sum() - slope) <= tol
 
 
+def test_linear_is_its_parts(rg):  # noqa: F811
+    """The layer's calls give what quantisation and products give one after the other, strided inputs included."""
+    x = normal((300, 270), 1, 1.0, torch.bfloat16).cuda()[:, 5:261]
+    w = normal((256, 200), 2, 0.1).cuda().t()  # [200, 256], columns contiguous
+    dy = normal((300, 400), 3, 0.01, torch.bfloat16).cuda()[:, ::2]
+    Y, saved = rg.linear_f8(x, w)
+    dX, dW = rg.linear_f8_backward(dy, saved, dw_dtype=torch.bfloat16)
+    qx, sx, qxt, sxt = rg.quantize_f8(x, "both")
+    qw, sw = rg.quantize_f8(w, "tiles")
+    qd, sd, qdt, sdt = rg.quantize_f8(dy, "both")
+    assert torch.equal(Y, rg.scaled_gemm_f8(qx, sx, qw, sw, transb=True))
+    assert torch.equal(dX, rg.scaled_gemm_f8(qd, sd, qw, sw))
+    assert torch.equal(dW, rg.scaled_gemm_f8(qdt, sdt, qxt, sxt, transb=True))
+
+
+def test_linear_empty(rg):  # noqa: F811
+    x, w = torch.zeros((0, 40), device="cuda"), torch.ones((30, 40), device="cuda")
+    Y, saved = rg.linear_f8(x, w)
+    dX, dW = rg.linear_f8_backward(Y, saved)
+    assert Y.shape == (0, 30) and dX.shape == (0, 40) and dW.shape == (30, 40) and (dW == 0).all()
+
+
+def test_linear_backward_reports_its_first_product(rg):  # noqa: F811
+    """A time-out in the input gradient's product is not hidden by the weight gradient's that follows it."""
+    lib = rg.library()
+    x, w = normal((300, 256), 1).cuda(), normal((256, 256), 2).cuda()
+    Y, saved = rg.linear_f8(x, w)
+    old = lib.rg_set_wait_limit_ns(50_000_000)
+    try:
+        lib.rg_inject_fault(1)
+        with pytest.raises(rg.ResGemmError) as err:
+            rg.linear_f8_backward(Y, saved)
+        assert err.value.code == rg.RG_ERR_TIMEOUT
+    finally:
+        lib.rg_inject_fault(0)
+        lib.rg_set_wait_limit_ns(old)
+    rg.linear_f8_backward(Y, saved)
+
+
 # ---------------------------------------------------------------------------
 # mixture of experts
 # ---------------------------------------------------------------------------
