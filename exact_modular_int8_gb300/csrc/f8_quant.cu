@@ -20,6 +20,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <cstring>
 
 #include "f8_kernels.h"
 
@@ -29,58 +30,135 @@ namespace {
 constexpr uint32_t kTinyBits = 0x21800000u;  // 2^-60
 constexpr int kTile = 128;
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// Magnitudes are compared as bit patterns: the order of the non-negative
-// floats, with NaN above inf, so that a NaN is never lost.
-__device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
-struct BlockScale {
-  float d, r;  // a / 512 and its reciprocal
-  float s;     // a / 448
-};
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
-  const float a = __uint_as_float(max(amax_bits, kTinyBits));
-  BlockScale b;
-  b.d = a * 0.001953125f;
-  b.r = __frcp_rn(b.d);
-  b.s = __fdiv_rn(a, 448.0f);
-  return b;
-}
-__device__ __forceinline__ float scaled(float x, float d, float r) {
-  const float n = x * 0.875f;
-  const float q0 = n * r;
-  return __fmaf_rn(__fmaf_rn(-q0, d, n), r, q0);
-}
-// Two values to two E4M3 bytes, the first in the low byte.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-
-// Eight entries of a row from column c (limit: entries left in the row);
-// missing ones read as 0.
+// Eight entries of a row as loaded, and largest magnitudes of them ("mags"): of
+// 16-bit entries two to a word, compared by the packed maximum that keeps a
+// NaN; of fp32 entries one to a word, compared as bit patterns, where NaN lies
+// above inf.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, long long left, bool vec, float (&v)[8]) {
+struct Entries {
+  static constexpr int kWords = 4;
+  static constexpr int kPer = 2;  // entries per word
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  }
+  __device__ __forceinline__ void set(int i, T v) {
+    uint16_t h;
+    memcpy(&h, &v, 2);
+    w[i >> 1] |= (uint32_t)h << (16 * (i & 1));
+  }
+  static __device__ __forceinline__ uint32_t mag(uint32_t a) { return a & 0x7FFF7FFFu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b);
+  static __device__ __forceinline__ float lo(uint32_t a);
+  static __device__ __forceinline__ float hi(uint32_t a);
+  __device__ __forceinline__ float at(int i) const { return i & 1 ? hi(w[i >> 1]) : lo(w[i >> 1]); }
+  // the larger of a mag's two entries, as an fp32 bit pattern
+  static __device__ __forceinline__ uint32_t top(uint32_t m) {
+    return max(__float_as_uint(lo(m)), __float_as_uint(hi(m)));
+  }
+};
+template <>
+__device__ __forceinline__ uint32_t Entries<__nv_bfloat16>::larger(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <>
+__device__ __forceinline__ float Entries<__nv_bfloat16>::lo(uint32_t a) { return __uint_as_float(a << 16); }
+template <>
+__device__ __forceinline__ float Entries<__nv_bfloat16>::hi(uint32_t a) { return __uint_as_float(a & 0xFFFF0000u); }
+template <>
+__device__ __forceinline__ uint32_t Entries<__half>::larger(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <>
+__device__ __forceinline__ float Entries<__half>::lo(uint32_t a) {
+  return __half2float(__ushort_as_half((unsigned short)a));
+}
+template <>
+__device__ __forceinline__ float Entries<__half>::hi(uint32_t a) {
+  return __half2float(__ushort_as_half((unsigned short)(a >> 16)));
+}
+template <>
+struct Entries<float> {
+  static constexpr int kWords = 8;
+  static constexpr int kPer = 1;
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p)), v = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+  }
+  __device__ __forceinline__ void set(int i, float v) { w[i] = __float_as_uint(v); }
+  static __device__ __forceinline__ uint32_t mag(uint32_t a) { return a & 0x7FFFFFFFu; }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+  __device__ __forceinline__ float at(int i) const { return __uint_as_float(w[i]); }
+  static __device__ __forceinline__ uint32_t top(uint32_t m) { return m; }
+};
+
+// Eight entries from p, of which `left` exist; missing ones read as 0.
+template <typename T>
+__device__ __forceinline__ void load8(Entries<T>& e, const T* p, long long left, bool vec) {
   if (vec && left >= 8) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const unsigned short h = (unsigned short)(w[i >> 1] >> (16 * (i & 1)));
-        v[i] = to_f32(*reinterpret_cast<const T*>(&h));
-      }
-    } else {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
+    e.load(p);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f32(p[i]) : 0.0f;
+    for (int i = 0; i < Entries<T>::kWords; ++i) e.w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) e.set(i, p[i]);
   }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t mag8(const Entries<T>& e) {
+  uint32_t m = Entries<T>::mag(e.w[0]);
+#pragma unroll
+  for (int i = 1; i < Entries<T>::kWords; ++i) m = Entries<T>::larger(m, Entries<T>::mag(e.w[i]));
+  return m;
+}
+
+struct BlockScale {
+  float nd, r;  // -a / 512 and the reciprocal of a / 512
+};
+__device__ __forceinline__ float amax_of(uint32_t bits) { return __uint_as_float(max(bits, kTinyBits)); }
+__device__ __forceinline__ BlockScale block_scale(float a) {
+  const float d = a * 0.001953125f;
+  return BlockScale{-d, __frcp_rn(d)};
+}
+__device__ __forceinline__ float scale_of(float a) { return __fdiv_rn(a, 448.0f); }
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ uint64_t pmul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pfma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// Two entries to two E4M3 bytes, the first in the low byte.
+__device__ __forceinline__ uint32_t quantise2(float x0, float x1, uint64_t nd, uint64_t r) {
+  const uint64_t n = pmul(pair(x0, x1), pair(0.875f, 0.875f));
+  const uint64_t q0 = pmul(n, r);
+  const uint64_t q = pfma(pfma(q0, nd, n), r, q0);
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(q));
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+template <typename F>
+__device__ __forceinline__ uint2 quantise8(F&& x, const BlockScale& b) {
+  const uint64_t nd = pair(b.nd, b.nd), r = pair(b.r, b.r);
+  return make_uint2(quantise2(x(0), x(1), nd, r) | (quantise2(x(2), x(3), nd, r) << 16),
+                    quantise2(x(4), x(5), nd, r) | (quantise2(x(6), x(7), nd, r) << 16));
 }
 
 __device__ __forceinline__ void store8(uint8_t* p, long long left, bool vec, uint2 q) {
@@ -94,116 +172,129 @@ __device__ __forceinline__ void store8(uint8_t* p, long long left, bool vec, uin
   }
 }
 
-__device__ __forceinline__ uint2 quantise8(const float (&v)[8], const BlockScale& b) {
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = scaled(v[i], b.d, b.r);
-  return make_uint2(e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16), e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16));
-}
-
-// One block of 128 per half-warp: 16 lanes of eight entries.
+// Blocks of 128 along rows, one per half-warp (16 lanes of eight entries).
 template <typename T>
 __global__ void __launch_bounds__(256) quantise_rows_kernel(QuantArgs a) {
+  using E = Entries<T>;
   const long long kb = (a.K + kTile - 1) / kTile, total = a.M * kb;
-  const int lane16 = threadIdx.x & 15;
+  const int l16 = threadIdx.x & 15;
   const T* X = static_cast<const T*>(a.X);
   const long long b = ((long long)blockIdx.x * 256 + threadIdx.x) >> 4;
   const bool live = b < total;
-  const long long row = live ? b / kb : 0, j = live ? b - row * kb : 0;
-  const long long c = j * kTile + lane16 * 8, left = live ? a.K - c : 0;
-  float v[8];
-  load8(X + row * a.ldx + c, left, a.vec_x, v);
-  uint32_t m = 0;
+  const long long row = live ? b / kb : 0, j = live ? b - row * kb : 0, c = j * kTile + l16 * 8;
+  E e;
+  load8(e, X + row * a.ldx + c, live ? a.K - c : 0, a.vec_x);
+  uint32_t m = mag8(e);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, mag(v[i]));
-#pragma unroll
-  for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  for (int o = 8; o; o >>= 1) m = E::larger(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   if (!live) return;
-  const BlockScale bs = block_scale(m);
-  store8(a.Q + row * a.ldq + c, left, a.vec_q, quantise8(v, bs));
-  if (lane16 == 0) a.S[row * kb + j] = bs.s;
+  const float top = amax_of(E::top(m));
+  store8(a.Q + row * a.ldq + c, a.K - c, a.vec_q, quantise8([&](int i) { return e.at(i); }, block_scale(top)));
+  if (l16 == 0) a.S[row * kb + j] = scale_of(top);
 }
 
 // One 128 x 128 tile per block of 256 threads; a thread holds eight rows of
 // eight columns.  ROWS / COLS: scales along rows and along columns (with both,
 // one read of X gives both results); neither: one scale for the tile.
 template <typename T, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(256) quantise_tile_kernel(QuantArgs a) {
-  __shared__ uint32_t col_max[16][kTile];           // per 8-row group
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) quantise_tile_kernel(QuantArgs a) {
+  using E = Entries<T>;
+  constexpr int kWordsPerRow = kTile / E::kPer;
+  __shared__ uint32_t col_mag[COLS ? 16 : 1][kWordsPerRow];  // per 8-row group
+  __shared__ __align__(16) float2 col_scale[COLS ? kTile : 1];
   __shared__ __align__(16) uint8_t t_tile[COLS ? kTile * kTile : 16];  // transposed bytes, 16-byte chunks swizzled
-  __shared__ uint32_t warp_max[8];
+  __shared__ uint32_t warp_mag[8];
   const long long kb = (a.K + kTile - 1) / kTile, mb = (a.M + kTile - 1) / kTile;
   const long long ti = blockIdx.x / kb, tj = blockIdx.x - ti * kb;
   const T* X = static_cast<const T*>(a.X);
-  const int grp = threadIdx.x >> 4;   // rows 8 grp .. 8 grp + 7 of the tile
-  const int l16 = threadIdx.x & 15;   // columns 8 l16 ..
+  const int grp = threadIdx.x >> 4;  // rows 8 grp .. 8 grp + 7 of the tile
+  const int l16 = threadIdx.x & 15;  // columns 8 l16 ..
   const long long r0 = ti * kTile + grp * 8, c0 = tj * kTile + l16 * 8, left = a.K - c0;
-  float v[8][8];
+  E e[8];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) load8(X + (r0 + r) * a.ldx + c0, r0 + r < a.M ? left : 0, a.vec_x, v[r]);
+  for (int r = 0; r < 8; ++r) load8(e[r], X + (r0 + r) * a.ldx + c0, r0 + r < a.M ? left : 0, a.vec_x);
 
   if constexpr (!ROWS && !COLS) {
-    uint32_t m = 0;
+    uint32_t m = mag8(e[0]);
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, mag(v[r][i]));
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+    for (int r = 1; r < 8; ++r) m = E::larger(m, mag8(e[r]));
+    m = __reduce_max_sync(0xFFFFFFFFu, E::top(m));
+    if ((threadIdx.x & 31) == 0) warp_mag[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = max(m, warp_max[w]);
-    const BlockScale bs = block_scale(m);
+    for (int w = 0; w < 8; ++w) m = max(m, warp_mag[w]);
+    const float top = amax_of(m);
+    const BlockScale bs = block_scale(top);
 #pragma unroll
     for (int r = 0; r < 8; ++r)
-      if (r0 + r < a.M) store8(a.Q + (r0 + r) * a.ldq + c0, left, a.vec_q, quantise8(v[r], bs));
-    if (threadIdx.x == 0) a.S[ti * kb + tj] = bs.s;
+      if (r0 + r < a.M)
+        store8(a.Q + (r0 + r) * a.ldq + c0, left, a.vec_q, quantise8([&](int i) { return e[r].at(i); }, bs));
+    if (threadIdx.x == 0) a.S[ti * kb + tj] = scale_of(top);
     return;
-  }
-  if constexpr (ROWS) {
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, mag(v[r][i]));
-#pragma unroll
-      for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const BlockScale bs = block_scale(m);
-      if (r0 + r < a.M) {
-        store8(a.Q + (r0 + r) * a.ldq + c0, left, a.vec_q, quantise8(v[r], bs));
-        if (l16 == 0) a.S[(r0 + r) * kb + tj] = bs.s;
-      }
-    }
   }
   if constexpr (COLS) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t m = 0;
+    for (int w = 0; w < E::kWords; ++w) {
+      uint32_t m = E::mag(e[0].w[w]);
 #pragma unroll
-      for (int r = 0; r < 8; ++r) m = max(m, mag(v[r][i]));
-      col_max[grp][l16 * 8 + i] = m;
+      for (int r = 1; r < 8; ++r) m = E::larger(m, E::mag(e[r].w[w]));
+      col_mag[grp][l16 * E::kWords + w] = m;
     }
+  }
+  if constexpr (ROWS) {
+    // The eight rows' maxima over 16 lanes: each step halves the rows a lane
+    // holds, so that lane l ends up with row l / 2's, and makes its scale.
+    uint32_t m[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) m[r] = mag8(e[r]);
+#pragma unroll
+    for (int n = 4, bit = 8; n; n >>= 1, bit >>= 1) {
+      const bool up = l16 & bit;
+#pragma unroll
+      for (int r = 0; r < n; ++r) {
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, up ? m[r] : m[r + n], bit);
+        m[r] = E::larger(up ? m[r + n] : m[r], other);
+      }
+    }
+    const uint32_t mine = E::larger(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], 1));
+    const float top = amax_of(E::top(mine));
+    const BlockScale bs = block_scale(top);
+    const long long my_row = r0 + (l16 >> 1);
+    if (!(l16 & 1) && my_row < a.M) a.S[my_row * kb + tj] = scale_of(top);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int src = (threadIdx.x & 16) + 2 * r;
+      const BlockScale rs{__shfl_sync(0xFFFFFFFFu, bs.nd, src), __shfl_sync(0xFFFFFFFFu, bs.r, src)};
+      if (r0 + r < a.M)
+        store8(a.Q + (r0 + r) * a.ldq + c0, left, a.vec_q, quantise8([&](int i) { return e[r].at(i); }, rs));
+    }
+  }
+  if constexpr (COLS) {
     __syncthreads();
     if (threadIdx.x < kTile) {
-      uint32_t m = 0;
+      constexpr int kPer = E::kPer;
+      const int w = threadIdx.x / kPer;
+      uint32_t m = col_mag[0][w];
 #pragma unroll
-      for (int g = 0; g < 16; ++g) m = max(m, col_max[g][threadIdx.x]);
-      col_max[0][threadIdx.x] = m;
+      for (int g = 1; g < 16; ++g) m = E::larger(m, col_mag[g][w]);
+      // this column's of the word's entries
+      if constexpr (kPer == 2) m = threadIdx.x & 1 ? m & 0xFFFF0000u : m << 16;
+      const float top = amax_of(E::top(m));
+      const BlockScale bs = block_scale(top);
+      col_scale[threadIdx.x] = make_float2(bs.nd, bs.r);
+      const long long col = tj * kTile + threadIdx.x;
+      if (col < a.K) a.ST[col * mb + ti] = scale_of(top);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = l16 * 8 + i;
-      const BlockScale bs = block_scale(col_max[0][c]);
-      float w[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) w[r] = v[r][i];
+      const float2 cs = col_scale[c];
       // column c's 128 bytes are a row of t_tile; this thread's 8 bytes are half of its 16-byte chunk grp / 2
       const int chunk = (grp >> 1) ^ (l16 & 7);
-      *reinterpret_cast<uint2*>(&t_tile[c * kTile + chunk * 16 + (grp & 1) * 8]) = quantise8(w, bs);
+      *reinterpret_cast<uint2*>(&t_tile[c * kTile + chunk * 16 + (grp & 1) * 8]) =
+          quantise8([&](int r) { return e[r].at(i); }, BlockScale{cs.x, cs.y});
     }
-    if (threadIdx.x < kTile && tj * kTile + threadIdx.x < a.K)
-      a.ST[(tj * kTile + threadIdx.x) * mb + ti] = block_scale(col_max[0][threadIdx.x]).s;
     __syncthreads();
     const int j = threadIdx.x & 7;  // 16-byte chunk: rows 16 j of the tile
 #pragma unroll
@@ -228,11 +319,20 @@ __global__ void __launch_bounds__(256) quantise_tile_kernel(QuantArgs a) {
 template <typename T>
 cudaError_t launch_t(const QuantArgs& a, int form, cudaStream_t st) {
   const long long kb = (a.K + kTile - 1) / kTile, mb = (a.M + kTile - 1) / kTile;
-  const long long blocks = form == RG_F8_ROWS ? (a.M * kb + 15) / 16 : mb * kb;
+  // Along rows: up to 2^15 blocks of 128, or fewer rows than half a tile, go a
+  // block to a half-warp, which spreads few blocks over more SMs (512 x 1024:
+  // 2.1 us, in tiles 3.0); more go in tiles, where a thread has eight loads on
+  // its way (8192 x 4096 bf16: 26 us a block to a half-warp).
+  const bool tiles = form != RG_F8_ROWS || (a.M >= 64 && a.M * kb > (1LL << 15));
+  const long long blocks = tiles ? mb * kb : (a.M * kb + 15) / 16;
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   const dim3 g((unsigned)blocks), b(256);
+  if (!tiles) {
+    quantise_rows_kernel<T><<<g, b, 0, st>>>(a);
+    return cudaGetLastError();
+  }
   switch (form) {
-    case RG_F8_ROWS: quantise_rows_kernel<T><<<g, b, 0, st>>>(a); break;
+    case RG_F8_ROWS: quantise_tile_kernel<T, true, false><<<g, b, 0, st>>>(a); break;
     case RG_F8_COLUMNS: quantise_tile_kernel<T, false, true><<<g, b, 0, st>>>(a); break;
     case RG_F8_BOTH: quantise_tile_kernel<T, true, true><<<g, b, 0, st>>>(a); break;
     default: quantise_tile_kernel<T, false, false><<<g, b, 0, st>>>(a); break;

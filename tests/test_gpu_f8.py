@@ -117,6 +117,12 @@ def test_quantise(rg, form, dtype, m, k):  # noqa: F811
     check_quantised(rg.quantize_f8(x.cuda(), form), x.double().numpy(), form)
 
 
+@pytest.mark.parametrize("m,k,dtype", [(601, 7100, torch.bfloat16), (4200, 1001, torch.float16)])
+def test_quantise_many_row_blocks(rg, m, k, dtype):  # noqa: F811
+    x = normal((m, k), m, 3.0, dtype)
+    check_quantised(rg.quantize_f8(x.cuda(), "rows"), x.double().numpy(), "rows")
+
+
 @pytest.mark.parametrize("form", ["rows", "columns", "both", "tiles"])
 def test_quantise_strides_and_alignment(rg, form):  # noqa: F811
     base = normal((300, 701), 5, 1.0, torch.bfloat16).cuda()
