@@ -328,7 +328,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   Ctl ctl{abort_flag, &plan->status, &plan->timeout_where, gp.wait_ns};
 
   if (threadIdx.x == 0) {
-    clear_status(gp, plan);
     for (int s = 0; s < STAGES1; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&done[s]), 1);
@@ -353,7 +352,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // the set-up above overlaps the predecessor's tail
   wait_for_predecessor();
+  allow_dependents();
+  if (threadIdx.x == 0) clear_status(gp, plan);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -541,7 +543,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   }
-  allow_dependents();
   if (S > 1) cluster_sync();  // no CTA leaves while another reads its slice
 }
 
@@ -703,7 +704,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   Ctl ctl{abort_flag, &plan->status, &plan->timeout_where, gp.wait_ns};
 
   if (threadIdx.x == 0) {
-    clear_status(gp, plan);
     for (int s = 0; s < STAGES2; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&done[s]), 1);
@@ -729,7 +729,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   cluster_sync();  // barriers of both CTAs are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // the set-up above overlaps the predecessor's tail
   wait_for_predecessor();
+  allow_dependents();
+  if (threadIdx.x == 0) clear_status(gp, plan);
   const int total = gp.mt * gp.nt;
 
   if (warp < 4) {
@@ -889,7 +892,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  allow_dependents();
   cluster_sync();  // neither CTA frees the pair's memory while the other still uses it
   if (warp == 1) {
     tc_fence_after();
@@ -925,8 +927,10 @@ cudaLaunchConfig_t cluster_config(dim3 grid, int threads, int smem, cudaStream_t
   attr[0].val.clusterDim.x = (unsigned)cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
@@ -962,7 +966,7 @@ cudaError_t f8_device(int dev, F8Device& out) {
         if (e != cudaSuccess) return e;
       }
     // not every SM can be paired within its GPC
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(sms & ~1)), NUM_THREADS, SMEM2_BYTES, nullptr, 2, attr);
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kPairKernels[1][1], &cfg) != cudaSuccess || n < 1) {
@@ -1012,7 +1016,7 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
   p.fault = fault;
   p.keep_status = a.keep_status;
   p.wait_ns = wait_ns;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   const long long tiles2 = ((a.M + 255) / 256) * ((a.N + BN2 - 1) / BN2);
   // Tiles of 128 x 128 while one wave of CTAs holds them all, split along K where
   // that leaves SMs idle; beyond that the pair kernel's tiles.  (4096 columns, K =

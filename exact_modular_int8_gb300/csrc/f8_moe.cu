@@ -205,6 +205,8 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kRouterThreads) moe_
   const T* X = static_cast<const T*>(p.X);
   const T* WR = static_cast<const T*>(p.WR);
   const int rank = (int)(blockIdx.x & 7u), t0 = (int)(blockIdx.x >> 3) * 8;
+  wait_for_predecessor();
+  allow_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     p.plan->status = 0;
     p.plan->timeout_where = 0;
@@ -771,6 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
   extern __shared__ __align__(128) uint8_t raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int cta = blockIdx.x, ctas = gridDim.x;
+  wait_for_predecessor();
   form_routing(p, sm.r);
   {
     Phase<true> up(p, sm, raw);
@@ -883,20 +886,21 @@ cudaError_t launch_moe_f8(const MoeArgs& a, DevPlan* plan, void* scratch, cudaSt
     sms = known[dev];
   }
   const unsigned blocks = 8u * (unsigned)((p.T + 7) / 8);
-  if (p.type == RG_TYPE_F16) moe_router_kernel<__half><<<blocks, kRouterThreads, 0, st>>>(p);
-  else moe_router_kernel<__nv_bfloat16><<<blocks, kRouterThreads, 0, st>>>(p);
-  e = cudaGetLastError();
+  e = launch_dependent(p.type == RG_TYPE_F16 ? moe_router_kernel<__half> : moe_router_kernel<__nv_bfloat16>,
+                       dim3(blocks), dim3(kRouterThreads), 0, st, p);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, moe_experts_kernel, p);
 }
 

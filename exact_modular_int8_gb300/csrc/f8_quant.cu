@@ -176,6 +176,8 @@ __device__ __forceinline__ void store8(uint8_t* p, long long left, bool vec, uin
 template <typename T>
 __global__ void __launch_bounds__(256) quantise_rows_kernel(QuantArgs a) {
   using E = Entries<T>;
+  wait_for_predecessor();
+  allow_dependents();
   const long long kb = (a.K + kTile - 1) / kTile, total = a.M * kb;
   const int l16 = threadIdx.x & 15;
   const T* X = static_cast<const T*>(a.X);
@@ -204,6 +206,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) quantise_tile_ker
   __shared__ __align__(16) float2 col_scale[COLS ? kTile : 1];
   __shared__ __align__(16) uint8_t t_tile[COLS ? kTile * kTile : 16];  // transposed bytes, 16-byte chunks swizzled
   __shared__ uint32_t warp_mag[8];
+  wait_for_predecessor();
+  allow_dependents();
   const long long kb = (a.K + kTile - 1) / kTile, mb = (a.M + kTile - 1) / kTile;
   const long long ti = blockIdx.x / kb, tj = blockIdx.x - ti * kb;
   const T* X = static_cast<const T*>(a.X);
@@ -328,16 +332,14 @@ cudaError_t launch_t(const QuantArgs& a, int form, cudaStream_t st) {
   if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
   const dim3 g((unsigned)blocks), b(256);
   if (!tiles) {
-    quantise_rows_kernel<T><<<g, b, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(quantise_rows_kernel<T>, g, b, 0, st, a);
   }
   switch (form) {
-    case RG_F8_ROWS: quantise_tile_kernel<T, true, false><<<g, b, 0, st>>>(a); break;
-    case RG_F8_COLUMNS: quantise_tile_kernel<T, false, true><<<g, b, 0, st>>>(a); break;
-    case RG_F8_BOTH: quantise_tile_kernel<T, true, true><<<g, b, 0, st>>>(a); break;
-    default: quantise_tile_kernel<T, false, false><<<g, b, 0, st>>>(a); break;
+    case RG_F8_ROWS: return launch_dependent(quantise_tile_kernel<T, true, false>, g, b, 0, st, a);
+    case RG_F8_COLUMNS: return launch_dependent(quantise_tile_kernel<T, false, true>, g, b, 0, st, a);
+    case RG_F8_BOTH: return launch_dependent(quantise_tile_kernel<T, true, true>, g, b, 0, st, a);
+    default: return launch_dependent(quantise_tile_kernel<T, false, false>, g, b, 0, st, a);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

@@ -91,6 +91,8 @@ __global__ void __launch_bounds__(kThreads) f8_skinny_kernel(const __grid_consta
   using S = Shape<NT, MT>;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  wait_for_predecessor();
+  allow_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0 && !p.keep_status) p.plan->status = 0;  // no wait here that could fail
   const uint32_t ring = su32(smem) + 2 * S::kRed + warp * S::kRing * S::kPiece;
 
@@ -235,8 +237,8 @@ cudaError_t launch(SkinnyParams p, cudaStream_t st) {
     blocks[dev].store(resident, std::memory_order_relaxed);
   }
   p.tiles = (p.N + 16 * MT - 1) / (16 * MT);
-  f8_skinny_kernel<NT, MT, TILE_B><<<std::min(p.tiles, resident), kThreads, S::kSmem, st>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(f8_skinny_kernel<NT, MT, TILE_B>, dim3((unsigned)std::min(p.tiles, resident)),
+                          dim3(kThreads), S::kSmem, st, p);
 }
 
 template <int NT, int MT>
