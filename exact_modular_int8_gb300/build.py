@@ -3,6 +3,8 @@
 Every translation unit under csrc/ (.cu, and host-only .cpp) is compiled in parallel and linked into
 ``_build/libresgemm.so`` next to this file.  A unit is rebuilt when it, a
 header it includes, or this script is newer than its object file.
+csrc/python/f8_call.c, the binding's native call path, becomes the extension
+module ``_build/f8_call.so``.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +20,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libresgemm.so")
+CALL_SRC = os.path.join(CSRC, "python", "f8_call.c")
+CALL_LIB = os.path.join(BUILD, "f8_call.so")
+CC = os.environ.get("CC", "gcc")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -33,6 +39,18 @@ def _stale(target, deps):
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_call():
+    """The Python extension module of csrc/python (no CUDA in it)."""
+    if not _stale(CALL_LIB, [CALL_SRC, os.path.join(ROOT, "include", "resgemm.h"), os.path.abspath(__file__)]):
+        return
+    tmp = CALL_LIB + f".tmp{os.getpid()}"
+    cmd = [CC, "-O2", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_paths()["include"], CALL_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CC} failed for {CALL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL_LIB)
 
 
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -53,7 +71,9 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         return obj, r.stdout + r.stderr
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(sources), os.cpu_count() or 1))) as ex:
+        call = ex.submit(_build_call)
         results = list(ex.map(compile_one, sources))
+        call.result()
     objs = [o for o, _ in results]
     if verbose or ptxas_info:
         for _, log in results:

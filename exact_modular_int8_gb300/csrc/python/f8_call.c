@@ -1,0 +1,234 @@
+/*
+ * f8_call.c -- the Python binding's short way into quantize_f8 and
+ * scaled_gemm_f8 (include/resgemm.h).
+ *
+ * A small call's time is its time on the host, and most of that was spent on
+ * marshalling: 5 of 13 us in the interpreter and ctypes.  These functions take
+ * the tensors of an ordinary call -- the current device's, rows contiguous and
+ * aligned, shapes that agree -- allocate the results and call the library.  For
+ * anything else they return None, and the caller's Python code checks, copies
+ * or refuses the arguments as it does without them.
+ */
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+#include <stdint.h>
+
+#include "../../../include/resgemm.h"
+
+typedef int (*quantize_fn)(const void*, int, int64_t, int64_t, int64_t, int, uint8_t*, int64_t, float*, uint8_t*,
+                           int64_t, float*, unsigned, void*);
+typedef int (*gemm_fn)(const uint8_t*, int64_t, const float*, const uint8_t*, int64_t, const float*, void*, int,
+                       int64_t, int64_t, int64_t, int64_t, unsigned, void*, size_t, void*);
+
+static quantize_fn lib_quantize;
+static gemm_fn lib_gemm;
+static PyObject *types[3], *f8_type;                     /* torch dtypes by RG_TYPE_*, float8_e4m3fn */
+static PyObject *empty, *raw_stream, *current_device;    /* torch functions */
+static PyObject *workspaces, *raise_status;              /* the binding's workspace cache and error function */
+static PyObject *s_shape, *s_stride, *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_numel, *empty_names;
+
+static int64_t blocks(int64_t x) { return (x + 127) / 128; }
+static int64_t up16(int64_t x) { return (x + 15) & ~(int64_t)15; }
+
+/* A method's or function's integer result; -1 with an exception set on failure. */
+static int64_t as_int(PyObject* r) {
+  if (!r) return -1;
+  const int64_t v = PyLong_AsLongLong(r);
+  Py_DECREF(r);
+  return v;
+}
+static int64_t call_int(PyObject* o, PyObject* name) { return as_int(PyObject_CallMethodNoArgs(o, name)); }
+
+/* The two entries of a tuple; 0 if it is not a pair of integers. */
+static int two(PyObject* t, int64_t* a, int64_t* b) {
+  int ok = 0;
+  if (t && PyTuple_Check(t) && PyTuple_GET_SIZE(t) == 2) {
+    *a = PyLong_AsLongLong(PyTuple_GET_ITEM(t, 0));
+    *b = PyLong_AsLongLong(PyTuple_GET_ITEM(t, 1));
+    ok = !PyErr_Occurred();
+  }
+  Py_XDECREF(t);
+  return ok;
+}
+
+typedef struct {
+  int64_t m, k, ld;
+  void* p;
+} matrix;
+
+/* A matrix with contiguous rows of `type` on device `dev`; 0 to decline. */
+static int matrix_of(PyObject* t, PyObject* type, int64_t dev, matrix* x) {
+  int64_t s0, s1;
+  PyObject* d = PyObject_GetAttr(t, s_dtype);
+  if (!d) return 0;
+  Py_DECREF(d); /* dtypes live for good */
+  if (d != type || call_int(t, s_get_device) != dev) return 0;
+  if (!two(PyObject_GetAttr(t, s_shape), &x->m, &x->k) || !two(PyObject_CallMethodNoArgs(t, s_stride), &s0, &s1))
+    return 0;
+  if (x->k > 1 && s1 != 1) return 0;
+  x->ld = x->m > 1 ? s0 : x->k;
+  if (x->ld < x->k || !x->k || !x->m) return 0;
+  x->p = (void*)(uintptr_t)call_int(t, s_data_ptr);
+  return x->p && !PyErr_Occurred();
+}
+/* Contiguous, of this shape. */
+static int scales_of(PyObject* t, int64_t dev, int64_t m, int64_t k, matrix* x) {
+  return matrix_of(t, types[RG_TYPE_F32], dev, x) && x->m == m && x->k == k && x->ld == k;
+}
+/* E4M3 rows on 16-byte boundaries. */
+static int values_of(PyObject* t, int64_t dev, matrix* x) {
+  if (!matrix_of(t, f8_type, dev, x)) return 0;
+  if (x->m == 1) x->ld = up16(x->ld);
+  return !(x->ld & 15) && !((uintptr_t)x->p & 15);
+}
+
+static PyObject* new_matrix(int64_t m, int64_t k, PyObject* type, PyObject* device) {
+  PyObject* size = Py_BuildValue("(LL)", (long long)m, (long long)k);
+  if (!size) return NULL;
+  PyObject* args[3] = {size, type, device};
+  PyObject* t = PyObject_Vectorcall(empty, args, 1, empty_names);
+  Py_DECREF(size);
+  return t;
+}
+
+/* The device that holds `t`, if it is the current one, and its current stream. */
+static int place(PyObject* t, int64_t* dev, void** stream) {
+  *dev = call_int(t, s_get_device);
+  if (*dev < 0 || as_int(PyObject_CallNoArgs(current_device)) != *dev) return 0;
+  PyObject* i = PyLong_FromLongLong(*dev);
+  if (!i) return 0;
+  PyObject* s = PyObject_CallOneArg(raw_stream, i);
+  Py_DECREF(i);
+  if (!s) return 0;
+  *stream = PyLong_AsVoidPtr(s);
+  Py_DECREF(s);
+  return !PyErr_Occurred();
+}
+
+/* None for the caller to take the long way; errors on the way here are its to report. */
+static PyObject* decline(void) {
+  PyErr_Clear();
+  Py_RETURN_NONE;
+}
+static PyObject* finish(int rc, const char* where, PyObject* result) {
+  if (!rc) return result;
+  Py_XDECREF(result);
+  PyObject* r = PyObject_CallFunction(raise_status, "is", rc, where);
+  if (r) {
+    Py_DECREF(r);
+    PyErr_SetString(PyExc_RuntimeError, where);
+  }
+  return NULL;
+}
+
+/* quantize(X, form, flags) -> (Q, S) or, transposed, (QT, ST); None to decline */
+static PyObject* quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 3) return decline();
+  const long form = PyLong_AsLong(a[1]), flags = PyLong_AsLong(a[2]);
+  int64_t dev;
+  void* stream;
+  matrix x, q, s;
+  if (PyErr_Occurred() || form == RG_F8_BOTH || !place(a[0], &dev, &stream)) return decline();
+  PyObject* type = PyObject_GetAttr(a[0], s_dtype);
+  Py_XDECREF(type);
+  int t = 0;
+  while (t < 3 && types[t] != type) ++t;
+  if (t == 3 || !matrix_of(a[0], type, dev, &x)) return decline();
+  const int turned = form == RG_F8_COLUMNS;
+  q.m = turned ? x.k : x.m;
+  q.k = turned ? x.m : x.k;
+  if (q.k & 15) return decline(); /* padded rows are a view */
+  PyObject* device = PyObject_GetAttr(a[0], s_device);
+  if (!device) return decline();
+  PyObject* Q = new_matrix(q.m, q.k, f8_type, device);
+  PyObject* S = Q ? new_matrix(form == RG_F8_TILES ? blocks(q.m) : q.m, blocks(q.k), types[RG_TYPE_F32], device) : NULL;
+  Py_DECREF(device);
+  if (!S) {
+    Py_XDECREF(Q);
+    return NULL;
+  }
+  q.p = (void*)(uintptr_t)call_int(Q, s_data_ptr);
+  s.p = (void*)(uintptr_t)call_int(S, s_data_ptr);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = turned ? lib_quantize(x.p, t, x.ld, x.m, x.k, (int)form, NULL, 0, NULL, q.p, q.k, s.p, (unsigned)flags, stream)
+              : lib_quantize(x.p, t, x.ld, x.m, x.k, (int)form, q.p, q.k, s.p, NULL, 0, NULL, (unsigned)flags, stream);
+  Py_END_ALLOW_THREADS
+  PyObject* r = PyTuple_Pack(2, Q, S);
+  Py_DECREF(Q);
+  Py_DECREF(S);
+  return r ? finish(rc, "quantize_f8", r) : NULL;
+}
+
+/* gemm(A, SA, B, SB, out_dtype, transb, flags) -> C; None to decline */
+static PyObject* gemm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 7) return decline();
+  const int transb = PyObject_IsTrue(a[5]);
+  unsigned flags = (unsigned)PyLong_AsUnsignedLong(a[6]);
+  int64_t dev;
+  void* stream;
+  matrix A, B, SA, SB;
+  if (PyErr_Occurred() || transb < 0 || !place(a[0], &dev, &stream)) return decline();
+  int t = 0;
+  while (t < 3 && types[t] != a[4]) ++t;
+  if (t == 3 || !values_of(a[0], dev, &A) || !values_of(a[2], dev, &B)) return decline();
+  const int64_t N = transb ? B.m : B.k, K = A.k, kb = blocks(K), nb = blocks(N);
+  if (K != (transb ? B.k : B.m) || !scales_of(a[1], dev, A.m, kb, &SA)) return decline();
+  if (scales_of(a[3], dev, transb ? nb : kb, transb ? kb : nb, &SB)) flags |= RG_FLAG_TILE_B;
+  else if (PyErr_Occurred() || !scales_of(a[3], dev, transb ? N : kb, transb ? kb : N, &SB)) return decline();
+  if (transb) flags |= RG_FLAG_TRANS_B;
+  PyObject* key = Py_BuildValue("(LN)", (long long)dev, PyLong_FromVoidPtr(stream));
+  if (!key) return decline();
+  PyObject* ws = PyDict_GetItemWithError(workspaces, key); /* borrowed */
+  Py_DECREF(key);
+  if (!ws) return decline();
+  const int64_t ws_bytes = call_int(ws, s_numel);
+  void* ws_p = (void*)(uintptr_t)call_int(ws, s_data_ptr);
+  PyObject* device = PyErr_Occurred() ? NULL : PyObject_GetAttr(a[0], s_device);
+  if (!device) return decline();
+  PyObject* C = new_matrix(A.m, N, a[4], device);
+  Py_DECREF(device);
+  if (!C) return NULL;
+  void* c = (void*)(uintptr_t)call_int(C, s_data_ptr);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = lib_gemm(A.p, A.ld, SA.p, B.p, B.ld, SB.p, c, t, N, A.m, N, K, flags, ws_p, (size_t)ws_bytes, stream);
+  Py_END_ALLOW_THREADS
+  return finish(rc, "scaled_gemm_f8", C);
+}
+
+/* setup(quantize address, gemm address, (f32, f16, bf16), f8, empty, raw_stream, current_device, workspaces, raise) */
+static PyObject* setup(PyObject* self, PyObject* args) {
+  (void)self;
+  unsigned long long q, g;
+  PyObject *t0, *t1, *t2;
+  if (!PyArg_ParseTuple(args, "KK(OOO)OOOOOO", &q, &g, &t0, &t1, &t2, &f8_type, &empty, &raw_stream, &current_device,
+                        &workspaces, &raise_status))
+    return NULL;
+  lib_quantize = (quantize_fn)(uintptr_t)q;
+  lib_gemm = (gemm_fn)(uintptr_t)g;
+  types[RG_TYPE_F32] = t0;
+  types[RG_TYPE_F16] = t1;
+  types[RG_TYPE_BF16] = t2;
+  PyObject* keep[] = {t0, t1, t2, f8_type, empty, raw_stream, current_device, workspaces, raise_status};
+  for (size_t i = 0; i < sizeof keep / sizeof *keep; ++i) Py_INCREF(keep[i]); /* for the life of the process */
+  s_shape = PyUnicode_InternFromString("shape");
+  s_stride = PyUnicode_InternFromString("stride");
+  s_dtype = PyUnicode_InternFromString("dtype");
+  s_device = PyUnicode_InternFromString("device");
+  s_data_ptr = PyUnicode_InternFromString("data_ptr");
+  s_get_device = PyUnicode_InternFromString("get_device");
+  s_numel = PyUnicode_InternFromString("numel");
+  empty_names = Py_BuildValue("(ss)", "dtype", "device");
+  if (!empty_names || !s_numel) return NULL;
+  Py_RETURN_NONE;
+}
+
+static PyMethodDef methods[] = {{"setup", setup, METH_VARARGS, NULL},
+                                {"quantize", (PyCFunction)(void (*)(void))quantize, METH_FASTCALL, NULL},
+                                {"gemm", (PyCFunction)(void (*)(void))gemm, METH_FASTCALL, NULL},
+                                {NULL, NULL, 0, NULL}};
+static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "f8_call", NULL, -1, methods, NULL, NULL, NULL, NULL};
+PyMODINIT_FUNC PyInit_f8_call(void) { return PyModule_Create(&module); }

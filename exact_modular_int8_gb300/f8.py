@@ -10,11 +10,15 @@ With sync=False a call only enqueues its work, and errors found on the device ar
 """
 from __future__ import annotations
 
+import ctypes
 import functools
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
-from . import (RG_ERR_ARG, RG_ERR_RANGE, RG_F8_BOTH, RG_F8_COLUMNS, RG_F8_ROWS, RG_F8_TILES, RG_FLAG_SYNC,
+from . import (LIB_PATH, RG_ERR_ARG, RG_ERR_RANGE, RG_F8_BOTH, RG_F8_COLUMNS, RG_F8_ROWS, RG_F8_TILES, RG_FLAG_SYNC,
                RG_FLAG_TILE_B, RG_FLAG_TRANS_B, RG_TYPE_BF16, RG_TYPE_F16, RG_TYPE_F32, ResGemmError, _check, _output,
                _ws_cache, library, workspace)
 
@@ -23,6 +27,27 @@ F8 = torch.float8_e4m3fn
 _TYPES = {torch.float32: RG_TYPE_F32, torch.float16: RG_TYPE_F16, torch.bfloat16: RG_TYPE_BF16}
 _FORMS = {"rows": RG_F8_ROWS, "columns": RG_F8_COLUMNS, "both": RG_F8_BOTH, "tiles": RG_F8_TILES}
 _WS_BYTES = 4096
+
+
+def _native():
+    """The native call path (csrc/python/f8_call.c), set up once."""
+    global _call
+    if _call is None:
+        lib = library()
+        path = os.path.join(os.path.dirname(LIB_PATH), "f8_call.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m exact_modular_int8_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("f8_call", path)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("f8_call", path, loader=loader))
+        loader.exec_module(m)
+        address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+        m.setup(address(lib.quantize_f8), address(lib.scaled_gemm_f8), (torch.float32, torch.float16, torch.bfloat16),
+                F8, torch.empty, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache, _check)
+        _call = m
+    return _call
+
+
+_call = None
 
 
 def _blocks(x: int) -> int:
@@ -98,6 +123,10 @@ def quantize_f8(X: torch.Tensor, form: str = "rows", sync: bool = True):
     f = _FORMS.get(form)
     if f is None:
         raise ValueError(f"quantize_f8: form must be one of {', '.join(_FORMS)}")
+    if X.is_cuda and f != RG_F8_BOTH:
+        r = _native().quantize(X, f, RG_FLAG_SYNC if sync else 0)
+        if r is not None:
+            return r
     t = _TYPES.get(X.dtype)
     if t is None or X.dim() != 2:
         raise ValueError("quantize_f8: X [M, K] float32, float16 or bfloat16 expected")
@@ -133,6 +162,10 @@ def scaled_gemm_f8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch
     the contraction, told apart by shape: transb SB [ceil(N/128), ceil(K/128)] or [N, ceil(K/128)], else
     [ceil(K/128), ceil(N/128)] or [ceil(K/128), N] (N = 1 is either).  Products per block on the tensor
     cores, scales and sums in float32, one rounding to out_dtype (float32, float16 or bfloat16)."""
+    if out is None and ws is None and A.is_cuda:
+        C = _native().gemm(A, SA, B, SB, out_dtype, transb, RG_FLAG_SYNC if sync else 0)
+        if C is not None:
+            return C
     if A.dim() != 2 or B.dim() != 2 or A.dtype != F8 or B.dtype != F8:
         raise ValueError("scaled_gemm_f8: A [M, K] and B [K, N] (transb: [N, K]) float8_e4m3fn expected")
     M, K = A.shape

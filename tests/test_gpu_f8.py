@@ -11,6 +11,8 @@ experts   the same kind of count for each of the two products and first-order pr
           router (see _moe_reference).
 """
 import math
+import os
+import sys
 
 import numpy as np
 import pytest
@@ -538,6 +540,18 @@ def test_moe_empty_and_streams(rg):  # noqa: F811
     off[1:] = args[0].reshape(-1)  # tokens off a 16-byte boundary
     assert rg.moe_layer_f8(off[1:].view(3, 256), *args[1:], 2, out=out) is out
     assert torch.equal(out, want)
+
+
+def test_example_trains_and_decodes(rg):  # noqa: F811
+    """The example's layer learns (its loss falls to the quantisation's noise) and its decoding is finite."""
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import f8_layers
+
+    losses, w = f8_layers.train()
+    # the target's outputs have variance 1; E4M3 keeps every factor of a product within 2^-4
+    assert losses[0] > 0.5 and losses[-1] < (2 * 2.0**-4) ** 2 * losses[0]
+    y, z = f8_layers.decode(w)
+    assert torch.isfinite(y).all() and torch.isfinite(z).all() and float(z.float().abs().max()) > 0
 
 
 def test_graph_capture(rg):  # noqa: F811
