@@ -35,13 +35,16 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRouterWarps = 8;
+constexpr int kRouterWarps = 16;
 constexpr int kRouterThreads = 32 * kRouterWarps;
 constexpr int kMaxT = RG_MOE_MAX_TOKENS;
 constexpr int kMaxK = RG_MOE_MAX_TOP_K;
 constexpr int kMaxE = RG_MOE_MAX_EXPERTS;
 constexpr int kSlots = kMaxT * kMaxK;
-constexpr int kMaxNT = 4;            // column tiles of eight tokens per pass over the weights
+// column tiles of eight tokens per pass over the weights (a kernel with four
+// spills registers: 64 tokens in 300 against 290 us, and no faster where experts
+// get more than 16 tokens)
+constexpr int kMaxNT = 2;
 constexpr int kMinRing = 3, kMaxRing = 8;  // weight pieces (16 rows x 128 k) per warp, on their way or in use
 constexpr int kPiece = 16 * 128 + 16;      // and the two scales of its rows
 constexpr int kMaxStride = 32;             // words between two slots' maxima
@@ -50,8 +53,6 @@ constexpr int kSmemBytes = 231424;         // all of an SM's
 struct MoeWs {
   float* gate;       // [T * top_k] weights, and
   int* expert;       // experts, by slot = token * top_k + rank
-  __half* xs;        // [T][H] x times 2^n
-  float* x_inv;      // [T] 2^-n
   float* h;          // [T * top_k][I]
   uint32_t* h_max;   // [T * top_k][kMaxStride] largest |h|, as bits, in the first word
   unsigned* arrived;  // CTAs that have reached the grid's barriers
@@ -103,8 +104,7 @@ __device__ __forceinline__ float2 pow2_scale(uint32_t max_bits) {
 // form the logits of a share of the experts each (tiles of 8 or 16 experts x 8
 // tokens, a CTA's warps splitting k; the products of 16-bit entries are exact in
 // the MMA's fp32), then one token's top-k each, reading the logits from each
-// other's shared memory.  It also makes the scaled fp16 copies of the tokens
-// and clears the words that kernel 2 starts from.
+// other's shared memory.  It also clears the words that kernel 2 starts from.
 // ---------------------------------------------------------------------------
 template <typename T>
 __device__ __forceinline__ void mma_t(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -155,10 +155,11 @@ __device__ __forceinline__ void choose(const MoeParams& p, int t, F&& logit) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   uint32_t taken = 0;  // bit i: this lane's entry i is chosen
-  float mine = 0.0f, total = 0.0f;
+  float mine = 0.0f;   // lane j: the logit and the expert of rank j
   int my_expert = 0;
   for (int j = 0; j < p.top_k; ++j) {
     uint32_t key = 0;
+    float best_v = 0.0f;
     int at = 0;
     bool any = false;
 #pragma unroll
@@ -166,6 +167,7 @@ __device__ __forceinline__ void choose(const MoeParams& p, int t, F&& logit) {
       const uint32_t k = order_key(v[i] + 0.0f);  // -0 ties with +0
       if (i * 32 + lane < p.E && !(taken >> i & 1u) && (!any || k > key)) {
         key = k;
+        best_v = v[i];
         at = i;
         any = true;
       }
@@ -174,22 +176,19 @@ __device__ __forceinline__ void choose(const MoeParams& p, int t, F&& logit) {
     const uint32_t best = __reduce_max_sync(0xFFFFFFFFu, any ? key : 0u);
     const uint32_t cand = any && key == best ? (uint32_t)(at * 32 + lane) : 0xFFFFFFFFu;
     const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, cand);
-    float pe = 0.0f;
-    if (cand == e) {
-      taken |= 1u << at;
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i == at) pe = expf(v[i] - mx) / sum;
-    }
-    pe = __shfl_sync(0xFFFFFFFFu, pe, (int)(e & 31u));
-    total += pe;
+    if (cand == e) taken |= 1u << at;
+    best_v = __shfl_sync(0xFFFFFFFFu, best_v, (int)(e & 31u));
     if (lane == j) {
-      mine = pe;
+      mine = best_v;
       my_expert = (int)e;
     }
   }
+  const float prob = lane < p.top_k ? expf(mine - mx) / sum : 0.0f;
+  float total = prob;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
   if (lane < p.top_k) {
-    const float w = p.renorm ? mine / total : mine;
+    const float w = p.renorm ? prob / total : prob;
     p.w.gate[t * p.top_k + lane] = nan ? __int_as_float(0x7FC00000) : w;
     p.w.expert[t * p.top_k + lane] = my_expert;
     p.w.h_max[(t * p.top_k + lane) * kMaxStride] = 0;
@@ -200,7 +199,6 @@ template <typename T>
 __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kRouterThreads) moe_router_kernel(MoeParams p) {
   __shared__ float red[kRouterWarps][16][8];
   __shared__ float logits[8][kMaxE / 8];  // [token][16-expert (8-expert) tiles of this CTA]
-  __shared__ uint32_t wmax[kRouterWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const T* X = static_cast<const T*>(p.X);
   const T* WR = static_cast<const T*>(p.WR);
@@ -244,35 +242,7 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kRouterThreads) moe_
     }
     __syncthreads();
   }
-  const int t = t0 + rank;
-  if (t < p.T) {  // this CTA's token: its largest entry, then the scaled copy
-    const T* x = X + (long long)t * p.H;
-    uint32_t m = 0;
-    for (int k = threadIdx.x * 8; k < p.H; k += kRouterThreads * 8) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k));
-      const T* v = reinterpret_cast<const T*>(&a);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(to_f(v[j])) & 0x7FFFFFFFu);
-    }
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (lane == 0) wmax[warp] = m;
-    __syncthreads();
-    for (int w = 0; w < kRouterWarps; ++w) m = max(m, wmax[w]);
-    const float2 sc = pow2_scale(m);
-    for (int k = threadIdx.x * 8; k < p.H; k += kRouterThreads * 8) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k));
-      const T* v = reinterpret_cast<const T*>(&a);
-      uint4 o;
-      uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half2 h = __floats2half2_rn(to_f(v[2 * j]) * sc.x, to_f(v[2 * j + 1]) * sc.x);
-        ow[j] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      *reinterpret_cast<uint4*>(p.w.xs + (long long)t * p.H + k) = o;
-    }
-    if (threadIdx.x == 0) p.w.x_inv[t] = sc.y;
-  }
+  const int t = t0 + rank;  // this CTA's token
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (t < p.T && warp == 0) {
     auto logit = [&](int e) {
@@ -574,33 +544,58 @@ struct Phase {
 
   __device__ int stride() const { return nkb * 256 + 16; }  // bytes per staged token: conflict-free for the lanes' loads
 
-  // The operand of tokens [first, first + n) of the order: fp16, zeros past K.
+  // The operand of tokens [first, first + n) of the order: fp16 scaled by the power
+  // of two that col_scale undoes, zeros past K.  A warp makes a token's row.
   __device__ void stage(int first, int n) {
-    const Routing& r = sm.r;
-    const int chunks = nkb * 16, st = stride();
-    if ((int)threadIdx.x < n) {
-      const int s = r.order[first + threadIdx.x];
-      sm.col_scale[threadIdx.x] = UP ? __ldcg(&p.w.x_inv[s / p.top_k]) : pow2_scale(__ldcg(&p.w.h_max[s * kMaxStride])).y;
-    }
-    for (int i = threadIdx.x; i < n * chunks; i += kThreads) {
-      const int c = i / chunks, k = (i - c * chunks) * 8, s = r.order[first + c];
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (k < K) {
-        if constexpr (UP) {
-          v = __ldcg(reinterpret_cast<const uint4*>(p.w.xs + (long long)(s / p.top_k) * K + k));
-        } else {
-          const float sc = pow2_scale(__ldcg(&p.w.h_max[s * kMaxStride])).x;
-          const float4* h = reinterpret_cast<const float4*>(p.w.h + (long long)s * K + k);
-          const float4 a = __ldcg(h), b = __ldcg(h + 1);
-          const __half2 h0 = __floats2half2_rn(a.x * sc, a.y * sc), h1 = __floats2half2_rn(a.z * sc, a.w * sc);
-          const __half2 h2 = __floats2half2_rn(b.x * sc, b.y * sc), h3 = __floats2half2_rn(b.z * sc, b.w * sc);
-          v.x = *reinterpret_cast<const uint32_t*>(&h0);
-          v.y = *reinterpret_cast<const uint32_t*>(&h1);
-          v.z = *reinterpret_cast<const uint32_t*>(&h2);
-          v.w = *reinterpret_cast<const uint32_t*>(&h3);
+    for (int c = warp; c < n; c += kWarps) {
+      const int s = sm.r.order[first + c];
+      uint8_t* out = cols + c * stride();
+      if constexpr (UP) {
+        const long long at = (long long)(s / p.top_k) * K;
+        if (p.type == RG_TYPE_F16) stage_token(static_cast<const __half*>(p.X) + at, out, c);
+        else stage_token(static_cast<const __nv_bfloat16*>(p.X) + at, out, c);
+      } else {
+        const float* h = p.w.h + (long long)s * K;
+        const float2 sc = pow2_scale(__ldcg(&p.w.h_max[s * kMaxStride]));
+        if (lane == 0) sm.col_scale[c] = sc.y;
+#pragma unroll 4
+        for (int k = lane * 8; k < nkb * 128; k += 256) {
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+          if (k < K) {
+            a = __ldcg(reinterpret_cast<const float4*>(h + k));
+            b = __ldcg(reinterpret_cast<const float4*>(h + k) + 1);
+          }
+          *reinterpret_cast<uint4*>(out + k * 2) =
+              make_uint4(half_pair(a.x, a.y, sc.x), half_pair(a.z, a.w, sc.x), half_pair(b.x, b.y, sc.x),
+                         half_pair(b.z, b.w, sc.x));
         }
       }
-      *reinterpret_cast<uint4*>(cols + c * st + k * 2) = v;
+    }
+  }
+  static __device__ __forceinline__ uint32_t half_pair(float a, float b, float scale) {
+    const __half2 h = __floats2half2_rn(a * scale, b * scale);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  template <typename T>
+  __device__ __forceinline__ void stage_token(const T* x, uint8_t* out, int c) {
+    uint32_t m = 0;
+#pragma unroll 8
+    for (int k = lane * 8; k < K; k += 256) {  // K is a multiple of 16
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(x + k));
+      const T* v = reinterpret_cast<const T*>(&a);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(to_f(v[j])) & 0x7FFFFFFFu);
+    }
+    const float2 sc = pow2_scale(__reduce_max_sync(0xFFFFFFFFu, m));
+    if (lane == 0) sm.col_scale[c] = sc.y;
+#pragma unroll 4
+    for (int k = lane * 8; k < nkb * 128; k += 256) {  // the row again, now from near
+      uint4 a = make_uint4(0, 0, 0, 0);
+      if (k < K) a = __ldg(reinterpret_cast<const uint4*>(x + k));
+      const T* v = reinterpret_cast<const T*>(&a);
+      *reinterpret_cast<uint4*>(out + k * 2) =
+          make_uint4(half_pair(to_f(v[0]), to_f(v[1]), sc.x), half_pair(to_f(v[2]), to_f(v[3]), sc.x),
+                     half_pair(to_f(v[4]), to_f(v[5]), sc.x), half_pair(to_f(v[6]), to_f(v[7]), sc.x));
     }
   }
 
@@ -698,11 +693,11 @@ struct Phase {
         }
       return;
     }
-    // up to 16 columns: units alternate between two halves of the buffer, so that
-    // one meeting of the group per unit is enough
-    constexpr bool kHalves = NT <= kMaxNT / 2;
+    // units alternate between two halves of the buffer, so that one meeting of the
+    // group per unit is enough (a segment's units all have the same NT, and the
+    // block meets between segments)
     const int ld = p.red_ld;
-    float* part = red + (size_t)group * ks * 16 * ld + (kHalves ? parity * (8 * NT) : 0);
+    float* part = red + (size_t)group * ks * 16 * ld + parity * (8 * NT);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       *reinterpret_cast<float2*>(&part[(kpart * 16 + g) * ld + i * 8 + 2 * t4]) = make_float2(tot[i][0], tot[i][1]);
@@ -719,8 +714,7 @@ struct Phase {
         }
       store(rb, row, first, c, c < n, lo, hi, 1);
     }
-    if constexpr (kHalves) parity ^= 1;
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ks * 32) : "memory");
+    parity ^= 1;
   }
 
   template <typename F>
@@ -742,7 +736,6 @@ struct Phase {
       for (; mine < end; mine += groups) {
         const int rb = mine - base;
         if (n <= 8) unit<1>(rb, first, n);
-        else if (n <= 16) unit<2>(rb, first, n);
         else unit<kMaxNT>(rb, first, n);
       }
       at = end;
@@ -806,8 +799,6 @@ size_t layout(long long T, long long H, long long I, long long top_k, uint8_t* b
   MoeWs m;
   m.gate = reinterpret_cast<float*>(take(slots * 4));
   m.expert = reinterpret_cast<int*>(take(slots * 4));
-  m.xs = reinterpret_cast<__half*>(take((size_t)T * H * 2));
-  m.x_inv = reinterpret_cast<float*>(take((size_t)T * 4));
   m.h = reinterpret_cast<float*>(take(slots * I * 4));
   m.h_max = reinterpret_cast<uint32_t*>(take(slots * 4 * kMaxStride));
   m.arrived = reinterpret_cast<unsigned*>(take(4));
@@ -842,9 +833,8 @@ void plan_smem(MoeParams& p) {
   if (tokens > 8) tokens = (tokens + 7) / 8 * 8;
   if (tokens > 8 * kMaxNT) tokens = 8 * kMaxNT;
   if (tokens > p.T) tokens = p.T;
-  // one or two column tiles: two halves (see unit())
-  auto tiles = [](int n) { return n <= 8 ? 1 : n <= 16 ? 2 : kMaxNT; };
-  auto ld = [&](int n) { return (tiles(n) < kMaxNT ? 16 * tiles(n) : 8 * kMaxNT) + 4; };
+  auto tiles = [](int n) { return n <= 8 ? 1 : kMaxNT; };
+  auto ld = [&](int n) { return 16 * tiles(n) + 4; };  // two halves, see unit()
   auto room_for = [&](int n) { return kSmemBytes - kFixedBytes - kMinRing * ring1 - kWarps * 16 * 4 * ld(n); };
   while (tokens * wide > room_for(tokens)) tokens = tokens > 8 ? (tokens - 1) / 8 * 8 : tokens - 1;
   int room = room_for(tokens) - tokens * wide;
