@@ -211,7 +211,7 @@ __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar_cluster
 // before most of the arithmetic.
 //
 // With one scale for all the columns (TILE_B) a lane holds a row: acc += p s, the
-// column scale already in s.  (8192 x 8192 x 4096: 242 us, 284 in the other form.)
+// column scale already in s.  (8192 x 8192 x 4096: 239 us, 284 in the other form.)
 template <int COLS, bool TILE_B>
 struct Sums {
   static constexpr int kRows = 1;
@@ -292,6 +292,9 @@ struct Sums<COLS, false> {
 // ---------------------------------------------------------------------------
 // Tiles of 128 x 128, one per cluster of S CTAs: each CTA sums a slice of K,
 // and the slices are joined through distributed shared memory in rank order.
+// For products that one wave of CTAs holds, where the time is the latency of
+// set-up, K / S / 128 blocks of 0.3 us and the join: 512 x 4096 x 4096 15.2 us,
+// 128 x 4096 x 4096 (S = 4) 9.4 us, 1000 x 1544 x 2056 11.7 us.
 // ---------------------------------------------------------------------------
 constexpr int BN1 = 128;
 constexpr int STAGES1 = 6;
@@ -558,6 +561,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // through the barriers is a chain of about 1300 cycles with whole 256-column
 // MMAs, of which only two are in flight; the halves' chains are shorter and
 // interleave.
+//
+// 8192 x 8192 x 4096: 239 us, 2300 TFLOP/s, half of the E4M3 instruction rate (the
+// tensor pipe is active 46% of the time).  A block of a tile takes 1000 cycles
+// where its MMAs take 512: the epilogue warp's own chain of wait (about 150),
+// read-back (130), multiply-adds (170), store (100, spread over the blocks) and
+// barriers.  More epilogue warps (16: spills, 293 us), 256 x 192 tiles with
+// twelve warps (271 us) and single-CTA 128 x 192 tiles (261 us) were slower.
 //
 // The block is launched with 168 registers a thread; the first warpgroup
 // (producer, MMA issue, scales) gives up 112 of them and the two epilogue
@@ -986,9 +996,9 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
                            unsigned long long wait_ns) {
   const int variant = gemm_variant();
   // Few rows: up to 16 the warp-level kernel is faster at every size measured
-  // (8192 x 4096: 9.3 us for one row, 11.7 for 16, against 14.5 with padded tiles);
+  // (8192 x 4096: 9.3 us for one row, 11.7 for 16, against 13.5 with padded tiles);
   // from 17 to 32 while B is small enough for latency to count (24 rows: 2.7
-  // against 6.4 us at 1024 x 1024, 17.8 against 14.3 at 8192 x 4096).
+  // against 5.6 us at 1024 x 1024, 17.8 against 13.4 at 8192 x 4096).
   if (variant == 0 && a.b_kmajor && (a.M <= 16 || (a.M <= kSkinnyRows && a.N * a.K <= (1LL << 24))))
     return launch_f8_skinny(a, plan, st);
   int dev = 0;

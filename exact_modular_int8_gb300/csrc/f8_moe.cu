@@ -15,11 +15,17 @@
 // MMAs without any shuffle.  tcgen05 would want the tokens padded to its tiles
 // and quantised to E4M3 too; here the pass is bound by memory.  Activations
 // enter as fp16 scaled by a power of two per row (their largest magnitude in
-// [2^14, 2^15)): exact for bf16 and fp16 entries within 2^-29 of the row's
-// largest, off by at most 2^-40 of it below.  The gated product h is kept in
+// [2^14, 2^15)): exact for bf16 and fp16 entries within 2^-28 of the row's
+// largest, off by at most 2^-39 of it below.  The gated product h is kept in
 // fp32 and rounded to fp16 the same way when it enters the second product
-// (relative 2^-12 per entry, an eighth of a bf16 result's rounding).  Each
+// (relative 2^-11 per entry, an eighth of a bf16 result's rounding).  Each
 // 128-block's sum is scaled in fp32 and added to fp32 sums.
+//
+// 64 tokens through 128 experts of 4096 x 1024 (top 8): 292 us, the weights at
+// the copy rate 237; the two products stream at 6.3 TB/s, and the grid's meetings
+// wait for the slowest SM, 10% behind the median.  One token through 8 of 64
+// experts of 2048 x 1024: 28 us (7.6): router 4, routing 1.5, first product 9,
+// second 4, two meetings of the grid 2 each, sum 1, launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -12,6 +12,11 @@
 // tiles.  What a warp needs of one 128-block -- B's and A's rows and the scales --
 // is a piece, copied to shared memory (cp.async) kRing - 1 pieces ahead of its
 // use and across tiles.  The warps' sums meet in shared memory in a fixed order.
+//
+// Bound by memory and, for short calls, by its latency: one row of 4096 x 2048 in
+// 3.2 us (the bytes alone take 1.25), of 8192 x 4096 in 9.3 us (5.0), of 70000 x
+// 4096 in 57 us (5.0 TB/s).  Before the copies (loads to registers, a tile per
+// block) the second took 11.4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
