@@ -1,11 +1,12 @@
 /*
- * f8_call.c -- the Python binding's short way into quantize_f8 and
- * scaled_gemm_f8 (include/resgemm.h).
+ * f8_call.c -- the Python binding's short way into quantize_f8, scaled_gemm_f8
+ * and linear_f8 with its backward pass (include/resgemm.h).
  *
- * A small call's time is its time on the host, and most of that was spent on
- * marshalling: 5 of 13 us in the interpreter and ctypes.  These functions take
- * the tensors of an ordinary call -- the current device's, rows contiguous and
- * aligned, shapes that agree -- allocate the results and call the library.  For
+ * A small call's time is its time on the host, and much of that was spent on
+ * marshalling: 5 of a product's 13 us in the interpreter and ctypes, 4 of the
+ * 16 that each pass of a linear layer took.  These functions take the tensors
+ * of an ordinary call -- the current device's, rows contiguous and aligned,
+ * shapes that agree -- allocate the results and call the library.  For
  * anything else they return None, and the caller's Python code checks, copies
  * or refuses the arguments as it does without them.
  */
@@ -20,9 +21,18 @@ typedef int (*quantize_fn)(const void*, int, int64_t, int64_t, int64_t, int, uin
 typedef int (*gemm_fn)(const uint8_t*, int64_t, const float*, const uint8_t*, int64_t, const float*, void*, int,
                        int64_t, int64_t, int64_t, int64_t, unsigned, void*, size_t, void*);
 
+typedef int (*linear_fn)(const void*, int, int64_t, const void*, int, int64_t, void*, int64_t, int64_t, int64_t, void*,
+                         size_t, unsigned, void*, size_t, void*);
+typedef int (*backward_fn)(const void*, int, int64_t, const void*, size_t, void*, void*, int, int64_t, int64_t, int64_t,
+                           unsigned, void*, size_t, void*);
+typedef size_t (*bytes_fn)(int64_t, int64_t, int64_t);
+
 static quantize_fn lib_quantize;
 static gemm_fn lib_gemm;
-static PyObject *types[3], *f8_type;                     /* torch dtypes by RG_TYPE_*, float8_e4m3fn */
+static linear_fn lib_linear;
+static backward_fn lib_backward;
+static bytes_fn lib_saved_bytes, lib_ws_bytes;
+static PyObject *types[3], *f8_type, *byte_type;         /* torch dtypes by RG_TYPE_*, float8_e4m3fn, uint8 */
 static PyObject *empty, *raw_stream, *current_device;    /* torch functions */
 static PyObject *workspaces, *raise_status;              /* the binding's workspace cache and error function */
 static PyObject *s_shape, *s_stride, *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_numel, *empty_names;
@@ -82,13 +92,39 @@ static int values_of(PyObject* t, int64_t dev, matrix* x) {
   return !(x->ld & 15) && !((uintptr_t)x->p & 15);
 }
 
-static PyObject* new_matrix(int64_t m, int64_t k, PyObject* type, PyObject* device) {
-  PyObject* size = Py_BuildValue("(LL)", (long long)m, (long long)k);
+/* A floating-point matrix with contiguous rows, and its RG_TYPE_*; -1 to decline. */
+static int real_of(PyObject* t, int64_t dev, matrix* x) {
+  PyObject* type = PyObject_GetAttr(t, s_dtype);
+  if (!type) return -1;
+  Py_DECREF(type);
+  int i = 0;
+  while (i < 3 && types[i] != type) ++i;
+  return i < 3 && matrix_of(t, type, dev, x) ? i : -1;
+}
+
+/* An uninitialised tensor of this size (stolen) on a device. */
+static PyObject* new_tensor(PyObject* size, PyObject* type, PyObject* device) {
   if (!size) return NULL;
   PyObject* args[3] = {size, type, device};
   PyObject* t = PyObject_Vectorcall(empty, args, 1, empty_names);
   Py_DECREF(size);
   return t;
+}
+static PyObject* new_matrix(int64_t m, int64_t k, PyObject* type, PyObject* device) {
+  return new_tensor(Py_BuildValue("(LL)", (long long)m, (long long)k), type, device);
+}
+static void* data_of(PyObject* t) { return (void*)(uintptr_t)call_int(t, s_data_ptr); }
+
+/* The stream's cached workspace and its size; NULL to decline. */
+static void* workspace_of(int64_t dev, void* stream, int64_t* bytes) {
+  PyObject* key = Py_BuildValue("(LN)", (long long)dev, PyLong_FromVoidPtr(stream));
+  if (!key) return NULL;
+  PyObject* ws = PyDict_GetItemWithError(workspaces, key); /* borrowed */
+  Py_DECREF(key);
+  if (!ws) return NULL;
+  *bytes = call_int(ws, s_numel);
+  void* p = data_of(ws);
+  return PyErr_Occurred() ? NULL : p;
 }
 
 /* The device that holds `t`, if it is the current one, and its current stream. */
@@ -130,11 +166,8 @@ static PyObject* quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   void* stream;
   matrix x, q, s;
   if (PyErr_Occurred() || form == RG_F8_BOTH || !place(a[0], &dev, &stream)) return decline();
-  PyObject* type = PyObject_GetAttr(a[0], s_dtype);
-  Py_XDECREF(type);
-  int t = 0;
-  while (t < 3 && types[t] != type) ++t;
-  if (t == 3 || !matrix_of(a[0], type, dev, &x)) return decline();
+  const int t = real_of(a[0], dev, &x);
+  if (t < 0) return decline();
   const int turned = form == RG_F8_COLUMNS;
   q.m = turned ? x.k : x.m;
   q.k = turned ? x.m : x.k;
@@ -148,8 +181,8 @@ static PyObject* quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Py_XDECREF(Q);
     return NULL;
   }
-  q.p = (void*)(uintptr_t)call_int(Q, s_data_ptr);
-  s.p = (void*)(uintptr_t)call_int(S, s_data_ptr);
+  q.p = data_of(Q);
+  s.p = data_of(S);
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = turned ? lib_quantize(x.p, t, x.ld, x.m, x.k, (int)form, NULL, 0, NULL, q.p, q.k, s.p, (unsigned)flags, stream)
@@ -179,19 +212,15 @@ static PyObject* gemm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (scales_of(a[3], dev, transb ? nb : kb, transb ? kb : nb, &SB)) flags |= RG_FLAG_TILE_B;
   else if (PyErr_Occurred() || !scales_of(a[3], dev, transb ? N : kb, transb ? kb : N, &SB)) return decline();
   if (transb) flags |= RG_FLAG_TRANS_B;
-  PyObject* key = Py_BuildValue("(LN)", (long long)dev, PyLong_FromVoidPtr(stream));
-  if (!key) return decline();
-  PyObject* ws = PyDict_GetItemWithError(workspaces, key); /* borrowed */
-  Py_DECREF(key);
-  if (!ws) return decline();
-  const int64_t ws_bytes = call_int(ws, s_numel);
-  void* ws_p = (void*)(uintptr_t)call_int(ws, s_data_ptr);
-  PyObject* device = PyErr_Occurred() ? NULL : PyObject_GetAttr(a[0], s_device);
+  int64_t ws_bytes;
+  void* ws_p = workspace_of(dev, stream, &ws_bytes);
+  if (!ws_p) return decline();
+  PyObject* device = PyObject_GetAttr(a[0], s_device);
   if (!device) return decline();
   PyObject* C = new_matrix(A.m, N, a[4], device);
   Py_DECREF(device);
   if (!C) return NULL;
-  void* c = (void*)(uintptr_t)call_int(C, s_data_ptr);
+  void* c = data_of(C);
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = lib_gemm(A.p, A.ld, SA.p, B.p, B.ld, SB.p, c, t, N, A.m, N, K, flags, ws_p, (size_t)ws_bytes, stream);
@@ -199,20 +228,94 @@ static PyObject* gemm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return finish(rc, "scaled_gemm_f8", C);
 }
 
-/* setup(quantize address, gemm address, (f32, f16, bf16), f8, empty, raw_stream, current_device, workspaces, raise) */
+/* linear(X, W, flags) -> (Y, (saved, M, N, K)); None to decline */
+static PyObject* linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 3) return decline();
+  const unsigned flags = (unsigned)PyLong_AsUnsignedLong(a[2]);
+  int64_t dev, ws_bytes;
+  void* stream;
+  matrix X, W;
+  if (PyErr_Occurred() || !place(a[0], &dev, &stream)) return decline();
+  const int tx = real_of(a[0], dev, &X), tw = tx < 0 ? -1 : real_of(a[1], dev, &W);
+  if (tw < 0 || X.k != W.k) return decline();
+  const int64_t M = X.m, N = W.m, K = X.k;
+  const size_t kept_bytes = lib_saved_bytes(M, N, K);
+  void* ws_p = kept_bytes ? workspace_of(dev, stream, &ws_bytes) : NULL;
+  if (!ws_p || (size_t)ws_bytes < lib_ws_bytes(M, N, K)) return decline();
+  PyObject* device = PyObject_GetAttr(a[0], s_device);
+  if (!device) return decline();
+  PyObject* Y = new_matrix(M, N, types[tx], device);
+  PyObject* kept = Y ? new_tensor(PyLong_FromSize_t(kept_bytes), byte_type, device) : NULL;
+  Py_DECREF(device);
+  if (!kept) {
+    Py_XDECREF(Y);
+    return NULL;
+  }
+  void *y = data_of(Y), *s = data_of(kept);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = lib_linear(X.p, tx, X.ld, W.p, tw, W.ld, y, M, N, K, s, kept_bytes, flags, ws_p, (size_t)ws_bytes, stream);
+  Py_END_ALLOW_THREADS
+  PyObject* r = Py_BuildValue("(N(NLLL))", Y, kept, (long long)M, (long long)N, (long long)K);
+  return r ? finish(rc, "linear_f8", r) : NULL;
+}
+
+/* backward(dY, saved, M, N, K, dw_dtype, flags) -> (dX, dW); None to decline */
+static PyObject* backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 7) return decline();
+  const int64_t M = PyLong_AsLongLong(a[2]), N = PyLong_AsLongLong(a[3]), K = PyLong_AsLongLong(a[4]);
+  const unsigned flags = (unsigned)PyLong_AsUnsignedLong(a[6]);
+  int64_t dev, ws_bytes;
+  void* stream;
+  matrix dY;
+  if (PyErr_Occurred() || !place(a[0], &dev, &stream)) return decline();
+  const int t = real_of(a[0], dev, &dY);
+  int tw = 0;
+  while (tw < 3 && types[tw] != a[5]) ++tw;
+  if (t < 0 || tw == 3 || dY.m != M || dY.k != N || K <= 0 || call_int(a[1], s_get_device) != dev) return decline();
+  const int64_t kept_bytes = call_int(a[1], s_numel);
+  void *s = data_of(a[1]), *ws_p = PyErr_Occurred() ? NULL : workspace_of(dev, stream, &ws_bytes);
+  if (!ws_p || (size_t)ws_bytes < lib_ws_bytes(M, N, K)) return decline();
+  PyObject* device = PyObject_GetAttr(a[0], s_device);
+  if (!device) return decline();
+  PyObject* dX = new_matrix(M, K, types[t], device);
+  PyObject* dW = dX ? new_matrix(N, K, types[tw], device) : NULL;
+  Py_DECREF(device);
+  if (!dW) {
+    Py_XDECREF(dX);
+    return NULL;
+  }
+  void *dx = data_of(dX), *dw = data_of(dW);
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = lib_backward(dY.p, t, dY.ld, s, (size_t)kept_bytes, dx, dw, tw, M, N, K, flags, ws_p, (size_t)ws_bytes, stream);
+  Py_END_ALLOW_THREADS
+  PyObject* r = PyTuple_Pack(2, dX, dW);
+  Py_DECREF(dX);
+  Py_DECREF(dW);
+  return r ? finish(rc, "linear_f8_backward", r) : NULL;
+}
+
+/* setup((six addresses), (f32, f16, bf16), f8, uint8, empty, raw_stream, current_device, workspaces, raise) */
 static PyObject* setup(PyObject* self, PyObject* args) {
   (void)self;
-  unsigned long long q, g;
+  unsigned long long f[6];
   PyObject *t0, *t1, *t2;
-  if (!PyArg_ParseTuple(args, "KK(OOO)OOOOOO", &q, &g, &t0, &t1, &t2, &f8_type, &empty, &raw_stream, &current_device,
-                        &workspaces, &raise_status))
+  if (!PyArg_ParseTuple(args, "(KKKKKK)(OOO)OOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &t0, &t1, &t2, &f8_type,
+                        &byte_type, &empty, &raw_stream, &current_device, &workspaces, &raise_status))
     return NULL;
-  lib_quantize = (quantize_fn)(uintptr_t)q;
-  lib_gemm = (gemm_fn)(uintptr_t)g;
+  lib_quantize = (quantize_fn)(uintptr_t)f[0];
+  lib_gemm = (gemm_fn)(uintptr_t)f[1];
+  lib_linear = (linear_fn)(uintptr_t)f[2];
+  lib_backward = (backward_fn)(uintptr_t)f[3];
+  lib_saved_bytes = (bytes_fn)(uintptr_t)f[4];
+  lib_ws_bytes = (bytes_fn)(uintptr_t)f[5];
   types[RG_TYPE_F32] = t0;
   types[RG_TYPE_F16] = t1;
   types[RG_TYPE_BF16] = t2;
-  PyObject* keep[] = {t0, t1, t2, f8_type, empty, raw_stream, current_device, workspaces, raise_status};
+  PyObject* keep[] = {t0, t1, t2, f8_type, byte_type, empty, raw_stream, current_device, workspaces, raise_status};
   for (size_t i = 0; i < sizeof keep / sizeof *keep; ++i) Py_INCREF(keep[i]); /* for the life of the process */
   s_shape = PyUnicode_InternFromString("shape");
   s_stride = PyUnicode_InternFromString("stride");
@@ -229,6 +332,8 @@ static PyObject* setup(PyObject* self, PyObject* args) {
 static PyMethodDef methods[] = {{"setup", setup, METH_VARARGS, NULL},
                                 {"quantize", (PyCFunction)(void (*)(void))quantize, METH_FASTCALL, NULL},
                                 {"gemm", (PyCFunction)(void (*)(void))gemm, METH_FASTCALL, NULL},
+                                {"linear", (PyCFunction)(void (*)(void))linear, METH_FASTCALL, NULL},
+                                {"backward", (PyCFunction)(void (*)(void))backward, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "f8_call", NULL, -1, methods, NULL, NULL, NULL, NULL};
 PyMODINIT_FUNC PyInit_f8_call(void) { return PyModule_Create(&module); }

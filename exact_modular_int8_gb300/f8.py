@@ -41,8 +41,10 @@ def _native():
         m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("f8_call", path, loader=loader))
         loader.exec_module(m)
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
-        m.setup(address(lib.quantize_f8), address(lib.scaled_gemm_f8), (torch.float32, torch.float16, torch.bfloat16),
-                F8, torch.empty, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache, _check)
+        entries = (lib.quantize_f8, lib.scaled_gemm_f8, lib.linear_f8, lib.linear_f8_backward, lib.linear_f8_saved_bytes,
+                   lib.linear_f8_ws_bytes)
+        m.setup(tuple(address(f) for f in entries), (torch.float32, torch.float16, torch.bfloat16), F8, torch.uint8,
+                torch.empty, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache, _check)
         _call = m
     return _call
 
@@ -215,6 +217,10 @@ def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True):
     dtype (both float32, float16 or bfloat16).  `saved` is what linear_f8_backward needs: one buffer with X
     quantised along M and the quantised weights.  One library call; the same as quantize_f8(X, "both"),
     quantize_f8(W, "tiles") and scaled_gemm_f8."""
+    if X.is_cuda:
+        r = _native().linear(X, W, RG_FLAG_SYNC if sync else 0)
+        if r is not None:
+            return r
     tx, tw = _TYPES.get(X.dtype), _TYPES.get(W.dtype)
     if tx is None or tw is None or X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1]:
         raise ValueError("linear_f8: X [M, K] and W [N, K] float32, float16 or bfloat16 expected")
@@ -236,16 +242,20 @@ def linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: tor
     """(dX, dW) of linear_f8 for the output's gradient dY [M, N]: dX = dY W with dY quantised along N, in dY's
     dtype, and dW = dY^T X with both quantised along M, in dw_dtype."""
     kept, M, N, K = saved
+    if dY.is_cuda:
+        r = _native().backward(dY, kept, M, N, K, dw_dtype, RG_FLAG_SYNC if sync else 0)
+        if r is not None:
+            return r
     t, tw = _TYPES.get(dY.dtype), _TYPES.get(dw_dtype)
     if t is None or tw is None or dY.shape != (M, N):
         raise ValueError("linear_f8_backward: dY with the output's shape, float32, float16 or bfloat16, expected")
     idx = _device_index("linear_f8_backward", dY, kept)
-    nsaved, need = _linear_bytes(M, N, K)
+    need = _linear_bytes(M, N, K)[1]
     dY, lddy = _rows_of(dY)
     dX = torch.empty((M, K), dtype=dY.dtype, device=dY.device)
     dW = torch.empty((N, K), dtype=dw_dtype, device=dY.device)
     w = _scratch(need, idx)
-    _launch(idx, "linear_f8_backward", library().linear_f8_backward, dY.data_ptr(), t, lddy, kept.data_ptr(), nsaved,
+    _launch(idx, "linear_f8_backward", library().linear_f8_backward, dY.data_ptr(), t, lddy, kept.data_ptr(), kept.numel(),
             dX.data_ptr(), dW.data_ptr(), tw, M, N, K, RG_FLAG_SYNC if sync else 0, w.data_ptr(), w.numel())
     return dX, dW
 

@@ -379,6 +379,36 @@ def test_linear_is_its_parts(rg):  # noqa: F811
     assert torch.equal(dW, rg.scaled_gemm_f8(qdt, sdt, qxt, sxt, transb=True))
 
 
+@pytest.mark.parametrize("dtype,dw", [(torch.bfloat16, torch.float32), (torch.float16, torch.float16),
+                                      (torch.float32, torch.bfloat16)])
+def test_linear_ordinary_call_is_its_parts(rg, dtype, dw):  # noqa: F811
+    """Contiguous tensors, the second call on a warm workspace: the native call path."""
+    x, w, dy = normal((70, 200), 1, 1.0, dtype).cuda(), normal((96, 200), 2).cuda(), normal((70, 96), 3, 0.1, dtype).cuda()
+    qx, sx, qxt, sxt = rg.quantize_f8(x, "both")
+    qw, sw = rg.quantize_f8(w, "tiles")
+    qd, sd, qdt, sdt = rg.quantize_f8(dy, "both")
+    for _ in range(2):
+        Y, saved = rg.linear_f8(x, w)
+        dX, dW = rg.linear_f8_backward(dy, saved, dw_dtype=dw)
+        assert Y.dtype == dX.dtype == dtype and dW.dtype == dw
+        assert torch.equal(Y, rg.scaled_gemm_f8(qx, sx, qw, sw, transb=True, out_dtype=dtype))
+        assert torch.equal(dX, rg.scaled_gemm_f8(qd, sd, qw, sw, out_dtype=dtype))
+        assert torch.equal(dW, rg.scaled_gemm_f8(qdt, sdt, qxt, sxt, transb=True, out_dtype=dw))
+
+
+def test_linear_saved_buffer_is_checked(rg):  # noqa: F811
+    """A buffer shorter than the forward pass made, and a gradient of another shape or type, are refused."""
+    x, w = normal((70, 200), 1).cuda(), normal((96, 200), 2).cuda()
+    Y, (kept, M, N, K) = rg.linear_f8(x, w)
+    with pytest.raises(rg.ResGemmError) as err:
+        rg.linear_f8_backward(Y, (kept[:-256], M, N, K))
+    assert err.value.code == rg.RG_ERR_WORKSPACE
+    for dy, dw in ((Y[:, :-1], torch.float32), (Y[:-1], torch.float32), (Y.double(), torch.float32),
+                   (Y, torch.float64)):
+        with pytest.raises(ValueError):
+            rg.linear_f8_backward(dy, (kept, M, N, K), dw_dtype=dw)
+
+
 def test_linear_empty(rg):  # noqa: F811
     x, w = torch.zeros((0, 40), device="cuda"), torch.ones((30, 40), device="cuda")
     Y, saved = rg.linear_f8(x, w)
