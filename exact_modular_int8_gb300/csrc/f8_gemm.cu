@@ -244,13 +244,14 @@ struct Sums {
 // 8 j + 2 (lane & 3) + {0, 1}, registers 4 j + {2, 3} the same of row lane / 4 + 8, so
 // a lane needs the scales of a quarter of the columns.  With a row to a lane it
 // needs all of them: 32 loads of 16 bytes per block and warp, each filling 512
-// bytes of registers, were a third of the time.  (8192 x 8192 x 4096: 382 us, 425 in
-// the other form.)
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
+// bytes of registers, were a third of the time.  The read of 32 columns is under way
+// during the arithmetic on the 32 before.  (8192 x 8192 x 4096: 365 us, 382 with 64
+// columns read at a time and then added, 425 with a row to a lane.  The other form,
+// with half the arithmetic, gains nothing from smaller reads: 239 us against 236.)
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : RG_R8(0), RG_R8(8), RG_R8(16), RG_R8(24)
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : RG_R8(0), RG_R8(8)
       : "r"(taddr));
 }
 template <int COLS>
@@ -264,26 +265,32 @@ struct Sums<COLS, false> {
   __device__ __forceinline__ void add(uint32_t taddr, const float (&s)[4], const float* sb, F&& release) {
     const uint64_t s2[4] = {pack2(s[0], s[0]), pack2(s[1], s[1]), pack2(s[2], s[2]), pack2(s[3], s[3])};
     const int t4 = threadIdx.x & 3;
+    uint32_t c[2][2][16];  // by chunk of 32 columns: rows 0..15 and 16..31
+    tmem_ld_frag(taddr, c[0][0]);
+    tmem_ld_frag(taddr + (16u << 16), c[0][1]);
 #pragma unroll
-    for (int h = 0; h < COLS / 64; ++h) {
-      uint32_t c[2][32];  // rows 0..15 and 16..31
-      tmem_ld_frag(taddr + 64 * h, c[0]);
-      tmem_ld_frag(taddr + 64 * h + (16u << 16), c[1]);
+    for (int h = 0; h < COLS / 32; ++h) {
+      const int b = h & 1;
+      uint64_t w[4];
       tmem_wait_ld();
-      pin32(c[0]);
-      pin32(c[1]);
-      if (h == COLS / 64 - 1) release();
-      uint64_t w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint64_t*>(sb + 64 * h + 8 * j + 2 * t4);
+      for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(c[b][i >> 4][i & 15]));
+      if (h + 1 < COLS / 32) {
+        tmem_ld_frag(taddr + 32 * (h + 1), c[b ^ 1][0]);
+        tmem_ld_frag(taddr + 32 * (h + 1) + (16u << 16), c[b ^ 1][1]);
+      } else {
+        release();
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint64_t*>(sb + 32 * h + 8 * j + 2 * t4);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            uint64_t& a = acc[2 * q + i][8 * h + j];
-            a = fma2(mul2(pack2u(c[q][4 * j + 2 * i], c[q][4 * j + 2 * i + 1]), s2[2 * q + i]), w[j], a);
+            uint64_t& a = acc[2 * q + i][4 * h + j];
+            a = fma2(mul2(pack2u(c[b][q][4 * j + 2 * i], c[b][q][4 * j + 2 * i + 1]), s2[2 * q + i]), w[j], a);
           }
     }
   }
