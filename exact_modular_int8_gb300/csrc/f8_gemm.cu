@@ -312,6 +312,77 @@ constexpr int SCALE1_BYTES = SCALE_BUFS * (int)sizeof(ScaleChunk<BN1>);
 constexpr int SMEM1_BYTES = 1024 + STAGES1 * STAGE1_BYTES + SCALE1_BYTES + 256;
 static_assert(SMEM1_BYTES <= 232448, "shared memory");
 
+// Four neighbouring entries of C's row from column c of the tile on.
+__device__ __forceinline__ void store4(const Params& gp, long long out, int c, int cols, float4 v) {
+  if (gp.vec_c && c + 4 <= cols) {
+    if (gp.out_type == RG_TYPE_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(gp.C) + out) = v;
+    } else {
+      uint2 w;
+      if (gp.out_type == RG_TYPE_F16) {
+        const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+        w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(gp.C) + out) = w;
+    }
+  } else {
+    const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (c + q < cols) store_out(gp.C, out + q, gp.out_type, e[q]);
+  }
+}
+
+// Rows rank, rank + S, ... of the tile: the slices' sums in rank order.  A warp
+// fetches all of its rows (S = 1: half of them) from every slice before it adds
+// the first, so that the way to another CTA's shared memory, most of a
+// microsecond, is waited for once.  The CTAs part when their reads are done,
+// before their stores to C.
+template <int S>
+__device__ __forceinline__ void join_slices(const Params& gp, uint32_t part, int rank, int tm, int tn, int warp, int lane,
+                                            bool live) {
+  constexpr int WARPS = NUM_THREADS / 32, ROWS = (128 / S + WARPS - 1) / WARPS, R = S == 1 ? (ROWS + 1) / 2 : ROWS;
+  const int rows = min(128, gp.M - tm * 128), cols = min(BN1, gp.N - tn * BN1);
+  const int c = 4 * lane;  // this lane's columns
+#pragma unroll
+  for (int i0 = 0; i0 < ROWS; i0 += R) {
+    float4 v[S][R];
+#pragma unroll
+    for (int k = 0; k < S; ++k)
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int r = rank + S * (warp + WARPS * (i0 + i));
+        v[k][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (live && r < rows && c < cols) {
+          const uint32_t at = part + (uint32_t)(r * PART_LD + c) * 4;
+          v[k][i] = ld_cluster4(S == 1 ? at : mapa_shared(at, (uint32_t)k));
+        }
+      }
+#pragma unroll
+    for (int k = 1; k < S; ++k)
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        v[0][i].x += v[k][i].x;
+        v[0][i].y += v[k][i].y;
+        v[0][i].z += v[k][i].z;
+        v[0][i].w += v[k][i].w;
+      }
+    __syncwarp();
+    if (S > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int r = rank + S * (warp + WARPS * (i0 + i));
+      if (live && r < rows && c < cols)
+        store4(gp, (long long)(tm * 128 + r) * gp.ldc + (long long)tn * BN1 + c, c, cols, v[0][i]);
+    }
+  }
+  __syncwarp();
+  if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 template <bool B_KMAJOR, bool TILE_B>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     f8_gemm_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -507,53 +578,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
   if (S > 1) cluster_sync();
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
                  "r"((uint32_t)(2 * BN1)));
   }
-  // rows rank, rank + S, ... of the tile: the slices' sums in rank order
-  if (!*abort_flag) {
-    const int rows = min(128, gp.M - tm * 128), cols = min(BN1, gp.N - tn * BN1);
-    const uint32_t base = smem_u32(stage_base);
-    const int c = 4 * lane;  // this lane's columns
-    for (int r = rank + S * warp; r < rows && c < cols; r += S * (NUM_THREADS / 32)) {
-      const uint32_t at = base + (uint32_t)(r * PART_LD + c) * 4;
-      float4 v = ld_cluster4(mapa_shared(at, 0));
-#pragma unroll 4
-      for (int k = 1; k < S; ++k) {
-        const float4 u = ld_cluster4(mapa_shared(at, (uint32_t)k));
-        v.x += u.x;
-        v.y += u.y;
-        v.z += u.z;
-        v.w += u.w;
-      }
-      const long long out = (long long)(tm * 128 + r) * gp.ldc + (long long)tn * BN1 + c;
-      if (gp.vec_c && c + 4 <= cols) {
-        if (gp.out_type == RG_TYPE_F32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(gp.C) + out) = v;
-        } else {
-          uint2 w;
-          if (gp.out_type == RG_TYPE_F16) {
-            const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-            w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-          } else {
-            const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-            w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-          }
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(gp.C) + out) = w;
-        }
-      } else {
-        const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (c + q < cols) store_out(gp.C, out + q, gp.out_type, e[q]);
-      }
-    }
-  }
-  if (S > 1) cluster_sync();  // no CTA leaves while another reads its slice
+  const bool live = !*abort_flag;
+  const uint32_t part = smem_u32(stage_base);
+  if (S == 1) join_slices<1>(gp, part, rank, tm, tn, warp, lane, live);
+  else if (S == 2) join_slices<2>(gp, part, rank, tm, tn, warp, lane, live);
+  else if (S == 4) join_slices<4>(gp, part, rank, tm, tn, warp, lane, live);
+  else join_slices<8>(gp, part, rank, tm, tn, warp, lane, live);
 }
 
 // ---------------------------------------------------------------------------
