@@ -300,8 +300,9 @@ struct Sums<COLS, false> {
 // Tiles of 128 x 128, one per cluster of S CTAs: each CTA sums a slice of K,
 // and the slices are joined through distributed shared memory in rank order.
 // For products that one wave of CTAs holds, where the time is the latency of
-// set-up, K / S / 128 blocks of 0.3 us and the join: 512 x 4096 x 4096 15.2 us,
-// 128 x 4096 x 4096 (S = 4) 9.4 us, 1000 x 1544 x 2056 11.7 us.
+// set-up, K / S / 128 blocks of 0.3 us and the join: 512 x 4096 x 4096 12.7 us,
+// 128 x 4096 x 4096 (S = 4) 7.9 us, 1000 x 1544 x 2056 10.1 us, one after another
+// (13.8, 8.2 and 10.7 with a row of the join at a time).
 // ---------------------------------------------------------------------------
 constexpr int BN1 = 128;
 constexpr int STAGES1 = 6;
@@ -1097,8 +1098,11 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
     return cudaLaunchKernelEx(&cfg, kPairKernels[a.b_kmajor][a.tile_b], ma, mb, mc, p, plan);
   }
   const long long tiles = (long long)p.mt * p.nt;
+  // Slices of K while the grid has room, of at least four blocks: a slice of two
+  // saves less than its join costs (512 x 1024 x 1024 in four slices 6.0 us, in two
+  // 5.85; 1024 x 1024 x 512 in two 6.35, whole 5.9).
   int S = 1;
-  while (S < 8 && tiles * S * 2 <= fd.sms && p.KB >= 4 * S) S *= 2;
+  while (S < 8 && tiles * S * 2 <= fd.sms && p.KB >= 8 * S) S *= 2;
   cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(tiles * S)), NUM_THREADS, SMEM1_BYTES, st, S, attr);
   return cudaLaunchKernelEx(&cfg, kTileKernels[a.b_kmajor][a.tile_b], ma, mb, p, S, plan);
 }
