@@ -21,7 +21,7 @@
 // (relative 2^-11 per entry, an eighth of a bf16 result's rounding).  Each
 // 128-block's sum is scaled in fp32 and added to fp32 sums.
 //
-// 64 tokens through 128 experts of 4096 x 1024 (top 8): 292 us, the weights at
+// 64 tokens through 128 experts of 4096 x 1024 (top 8): 295 us, the weights at
 // the copy rate 237; the two products stream at 6.3 TB/s, and the grid's meetings
 // wait for the slowest SM, 10% behind the median.  One token through 8 of 64
 // experts of 2048 x 1024: 28 us (7.6): router 4, routing 1.5, first product 9,
@@ -278,6 +278,7 @@ struct Routing {
   int counts[kMaxE];
   int units[kMaxE + 1];          // of a product phase: first unit of each active expert
   int num_active;
+  int first_active;              // of a product phase: the active expert of this CTA's first unit
   int go;                        // the grid's barrier was passed
 };
 
@@ -396,11 +397,18 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   return v;
 }
 
+// The units of one pass over one expert, as far as they are this CTA's.
+struct Segment {
+  int base, end;  // unit of row block 0, and the one after the segment's last
+  int first, n;   // tokens of the order,
+  int c0;         // staged in columns c0 onwards
+};
 // Shared memory: this, then the warps' partial sums, the staged tokens and the
 // rings of weight pieces, laid out by the host for the call's shape.
 struct Smem {
   Routing r;
   float col_scale[8 * kMaxNT];   // of the staged columns: takes a sum back from the operand's power of two
+  Segment segs[8 * kMaxNT];      // the staged segments
 };
 constexpr int kFixedBytes = ((int)sizeof(Smem) + 127) / 128 * 128;
 // the widest layer: three pieces per warp, one column tile, one token
@@ -462,9 +470,12 @@ struct Phase {
     const long long total = r.units[r.num_active];
     u0 = (int)(total * cta / ctas);
     u1 = (int)(total * (cta + 1) / ctas);
+    for (int a = threadIdx.x; a < r.num_active; a += kThreads)
+      if (r.units[a] <= u0 && u0 < r.units[a + 1]) r.first_active = a;
+    __syncthreads();
     pu = u0 + group;
     pkb = kpart;
-    pa = 0;
+    pa = u0 < u1 ? r.first_active : 0;
     if (pu < u1) point_expert();
   }
 
@@ -550,11 +561,12 @@ struct Phase {
 
   __device__ int stride() const { return nkb * 256 + 16; }  // bytes per staged token: conflict-free for the lanes' loads
 
-  // The operand of tokens [first, first + n) of the order: fp16 scaled by the power
-  // of two that col_scale undoes, zeros past K.  A warp makes a token's row.
-  __device__ void stage(int first, int n) {
-    for (int c = warp; c < n; c += kWarps) {
-      const int s = sm.r.order[first + c];
+  // The operand of tokens [first, first + n) of the order in columns c0 onwards:
+  // fp16 scaled by the power of two that col_scale undoes, zeros past K.  A warp
+  // makes a token's row.
+  __device__ void stage(int first, int n, int c0) {
+    for (int c = c0 + ((warp - c0) & (kWarps - 1)); c < c0 + n; c += kWarps) {
+      const int s = sm.r.order[first + c - c0];
       uint8_t* out = cols + c * stride();
       if constexpr (UP) {
         const long long at = (long long)(s / p.top_k) * K;
@@ -605,14 +617,16 @@ struct Phase {
     }
   }
 
-  // Column c's sums of row pair `row` of row block rb, by whole warps; the lanes
-  // that differ in the bits of `lanes` hold the rows of one column.
-  __device__ __forceinline__ void store(int rb, int row, int first, int c, bool live, float lo, float hi, int lanes) {
+  // Token first + c's sums (staged column c0 + c) of row pair `row` of row block rb,
+  // by whole warps; the lanes that differ in the bits of `lanes` hold the rows of
+  // one token.
+  __device__ __forceinline__ void store(int rb, int row, int first, int c0, int c, bool live, float lo, float hi,
+                                        int lanes) {
     const int s = live ? sm.r.order[first + c] : 0;
     if constexpr (UP) {
       uint32_t m = 0;
       if (live) {
-        const float a = lo * sm.col_scale[c], u = hi * sm.col_scale[c];
+        const float a = lo * sm.col_scale[c0 + c], u = hi * sm.col_scale[c0 + c];
         const float h = a / (1.0f + expf(-a)) * u;
         p.w.h[(long long)s * p.I + rb * 8 + row] = h;
         m = __float_as_uint(h) & 0x7FFFFFFFu;
@@ -625,23 +639,28 @@ struct Phase {
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4 * lanes));
       if (live && row == 0) atomicMax(&p.w.h_max[s * kMaxStride], m);
     } else if (live) {
-      const float back = sm.col_scale[c];
+      const float back = sm.col_scale[c0 + c];
       float* out = p.w.part + (long long)s * p.H + rb * 16 + row;
       out[0] = lo * back;
       out[8] = hi * back;
     }
   }
 
-  // One unit: row block rb of the pass over tokens [first, first + n).
+  // One unit, of staged segment q.  (What the segment is is read where it is used:
+  // the loop over k has no registers for it.)
   template <int NT>
-  __device__ void unit(int rb, int first, int n) {
+  __device__ void unit(int q, int at) {
+    const volatile Segment& seg = sm.segs[q];
     float tot[NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) tot[i][0] = tot[i][1] = tot[i][2] = tot[i][3] = 0.0f;
     // columns past the last repeat it and are not stored
     uint32_t col[NT];
+    {
+      const int n = seg.n, c0 = seg.c0;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) col[i] = su32(cols) + min(i * 8 + g, n - 1) * stride() + t4 * 32;
+    for (int i = 0; i < NT; ++i) col[i] = su32(cols) + (c0 + min(i * 8 + g, n - 1)) * stride() + t4 * 32;
+    }
     for (int kb = kpart; kb < nkb; kb += ks) {
       wait_oldest();
       __syncwarp();
@@ -688,61 +707,87 @@ struct Phase {
       copy_next(slot == 0 ? p.ring - 1 : slot - 1);
       slot = slot + 1 == p.ring ? 0 : slot + 1;
     }
+    const int rb = at - seg.base, first = seg.first, n = seg.n, c0 = seg.c0;
     if (ks == 1) {
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-        {
+        for (int j = 0; j < 2; ++j) {
           const int c = i * 8 + 2 * t4 + j;
-          store(rb, g, first, c, c < n, tot[i][j], tot[i][2 + j], 4);
+          store(rb, g, first, c0, c, c < n, tot[i][j], tot[i][2 + j], 4);
         }
       return;
     }
     // units alternate between two halves of the buffer, so that one meeting of the
-    // group per unit is enough (a segment's units all have the same NT, and the
-    // block meets between segments)
+    // group per unit is enough
     const int ld = p.red_ld;
-    float* part = red + (size_t)group * ks * 16 * ld + parity * (8 * NT);
+    float* part = red + (size_t)group * ks * 16 * ld + parity * ((ld - 4) / 2);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       *reinterpret_cast<float2*>(&part[(kpart * 16 + g) * ld + i * 8 + 2 * t4]) = make_float2(tot[i][0], tot[i][1]);
       *reinterpret_cast<float2*>(&part[(kpart * 16 + g + 8) * ld + i * 8 + 2 * t4]) = make_float2(tot[i][2], tot[i][3]);
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(ks * 32) : "memory");
-    for (int c0 = kpart * 4; c0 < n; c0 += ks * 4) {  // four columns of eight row pairs per warp
-      const int c = c0 + (lane >> 3), row = lane & 7;
+    for (int c1 = kpart * 4; c1 < n; c1 += ks * 4) {  // four tokens' eight row pairs per warp
+      const int c = c1 + (lane >> 3), row = lane & 7;
       float lo = 0.0f, hi = 0.0f;
       if (c < n)
         for (int w = 0; w < ks; ++w) {
           lo += part[(w * 16 + row) * ld + c];
           hi += part[(w * 16 + row + 8) * ld + c];
         }
-      store(rb, row, first, c, c < n, lo, hi, 1);
+      store(rb, row, first, c0, c, c < n, lo, hi, 1);
     }
     parity ^= 1;
   }
 
+  // The segment of unit `at` (of active expert a or a later one, which a becomes).
+  __device__ __forceinline__ Segment segment(int at, int& a) const {
+    const Routing& r = sm.r;
+    while (at >= r.units[a + 1]) ++a;
+    const int pass = (at - r.units[a]) / rows_per_expert, e = r.active[a];
+    Segment s;
+    s.base = r.units[a] + pass * rows_per_expert;
+    s.end = min(s.base + rows_per_expert, u1);
+    s.first = r.start[e] + pass * cap();
+    s.n = min(r.counts[e] - pass * cap(), cap());
+    s.c0 = 0;
+    return s;
+  }
+
   template <typename F>
   __device__ bool run(int cta, int ctas, F&& before_use) {
-    Routing& r = sm.r;
     plan_units(cta, ctas);
     slot = 0;
     for (int s = 0; s < p.ring - 1; ++s) copy_next(s);
     if (!before_use()) return false;
-    int a = 0, mine = u0 + group;
-    for (int at = u0; at < u1;) {  // segments: the units of one pass over one expert
-      while (at >= r.units[a + 1]) ++a;
-      const int pass = (at - r.units[a]) / rows_per_expert, base = r.units[a] + pass * rows_per_expert;
-      const int end = min(base + rows_per_expert, u1);
-      const int e = r.active[a], first = r.start[e] + pass * cap(), n = min(r.counts[e] - pass * cap(), cap());
+    // Segments whose tokens fit into the staged columns together are staged together:
+    // a CTA that meets the border between two experts would otherwise do one part
+    // after the other, and the grid waits for it (7 tokens, 2 of 16 experts of 1808 x
+    // 1552: 39 us, 47 one after the other; 16 tokens, 4 of 64 of 4096 x 1024: 111 and
+    // 117; 64 tokens, 8 of 128: 295 and 289).
+    int mine = u0 + group;
+    for (int at = u0, a = u0 < u1 ? sm.r.first_active : 0; at < u1;) {
       __syncthreads();
-      stage(first, n);
+      int end = at, used = 0;
+      int k = 0;
+      while (end < u1) {
+        Segment g1 = segment(end, a);
+        if (used && used + g1.n > cap()) break;
+        g1.c0 = used;
+        if (threadIdx.x == 0) sm.segs[k] = g1;
+        stage(g1.first, g1.n, used);
+        used += g1.n;
+        end = g1.end;
+        ++k;
+      }
       __syncthreads();
-      for (; mine < end; mine += groups) {
-        const int rb = mine - base;
-        if (n <= 8) unit<1>(rb, first, n);
-        else unit<kMaxNT>(rb, first, n);
+      for (int q = 0; q < k; ++q) {
+        const int last = sm.segs[q].end;
+        for (; mine < last; mine += groups) {
+          if (sm.segs[q].n <= 8) unit<1>(q, mine);
+          else unit<kMaxNT>(q, mine);
+        }
       }
       at = end;
     }
