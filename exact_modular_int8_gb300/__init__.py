@@ -13,6 +13,11 @@ Entry points (same names as the C ABI):
   res_gemm_limbs(A, B, lc)       exact multi-limb product
   enclose_gemm_f64(A, B)         (lo, hi) with lo <= A @ B <= hi exactly
   res_gemm_stage(RA, RB, ...)    the per-prime tensor-core stage alone
+8-bit block-scaled operators (f8.py):
+  quantize_f8(X, form)           E4M3 values with a scale per 128 entries or per 128 x 128 tile
+  scaled_gemm_f8(A, SA, B, SB)   product of two of them
+  linear_f8, linear_f8_backward  a linear layer's three products, quantised inside
+  moe_layer_f8(X, WR, ...)       a mixture-of-experts layer for up to 64 tokens
 Helpers: width_ulps, digest, get_plan, workspace_bytes.
 """
 from __future__ import annotations
