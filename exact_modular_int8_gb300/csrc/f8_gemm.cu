@@ -999,6 +999,7 @@ constexpr PairKernel kPairKernels[2][2] = {{f8_gemm_pair_kernel<false, false>, f
 
 struct F8Device {
   int sms = 0, max_pairs = 0;
+  int max_slices[4] = {};  // clusters of 1, 2, 4, 8 CTAs of the one-wave kernel that are resident together
 };
 cudaError_t f8_device(int dev, F8Device& out) {
   static std::mutex mu;
@@ -1020,15 +1021,23 @@ cudaError_t f8_device(int dev, F8Device& out) {
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM2_BYTES);
         if (e != cudaSuccess) return e;
       }
-    // not every SM can be paired within its GPC
+    // not every SM can be paired, or put into a larger cluster, within its GPC
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(sms & ~1)), NUM_THREADS, SMEM2_BYTES, nullptr, 2, attr);
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kPairKernels[1][1], &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();  // the query's own failure is not the call's
-      n = sms / 2;
-    }
-    d.max_pairs = n;
+    auto resident = [&](const void* kernel, int smem, int cluster) {
+      const int ctas = sms / cluster * cluster;
+      cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)ctas), NUM_THREADS, smem, nullptr, cluster, attr);
+      int n = 0;
+      if (ctas == 0) return 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();  // the query's own failure is not the call's
+        n = sms / cluster;
+      }
+      return n;
+    };
+    d.max_pairs = resident(reinterpret_cast<const void*>(kPairKernels[1][1]), SMEM2_BYTES, 2);
+    d.max_slices[0] = sms;
+    for (int i = 1; i < 4; ++i)
+      d.max_slices[i] = resident(reinterpret_cast<const void*>(kTileKernels[1][1]), SMEM1_BYTES, 1 << i);
     d.sms = sms;
   }
   out = d;
@@ -1041,10 +1050,11 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
                            unsigned long long wait_ns) {
   const int variant = gemm_variant();
   // Few rows: up to 16 the warp-level kernel is faster at every size measured
-  // (8192 x 4096: 9.3 us for one row, 11.7 for 16, against 13.5 with padded tiles);
-  // from 17 to 32 while B is small enough for latency to count (24 rows: 2.7
-  // against 5.6 us at 1024 x 1024, 17.8 against 13.4 at 8192 x 4096).
-  if (variant == 0 && a.b_kmajor && (a.M <= 16 || (a.M <= kSkinnyRows && a.N * a.K <= (1LL << 24))))
+  // (8192 x 4096: 8.1 us for one row, 10.3 for 16, against 12.5 and 11.4 with padded
+  // tiles); from 17 to 32 while B is small enough for latency to count (24 rows:
+  // 3.3 against 4.7 us at 2048 x 2048, 5.4 against 5.7 at 4096 x 2048, 9.2 against
+  // 7.1 at 4096 x 4096).
+  if (variant == 0 && a.b_kmajor && (a.M <= 16 || (a.M <= kSkinnyRows && a.N * a.K <= (1LL << 22))))
     return launch_f8_skinny(a, plan, st);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1075,8 +1085,8 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
   const long long tiles2 = ((a.M + 255) / 256) * ((a.N + BN2 - 1) / BN2);
   // Tiles of 128 x 128 while one wave of CTAs holds them all, split along K where
   // that leaves SMs idle; beyond that the pair kernel's tiles.  (4096 columns, K =
-  // 4096: 512 rows, 128 tiles, 15.2 against the pairs' 20.6 us; 768 rows, 192
-  // tiles, 27.8 against 20.9 us.)
+  // 4096: 512 rows, 128 tiles, 12.9 against the pairs' 19.3 us; 640 rows, 160
+  // tiles, 24.8 against 19.9 us.)
   const bool pair = variant == 2 || (variant == 0 && (long long)p.mt * p.nt > fd.sms);
   const uint32_t b_cols = pair ? 64 : 128;  // columns of B per copy
   CUtensorMap ma, mb;
@@ -1098,11 +1108,13 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
     return cudaLaunchKernelEx(&cfg, kPairKernels[a.b_kmajor][a.tile_b], ma, mb, mc, p, plan);
   }
   const long long tiles = (long long)p.mt * p.nt;
-  // Slices of K while the grid has room, of at least four blocks: a slice of two
-  // saves less than its join costs (512 x 1024 x 1024 in four slices 6.0 us, in two
-  // 5.85; 1024 x 1024 x 512 in two 6.35, whole 5.9).
+  // Slices of K while all clusters are resident together (128 x 2048 x 4096: 13.5 us
+  // in 16 clusters of eight, some of which wait for others to end, 7.4 in fours), of
+  // at least four blocks: a slice of two saves less than its join costs (512 x 1024
+  // x 1024 in four slices 6.0 us, in two 5.85; 1024 x 1024 x 512 in two 6.35, whole
+  // 5.9).
   int S = 1;
-  while (S < 8 && tiles * S * 2 <= fd.sms && p.KB >= 8 * S) S *= 2;
+  for (int i = 1; i < 4 && tiles <= fd.max_slices[i] && p.KB >= 8 * S; ++i) S *= 2;
   cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(tiles * S)), NUM_THREADS, SMEM1_BYTES, st, S, attr);
   return cudaLaunchKernelEx(&cfg, kTileKernels[a.b_kmajor][a.tile_b], ma, mb, p, S, plan);
 }

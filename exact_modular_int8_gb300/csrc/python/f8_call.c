@@ -3,8 +3,8 @@
  * and linear_f8 with its backward pass (include/resgemm.h).
  *
  * A small call's time is its time on the host, and much of that was spent on
- * marshalling: 5 of a product's 13 us in the interpreter and ctypes, 4 of the
- * 16 that each pass of a linear layer took.  These functions take the tensors
+ * marshalling: 5 of a product's or a quantisation's 13 us in the interpreter and
+ * ctypes, 4 of the 16 that each pass of a linear layer took.  These functions take the tensors
  * of an ordinary call -- the current device's, rows contiguous and aligned,
  * shapes that agree -- allocate the results and call the library.  For
  * anything else they return None, and the caller's Python code checks, copies
@@ -32,9 +32,9 @@ static gemm_fn lib_gemm;
 static linear_fn lib_linear;
 static backward_fn lib_backward;
 static bytes_fn lib_saved_bytes, lib_ws_bytes;
-static PyObject *types[3], *f8_type, *byte_type;         /* torch dtypes by RG_TYPE_*, float8_e4m3fn, uint8 */
-static PyObject *empty, *raw_stream, *current_device;    /* torch functions */
-static PyObject *workspaces, *raise_status;              /* the binding's workspace cache and error function */
+static PyObject *types[3], *f8_type, *byte_type;                       /* torch dtypes by RG_TYPE_*, E4M3, uint8 */
+static PyObject *empty, *empty_strided, *raw_stream, *current_device;  /* torch functions */
+static PyObject *workspaces, *raise_status;  /* the binding's workspace cache and error function */
 static PyObject *s_shape, *s_stride, *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_numel, *empty_names;
 
 static int64_t blocks(int64_t x) { return (x + 127) / 128; }
@@ -157,41 +157,68 @@ static PyObject* finish(int rc, const char* where, PyObject* result) {
   return NULL;
 }
 
-/* quantize(X, form, flags) -> (Q, S) or, transposed, (QT, ST); None to decline */
+/* An E4M3 matrix with rows on 16-byte boundaries, and its scales; 0 with an exception set on failure. */
+typedef struct {
+  PyObject *q, *s;
+  void *qp, *sp;
+  int64_t ld;
+} quantised;
+static int new_quantised(int64_t m, int64_t k, int64_t scale_rows, PyObject* device, quantised* r) {
+  r->ld = up16(k);
+  r->s = NULL;
+  if (r->ld == k) {
+    r->q = new_matrix(m, k, f8_type, device);
+  } else {
+    PyObject* args[4] = {Py_BuildValue("(LL)", (long long)m, (long long)k),
+                         Py_BuildValue("(LL)", (long long)r->ld, 1LL), f8_type, device};
+    r->q = args[0] && args[1] ? PyObject_Vectorcall(empty_strided, args, 2, empty_names) : NULL;
+    Py_XDECREF(args[0]);
+    Py_XDECREF(args[1]);
+  }
+  if (!r->q) return 0;
+  r->qp = data_of(r->q);
+  r->s = new_matrix(scale_rows, blocks(k), types[RG_TYPE_F32], device);
+  if (r->s) r->sp = data_of(r->s);
+  if (r->s && !PyErr_Occurred()) return 1;
+  Py_CLEAR(r->q);
+  Py_CLEAR(r->s);
+  return 0;
+}
+
+/* quantize(X, form, flags) -> (Q, S), (QT, ST) or all four; None to decline */
 static PyObject* quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   if (n != 3) return decline();
   const long form = PyLong_AsLong(a[1]), flags = PyLong_AsLong(a[2]);
   int64_t dev;
   void* stream;
-  matrix x, q, s;
-  if (PyErr_Occurred() || form == RG_F8_BOTH || !place(a[0], &dev, &stream)) return decline();
+  matrix x;
+  if (PyErr_Occurred() || !place(a[0], &dev, &stream)) return decline();
   const int t = real_of(a[0], dev, &x);
   if (t < 0) return decline();
-  const int turned = form == RG_F8_COLUMNS;
-  q.m = turned ? x.k : x.m;
-  q.k = turned ? x.m : x.k;
-  if (q.k & 15) return decline(); /* padded rows are a view */
   PyObject* device = PyObject_GetAttr(a[0], s_device);
   if (!device) return decline();
-  PyObject* Q = new_matrix(q.m, q.k, f8_type, device);
-  PyObject* S = Q ? new_matrix(form == RG_F8_TILES ? blocks(q.m) : q.m, blocks(q.k), types[RG_TYPE_F32], device) : NULL;
+  quantised d = {0}, c = {0}; /* along rows (or in tiles), along columns */
+  const int direct = form != RG_F8_COLUMNS, turned = form == RG_F8_COLUMNS || form == RG_F8_BOTH;
+  int ok = !direct || new_quantised(x.m, x.k, form == RG_F8_TILES ? blocks(x.m) : x.m, device, &d);
+  ok = ok && (!turned || new_quantised(x.k, x.m, x.k, device, &c));
   Py_DECREF(device);
-  if (!S) {
-    Py_XDECREF(Q);
-    return NULL;
+  PyObject* r = NULL;
+  if (ok) {
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = lib_quantize(x.p, t, x.ld, x.m, x.k, (int)form, d.qp, d.ld, d.sp, c.qp, c.ld, c.sp, (unsigned)flags, stream);
+    Py_END_ALLOW_THREADS
+    r = direct && turned ? PyTuple_Pack(4, d.q, d.s, c.q, c.s)
+        : direct         ? PyTuple_Pack(2, d.q, d.s)
+                         : PyTuple_Pack(2, c.q, c.s);
+    if (r) r = finish(rc, "quantize_f8", r);
   }
-  q.p = data_of(Q);
-  s.p = data_of(S);
-  int rc;
-  Py_BEGIN_ALLOW_THREADS
-  rc = turned ? lib_quantize(x.p, t, x.ld, x.m, x.k, (int)form, NULL, 0, NULL, q.p, q.k, s.p, (unsigned)flags, stream)
-              : lib_quantize(x.p, t, x.ld, x.m, x.k, (int)form, q.p, q.k, s.p, NULL, 0, NULL, (unsigned)flags, stream);
-  Py_END_ALLOW_THREADS
-  PyObject* r = PyTuple_Pack(2, Q, S);
-  Py_DECREF(Q);
-  Py_DECREF(S);
-  return r ? finish(rc, "quantize_f8", r) : NULL;
+  Py_XDECREF(d.q);
+  Py_XDECREF(d.s);
+  Py_XDECREF(c.q);
+  Py_XDECREF(c.s);
+  return r;
 }
 
 /* gemm(A, SA, B, SB, out_dtype, transb, flags) -> C; None to decline */
@@ -298,13 +325,14 @@ static PyObject* backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return r ? finish(rc, "linear_f8_backward", r) : NULL;
 }
 
-/* setup((six addresses), (f32, f16, bf16), f8, uint8, empty, raw_stream, current_device, workspaces, raise) */
+/* setup((six addresses), (f32, f16, bf16), f8, uint8, empty, empty_strided, raw_stream, current_device, workspaces,
+ * raise) */
 static PyObject* setup(PyObject* self, PyObject* args) {
   (void)self;
   unsigned long long f[6];
   PyObject *t0, *t1, *t2;
-  if (!PyArg_ParseTuple(args, "(KKKKKK)(OOO)OOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &t0, &t1, &t2, &f8_type,
-                        &byte_type, &empty, &raw_stream, &current_device, &workspaces, &raise_status))
+  if (!PyArg_ParseTuple(args, "(KKKKKK)(OOO)OOOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &t0, &t1, &t2, &f8_type,
+                        &byte_type, &empty, &empty_strided, &raw_stream, &current_device, &workspaces, &raise_status))
     return NULL;
   lib_quantize = (quantize_fn)(uintptr_t)f[0];
   lib_gemm = (gemm_fn)(uintptr_t)f[1];
@@ -315,7 +343,8 @@ static PyObject* setup(PyObject* self, PyObject* args) {
   types[RG_TYPE_F32] = t0;
   types[RG_TYPE_F16] = t1;
   types[RG_TYPE_BF16] = t2;
-  PyObject* keep[] = {t0, t1, t2, f8_type, byte_type, empty, raw_stream, current_device, workspaces, raise_status};
+  PyObject* keep[] = {t0,         t1,         t2,         f8_type,        byte_type,  empty, empty_strided,
+                      raw_stream, current_device, workspaces, raise_status};
   for (size_t i = 0; i < sizeof keep / sizeof *keep; ++i) Py_INCREF(keep[i]); /* for the life of the process */
   s_shape = PyUnicode_InternFromString("shape");
   s_stride = PyUnicode_InternFromString("stride");

@@ -3,7 +3,7 @@
 The format: E4M3 values (``torch.float8_e4m3fn``) with one float32 scale for every 128 values along the
 contraction, or for every 128 x 128 tile of a weight matrix; an entry stands for value * scale.  Argument
 marshalling only, as in the rest of the binding: every step runs in the library's kernels on the current
-stream.  Quantised matrices are views whose rows start on 16-byte boundaries, which is what the product
+stream.  Quantised matrices have rows that start on 16-byte boundaries, which is what the product
 reads; operands from elsewhere that do not are copied into such rows first.
 
 With sync=False a call only enqueues its work, and errors found on the device are read with status().
@@ -41,10 +41,11 @@ def _native():
         m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("f8_call", path, loader=loader))
         loader.exec_module(m)
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
-        entries = (lib.quantize_f8, lib.scaled_gemm_f8, lib.linear_f8, lib.linear_f8_backward, lib.linear_f8_saved_bytes,
-                   lib.linear_f8_ws_bytes)
+        entries = (lib.quantize_f8, lib.scaled_gemm_f8, lib.linear_f8, lib.linear_f8_backward,
+                   lib.linear_f8_saved_bytes, lib.linear_f8_ws_bytes)
         m.setup(tuple(address(f) for f in entries), (torch.float32, torch.float16, torch.bfloat16), F8, torch.uint8,
-                torch.empty, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache, _check)
+                torch.empty, torch.empty_strided, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache,
+                _check)
         _call = m
     return _call
 
@@ -86,9 +87,7 @@ def _scratch(nbytes: int, idx: int) -> torch.Tensor:
 
 def _empty_rows(m: int, k: int, device) -> torch.Tensor:
     """[m, k] E4M3 with rows on 16-byte boundaries."""
-    ld = (k + 15) & ~15
-    q = torch.empty((m, ld), dtype=F8, device=device)
-    return q if ld == k else q[:, :k]
+    return torch.empty_strided((m, k), ((k + 15) & ~15, 1), dtype=F8, device=device)
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -125,7 +124,7 @@ def quantize_f8(X: torch.Tensor, form: str = "rows", sync: bool = True):
     f = _FORMS.get(form)
     if f is None:
         raise ValueError(f"quantize_f8: form must be one of {', '.join(_FORMS)}")
-    if X.is_cuda and f != RG_F8_BOTH:
+    if X.is_cuda:
         r = _native().quantize(X, f, RG_FLAG_SYNC if sync else 0)
         if r is not None:
             return r
@@ -255,8 +254,9 @@ def linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: tor
     dX = torch.empty((M, K), dtype=dY.dtype, device=dY.device)
     dW = torch.empty((N, K), dtype=dw_dtype, device=dY.device)
     w = _scratch(need, idx)
-    _launch(idx, "linear_f8_backward", library().linear_f8_backward, dY.data_ptr(), t, lddy, kept.data_ptr(), kept.numel(),
-            dX.data_ptr(), dW.data_ptr(), tw, M, N, K, RG_FLAG_SYNC if sync else 0, w.data_ptr(), w.numel())
+    _launch(idx, "linear_f8_backward", library().linear_f8_backward, dY.data_ptr(), t, lddy, kept.data_ptr(),
+            kept.numel(), dX.data_ptr(), dW.data_ptr(), tw, M, N, K, RG_FLAG_SYNC if sync else 0, w.data_ptr(),
+            w.numel())
     return dX, dW
 
 
