@@ -608,11 +608,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // interleave.
 //
 // 8192 x 8192 x 4096: 239 us, 2300 TFLOP/s, half of the E4M3 instruction rate (the
-// tensor pipe is active 46% of the time).  A block of a tile takes 1000 cycles
-// where its MMAs take 512: the epilogue warp's own chain of wait (about 150),
-// read-back (130), multiply-adds (170), store (100, spread over the blocks) and
-// barriers.  More epilogue warps (16: spills, 293 us), 256 x 192 tiles with
-// twelve warps (271 us) and single-CTA 128 x 192 tiles (261 us) were slower.
+// tensor pipe is active 46% of the time).  A block of a tile takes 1050 cycles
+// where its MMAs take 512 and the same loop with an empty epilogue 720: an
+// epilogue warp waits for 165, has read its columns 440 later and needs the rest
+// for the multiply-adds and a share of the stores, with two warps to a scheduler.
+// More epilogue warps (16: spills, 293 us), 256 x 192 tiles with twelve warps (271
+// us) and single-CTA 128 x 192 tiles (261 us) were slower; one 256-column MMA for
+// both halves took the same time.  With a scale for each of B's rows: 365 us, 1535
+// cycles a block; 2048 x 4096 x 8100 106 us.
 //
 // The block is launched with 168 registers a thread; the first warpgroup
 // (producer, MMA issue, scales) gives up 112 of them and the two epilogue
