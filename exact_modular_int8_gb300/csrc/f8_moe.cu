@@ -17,15 +17,18 @@
 // enter as fp16 scaled by a power of two per row (their largest magnitude in
 // [2^14, 2^15)): exact for bf16 and fp16 entries within 2^-28 of the row's
 // largest, off by at most 2^-39 of it below.  The gated product h is kept in
-// fp32 and rounded to fp16 the same way when it enters the second product
-// (relative 2^-11 per entry, an eighth of a bf16 result's rounding).  Each
-// 128-block's sum is scaled in fp32 and added to fp32 sums.
+// fp32 and enters the second product, scaled the same way, as the sum of two
+// fp16 terms: h to 11 bits and what that leaves out.  Together they are within
+// 2^-23 of the entry or 2^-39 of the row's largest, as fp32 is, for twice that
+// product's MMAs (with the first term alone, 11 bits, 64 tokens take 311 us
+// instead of 317 and one token 28.7 instead of 30.1).  Each 128-block's sum is
+// scaled in fp32 and added to fp32 sums.
 //
-// 64 tokens through 128 experts of 4096 x 1024 (top 8): 295 us, the weights at
+// 64 tokens through 128 experts of 4096 x 1024 (top 8): 317 us, the weights at
 // the copy rate 237; the two products stream at 6.3 TB/s, and the grid's meetings
 // wait for the slowest SM, 10% behind the median.  One token through 8 of 64
-// experts of 2048 x 1024: 28 us (7.6): router 4, routing 1.5, first product 9,
-// second 4, two meetings of the grid 2 each, sum 1, launches.
+// experts of 2048 x 1024: 30 us (7.6): router 4, routing 1.5, first product 9,
+// second 5, two meetings of the grid 4 and 1.5, sum 1, launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -52,6 +55,7 @@ constexpr int kSlots = kMaxT * kMaxK;
 // get more than 16 tokens)
 constexpr int kMaxNT = 2;
 constexpr int kMinRing = 3, kMaxRing = 8;  // weight pieces (16 rows x 128 k) per warp, on their way or in use
+constexpr int kTightRing = 2;              // where one token's operands leave no room for kMinRing
 constexpr int kPiece = 16 * 128 + 16;      // and the two scales of its rows
 constexpr int kMaxStride = 32;             // words between two slots' maxima
 constexpr int kSmemBytes = 231424;         // all of an SM's
@@ -409,12 +413,18 @@ struct Smem {
   Routing r;
   float col_scale[8 * kMaxNT];   // of the staged columns: takes a sum back from the operand's power of two
   Segment segs[8 * kMaxNT];      // the staged segments
+  short slot[8 * kMaxNT];        // the slots of the staged columns
 };
 constexpr int kFixedBytes = ((int)sizeof(Smem) + 127) / 128 * 128;
-// the widest layer: three pieces per warp, one column tile, one token
-static_assert(kFixedBytes + kWarps * 16 * 20 * 4 + kWarps * kMinRing * kPiece + (RG_MOE_MAX_WIDTH / 128) * 256 + 16 <=
+// the widest layer: two pieces per warp, one column tile, one token of two terms
+static_assert(kFixedBytes + kWarps * 16 * 20 * 4 + kWarps * kTightRing * kPiece + (RG_MOE_MAX_WIDTH / 128) * 512 + 16 <=
                   kSmemBytes,
               "shared memory");
+// Bytes of a staged token of K entries, one fp16 term or two: a multiple of 128
+// and 16, so that the lanes' loads of eight tokens do not conflict.
+__host__ __device__ constexpr int token_bytes(int K, bool two_terms) {
+  return (K + 127) / 128 * (two_terms ? 512 : 256) + 16;
+}
 
 template <bool UP>
 struct Phase {
@@ -424,9 +434,7 @@ struct Phase {
   const int K, nkb, ks, groups, group, kpart, rows_per_expert;
   int u0, u1;            // this CTA's units
   // the next piece to copy
-  int pu, pkb, pa, prb, pend;  // unit, 128-block, active expert, its row block, its last unit + 1
-  const uint8_t* pw;
-  const float* ps;
+  int pu, pkb, pa, prb;  // unit, 128-block, active expert, its row block
   const uint8_t* p_lo;
   const uint8_t* p_hi;
   const float* p_s;      // the even lanes' (gate, or all) or the odd lanes' (up) row scales
@@ -483,36 +491,28 @@ struct Phase {
   __device__ __forceinline__ void point_expert() {
     const Routing& r = sm.r;
     while (pu >= r.units[pa + 1]) ++pa;
-    const int e = r.active[pa], hb = (p.H + 127) / 128;
     prb = (pu - r.units[pa]) % rows_per_expert;
-    pend = r.units[pa + 1];
-    if constexpr (UP) {
-      pw = p.W13 + ((long long)e * 2 * p.I + (lane >> 3)) * p.H;
-      ps = p.S13 + (long long)e * ((2 * p.I + 127) / 128) * hb;
-    } else {
-      pw = p.W2 + ((long long)e * p.H + (lane >> 3)) * p.I;
-      ps = p.S2 + (long long)e * hb * nkb;
-    }
     point();
   }
   // Row block prb's weights and scales.  A lane copies 16 bytes of rows lane / 8 +
   // 4 j of the 16 (whole 128-byte lines per eight lanes); the even lanes' scales
   // are the gate's (or all rows'), the odd lanes' the up rows'.
   __device__ __forceinline__ void point() {
+    const long long e = sm.r.active[pa];
     if constexpr (UP) {  // eight gate rows, eight up rows
-      p_lo = pw + (long long)(prb * 8) * K;
+      p_lo = p.W13 + (e * 2 * p.I + (lane >> 3) + prb * 8) * K;
       p_hi = p_lo + (long long)p.I * K;
-      p_s = ps + (((lane & 1) * p.I + prb * 8) >> 7) * nkb;
+      p_s = p.S13 + (e * ((2 * p.I + 127) / 128) + (((lane & 1) * p.I + prb * 8) >> 7)) * nkb;
     } else {
-      p_lo = pw + (long long)(prb * 16) * K;
+      p_lo = p.W2 + (e * p.H + (lane >> 3) + prb * 16) * K;
       p_hi = p_lo + 8LL * K;
-      p_s = ps + (prb >> 3) * nkb;
+      p_s = p.S2 + (e * ((p.H + 127) / 128) + (prb >> 3)) * nkb;
     }
   }
   __device__ __forceinline__ void next_unit() {
     pu += groups;
     if (pu >= u1) return;
-    if (pu >= pend) {
+    if (pu >= sm.r.units[pa + 1]) {
       point_expert();
     } else {
       prb += groups;
@@ -550,6 +550,7 @@ struct Phase {
   // All but the newest ring - 2 copies of this lane have landed.
   __device__ __forceinline__ void wait_oldest() {
     switch (p.ring) {
+      case 2: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
       case 3: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
       case 4: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
       case 5: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
@@ -559,14 +560,18 @@ struct Phase {
     }
   }
 
-  __device__ int stride() const { return nkb * 256 + 16; }  // bytes per staged token: conflict-free for the lanes' loads
+  __device__ int stride() const { return token_bytes(K, !UP); }
 
-  // The operand of tokens [first, first + n) of the order in columns c0 onwards:
-  // fp16 scaled by the power of two that col_scale undoes, zeros past K.  A warp
-  // makes a token's row.
-  __device__ void stage(int first, int n, int c0) {
-    for (int c = c0 + ((warp - c0) & (kWarps - 1)); c < c0 + n; c += kWarps) {
-      const int s = sm.r.order[first + c - c0];
+  // The operands of the staged columns' slots: fp16 scaled by the power of two that
+  // col_scale undoes, zeros past K; in the second product each 128-block's first
+  // terms, then its second ones.  A warp makes a token's row; in the second product,
+  // which need not find its largest entry first, all warps share the rows.
+  __device__ void stage(int used) {
+    static_assert(kWarps == 16 && 8 * kMaxNT <= kWarps, "a column to a warp at least");
+    const int sh = UP || used > 8 ? 0 : used > 4 ? 1 : used > 2 ? 2 : used > 1 ? 3 : 4;
+    const int c = warp >> sh;
+    if (c < used) {
+      const int s = sm.slot[c];
       uint8_t* out = cols + c * stride();
       if constexpr (UP) {
         const long long at = (long long)(s / p.top_k) * K;
@@ -577,15 +582,17 @@ struct Phase {
         const float2 sc = pow2_scale(__ldcg(&p.w.h_max[s * kMaxStride]));
         if (lane == 0) sm.col_scale[c] = sc.y;
 #pragma unroll 4
-        for (int k = lane * 8; k < nkb * 128; k += 256) {
+        for (int k = (warp & ((1 << sh) - 1)) * 256 + lane * 8; k < nkb * 128; k += 256 << sh) {
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
           if (k < K) {
             a = __ldcg(reinterpret_cast<const float4*>(h + k));
             b = __ldcg(reinterpret_cast<const float4*>(h + k) + 1);
           }
-          *reinterpret_cast<uint4*>(out + k * 2) =
-              make_uint4(half_pair(a.x, a.y, sc.x), half_pair(a.z, a.w, sc.x), half_pair(b.x, b.y, sc.x),
-                         half_pair(b.z, b.w, sc.x));
+          const uint2 t[4] = {half_terms(a.x, a.y, sc.x), half_terms(a.z, a.w, sc.x), half_terms(b.x, b.y, sc.x),
+                              half_terms(b.z, b.w, sc.x)};
+          uint4* to = reinterpret_cast<uint4*>(out + (k & ~127) * 4 + (k & 127) * 2);
+          to[0] = make_uint4(t[0].x, t[1].x, t[2].x, t[3].x);
+          to[16] = make_uint4(t[0].y, t[1].y, t[2].y, t[3].y);
         }
       }
     }
@@ -593,6 +600,15 @@ struct Phase {
   static __device__ __forceinline__ uint32_t half_pair(float a, float b, float scale) {
     const __half2 h = __floats2half2_rn(a * scale, b * scale);
     return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  // Both terms of two entries.  The difference is exact in fp32; an entry beyond
+  // fp16 (of a row with an inf or NaN) has its first term alone.
+  static __device__ __forceinline__ uint2 half_terms(float a, float b, float scale) {
+    const float x = a * scale, y = b * scale;
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(fabsf(f.x) <= 65504.0f ? x - f.x : 0.0f, fabsf(f.y) <= 65504.0f ? y - f.y : 0.0f);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&h), *reinterpret_cast<const uint32_t*>(&l));
   }
   template <typename T>
   __device__ __forceinline__ void stage_token(const T* x, uint8_t* out, int c) {
@@ -686,12 +702,15 @@ struct Phase {
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const uint32_t xa = col[i] + kb * 256 + half * 128;
-          const uint4 x0 = lds16(xa), x1 = lds16(xa + 16);
-          mma_t<__half>(acc[i], a[0][0], a[0][1], a[0][2], a[0][3], x0.x, x0.y);
-          mma_t<__half>(odd[i], a[1][0], a[1][1], a[1][2], a[1][3], x0.z, x0.w);
-          mma_t<__half>(acc[i], a[2][0], a[2][1], a[2][2], a[2][3], x1.x, x1.y);
-          mma_t<__half>(odd[i], a[3][0], a[3][1], a[3][2], a[3][3], x1.z, x1.w);
+#pragma unroll
+          for (int term = 0; term < (UP ? 1 : 2); ++term) {
+            const uint32_t xa = col[i] + kb * (UP ? 256 : 512) + term * 256 + half * 128;
+            const uint4 x0 = lds16(xa), x1 = lds16(xa + 16);
+            mma_t<__half>(acc[i], a[0][0], a[0][1], a[0][2], a[0][3], x0.x, x0.y);
+            mma_t<__half>(odd[i], a[1][0], a[1][1], a[1][2], a[1][3], x0.z, x0.w);
+            mma_t<__half>(acc[i], a[2][0], a[2][1], a[2][2], a[2][3], x1.x, x1.y);
+            mma_t<__half>(odd[i], a[3][0], a[3][1], a[3][2], a[3][3], x1.z, x1.w);
+          }
         }
       }
       float s0, s1;
@@ -776,11 +795,13 @@ struct Phase {
         if (used && used + g1.n > cap()) break;
         g1.c0 = used;
         if (threadIdx.x == 0) sm.segs[k] = g1;
-        stage(g1.first, g1.n, used);
+        if ((int)threadIdx.x < g1.n) sm.slot[used + threadIdx.x] = sm.r.order[g1.first + threadIdx.x];
         used += g1.n;
         end = g1.end;
         ++k;
       }
+      __syncthreads();
+      stage(used);
       __syncthreads();
       for (int q = 0; q < k; ++q) {
         const int last = sm.segs[q].end;
@@ -875,9 +896,10 @@ int k_split(long long K) {
 }
 // The call's shared memory: room for the tokens that nearly every expert gets
 // in one pass (the mean of even routing and two deviations), at least three
-// pieces per warp, and what is left to deeper rings.
+// pieces per warp (two where one token leaves no room for three: I above
+// 24960), and what is left to deeper rings.
 void plan_smem(MoeParams& p) {
-  const int bytes_up = (p.H + 127) / 128 * 256 + 16, bytes_down = (p.I + 127) / 128 * 256 + 16;
+  const int bytes_up = token_bytes(p.H, false), bytes_down = token_bytes(p.I, true);
   const int wide = bytes_up > bytes_down ? bytes_up : bytes_down, ring1 = kWarps * kPiece;
   const double mean = (double)p.T * p.top_k / p.E;
   int tokens = (int)std::ceil(mean + 2.0 * std::sqrt(mean));
@@ -886,10 +908,11 @@ void plan_smem(MoeParams& p) {
   if (tokens > p.T) tokens = p.T;
   auto tiles = [](int n) { return n <= 8 ? 1 : kMaxNT; };
   auto ld = [&](int n) { return 16 * tiles(n) + 4; };  // two halves, see unit()
-  auto room_for = [&](int n) { return kSmemBytes - kFixedBytes - kMinRing * ring1 - kWarps * 16 * 4 * ld(n); };
+  p.ring = kMinRing;
+  auto room_for = [&](int n) { return kSmemBytes - kFixedBytes - p.ring * ring1 - kWarps * 16 * 4 * ld(n); };
+  if (wide > room_for(1)) p.ring = kTightRing;
   while (tokens * wide > room_for(tokens)) tokens = tokens > 8 ? (tokens - 1) / 8 * 8 : tokens - 1;
   int room = room_for(tokens) - tokens * wide;
-  p.ring = kMinRing;
   for (; p.ring < kMaxRing && room >= ring1; ++p.ring) room -= ring1;
   auto fit = [&](int bytes) {
     int n = (tokens * wide + room) / bytes;

@@ -507,9 +507,10 @@ int linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* sa
  * 128 tile of an expert's matrix: S13 [E][ceil(2I/128)][ceil(H/128)],
  * S2 [E][ceil(H/128)][ceil(I/128)].  All contiguous, starting on 16-byte
  * boundaries; H and I are multiples of 16.  Sums, softmax and the gated
- * product are fp32 (the latter rounded to 11 bits as an operand of the last
- * product); Y is rounded once, and equal calls give equal bits.  An inf or NaN
- * in a token makes that token's whole row NaN.
+ * product are fp32 (the latter within 2^-23 of an entry or 2^-39 of its row's
+ * largest as an operand of the last product); Y is rounded once, and equal
+ * calls give equal bits.  An inf or NaN in a token makes that token's whole
+ * row NaN.
  * ws: moe_layer_f8_ws_bytes() bytes, 256-byte aligned; that function returns 0
  * for invalid sizes.
  * Errors: RG_ERR_RANGE (T > RG_MOE_MAX_TOKENS: use quantize_f8 and
