@@ -69,7 +69,7 @@ EXPORTED = (
     "rg_solution_free", "rg_rational_reconstruct", "rg_big_gcd", "rg_set_crt_mode", "rg_set_stage_events",
     "rg_probe_mma_rate", "rg_big_mulmod", "quantize_f8", "scaled_gemm_f8",
     "moe_layer_f8", "moe_layer_f8_ws_bytes", "linear_f8", "linear_f8_backward", "linear_f8_saved_bytes",
-    "linear_f8_ws_bytes",
+    "linear_f8_ws_bytes", "rg_hold_workspace",
 )
 
 
@@ -191,6 +191,8 @@ def library():
                 getattr(lib, f).restype = sz
             lib.moe_layer_f8_ws_bytes.argtypes = [i64, i64, i64, i64, ci]
             lib.moe_layer_f8_ws_bytes.restype = sz
+            lib.rg_hold_workspace.argtypes = [vp, ci]
+            lib.rg_hold_workspace.restype = ci
             lib.rg_noalloc_scratch_bytes.argtypes = []
             lib.rg_noalloc_scratch_bytes.restype = sz
             _lib = lib

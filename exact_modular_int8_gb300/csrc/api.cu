@@ -8,10 +8,12 @@
 // device.
 #include <atomic>
 #include <climits>
+#include <condition_variable>
 #include <mutex>
 #include <cstdint>
 #include <cstring>
 
+#include "rg_call.h"
 #include "rg_kernels.h"
 
 namespace {
@@ -297,15 +299,46 @@ bool stage_events_on() {
   return g_ev_on;
 }
 
+// The workspaces that calls are using now (see rg_call.h).
+struct Turns {
+  static constexpr int kMax = 64;  // further calls wait for an entry
+  std::mutex mu;
+  std::condition_variable freed;
+  const void* busy[kMax] = {};
+  int n = 0;
+
+  int find(const void* ws) const {
+    int i = 0;
+    while (i < n && busy[i] != ws) ++i;
+    return i;
+  }
+  void take(const void* ws) {
+    std::unique_lock<std::mutex> lk(mu);
+    freed.wait(lk, [&] { return n < kMax && find(ws) == n; });
+    busy[n++] = ws;
+  }
+  bool give(const void* ws) {
+    {
+      std::lock_guard<std::mutex> lk(mu);
+      const int i = find(ws);
+      if (i == n) return false;
+      busy[i] = busy[--n];
+    }
+    freed.notify_all();
+    return true;
+  }
+};
+Turns g_turns;
+
 // Shared driver for every entry point; `batch` products of the same shape
 // share one plan (one prime count, one pair of scale exponents).  A2 and B2
 // are the radii of interval operands (null otherwise).  `status_host`, if
 // given, is the host int the final status read lands in (see finish()).
 // `pipeline`: large host-buffer int64 products may take the pipelined path
 // (which creates copy streams and events on first use).
-int run(int op, const void* A, const void* A2, int la, const void* B, const void* B2, int lb, void* C, void* C2,
-        int lc, long long batch, long long M, long long N, long long K, int nprimes, unsigned flags, void* ws,
-        size_t ws_bytes, void* stream, int* status_host = nullptr, bool pipeline = true) {
+int run_in_turn(int op, const void* A, const void* A2, int la, const void* B, const void* B2, int lb, void* C, void* C2,
+                int lc, long long batch, long long M, long long N, long long K, int nprimes, unsigned flags, void* ws,
+                size_t ws_bytes, void* stream, int* status_host = nullptr, bool pipeline = true) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return RG_ERR_ARG;
   if (batch < 0 || M < 0 || N < 0 || K < 0 || nprimes < 0 || nprimes > kNumPrimes) return RG_ERR_ARG;
   // an empty problem reads no operand, and writes outputs only if it has entries
@@ -420,9 +453,22 @@ int run(int op, const void* A, const void* A2, int la, const void* B, const void
   return finish(ws, s, flags, status_host);
 }
 
+template <typename... Args>
+int run(int op, const void* A, const void* A2, int la, const void* B, const void* B2, int lb, void* C, void* C2, int lc,
+        long long batch, long long M, long long N, long long K, int nprimes, unsigned flags, void* ws, Args... rest) {
+  const WorkspaceTurn turn(ws);
+  return run_in_turn(op, A, A2, la, B, B2, lb, C, C2, lc, batch, M, N, K, nprimes, flags, ws, rest...);
+}
+
 }  // namespace
 
 namespace rg {
+WorkspaceTurn::WorkspaceTurn(const void* ws) : ws_(ws) {
+  if (ws_) g_turns.take(ws_);
+}
+WorkspaceTurn::~WorkspaceTurn() {
+  if (ws_) g_turns.give(ws_);
+}
 int finish_call(void* ws, cudaStream_t s, unsigned flags) { return finish(ws, s, flags); }
 int take_fault() { return g_fault.exchange(0); }
 unsigned long long wait_limit_ns() { return g_wait_ns.load(); }
@@ -444,7 +490,9 @@ int res_gemm_limbs(const int64_t* A, int la, const int64_t* B, int lb, int64_t* 
 int enclose_gemm_f64(const double* A, const double* B, double* lo, double* hi, int64_t M, int64_t N, int64_t K,
                      unsigned flags, int* info, void* ws, size_t ws_bytes, void* stream) {
   if (info) flags |= RG_FLAG_SYNC;  // the regime is known once the call has run
-  const int rc = run(RG_OP_ENCLOSE, A, nullptr, 1, B, nullptr, 1, lo, hi, 1, 1, M, N, K, 0, flags, ws, ws_bytes, stream);
+  const WorkspaceTurn turn(ws);
+  const int rc =
+      run_in_turn(RG_OP_ENCLOSE, A, nullptr, 1, B, nullptr, 1, lo, hi, 1, 1, M, N, K, 0, flags, ws, ws_bytes, stream);
   if (rc != RG_OK || !info) return rc;
   int lossless = 1;
   if (M && N && K) {  // an empty product is exactly zero: lossless
@@ -524,6 +572,7 @@ int res_gemm_stage(const uint16_t* RA, int64_t lda, const uint16_t* RB, int64_t 
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return RG_ERR_ARG;
   if (K > RG_MAX_K) return RG_ERR_RANGE;
   if (ws_bytes < kPlanBytes) return RG_ERR_WORKSPACE;
+  const WorkspaceTurn turn(ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   DevPlan* plan = static_cast<DevPlan*>(ws);
   RG_TRY(cudaMemsetAsync(plan, 0, sizeof(DevPlan), s));
@@ -608,6 +657,13 @@ const char* rg_strerror(int code) {
 }
 
 uint64_t rg_set_wait_limit_ns(uint64_t ns) { return g_wait_ns.exchange(ns ? ns : 1000000000ull); }
+
+int rg_hold_workspace(const void* ws, int hold) {
+  if (!ws) return RG_ERR_ARG;
+  if (hold) g_turns.take(ws);
+  else if (!g_turns.give(ws)) return RG_ERR_ARG;
+  return RG_OK;
+}
 
 void rg_inject_fault(int kind) { g_fault.store(kind); }
 

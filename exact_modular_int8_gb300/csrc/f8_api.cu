@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "f8_kernels.h"
+#include "rg_call.h"
 #include "rg_kernels.h"
 
 namespace {
@@ -128,6 +129,7 @@ int scaled_gemm_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t
       return RG_ERR_ARG;
     if (blocks128(M) * blocks128(N) > INT_MAX / 8) return RG_ERR_ARG;
   }
+  const WorkspaceTurn turn(ws);
   const int rc = product(gemm_args(A, lda, SA, B, ldb, SB, C, c_type, ldc, M, N, K, transb, tile_b), plan, st);
   return rc ? rc : finish_call(ws, st, flags);
 }
@@ -154,6 +156,7 @@ int linear_f8(const void* X, int x_type, int64_t ldx, const void* W, int w_type,
   if (ws_bytes < linear_f8_ws_bytes(M, N, K) || saved_bytes < linear_f8_saved_bytes(M, N, K)) return RG_ERR_WORKSPACE;
   if ((M && K && (!X || ldx < K)) || (N && K && (!W || ldw < K)) || (M && N && !Y)) return RG_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const WorkspaceTurn turn(ws);
   const Saved v = carve_saved(static_cast<uint8_t*>(saved), M, N, K);
   Carver c{static_cast<uint8_t*>(ws) + kCallBlockBytes};
   const Quantised x = carve(c, M, K, M);
@@ -177,6 +180,7 @@ int linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* sa
   if (ws_bytes < linear_f8_ws_bytes(M, N, K) || saved_bytes < linear_f8_saved_bytes(M, N, K)) return RG_ERR_WORKSPACE;
   if ((M && N && (!dY || lddy < N)) || (M && K && !dX) || (N && K && !dW)) return RG_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const WorkspaceTurn turn(ws);
   const Saved v = carve_saved(static_cast<uint8_t*>(const_cast<void*>(saved)), M, N, K);
   DevPlan* plan = static_cast<DevPlan*>(ws);
   Carver c{static_cast<uint8_t*>(ws) + kCallBlockBytes};
@@ -210,6 +214,7 @@ int moe_layer_f8(const void* X, int x_type, const void* WR, const uint8_t* W13, 
             !aligned16(W13, 0) || !aligned16(W2, 0) || !aligned16(Y, 0)))
     return RG_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const WorkspaceTurn turn(ws);
   if (T) {
     const MoeArgs a{X, WR, W13, S13, W2, S2, Y, T, H, I, E, top_k, x_type, renorm != 0};
     if (launch_moe_f8(a, static_cast<DevPlan*>(ws), static_cast<uint8_t*>(ws) + kCallBlockBytes, st,

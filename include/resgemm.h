@@ -43,7 +43,9 @@
  *    stream and returns the device status.
  *  - On any error the outputs are unspecified.
  *  - Calls sharing one workspace must not overlap on the GPU; calls on
- *    different workspaces may run concurrently.
+ *    different workspaces may run concurrently.  Host threads that share a
+ *    workspace and its stream take turns: a call's launches (and with
+ *    RG_FLAG_SYNC its synchronisation) are not interleaved with another's.
  */
 #ifndef RESGEMM_H
 #define RESGEMM_H
@@ -565,6 +567,11 @@ const char* rg_strerror(int code);
  * previous limit.  Not thread-safe; for tests only. */
 uint64_t rg_set_wait_limit_ns(uint64_t ns);
 void rg_inject_fault(int kind);
+
+/* Test hook: takes (hold = 1) and gives back (hold = 0) a call's turn on the
+ * workspace `ws`, so that a test can show that calls wait for it.  RG_OK, or
+ * RG_ERR_ARG for a null pointer or a turn that is not taken. */
+int rg_hold_workspace(const void* ws, int hold);
 
 /* Measurement hook: with n = 4, every later GEMM call (res_gemm_i64/limbs,
  * enclose_gemm_*, interval_gemm_*, batched or not) records events[0] on its

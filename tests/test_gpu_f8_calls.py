@@ -1,0 +1,49 @@
+"""How the 8-bit operators are called: from several host threads, under graph capture, with tensors that require
+gradients, and what they report."""
+import threading
+
+import pytest
+import torch
+
+from gpu_util import rg  # noqa: F401
+from test_gpu_f8 import moe_inputs, normal
+
+pytestmark = pytest.mark.gpu
+
+
+def steps(rg, seed):  # noqa: F811
+    """A training step and an expert layer on inputs of their own: a call of several launches each."""
+    x = normal((300, 256), seed, 1.0, torch.bfloat16).cuda()
+    w, dy = normal((200, 256), seed + 1).cuda(), normal((300, 200), seed + 2, 0.1, torch.bfloat16).cuda()
+    args = [a.cuda() for a in moe_inputs(5 + seed % 3, 256, 64, 8, torch.bfloat16, seed)]
+
+    def run():
+        y, saved = rg.linear_f8(x, w, sync=False)
+        return (y, *rg.linear_f8_backward(dy, saved, sync=False), rg.moe_layer_f8(*args, 2, sync=False))
+
+    return run
+
+
+def test_threads_on_one_stream(rg):  # noqa: F811
+    """Each thread's calls give what they give alone, although all share the default stream's workspace."""
+    runs = [steps(rg, 100 * i) for i in range(4)]
+    want = [run() for run in runs]
+    torch.cuda.synchronize()
+    got = [[] for _ in runs]
+    start = threading.Barrier(len(runs))
+
+    def work(i):
+        start.wait()
+        for _ in range(50):
+            got[i].append(runs[i]())
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(len(runs))]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert len(g) == 50
+        for outs in g:
+            assert all(torch.equal(a, b) for a, b in zip(w, outs))
