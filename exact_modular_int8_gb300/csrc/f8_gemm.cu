@@ -961,7 +961,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-bool make_map_2d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t stride_bytes, uint32_t b0,
+// The encoder is a driver function: it needs a current context, which a host
+// thread has only after a runtime call that makes one, and a product in a new
+// thread comes here before any other.  It is made where the encoder has failed
+// (the other calls pay nothing).
+bool make_map_2d(CUtensorMap* m, int dev, const void* base, uint64_t d0, uint64_t d1, uint64_t stride_bytes, uint32_t b0,
                  uint32_t b1, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B,
                  CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT8) {
   auto fn = encode_fn();
@@ -970,9 +974,11 @@ bool make_map_2d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uin
   cuuint64_t strides[1] = {stride_bytes};
   cuuint32_t box[2] = {b0, b1};
   cuuint32_t es[2] = {1, 1};
-  return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&] {
+    return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  return encode() || (cudaSetDevice(dev) == cudaSuccess && encode());
 }
 
 cudaLaunchConfig_t cluster_config(dim3 grid, int threads, int smem, cudaStream_t st, int cluster, cudaLaunchAttribute* attr) {
@@ -1093,9 +1099,9 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
   const bool pair = variant == 2 || (variant == 0 && (long long)p.mt * p.nt > fd.sms);
   const uint32_t b_cols = pair ? 64 : 128;  // columns of B per copy
   CUtensorMap ma, mb;
-  if (!make_map_2d(&ma, a.A, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.lda, BK, 128) ||
-      !(a.b_kmajor ? make_map_2d(&mb, a.B, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.ldb, BK, b_cols)
-                   : make_map_2d(&mb, a.B, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.ldb, b_cols, BK,
+  if (!make_map_2d(&ma, dev, a.A, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.lda, BK, 128) ||
+      !(a.b_kmajor ? make_map_2d(&mb, dev, a.B, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)a.ldb, BK, b_cols)
+                   : make_map_2d(&mb, dev, a.B, (uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.ldb, b_cols, BK,
                                  pair ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B)))
     return cudaErrorInvalidValue;
   if (pair) {
@@ -1104,7 +1110,7 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
     const long long clusters = tiles2 < fd.max_pairs ? tiles2 : fd.max_pairs;
     cudaLaunchConfig_t cfg = cluster_config(dim3((unsigned)(2 * clusters)), NUM_THREADS, SMEM2_BYTES, st, 2, attr);
     CUtensorMap mc = {};
-    if (p.vec_c && !make_map_2d(&mc, a.C, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.ldc * es, 64 / es, 32,
+    if (p.vec_c && !make_map_2d(&mc, dev, a.C, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.ldc * es, 64 / es, 32,
                                 CU_TENSOR_MAP_SWIZZLE_64B,
                                 es == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16))
       return cudaErrorInvalidValue;

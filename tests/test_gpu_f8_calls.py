@@ -47,3 +47,15 @@ def test_threads_on_one_stream(rg):  # noqa: F811
         assert len(g) == 50
         for outs in g:
             assert all(torch.equal(a, b) for a, b in zip(w, outs))
+
+
+@pytest.mark.parametrize("m", [4, 70, 2100])
+def test_product_is_a_threads_first_call(rg, m):  # noqa: F811
+    """A host thread whose first use of the GPU is a product, by each of the product's kernels."""
+    q, s = rg.quantize_f8(normal((m, 200), 1).cuda())
+    qw, sw = rg.quantize_f8(normal((2304, 200), 2).cuda(), "tiles")
+    want, out = rg.scaled_gemm_f8(q, s, qw, sw, transb=True), []
+    t = threading.Thread(target=lambda: out.append(rg.scaled_gemm_f8(q, s, qw, sw, transb=True)))
+    t.start()
+    t.join()
+    assert len(out) == 1 and torch.equal(out[0], want)
