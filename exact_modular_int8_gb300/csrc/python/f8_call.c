@@ -115,16 +115,26 @@ static PyObject* new_matrix(int64_t m, int64_t k, PyObject* type, PyObject* devi
 }
 static void* data_of(PyObject* t) { return (void*)(uintptr_t)call_int(t, s_data_ptr); }
 
-/* The stream's cached workspace and its size; NULL to decline. */
-static void* workspace_of(int64_t dev, void* stream, int64_t* bytes) {
+/* The stream's cached workspace, at least `need` bytes.  The tensor is held until after the call (a new reference):
+ * while the call runs without the interpreter's lock, another thread may replace or drop the cached one. */
+typedef struct {
+  PyObject* tensor;
+  void* p;
+  int64_t bytes;
+} workspace;
+/* 0 to decline */
+static int workspace_of(int64_t dev, void* stream, size_t need, workspace* w) {
   PyObject* key = Py_BuildValue("(LN)", (long long)dev, PyLong_FromVoidPtr(stream));
-  if (!key) return NULL;
-  PyObject* ws = PyDict_GetItemWithError(workspaces, key); /* borrowed */
+  if (!key) return 0;
+  w->tensor = PyDict_GetItemWithError(workspaces, key); /* borrowed */
   Py_DECREF(key);
-  if (!ws) return NULL;
-  *bytes = call_int(ws, s_numel);
-  void* p = data_of(ws);
-  return PyErr_Occurred() ? NULL : p;
+  if (!w->tensor) return 0;
+  Py_INCREF(w->tensor);
+  w->bytes = call_int(w->tensor, s_numel);
+  w->p = data_of(w->tensor);
+  if (!PyErr_Occurred() && w->p && (size_t)w->bytes >= need) return 1;
+  Py_DECREF(w->tensor);
+  return 0;
 }
 
 /* The device that holds `t`, if it is the current one, and its current stream. */
@@ -239,19 +249,25 @@ static PyObject* gemm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (scales_of(a[3], dev, transb ? nb : kb, transb ? kb : nb, &SB)) flags |= RG_FLAG_TILE_B;
   else if (PyErr_Occurred() || !scales_of(a[3], dev, transb ? N : kb, transb ? kb : N, &SB)) return decline();
   if (transb) flags |= RG_FLAG_TRANS_B;
-  int64_t ws_bytes;
-  void* ws_p = workspace_of(dev, stream, &ws_bytes);
-  if (!ws_p) return decline();
   PyObject* device = PyObject_GetAttr(a[0], s_device);
   if (!device) return decline();
+  workspace ws;
+  if (!workspace_of(dev, stream, RG_F8_WS_BYTES, &ws)) {
+    Py_DECREF(device);
+    return decline();
+  }
   PyObject* C = new_matrix(A.m, N, a[4], device);
   Py_DECREF(device);
-  if (!C) return NULL;
+  if (!C) {
+    Py_DECREF(ws.tensor);
+    return NULL;
+  }
   void* c = data_of(C);
   int rc;
   Py_BEGIN_ALLOW_THREADS
-  rc = lib_gemm(A.p, A.ld, SA.p, B.p, B.ld, SB.p, c, t, N, A.m, N, K, flags, ws_p, (size_t)ws_bytes, stream);
+  rc = lib_gemm(A.p, A.ld, SA.p, B.p, B.ld, SB.p, c, t, N, A.m, N, K, flags, ws.p, (size_t)ws.bytes, stream);
   Py_END_ALLOW_THREADS
+  Py_DECREF(ws.tensor);
   return finish(rc, "scaled_gemm_f8", C);
 }
 
@@ -260,7 +276,7 @@ static PyObject* linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   if (n != 3) return decline();
   const unsigned flags = (unsigned)PyLong_AsUnsignedLong(a[2]);
-  int64_t dev, ws_bytes;
+  int64_t dev;
   void* stream;
   matrix X, W;
   if (PyErr_Occurred() || !place(a[0], &dev, &stream)) return decline();
@@ -268,22 +284,27 @@ static PyObject* linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (tw < 0 || X.k != W.k) return decline();
   const int64_t M = X.m, N = W.m, K = X.k;
   const size_t kept_bytes = lib_saved_bytes(M, N, K);
-  void* ws_p = kept_bytes ? workspace_of(dev, stream, &ws_bytes) : NULL;
-  if (!ws_p || (size_t)ws_bytes < lib_ws_bytes(M, N, K)) return decline();
-  PyObject* device = PyObject_GetAttr(a[0], s_device);
+  PyObject* device = kept_bytes ? PyObject_GetAttr(a[0], s_device) : NULL;
   if (!device) return decline();
+  workspace ws;
+  if (!workspace_of(dev, stream, lib_ws_bytes(M, N, K), &ws)) {
+    Py_DECREF(device);
+    return decline();
+  }
   PyObject* Y = new_matrix(M, N, types[tx], device);
   PyObject* kept = Y ? new_tensor(PyLong_FromSize_t(kept_bytes), byte_type, device) : NULL;
   Py_DECREF(device);
   if (!kept) {
     Py_XDECREF(Y);
+    Py_DECREF(ws.tensor);
     return NULL;
   }
   void *y = data_of(Y), *s = data_of(kept);
   int rc;
   Py_BEGIN_ALLOW_THREADS
-  rc = lib_linear(X.p, tx, X.ld, W.p, tw, W.ld, y, M, N, K, s, kept_bytes, flags, ws_p, (size_t)ws_bytes, stream);
+  rc = lib_linear(X.p, tx, X.ld, W.p, tw, W.ld, y, M, N, K, s, kept_bytes, flags, ws.p, (size_t)ws.bytes, stream);
   Py_END_ALLOW_THREADS
+  Py_DECREF(ws.tensor);
   PyObject* r = Py_BuildValue("(N(NLLL))", Y, kept, (long long)M, (long long)N, (long long)K);
   return r ? finish(rc, "linear_f8", r) : NULL;
 }
@@ -294,7 +315,7 @@ static PyObject* backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (n != 7) return decline();
   const int64_t M = PyLong_AsLongLong(a[2]), N = PyLong_AsLongLong(a[3]), K = PyLong_AsLongLong(a[4]);
   const unsigned flags = (unsigned)PyLong_AsUnsignedLong(a[6]);
-  int64_t dev, ws_bytes;
+  int64_t dev;
   void* stream;
   matrix dY;
   if (PyErr_Occurred() || !place(a[0], &dev, &stream)) return decline();
@@ -303,22 +324,28 @@ static PyObject* backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   while (tw < 3 && types[tw] != a[5]) ++tw;
   if (t < 0 || tw == 3 || dY.m != M || dY.k != N || K <= 0 || call_int(a[1], s_get_device) != dev) return decline();
   const int64_t kept_bytes = call_int(a[1], s_numel);
-  void *s = data_of(a[1]), *ws_p = PyErr_Occurred() ? NULL : workspace_of(dev, stream, &ws_bytes);
-  if (!ws_p || (size_t)ws_bytes < lib_ws_bytes(M, N, K)) return decline();
-  PyObject* device = PyObject_GetAttr(a[0], s_device);
+  void* s = data_of(a[1]);
+  PyObject* device = PyErr_Occurred() ? NULL : PyObject_GetAttr(a[0], s_device);
   if (!device) return decline();
+  workspace ws;
+  if (!workspace_of(dev, stream, lib_ws_bytes(M, N, K), &ws)) {
+    Py_DECREF(device);
+    return decline();
+  }
   PyObject* dX = new_matrix(M, K, types[t], device);
   PyObject* dW = dX ? new_matrix(N, K, types[tw], device) : NULL;
   Py_DECREF(device);
   if (!dW) {
     Py_XDECREF(dX);
+    Py_DECREF(ws.tensor);
     return NULL;
   }
   void *dx = data_of(dX), *dw = data_of(dW);
   int rc;
   Py_BEGIN_ALLOW_THREADS
-  rc = lib_backward(dY.p, t, dY.ld, s, (size_t)kept_bytes, dx, dw, tw, M, N, K, flags, ws_p, (size_t)ws_bytes, stream);
+  rc = lib_backward(dY.p, t, dY.ld, s, (size_t)kept_bytes, dx, dw, tw, M, N, K, flags, ws.p, (size_t)ws.bytes, stream);
   Py_END_ALLOW_THREADS
+  Py_DECREF(ws.tensor);
   PyObject* r = PyTuple_Pack(2, dX, dW);
   Py_DECREF(dX);
   Py_DECREF(dW);

@@ -1,6 +1,7 @@
 """How the 8-bit operators are called: from several host threads, under graph capture, with tensors that require
 gradients, and what they report."""
 import threading
+import weakref
 
 import pytest
 import torch
@@ -59,3 +60,31 @@ def test_product_is_a_threads_first_call(rg, m):  # noqa: F811
     t.start()
     t.join()
     assert len(out) == 1 and torch.equal(out[0], want)
+
+
+def test_a_call_keeps_its_workspace(rg):  # noqa: F811
+    """A workspace that another thread drops from the cache lives until the calls that use it have ended."""
+    x, w = normal((70, 200), 1).cuda(), normal((96, 200), 2).cuda()
+    q, s = rg.quantize_f8(x)
+    qw, sw = rg.quantize_f8(w, "tiles")
+    Y, saved = rg.linear_f8(x, w)
+    calls = (lambda: rg.linear_f8(x, w)[0], lambda: rg.linear_f8_backward(Y, saved)[0],
+             lambda: rg.scaled_gemm_f8(q, s, qw, sw, transb=True))
+    want = [f() for f in calls]
+    for f, y in zip(calls, want):
+        f()  # fills the cache again
+        ws = rg.workspace(4096, x.device)
+        p, alive, out = ws.data_ptr(), weakref.ref(ws), []
+        del ws
+        assert rg.library().rg_hold_workspace(p, 1) == rg.RG_OK
+        try:
+            t = threading.Thread(target=lambda: out.append(f()))
+            t.start()
+            t.join(0.3)
+            assert t.is_alive()  # in the library, waiting for its turn
+            rg.release_workspaces()
+            assert alive() is not None
+        finally:
+            assert rg.library().rg_hold_workspace(p, 0) == rg.RG_OK
+        t.join()
+        assert alive() is None and torch.equal(out[0], y)
