@@ -240,13 +240,27 @@ def workspace_layout(op, M, N, K, la=1, lb=1, lc=1, nprimes=0, host=False, trans
 
 
 # ---------------------------------------------------------------------------
-# workspace cache: one growing device buffer per (device, stream)
+# workspace cache: one growing device buffer per (device, stream).  A CUDA graph keeps the addresses it
+# was captured with, so a call under capture takes a buffer of its own from the graph's memory instead:
+# a cached one would be replaced by a larger one or shared by graphs that replay at the same time.
 # ---------------------------------------------------------------------------
 _ws_cache: dict = {}
 
 
+def capturing(index) -> bool:
+    """Whether the current stream of device `index` is being captured into a CUDA graph."""
+    if index is None or torch._C._cuda_getDevice() == index:
+        return torch._C._cuda_isCurrentStreamCapturing()
+    with torch.cuda.device(index):
+        return torch._C._cuda_isCurrentStreamCapturing()
+
+
 def workspace(nbytes: int, device: torch.device, stream=None) -> torch.Tensor:
-    """A device buffer of at least nbytes, reused across calls on one stream."""
+    """A device buffer of at least nbytes, reused across calls on one stream; a new one while the current
+    stream is being captured into a CUDA graph (the call's status is then read from a workspace that the
+    caller passes)."""
+    if capturing(device.index):
+        return torch.empty(max(nbytes, 4096), dtype=torch.uint8, device=device)
     stream = stream or torch.cuda.current_stream(device)
     key = (device.index, stream.cuda_stream)
     buf = _ws_cache.get(key)

@@ -32,8 +32,8 @@ static gemm_fn lib_gemm;
 static linear_fn lib_linear;
 static backward_fn lib_backward;
 static bytes_fn lib_saved_bytes, lib_ws_bytes;
-static PyObject *types[3], *f8_type, *byte_type;                       /* torch dtypes by RG_TYPE_*, E4M3, uint8 */
-static PyObject *empty, *empty_strided, *raw_stream, *current_device;  /* torch functions */
+static PyObject *types[3], *f8_type, *byte_type; /* torch dtypes by RG_TYPE_*, E4M3, uint8 */
+static PyObject *empty, *empty_strided, *raw_stream, *current_device, *capturing; /* torch functions */
 static PyObject *workspaces, *raise_status;  /* the binding's workspace cache and error function */
 static PyObject *s_shape, *s_stride, *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_numel, *empty_names;
 
@@ -115,8 +115,9 @@ static PyObject* new_matrix(int64_t m, int64_t k, PyObject* type, PyObject* devi
 }
 static void* data_of(PyObject* t) { return (void*)(uintptr_t)call_int(t, s_data_ptr); }
 
-/* The stream's cached workspace, at least `need` bytes.  The tensor is held until after the call (a new reference):
- * while the call runs without the interpreter's lock, another thread may replace or drop the cached one. */
+/* The stream's cached workspace, at least `need` bytes; none under capture into a graph, whose calls have their own.
+ * The tensor is held until after the call (a new reference): while the call runs without the interpreter's lock,
+ * another thread may replace or drop the cached one. */
 typedef struct {
   PyObject* tensor;
   void* p;
@@ -124,6 +125,9 @@ typedef struct {
 } workspace;
 /* 0 to decline */
 static int workspace_of(int64_t dev, void* stream, size_t need, workspace* w) {
+  PyObject* captured = PyObject_CallNoArgs(capturing);
+  Py_XDECREF(captured);
+  if (captured != Py_False) return 0;
   PyObject* key = Py_BuildValue("(LN)", (long long)dev, PyLong_FromVoidPtr(stream));
   if (!key) return 0;
   w->tensor = PyDict_GetItemWithError(workspaces, key); /* borrowed */
@@ -352,14 +356,15 @@ static PyObject* backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return r ? finish(rc, "linear_f8_backward", r) : NULL;
 }
 
-/* setup((six addresses), (f32, f16, bf16), f8, uint8, empty, empty_strided, raw_stream, current_device, workspaces,
- * raise) */
+/* setup((six addresses), (f32, f16, bf16), f8, uint8, empty, empty_strided, raw_stream, current_device, capturing,
+ * workspaces, raise) */
 static PyObject* setup(PyObject* self, PyObject* args) {
   (void)self;
   unsigned long long f[6];
   PyObject *t0, *t1, *t2;
-  if (!PyArg_ParseTuple(args, "(KKKKKK)(OOO)OOOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &t0, &t1, &t2, &f8_type,
-                        &byte_type, &empty, &empty_strided, &raw_stream, &current_device, &workspaces, &raise_status))
+  if (!PyArg_ParseTuple(args, "(KKKKKK)(OOO)OOOOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &t0, &t1, &t2, &f8_type,
+                        &byte_type, &empty, &empty_strided, &raw_stream, &current_device, &capturing, &workspaces,
+                        &raise_status))
     return NULL;
   lib_quantize = (quantize_fn)(uintptr_t)f[0];
   lib_gemm = (gemm_fn)(uintptr_t)f[1];
@@ -371,7 +376,7 @@ static PyObject* setup(PyObject* self, PyObject* args) {
   types[RG_TYPE_F16] = t1;
   types[RG_TYPE_BF16] = t2;
   PyObject* keep[] = {t0,         t1,         t2,         f8_type,        byte_type,  empty, empty_strided,
-                      raw_stream, current_device, workspaces, raise_status};
+                      raw_stream, current_device, capturing, workspaces, raise_status};
   for (size_t i = 0; i < sizeof keep / sizeof *keep; ++i) Py_INCREF(keep[i]); /* for the life of the process */
   s_shape = PyUnicode_InternFromString("shape");
   s_stride = PyUnicode_InternFromString("stride");

@@ -6,7 +6,10 @@ marshalling only, as in the rest of the binding: every step runs in the library'
 stream.  Quantised matrices have rows that start on 16-byte boundaries, which is what the product
 reads; operands from elsewhere that do not are copied into such rows first.
 
-With sync=False a call only enqueues its work, and errors found on the device are read with status().
+With sync=False a call only enqueues its work, and errors found on the device are read with status() before
+the next call on that stream.  Calls can be captured into CUDA graphs (with sync=False): their scratch then
+belongs to the graph, and a status can be read from a workspace passed as ws (a uint8 tensor; its size is what
+the library's *_ws_bytes functions give, 4096 for scaled_gemm_f8).
 """
 from __future__ import annotations
 
@@ -20,7 +23,7 @@ import torch
 
 from . import (LIB_PATH, RG_ERR_ARG, RG_ERR_RANGE, RG_F8_BOTH, RG_F8_COLUMNS, RG_F8_ROWS, RG_F8_TILES, RG_FLAG_SYNC,
                RG_FLAG_TILE_B, RG_FLAG_TRANS_B, RG_TYPE_BF16, RG_TYPE_F16, RG_TYPE_F32, ResGemmError, _check, _output,
-               _ws_cache, library, workspace)
+               _ws_cache, capturing, library, workspace)
 
 BLOCK = 128
 F8 = torch.float8_e4m3fn
@@ -44,8 +47,8 @@ def _native():
         entries = (lib.quantize_f8, lib.scaled_gemm_f8, lib.linear_f8, lib.linear_f8_backward,
                    lib.linear_f8_saved_bytes, lib.linear_f8_ws_bytes)
         m.setup(tuple(address(f) for f in entries), (torch.float32, torch.float16, torch.bfloat16), F8, torch.uint8,
-                torch.empty, torch.empty_strided, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache,
-                _check)
+                torch.empty, torch.empty_strided, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
+                torch._C._cuda_isCurrentStreamCapturing, _ws_cache, _check)
         _call = m
     return _call
 
@@ -80,8 +83,8 @@ def _launch(idx: int, where: str, f, *args):
 
 
 def _scratch(nbytes: int, idx: int) -> torch.Tensor:
-    """The cached workspace of the device's current stream (see workspace())."""
-    w = _ws_cache.get((idx, torch._C._cuda_getCurrentRawStream(idx)))
+    """The cached workspace of the device's current stream, or the graph's own (see workspace())."""
+    w = None if capturing(idx) else _ws_cache.get((idx, torch._C._cuda_getCurrentRawStream(idx)))
     return w if w is not None and w.numel() >= nbytes else workspace(nbytes, torch.device("cuda", idx))
 
 
@@ -211,12 +214,12 @@ def _rows_of(t: torch.Tensor):
     return (t, ld) if ld else (t.contiguous(), t.shape[1])
 
 
-def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True):
+def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True, ws: torch.Tensor | None = None):
     """(Y, saved): Y = X W^T with X [M, K] quantised along K and the weights W [N, K] in 128 x 128 tiles, in X's
     dtype (both float32, float16 or bfloat16).  `saved` is what linear_f8_backward needs: one buffer with X
     quantised along M and the quantised weights.  One library call; the same as quantize_f8(X, "both"),
     quantize_f8(W, "tiles") and scaled_gemm_f8."""
-    if X.is_cuda:
+    if X.is_cuda and ws is None:
         r = _native().linear(X, W, RG_FLAG_SYNC if sync else 0)
         if r is not None:
             return r
@@ -231,17 +234,18 @@ def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True):
     dev = X.device
     Y = torch.empty((M, N), dtype=X.dtype, device=dev)
     kept = torch.empty(nsaved, dtype=torch.uint8, device=dev)
-    w = _scratch(need, idx)
+    w = ws if ws is not None else _scratch(need, idx)
     _launch(idx, "linear_f8", library().linear_f8, X.data_ptr(), tx, ldx, W.data_ptr(), tw, ldw, Y.data_ptr(), M, N, K,
             kept.data_ptr(), nsaved, RG_FLAG_SYNC if sync else 0, w.data_ptr(), w.numel())
     return Y, (kept, M, N, K)
 
 
-def linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: torch.dtype = torch.float32):
+def linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: torch.dtype = torch.float32,
+                       ws: torch.Tensor | None = None):
     """(dX, dW) of linear_f8 for the output's gradient dY [M, N]: dX = dY W with dY quantised along N, in dY's
     dtype, and dW = dY^T X with both quantised along M, in dw_dtype."""
     kept, M, N, K = saved
-    if dY.is_cuda:
+    if dY.is_cuda and ws is None:
         r = _native().backward(dY, kept, M, N, K, dw_dtype, RG_FLAG_SYNC if sync else 0)
         if r is not None:
             return r
@@ -253,7 +257,7 @@ def linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: tor
     dY, lddy = _rows_of(dY)
     dX = torch.empty((M, K), dtype=dY.dtype, device=dY.device)
     dW = torch.empty((N, K), dtype=dw_dtype, device=dY.device)
-    w = _scratch(need, idx)
+    w = ws if ws is not None else _scratch(need, idx)
     _launch(idx, "linear_f8_backward", library().linear_f8_backward, dY.data_ptr(), t, lddy, kept.data_ptr(),
             kept.numel(), dX.data_ptr(), dW.data_ptr(), tw, M, N, K, RG_FLAG_SYNC if sync else 0, w.data_ptr(),
             w.numel())

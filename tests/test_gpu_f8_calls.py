@@ -88,3 +88,78 @@ def test_a_call_keeps_its_workspace(rg):  # noqa: F811
             assert rg.library().rg_hold_workspace(p, 0) == rg.RG_OK
         t.join()
         assert alive() is None and torch.equal(out[0], y)
+
+
+def captured(rg, run, stream):  # noqa: F811
+    """(graph, outputs) of run(), captured on a stream that has run it before."""
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        outs = run()
+    return graph, outs
+
+
+def exact_and_f8(rg, seed):  # noqa: F811
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    A, B = (torch.randint(-(2**20), 2**20, s, generator=g, device="cuda") for s in ((130, 70), (70, 200)))
+    rest = steps(rg, seed)
+    return lambda: (rg.res_gemm_i64(A, B, sync=False), *rest())
+
+
+@pytest.mark.parametrize("drop", [True, False])
+def test_graph_keeps_its_scratch(rg, drop):  # noqa: F811
+    """A graph replays in scratch of its own after the capture stream's workspace was replaced or dropped and its
+    memory went to other tensors, which stay as they are."""
+    run, stream = exact_and_f8(rg, 5), torch.cuda.Stream()
+    want = [t.clone() for t in run()]
+    graph, outs = captured(rg, run, stream)
+    with torch.cuda.stream(stream):
+        old = rg.workspace(4096, outs[0].device).numel()
+        if drop:
+            rg.release_workspaces()
+        else:
+            rg.workspace(4 * old, outs[0].device)
+        fill = [torch.full((old,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        for t in outs:
+            t.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert all(bool((f == 7).all()) for f in fill)
+
+
+def test_graphs_replay_at_the_same_time(rg):  # noqa: F811
+    """Graphs captured on one stream share no scratch: replayed on two streams at once they give what they give alone."""
+    stream, others = torch.cuda.Stream(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    runs = [exact_and_f8(rg, 11), exact_and_f8(rg, 31)]
+    want = [[t.clone() for t in run()] for run in runs]
+    graphs = [captured(rg, run, stream) for run in runs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (graph, outs), s in zip(graphs, others):
+            with torch.cuda.stream(s):
+                for t in outs:
+                    t.zero_()
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, outs), w in zip(graphs, want):
+        assert all(torch.equal(a, b) for a, b in zip(outs, w))
+
+
+def test_status_of_a_captured_call(rg):  # noqa: F811
+    """The caller's workspace serves a captured step, eager calls of the same tensors, and the status afterwards."""
+    x, w, dy = normal((70, 200), 1).cuda(), normal((96, 200), 2).cuda(), normal((70, 96), 3).cuda()
+    ws = torch.empty(rg.library().linear_f8_ws_bytes(70, 96, 200), dtype=torch.uint8, device="cuda")
+
+    def step(**kw):
+        y, saved = rg.linear_f8(x, w, sync=False, **kw)
+        return (y, *rg.linear_f8_backward(dy, saved, sync=False, **kw))
+
+    want = step()
+    graph, outs = captured(rg, lambda: step(ws=ws), torch.cuda.Stream())
+    graph.replay()
+    assert rg.status(ws) == rg.RG_OK
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
