@@ -56,6 +56,43 @@ def _native():
 _call = None
 
 
+class _LinearGrad(torch.autograd.Function):
+    """linear_f8 with linear_f8_backward as its gradient; `saved` receives what the latter reads."""
+
+    @staticmethod
+    def forward(ctx, X, W, sync, ws, saved):
+        Y, (kept, *ctx.sizes) = linear_f8(X, W, sync, ws)
+        ctx.save_for_backward(kept)
+        ctx.call = sync, W.dtype, ws
+        saved.extend((kept, *ctx.sizes))
+        return Y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        return (*linear_f8_backward(dY, (*ctx.saved_tensors, *ctx.sizes), *ctx.call), None, None, None)
+
+
+class _NoGrad(torch.autograd.Function):
+    """A call without a gradient, on tensors that require one: a backward pass through its result raises, where
+    a plain result would cut the gradient unnoticed."""
+
+    @staticmethod
+    def forward(ctx, where, call, *tensors):
+        ctx.where = where
+        return call()
+
+    @staticmethod
+    def backward(ctx, _):
+        raise NotImplementedError(f"{ctx.where} has no gradient; linear_f8 has one")
+
+
+def _no_grad(where: str, out, call, *tensors):
+    if out is not None:
+        raise ValueError(f"{where}: out takes no part in differentiation: call under torch.no_grad()")
+    return _NoGrad.apply(where, call, *tensors)
+
+
 def _blocks(x: int) -> int:
     return (x + BLOCK - 1) // BLOCK
 
@@ -123,7 +160,7 @@ def quantize_f8(X: torch.Tensor, form: str = "rows", sync: bool = True):
          "both":    (Q, S, Qt, St), the two of them from one read of X
          "tiles":   Q [M, K], S [ceil(M/128), ceil(K/128)]: 128 x 128 tiles
     Per block, a = max |x| (at least 2^-60), S = a / 448, Q = 448 x / a to the nearest E4M3 value, ties to
-    even; an inf or NaN makes its whole block NaN."""
+    even; an inf or NaN makes its whole block NaN.  To autograd the results are constants."""
     f = _FORMS.get(form)
     if f is None:
         raise ValueError(f"quantize_f8: form must be one of {', '.join(_FORMS)}")
@@ -165,7 +202,11 @@ def scaled_gemm_f8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch
     A [M, K] E4M3 with SA [M, ceil(K/128)].  B's scales are per 128 x 128 tile of B or per 128 values along
     the contraction, told apart by shape: transb SB [ceil(N/128), ceil(K/128)] or [N, ceil(K/128)], else
     [ceil(K/128), ceil(N/128)] or [ceil(K/128), N] (N = 1 is either).  Products per block on the tensor
-    cores, scales and sums in float32, one rounding to out_dtype (float32, float16 or bfloat16)."""
+    cores, scales and sums in float32, one rounding to out_dtype (float32, float16 or bfloat16).  No gradient: a
+    backward pass through C raises."""
+    if torch.is_grad_enabled() and (A.requires_grad or SA.requires_grad or B.requires_grad or SB.requires_grad):
+        return _no_grad("scaled_gemm_f8", out,
+                        lambda: scaled_gemm_f8(A, SA, B, SB, out_dtype, transb, sync, None, ws), A, SA, B, SB)
     if out is None and ws is None and A.is_cuda:
         C = _native().gemm(A, SA, B, SB, out_dtype, transb, RG_FLAG_SYNC if sync else 0)
         if C is not None:
@@ -218,7 +259,11 @@ def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True, ws: torch.Ten
     """(Y, saved): Y = X W^T with X [M, K] quantised along K and the weights W [N, K] in 128 x 128 tiles, in X's
     dtype (both float32, float16 or bfloat16).  `saved` is what linear_f8_backward needs: one buffer with X
     quantised along M and the quantised weights.  One library call; the same as quantize_f8(X, "both"),
-    quantize_f8(W, "tiles") and scaled_gemm_f8."""
+    quantize_f8(W, "tiles") and scaled_gemm_f8.  Where X or W requires a gradient autograd calls
+    linear_f8_backward for Y, with W's gradient in W's dtype."""
+    if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
+        saved = []
+        return _LinearGrad.apply(X, W, sync, ws, saved), tuple(saved)
     if X.is_cuda and ws is None:
         r = _native().linear(X, W, RG_FLAG_SYNC if sync else 0)
         if r is not None:
@@ -281,7 +326,11 @@ def moe_layer_f8(X: torch.Tensor, WR: torch.Tensor, W13: torch.Tensor, S13: torc
 
     W13 [E, 2I, H] E4M3 holds each expert's gate rows, then its up rows, with S13 [E, ceil(2I/128),
     ceil(H/128)]; W2 [E, H, I] with S2 [E, ceil(H/128), ceil(I/128)]: per expert what quantize_f8(W, "tiles")
-    gives.  H and I are multiples of 16."""
+    gives.  H and I are multiples of 16.  No gradient: a backward pass through Y raises."""
+    if torch.is_grad_enabled() and any(t.requires_grad for t in (X, WR, W13, S13, W2, S2)):
+        return _no_grad("moe_layer_f8", out,
+                        lambda: moe_layer_f8(X, WR, W13, S13, W2, S2, top_k, renorm, sync, None, ws),
+                        X, WR, W13, S13, W2, S2)
     if X.dim() != 2 or X.dtype not in (torch.float16, torch.bfloat16) or WR.dtype != X.dtype:
         raise ValueError("moe_layer_f8: X [T, H] and WR [E, H] of one dtype, float16 or bfloat16, expected")
     if W13.dtype != F8 or W2.dtype != F8 or S13.dtype != torch.float32 or S2.dtype != torch.float32:

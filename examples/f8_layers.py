@@ -3,7 +3,7 @@
     python examples/f8_layers.py
 
 1. A linear layer fits a target by gradient descent: its output and both gradients are 8-bit products
-   (linear_f8, linear_f8_backward behind a torch.autograd.Function), its weights stay float32.
+   (linear_f8, whose gradient is linear_f8_backward), its weights stay float32.
 2. The trained weights are quantised once (quantize_f8, 128 x 128 tiles) and serve single tokens with
    scaled_gemm_f8, and a mixture-of-experts layer with 8-bit weights decodes the same tokens (moe_layer_f8).
 """
@@ -17,17 +17,6 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import exact_modular_int8_gb300 as rg  # noqa: E402
 
 
-class LinearF8(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, w):
-        y, ctx.kept = rg.linear_f8(x, w, sync=False)
-        return y
-
-    @staticmethod
-    def backward(ctx, dy):
-        return rg.linear_f8_backward(dy, ctx.kept, sync=False)
-
-
 def train(steps=40, tokens=512, features=384, outputs=256, seed=0):
     """(losses, weights) of a layer that learns another layer's outputs."""
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -37,7 +26,8 @@ def train(steps=40, tokens=512, features=384, outputs=256, seed=0):
     for _ in range(steps):
         x = torch.randn((tokens, features), generator=g, device="cuda").to(torch.bfloat16)
         want = x.float() @ target.t()
-        loss = (LinearF8.apply(x, w).float() - want).square().mean()
+        y, _ = rg.linear_f8(x, w, sync=False)
+        loss = (y.float() - want).square().mean()
         loss.backward()
         with torch.no_grad():
             w -= 100.0 * w.grad

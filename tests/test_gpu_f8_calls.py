@@ -163,3 +163,48 @@ def test_status_of_a_captured_call(rg):  # noqa: F811
     graph.replay()
     assert rg.status(ws) == rg.RG_OK
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("dtype,wtype", [(torch.bfloat16, torch.float32), (torch.float16, torch.bfloat16),
+                                         (torch.float32, torch.float16)])
+def test_linear_has_a_gradient(rg, dtype, wtype):  # noqa: F811
+    """autograd through linear_f8 gives what linear_f8_backward gives, for either input alone too."""
+    x, w = normal((70, 200), 1, 1.0, dtype).cuda(), normal((96, 200), 2, 0.1, wtype).cuda()
+    dy = normal((70, 96), 3, 1.0, dtype).cuda()
+    want, saved = rg.linear_f8(x, w)
+    dx, dw = rg.linear_f8_backward(dy, saved, dw_dtype=wtype)
+    for needs in ((True, True), (True, False), (False, True)):
+        a, b = (t.clone().requires_grad_(n) for t, n in zip((x, w), needs))
+        y, kept = rg.linear_f8(a, b, sync=False)
+        assert y.requires_grad and torch.equal(y, want)
+        assert all(torch.equal(p, q) for p, q in zip(rg.linear_f8_backward(dy, kept, dw_dtype=wtype), (dx, dw)))
+        y.backward(dy)
+        for t, n, g in ((a, needs[0], dx), (b, needs[1], dw)):
+            assert (t.grad is not None) == n and (not n or (t.grad.dtype == t.dtype and torch.equal(t.grad, g)))
+        with torch.no_grad():
+            y, _ = rg.linear_f8(a, b)
+        assert not y.requires_grad and torch.equal(y, want)
+    a = x.clone().requires_grad_()
+    (grad,) = torch.autograd.grad(rg.linear_f8(a, w)[0].sum(), a)  # an expanded gradient
+    assert torch.equal(grad, rg.linear_f8_backward(torch.ones_like(want), saved)[0])
+
+
+def test_calls_without_a_gradient_do_not_cut_it_silently(rg):  # noqa: F811
+    x, w = normal((5, 256), 1).cuda(), normal((96, 256), 2).cuda()
+    q, s = rg.quantize_f8(x)
+    qw, sw = rg.quantize_f8(w, "tiles")
+    args = [a.cuda() for a in moe_inputs(5, 256, 64, 8, torch.bfloat16, 3)]
+    gemm = lambda sa, **kw: rg.scaled_gemm_f8(q, sa, qw, sw, transb=True, **kw)  # noqa: E731
+    experts = lambda t, **kw: rg.moe_layer_f8(t, *args[1:], 2, **kw)  # noqa: E731
+    for call, t in ((gemm, s), (experts, args[0])):
+        want, needs = call(t), t.clone().requires_grad_()
+        y = call(needs, sync=False)
+        assert torch.equal(y, want) and y.requires_grad
+        with pytest.raises(NotImplementedError):
+            y.sum().backward()
+        with pytest.raises(ValueError):
+            call(needs, out=torch.empty_like(want))
+        with torch.no_grad():
+            out = torch.empty_like(want)
+            assert call(needs, out=out) is out and torch.equal(out, want)
+            assert not call(needs).requires_grad
