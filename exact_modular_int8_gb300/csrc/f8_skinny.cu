@@ -98,7 +98,10 @@ __global__ void __launch_bounds__(kThreads) f8_skinny_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   wait_for_predecessor();
   allow_dependents();
-  if (blockIdx.x == 0 && threadIdx.x == 0 && !p.keep_status) p.plan->status = 0;  // no wait here that could fail
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !p.keep_status) {  // no wait here that could fail
+    p.plan->status = 0;
+    p.plan->timeout_where = 0;
+  }
   const uint32_t ring = su32(smem) + 2 * S::kRed + warp * S::kRing * S::kPiece;
 
   // Copies of the next piece: 128-block pkb of tile pt.  Row r's 16-byte chunk c

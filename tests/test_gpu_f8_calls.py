@@ -208,3 +208,23 @@ def test_calls_without_a_gradient_do_not_cut_it_silently(rg):  # noqa: F811
             out = torch.empty_like(want)
             assert call(needs, out=out) is out and torch.equal(out, want)
             assert not call(needs).requires_grad
+
+
+def test_few_row_product_clears_an_earlier_time_out(rg):  # noqa: F811
+    """Both words of an earlier call's time-out, the status and where it happened, are gone after the next call."""
+    lib = rg.library()
+    q, s = rg.quantize_f8(normal((300, 256), 1).cuda())
+    qw, sw = rg.quantize_f8(normal((256, 256), 2).cuda(), "tiles")
+    ws = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    words = lambda: (int(ws[:4].view(torch.int32)), int(ws[136:140].view(torch.int32)))  # noqa: E731
+    old = lib.rg_set_wait_limit_ns(50_000_000)
+    try:
+        lib.rg_inject_fault(1)
+        with pytest.raises(rg.ResGemmError):
+            rg.scaled_gemm_f8(q, s, qw, sw, transb=True, ws=ws)
+        assert words()[0] == rg.RG_ERR_TIMEOUT and words()[1] != 0
+    finally:
+        lib.rg_inject_fault(0)
+        lib.rg_set_wait_limit_ns(old)
+    rg.scaled_gemm_f8(q[:3], s[:3], qw, sw, transb=True, ws=ws)
+    assert words() == (0, 0)
