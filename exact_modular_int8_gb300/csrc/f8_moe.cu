@@ -100,12 +100,12 @@ __device__ __forceinline__ void from_f(float v, __half& o) { o = __float2half_rn
 __device__ __forceinline__ void from_f(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
 
 // The power of two that brings a largest magnitude (as bits) to [2^14, 2^15),
-// and its inverse.  Zero, inf and NaN rows are left alone; the exponent is
-// bounded so that both stay normal.
+// and its inverse.  A row with an inf or NaN is scaled as if its largest were
+// finite, so that its other entries stay finite in fp16; a row of zeros is left
+// alone; the exponent is bounded so that both stay normal.
 __device__ __forceinline__ float2 pow2_scale(uint32_t max_bits) {
-  int e = (int)(max_bits >> 23) - 127;
-  if (max_bits == 0 || e == 128) return make_float2(1.0f, 1.0f);
-  e = max(e, -110);
+  if (max_bits == 0) return make_float2(1.0f, 1.0f);
+  const int e = min(max((int)(max_bits >> 23) - 127, -110), 127);
   return make_float2(__int_as_float((127 + 14 - e) << 23), __int_as_float((127 - 14 + e) << 23));
 }
 
@@ -601,8 +601,8 @@ struct Phase {
     const __half2 h = __floats2half2_rn(a * scale, b * scale);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
-  // Both terms of two entries.  The difference is exact in fp32; an entry beyond
-  // fp16 (of a row with an inf or NaN) has its first term alone.
+  // Both terms of two entries.  The difference is exact in fp32; an inf or NaN has
+  // its first term alone.
   static __device__ __forceinline__ uint2 half_terms(float a, float b, float scale) {
     const float x = a * scale, y = b * scale;
     const __half2 h = __floats2half2_rn(x, y);

@@ -40,3 +40,22 @@ def test_gated_product_keeps_its_low_bits(rg, t, i, dtype):  # noqa: F811
                         one(2 * i, h), f8(w2), one(h, i), 1)
     got = Y.double().cpu().numpy()
     assert (np.abs(got - y) <= err + U[dtype] * (np.abs(y) + err) + 2.0**-25).all(), np.abs(got - y).max()
+
+
+def test_overflowed_gated_product(rg):  # noqa: F811
+    """A gated product that leaves fp32's range in one place: outputs that take it are inf with the sign of its weight
+    (the other, finite entries must not become inf too and make them NaN)."""
+    t, h, i = 5, 32, 144
+    x = torch.zeros((t, h), dtype=torch.bfloat16)
+    x[:, 0], x[:, 1] = 2.0**60, 2.0**40
+    w13, w2 = torch.zeros((1, 2 * i, h)), torch.zeros((1, h, i))
+    w13[0, 7, 0] = w13[0, i + 7, 0] = 256.0  # h[7] = 2^136
+    w13[0, 130, 0], w13[0, i + 130, 1] = 1.0, 1.0  # h[130] = 2^100
+    w13[0, 131, 1] = w13[0, i + 131, 1] = 1.0  # h[131] = 2^80
+    w2[0, :, 7] = torch.tensor([1.0, -1.0] * (h // 2))
+    w2[0, :, 130] = -w2[0, :, 7]
+    w2[0, :, 131] = -2.0 * w2[0, :, 7]
+    one = lambda n, k: torch.ones((1, blocks(n), blocks(k)), device="cuda")  # noqa: E731
+    Y = rg.moe_layer_f8(x.cuda(), torch.zeros((1, h), dtype=torch.bfloat16, device="cuda"), w13.to(F8).cuda(),
+                        one(2 * i, h), w2.to(F8).cuda(), one(h, i), 1)
+    assert torch.equal(Y.float().cpu(), (w2[0, :, 7] * float("inf")).expand(t, h))
