@@ -783,6 +783,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                  "r"((uint32_t)(2 * BN2)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
+  __syncwarp();  // the cluster's barrier is for whole warps
   tc_fence_before();
   cluster_sync();  // barriers of both CTAs are initialised before any remote arrival
   tc_fence_after();

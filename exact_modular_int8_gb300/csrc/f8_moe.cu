@@ -267,6 +267,7 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(kRouterThreads) moe_
     if (p.E <= 128) choose<4>(p, t, logit);
     else choose<kMaxE / 32>(p, t, logit);
   }
+  __syncwarp();  // the barrier below is for whole warps
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
