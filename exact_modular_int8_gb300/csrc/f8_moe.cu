@@ -895,28 +895,38 @@ int k_split(long long K) {
   while (ks < 8 && nkb >= 16 * ks) ks *= 2;
   return ks;
 }
-// The call's shared memory: room for the tokens that nearly every expert gets
-// in one pass (the mean of even routing and two deviations), at least three
-// pieces per warp (two where one token leaves no room for three: I above
-// 24960), and what is left to deeper rings.
+// The call's shared memory: in each product room for the tokens that nearly every
+// expert gets in one pass (the mean of even routing and two deviations), as far
+// as it goes, at least three pieces per warp (two where one token leaves no
+// room for three: I above 24960), and what is left to deeper rings.
 void plan_smem(MoeParams& p) {
   const int bytes_up = token_bytes(p.H, false), bytes_down = token_bytes(p.I, true);
   const int wide = bytes_up > bytes_down ? bytes_up : bytes_down, ring1 = kWarps * kPiece;
   const double mean = (double)p.T * p.top_k / p.E;
-  int tokens = (int)std::ceil(mean + 2.0 * std::sqrt(mean));
-  if (tokens > 8) tokens = (tokens + 7) / 8 * 8;
-  if (tokens > 8 * kMaxNT) tokens = 8 * kMaxNT;
-  if (tokens > p.T) tokens = p.T;
+  int want = (int)std::ceil(mean + 2.0 * std::sqrt(mean));
+  if (want > 8) want = (want + 7) / 8 * 8;
+  if (want > 8 * kMaxNT) want = 8 * kMaxNT;
+  if (want > p.T) want = p.T;
   auto tiles = [](int n) { return n <= 8 ? 1 : kMaxNT; };
   auto ld = [&](int n) { return 16 * tiles(n) + 4; };  // two halves, see unit()
   p.ring = kMinRing;
   auto room_for = [&](int n) { return kSmemBytes - kFixedBytes - p.ring * ring1 - kWarps * 16 * 4 * ld(n); };
   if (wide > room_for(1)) p.ring = kTightRing;
-  while (tokens * wide > room_for(tokens)) tokens = tokens > 8 ? (tokens - 1) / 8 * 8 : tokens - 1;
-  int room = room_for(tokens) - tokens * wide;
-  for (; p.ring < kMaxRing && room >= ring1; ++p.ring) room -= ring1;
+  if (want > 8 && wide > room_for(want)) want = 8;  // the second column tile's sums take room too
+  auto most = [&](int bytes) {
+    int n = want;
+    while (n * bytes > room_for(n)) n = n > 8 ? (n - 1) / 8 * 8 : n - 1;
+    return n;
+  };
+  int n_up = most(bytes_up), n_down = most(bytes_down);
+  const int tokens = n_up > n_down ? n_up : n_down;
+  while (n_up * bytes_up > room_for(tokens)) --n_up;
+  while (n_down * bytes_down > room_for(tokens)) --n_down;
+  const int used = n_up * bytes_up > n_down * bytes_down ? n_up * bytes_up : n_down * bytes_down;
+  int room = room_for(tokens);
+  for (; p.ring < kMaxRing && room - used >= ring1; ++p.ring) room -= ring1;
   auto fit = [&](int bytes) {
-    int n = (tokens * wide + room) / bytes;
+    int n = room / bytes;
     if (n > 8) n = n / 8 * 8;
     return n > 8 * tiles(tokens) ? 8 * tiles(tokens) : n;
   };
