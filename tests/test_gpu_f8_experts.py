@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_util import rg  # noqa: F401
-from test_gpu_f8 import F8, U, blocks
+from test_gpu_f8 import F8, U, blocks, check_moe, moe_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,28 @@ def test_overflowed_gated_product(rg):  # noqa: F811
     Y = rg.moe_layer_f8(x.cuda(), torch.zeros((1, h), dtype=torch.bfloat16, device="cuda"), w13.to(F8).cuda(),
                         one(2 * i, h), w2.to(F8).cuda(), one(h, i), 1)
     assert torch.equal(Y.float().cpu(), (w2[0, :, 7] * float("inf")).expand(t, h))
+
+
+# Widths of 16 blocks of 128 and more split k over warps (2048: two of them, 4096: four, 8192: eight); 16 tokens
+# on one expert take two column tiles, and tokens of 16384 and more entries fit a few at a time, so that an expert takes
+# several passes.
+@pytest.mark.parametrize("t,h,i,e,top_k,renorm,dtype", [
+    (3, 2048, 2064, 4, 2, True, torch.bfloat16), (13, 2048, 2064, 1, 1, True, torch.float16),
+    (16, 1936, 80, 1, 1, False, torch.bfloat16), (17, 4112, 272, 3, 1, True, torch.bfloat16),
+    (9, 272, 8208, 2, 1, False, torch.float16), (64, 2064, 144, 5, 2, True, torch.bfloat16),
+    (17, 16384, 32, 1, 1, True, torch.bfloat16), (5, 32768, 48, 1, 1, True, torch.float16),
+    (6, 48, 16400, 1, 1, True, torch.bfloat16), (3, 64, 24960, 1, 1, True, torch.bfloat16),
+    (3, 64, 24976, 1, 1, True, torch.float16), (4, 48, 32768, 1, 1, True, torch.bfloat16)])
+def test_wide_layers(rg, t, h, i, e, top_k, renorm, dtype):  # noqa: F811
+    check_moe(rg, moe_inputs(t, h, i, e, dtype, 17 * t + h + i), top_k, renorm)
+
+
+@pytest.mark.parametrize("h,i", [(2048, 2048), (4096, 1040)])
+def test_a_token_alone_and_in_a_batch_of_a_wide_layer(rg, h, i):  # noqa: F811
+    """Equal calls give equal bits, and a token's result does not depend on what comes with it."""
+    args = [a.cuda() for a in moe_inputs(16, h, i, 3, torch.bfloat16, h + i)]
+    Y = rg.moe_layer_f8(*args, 2)
+    for _ in range(3):
+        assert torch.equal(rg.moe_layer_f8(*args, 2), Y)
+    for t in range(16):
+        assert torch.equal(rg.moe_layer_f8(args[0][t : t + 1], *args[1:], 2)[0], Y[t])
