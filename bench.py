@@ -21,6 +21,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -225,10 +226,26 @@ def run_reference(args):
 # ---------------------------------------------------------------------------
 
 
+def kernel_source_sha256(path_src):
+    """SHA-256 of a kernel's source and of the headers beside it that it includes, directly or not."""
+    sha, todo, seen = hashlib.sha256(), [path_src], set()
+    while todo:
+        path = todo.pop(0)
+        if path in seen:
+            continue
+        seen.add(path)
+        with open(path, "rb") as f:
+            text = f.read()
+        sha.update(text)
+        todo += [os.path.join(os.path.dirname(path), name.decode())
+                 for name in re.findall(rb'^#include "([^"/]+)"', text, re.M)]
+    return sha.hexdigest()
+
+
 def gemm_traffic_record(path_src):
     """Per-launch DRAM bytes of the GEMM kernel from the committed ncu summary
     (profiles/residue_gemm_traffic.txt), if it was taken on the current kernel
-    source; else None."""
+    source and headers; else None."""
     rec_path = os.path.join(ROOT, "profiles", "residue_gemm_traffic.txt")
     try:
         rec = {}
@@ -238,9 +255,7 @@ def gemm_traffic_record(path_src):
                 if line and not line.startswith("#") and "=" in line:
                     k, v = line.split("=", 1)
                     rec[k.strip()] = v.strip()
-        with open(path_src, "rb") as f:
-            sha = hashlib.sha256(f.read()).hexdigest()
-        return rec if rec.get("source_sha256") == sha else None
+        return rec if rec.get("source_sha256") == kernel_source_sha256(path_src) else None
     except OSError:
         return None
 
