@@ -1054,17 +1054,31 @@ cudaError_t f8_device(int dev, F8Device& out) {
   return cudaSuccess;
 }
 
+// Where the warp-level kernel, whose warps split K but whose blocks do not, is
+// faster than padded tiles, which do.  One launch after another, us, the
+// warp-level kernel first; rows x columns x K:
+//   to 8 rows     at nearly every size (8 x 1024 x 4096 3.5 / 4.6, 8 x 8192 x 4096 9.6
+//                 / 12.6), but not few columns and a long K (1 x 512 x 8192 5.6 / 5.3)
+//   to 16 rows    while K is short (16 x 512 x 2048 3.5 / 4.4, 16 x 8192 x 2048 7.1 /
+//                 7.6), longer with many columns (16 x 2048 x 4096 5.6 / 5.8, 16 x 8192
+//                 x 4096 11.1 / 12.0, but 16 x 512 x 4096 5.5 / 4.6 and 16 x 4096 x 8192
+//                 10.2 / 9.5); from 16384 columns on about equal
+//   to 32 rows    while B is small (32 x 2048 x 2048 3.5 / 4.7, 32 x 4096 x 1024 3.9 /
+//                 4.7, 32 x 4096 x 2048 5.9 / 5.8), within two tiles of 16 columns for
+//                 each SM (24 x 8192 x 512 5.1 / 4.3) and a short K (24 x 1024 x 4096
+//                 5.1 / 4.8)
+bool few_rows(long long M, long long N, long long K) {
+  if (M <= 8) return N > 1024 || K < 8192;
+  if (M <= 16) return K <= 2048 || (K <= 4096 && N >= 2048);
+  return M <= kSkinnyRows && N <= 4864 && K <= 2048 && N * K <= (1LL << 22);
+}
+
 }  // namespace
 
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, int fault,
                            unsigned long long wait_ns) {
   const int variant = gemm_variant();
-  // Few rows: up to 16 the warp-level kernel is faster at every size measured
-  // (8192 x 4096: 8.1 us for one row, 10.3 for 16, against 12.5 and 11.4 with padded
-  // tiles); from 17 to 32 while B is small enough for latency to count (24 rows:
-  // 3.3 against 4.7 us at 2048 x 2048, 5.4 against 5.7 at 4096 x 2048, 9.2 against
-  // 7.1 at 4096 x 4096).
-  if (variant == 0 && a.b_kmajor && (a.M <= 16 || (a.M <= kSkinnyRows && a.N * a.K <= (1LL << 22))))
+  if (variant == 0 && a.b_kmajor && few_rows(a.M, a.N, a.K))
     return launch_f8_skinny(a, plan, st);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
