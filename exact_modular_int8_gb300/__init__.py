@@ -69,7 +69,7 @@ EXPORTED = (
     "rg_solution_free", "rg_rational_reconstruct", "rg_big_gcd", "rg_set_crt_mode", "rg_set_stage_events",
     "rg_probe_mma_rate", "rg_big_mulmod", "quantize_f8", "scaled_gemm_f8",
     "moe_layer_f8", "moe_layer_f8_ws_bytes", "linear_f8", "linear_f8_backward", "linear_f8_saved_bytes",
-    "linear_f8_ws_bytes", "rg_hold_workspace",
+    "linear_f8_ws_bytes", "rg_hold_workspace", "rg_stream_capturing",
 )
 
 
@@ -191,6 +191,8 @@ def library():
                 getattr(lib, f).restype = sz
             lib.moe_layer_f8_ws_bytes.argtypes = [i64, i64, i64, i64, ci]
             lib.moe_layer_f8_ws_bytes.restype = sz
+            lib.rg_stream_capturing.argtypes = [vp]
+            lib.rg_stream_capturing.restype = ci
             lib.rg_hold_workspace.argtypes = [vp, ci]
             lib.rg_hold_workspace.restype = ci
             lib.rg_noalloc_scratch_bytes.argtypes = []
@@ -249,7 +251,7 @@ _ws_cache: dict = {}
 
 def capturing(index) -> bool:
     """Whether the current stream of device `index` is being captured into a CUDA graph."""
-    if index is None or torch._C._cuda_getDevice() == index:
+    if torch._C._cuda_getDevice() == index:
         return torch._C._cuda_isCurrentStreamCapturing()
     with torch.cuda.device(index):
         return torch._C._cuda_isCurrentStreamCapturing()
@@ -259,10 +261,10 @@ def workspace(nbytes: int, device: torch.device, stream=None) -> torch.Tensor:
     """A device buffer of at least nbytes, reused across calls on one stream; a new one while the current
     stream is being captured into a CUDA graph (the call's status is then read from a workspace that the
     caller passes)."""
-    if capturing(device.index):
+    index = torch.cuda.current_device() if device.index is None else device.index
+    if capturing(index):
         return torch.empty(max(nbytes, 4096), dtype=torch.uint8, device=device)
-    stream = stream or torch.cuda.current_stream(device)
-    key = (device.index, stream.cuda_stream)
+    key = (index, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
         _ws_cache.pop(key, None)

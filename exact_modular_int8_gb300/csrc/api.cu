@@ -640,6 +640,15 @@ int rg_status(const void* ws, void* stream) {
   return finish(const_cast<void*>(ws), static_cast<cudaStream_t>(stream), RG_FLAG_SYNC);
 }
 
+int rg_stream_capturing(void* stream) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &st) != cudaSuccess) {
+    cudaGetLastError();  // the query's own failure is not the next call's
+    return 0;
+  }
+  return st != cudaStreamCaptureStatusNone;
+}
+
 const char* rg_strerror(int code) {
   switch (code) {
     case RG_OK: return "ok";

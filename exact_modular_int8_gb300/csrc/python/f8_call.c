@@ -26,14 +26,16 @@ typedef int (*linear_fn)(const void*, int, int64_t, const void*, int, int64_t, v
 typedef int (*backward_fn)(const void*, int, int64_t, const void*, size_t, void*, void*, int, int64_t, int64_t, int64_t,
                            unsigned, void*, size_t, void*);
 typedef size_t (*bytes_fn)(int64_t, int64_t, int64_t);
+typedef int (*capturing_fn)(void*);
 
 static quantize_fn lib_quantize;
 static gemm_fn lib_gemm;
 static linear_fn lib_linear;
 static backward_fn lib_backward;
 static bytes_fn lib_saved_bytes, lib_ws_bytes;
+static capturing_fn lib_capturing;
 static PyObject *types[3], *f8_type, *byte_type; /* torch dtypes by RG_TYPE_*, E4M3, uint8 */
-static PyObject *empty, *empty_strided, *raw_stream, *current_device, *capturing; /* torch functions */
+static PyObject *empty, *empty_strided, *raw_stream, *current_device; /* torch functions */
 static PyObject *workspaces, *raise_status;  /* the binding's workspace cache and error function */
 static PyObject *s_shape, *s_stride, *s_dtype, *s_device, *s_data_ptr, *s_get_device, *s_numel, *empty_names;
 
@@ -49,6 +51,18 @@ static int64_t as_int(PyObject* r) {
 }
 static int64_t call_int(PyObject* o, PyObject* name) { return as_int(PyObject_CallMethodNoArgs(o, name)); }
 
+static PyObject* pair_of(int64_t a, int64_t b) {
+  PyObject *t = PyTuple_New(2), *x = PyLong_FromLongLong(a), *y = PyLong_FromLongLong(b);
+  if (t && x && y) {
+    PyTuple_SET_ITEM(t, 0, x);
+    PyTuple_SET_ITEM(t, 1, y);
+    return t;
+  }
+  Py_XDECREF(t);
+  Py_XDECREF(x);
+  Py_XDECREF(y);
+  return NULL;
+}
 /* The two entries of a tuple; 0 if it is not a pair of integers. */
 static int two(PyObject* t, int64_t* a, int64_t* b) {
   int ok = 0;
@@ -66,13 +80,19 @@ typedef struct {
   void* p;
 } matrix;
 
-/* A matrix with contiguous rows of `type` on device `dev`; 0 to decline. */
-static int matrix_of(PyObject* t, PyObject* type, int64_t dev, matrix* x) {
-  int64_t s0, s1;
+/* The RG_TYPE_* of a tensor's dtype, or 3; E4M3 is 4. */
+static int type_of(PyObject* t) {
   PyObject* d = PyObject_GetAttr(t, s_dtype);
-  if (!d) return 0;
+  if (!d) return 3;
   Py_DECREF(d); /* dtypes live for good */
-  if (d != type || call_int(t, s_get_device) != dev) return 0;
+  int i = 0;
+  while (i < 3 && types[i] != d) ++i;
+  return d == f8_type ? 4 : i;
+}
+/* A matrix with contiguous rows on device `dev` (-1: known to be there); 0 to decline. */
+static int matrix_of(PyObject* t, int64_t dev, matrix* x) {
+  int64_t s0, s1;
+  if (dev >= 0 && call_int(t, s_get_device) != dev) return 0;
   if (!two(PyObject_GetAttr(t, s_shape), &x->m, &x->k) || !two(PyObject_CallMethodNoArgs(t, s_stride), &s0, &s1))
     return 0;
   if (x->k > 1 && s1 != 1) return 0;
@@ -81,25 +101,21 @@ static int matrix_of(PyObject* t, PyObject* type, int64_t dev, matrix* x) {
   x->p = (void*)(uintptr_t)call_int(t, s_data_ptr);
   return x->p && !PyErr_Occurred();
 }
-/* Contiguous, of this shape. */
-static int scales_of(PyObject* t, int64_t dev, int64_t m, int64_t k, matrix* x) {
-  return matrix_of(t, types[RG_TYPE_F32], dev, x) && x->m == m && x->k == k && x->ld == k;
+/* fp32 scales; 0 to decline */
+static int scales_of(PyObject* t, int64_t dev, matrix* x) {
+  return type_of(t) == RG_TYPE_F32 && matrix_of(t, dev, x) && x->ld == x->k;
 }
 /* E4M3 rows on 16-byte boundaries. */
 static int values_of(PyObject* t, int64_t dev, matrix* x) {
-  if (!matrix_of(t, f8_type, dev, x)) return 0;
+  if (type_of(t) != 4 || !matrix_of(t, dev, x)) return 0;
   if (x->m == 1) x->ld = up16(x->ld);
   return !(x->ld & 15) && !((uintptr_t)x->p & 15);
 }
 
 /* A floating-point matrix with contiguous rows, and its RG_TYPE_*; -1 to decline. */
 static int real_of(PyObject* t, int64_t dev, matrix* x) {
-  PyObject* type = PyObject_GetAttr(t, s_dtype);
-  if (!type) return -1;
-  Py_DECREF(type);
-  int i = 0;
-  while (i < 3 && types[i] != type) ++i;
-  return i < 3 && matrix_of(t, type, dev, x) ? i : -1;
+  const int i = type_of(t);
+  return i < 3 && matrix_of(t, dev, x) ? i : -1;
 }
 
 /* An uninitialised tensor of this size (stolen) on a device. */
@@ -111,7 +127,7 @@ static PyObject* new_tensor(PyObject* size, PyObject* type, PyObject* device) {
   return t;
 }
 static PyObject* new_matrix(int64_t m, int64_t k, PyObject* type, PyObject* device) {
-  return new_tensor(Py_BuildValue("(LL)", (long long)m, (long long)k), type, device);
+  return new_tensor(pair_of(m, k), type, device);
 }
 static void* data_of(PyObject* t) { return (void*)(uintptr_t)call_int(t, s_data_ptr); }
 
@@ -125,10 +141,8 @@ typedef struct {
 } workspace;
 /* 0 to decline */
 static int workspace_of(int64_t dev, void* stream, size_t need, workspace* w) {
-  PyObject* captured = PyObject_CallNoArgs(capturing);
-  Py_XDECREF(captured);
-  if (captured != Py_False) return 0;
-  PyObject* key = Py_BuildValue("(LN)", (long long)dev, PyLong_FromVoidPtr(stream));
+  if (lib_capturing(stream)) return 0;
+  PyObject* key = pair_of(dev, (int64_t)(uintptr_t)stream);
   if (!key) return 0;
   w->tensor = PyDict_GetItemWithError(workspaces, key); /* borrowed */
   Py_DECREF(key);
@@ -183,8 +197,7 @@ static int new_quantised(int64_t m, int64_t k, int64_t scale_rows, PyObject* dev
   if (r->ld == k) {
     r->q = new_matrix(m, k, f8_type, device);
   } else {
-    PyObject* args[4] = {Py_BuildValue("(LL)", (long long)m, (long long)k),
-                         Py_BuildValue("(LL)", (long long)r->ld, 1LL), f8_type, device};
+    PyObject* args[4] = {pair_of(m, k), pair_of(r->ld, 1), f8_type, device};
     r->q = args[0] && args[1] ? PyObject_Vectorcall(empty_strided, args, 2, empty_names) : NULL;
     Py_XDECREF(args[0]);
     Py_XDECREF(args[1]);
@@ -208,7 +221,7 @@ static PyObject* quantize(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   void* stream;
   matrix x;
   if (PyErr_Occurred() || !place(a[0], &dev, &stream)) return decline();
-  const int t = real_of(a[0], dev, &x);
+  const int t = real_of(a[0], -1, &x);
   if (t < 0) return decline();
   PyObject* device = PyObject_GetAttr(a[0], s_device);
   if (!device) return decline();
@@ -247,11 +260,12 @@ static PyObject* gemm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred() || transb < 0 || !place(a[0], &dev, &stream)) return decline();
   int t = 0;
   while (t < 3 && types[t] != a[4]) ++t;
-  if (t == 3 || !values_of(a[0], dev, &A) || !values_of(a[2], dev, &B)) return decline();
+  if (t == 3 || !values_of(a[0], -1, &A) || !values_of(a[2], dev, &B)) return decline();
   const int64_t N = transb ? B.m : B.k, K = A.k, kb = blocks(K), nb = blocks(N);
-  if (K != (transb ? B.k : B.m) || !scales_of(a[1], dev, A.m, kb, &SA)) return decline();
-  if (scales_of(a[3], dev, transb ? nb : kb, transb ? kb : nb, &SB)) flags |= RG_FLAG_TILE_B;
-  else if (PyErr_Occurred() || !scales_of(a[3], dev, transb ? N : kb, transb ? kb : N, &SB)) return decline();
+  if (K != (transb ? B.k : B.m) || !scales_of(a[1], dev, &SA) || SA.m != A.m || SA.k != kb) return decline();
+  if (!scales_of(a[3], dev, &SB) || (transb ? SB.k : SB.m) != kb) return decline();
+  if ((transb ? SB.m : SB.k) == nb) flags |= RG_FLAG_TILE_B;
+  else if ((transb ? SB.m : SB.k) != N) return decline();
   if (transb) flags |= RG_FLAG_TRANS_B;
   PyObject* device = PyObject_GetAttr(a[0], s_device);
   if (!device) return decline();
@@ -284,7 +298,7 @@ static PyObject* linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   void* stream;
   matrix X, W;
   if (PyErr_Occurred() || !place(a[0], &dev, &stream)) return decline();
-  const int tx = real_of(a[0], dev, &X), tw = tx < 0 ? -1 : real_of(a[1], dev, &W);
+  const int tx = real_of(a[0], -1, &X), tw = tx < 0 ? -1 : real_of(a[1], dev, &W);
   if (tw < 0 || X.k != W.k) return decline();
   const int64_t M = X.m, N = W.m, K = X.k;
   const size_t kept_bytes = lib_saved_bytes(M, N, K);
@@ -323,7 +337,7 @@ static PyObject* backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   void* stream;
   matrix dY;
   if (PyErr_Occurred() || !place(a[0], &dev, &stream)) return decline();
-  const int t = real_of(a[0], dev, &dY);
+  const int t = real_of(a[0], -1, &dY);
   int tw = 0;
   while (tw < 3 && types[tw] != a[5]) ++tw;
   if (t < 0 || tw == 3 || dY.m != M || dY.k != N || K <= 0 || call_int(a[1], s_get_device) != dev) return decline();
@@ -356,14 +370,14 @@ static PyObject* backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return r ? finish(rc, "linear_f8_backward", r) : NULL;
 }
 
-/* setup((six addresses), (f32, f16, bf16), f8, uint8, empty, empty_strided, raw_stream, current_device, capturing,
- * workspaces, raise) */
+/* setup((seven addresses), (f32, f16, bf16), f8, uint8, empty, empty_strided, raw_stream, current_device, workspaces,
+ * raise) */
 static PyObject* setup(PyObject* self, PyObject* args) {
   (void)self;
-  unsigned long long f[6];
+  unsigned long long f[7];
   PyObject *t0, *t1, *t2;
-  if (!PyArg_ParseTuple(args, "(KKKKKK)(OOO)OOOOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &t0, &t1, &t2, &f8_type,
-                        &byte_type, &empty, &empty_strided, &raw_stream, &current_device, &capturing, &workspaces,
+  if (!PyArg_ParseTuple(args, "(KKKKKKK)(OOO)OOOOOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &t0, &t1, &t2,
+                        &f8_type, &byte_type, &empty, &empty_strided, &raw_stream, &current_device, &workspaces,
                         &raise_status))
     return NULL;
   lib_quantize = (quantize_fn)(uintptr_t)f[0];
@@ -372,11 +386,12 @@ static PyObject* setup(PyObject* self, PyObject* args) {
   lib_backward = (backward_fn)(uintptr_t)f[3];
   lib_saved_bytes = (bytes_fn)(uintptr_t)f[4];
   lib_ws_bytes = (bytes_fn)(uintptr_t)f[5];
+  lib_capturing = (capturing_fn)(uintptr_t)f[6];
   types[RG_TYPE_F32] = t0;
   types[RG_TYPE_F16] = t1;
   types[RG_TYPE_BF16] = t2;
   PyObject* keep[] = {t0,         t1,         t2,         f8_type,        byte_type,  empty, empty_strided,
-                      raw_stream, current_device, capturing, workspaces, raise_status};
+                      raw_stream, current_device, workspaces, raise_status};
   for (size_t i = 0; i < sizeof keep / sizeof *keep; ++i) Py_INCREF(keep[i]); /* for the life of the process */
   s_shape = PyUnicode_InternFromString("shape");
   s_stride = PyUnicode_InternFromString("stride");

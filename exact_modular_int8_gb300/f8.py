@@ -45,10 +45,10 @@ def _native():
         loader.exec_module(m)
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
         entries = (lib.quantize_f8, lib.scaled_gemm_f8, lib.linear_f8, lib.linear_f8_backward,
-                   lib.linear_f8_saved_bytes, lib.linear_f8_ws_bytes)
+                   lib.linear_f8_saved_bytes, lib.linear_f8_ws_bytes, lib.rg_stream_capturing)
         m.setup(tuple(address(f) for f in entries), (torch.float32, torch.float16, torch.bfloat16), F8, torch.uint8,
-                torch.empty, torch.empty_strided, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice,
-                torch._C._cuda_isCurrentStreamCapturing, _ws_cache, _check)
+                torch.empty, torch.empty_strided, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache,
+                _check)
         _call = m
     return _call
 

@@ -553,6 +553,10 @@ int rg_set_crt_mode(int mode);
  * RG_ERR_TIMEOUT) or RG_ERR_CUDA. */
 int rg_status(const void* ws, void* stream);
 
+/* 1 while `stream` is being captured into a CUDA graph, else 0.  A workspace
+ * that a captured call uses belongs to the graph as long as it is replayed. */
+int rg_stream_capturing(void* stream);
+
 /* The i-th prime of the residue base, largest first (251, 241, ...);
  * 0 if i is out of range. */
 int rg_prime(int i);
