@@ -84,6 +84,7 @@ struct MoeParams {
   int cap_up, cap_down;  // tokens per pass
   int ring;              // pieces per warp
   int red_ld;            // columns of the warps' partial sums, padded
+  int together;          // segments are staged together
   int red_off, cols_off, ring_off;  // shared memory beyond struct Smem
   unsigned long long wait_ns;
   DevPlan* plan;
@@ -781,11 +782,13 @@ struct Phase {
     slot = 0;
     for (int s = 0; s < p.ring - 1; ++s) copy_next(s);
     if (!before_use()) return false;
-    // Segments whose tokens fit into the staged columns together are staged together:
-    // a CTA that meets the border between two experts would otherwise do one part
-    // after the other, and the grid waits for it (7 tokens, 2 of 16 experts of 1808 x
-    // 1552: 39 us, 47 one after the other; 16 tokens, 4 of 64 of 4096 x 1024: 111 and
-    // 117; 64 tokens, 8 of 128: 295 and 289).
+    // While experts get few tokens, segments whose tokens fit into the staged columns
+    // together are staged together: a CTA that meets the border between two experts
+    // would otherwise do one part after the other, and the grid waits for it (7 tokens,
+    // 2 of 16 experts of 1808 x 1552: 39.1 us, 45.7 one after the other; 8 tokens, 4 of
+    // 16 of 2048 x 1024: 38.8 and 45.5; 32 tokens, 4 of 64: 88.3 and 93.2).  With more
+    // than two tokens to an expert one after the other is faster (48 tokens, 8 of 128
+    // experts of 4096 x 1024: 291.6 us, together 301; 64 tokens: 308 and 316).
     int mine = u0 + group;
     for (int at = u0, a = u0 < u1 ? sm.r.first_active : 0; at < u1;) {
       __syncthreads();
@@ -793,7 +796,7 @@ struct Phase {
       int k = 0;
       while (end < u1) {
         Segment g1 = segment(end, a);
-        if (used && used + g1.n > cap()) break;
+        if (used && (!p.together || used + g1.n > cap())) break;
         g1.c0 = used;
         if (threadIdx.x == 0) sm.segs[k] = g1;
         if ((int)threadIdx.x < g1.n) sm.slot[used + threadIdx.x] = sm.r.order[g1.first + threadIdx.x];
@@ -930,6 +933,7 @@ void plan_smem(MoeParams& p) {
     if (n > 8) n = n / 8 * 8;
     return n > 8 * tiles(tokens) ? 8 * tiles(tokens) : n;
   };
+  p.together = p.T * p.top_k <= 2 * p.E;
   p.cap_up = fit(bytes_up);
   p.cap_down = fit(bytes_down);
   p.red_ld = ld(tokens);
@@ -941,7 +945,7 @@ void plan_smem(MoeParams& p) {
 cudaError_t launch_moe_f8(const MoeArgs& a, DevPlan* plan, void* scratch, cudaStream_t st,
                           unsigned long long wait_ns) {
   MoeParams p{a.X, a.WR, a.W13, a.S13, a.W2, a.S2, a.Y, (int)a.T, (int)a.H, (int)a.I, (int)a.E, (int)a.top_k, a.type,
-              a.renorm ? 1 : 0, k_split(a.H), k_split(a.I), 0, 0, 0, 0, 0, 0, 0, wait_ns, plan, {}};
+              a.renorm ? 1 : 0, k_split(a.H), k_split(a.I), 0, 0, 0, 0, 0, 0, 0, 0, wait_ns, plan, {}};
   plan_smem(p);
   layout(a.T, a.H, a.I, a.top_k, static_cast<uint8_t*>(scratch), &p.w);
   int dev = 0, sms = 0;
