@@ -211,7 +211,8 @@ __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar_cluster
 // before most of the arithmetic.
 //
 // With one scale for all the columns (TILE_B) a lane holds a row: acc += p s, the
-// column scale already in s.  (8192 x 8192 x 4096: 239 us, 284 in the other form.)
+// column scale already in s.  (8192 x 8192 x 4096, at this choice: 239 us, 284 in the
+// other form.)
 template <int COLS, bool TILE_B>
 struct Sums {
   static constexpr int kRows = 1;
@@ -302,7 +303,8 @@ struct Sums<COLS, false> {
 // For products that one wave of CTAs holds, where the time is the latency of
 // set-up, K / S / 128 blocks of 0.3 us and the join: 512 x 4096 x 4096 12.7 us,
 // 128 x 4096 x 4096 (S = 4) 7.9 us, 1000 x 1544 x 2056 10.1 us, one after another
-// (13.8, 8.2 and 10.7 with a row of the join at a time).
+// with operands in L2 (13.8, 8.2 and 10.7 with a row of the join at a time); with
+// operands from memory 13.4, 9.2 and 10.2.
 // ---------------------------------------------------------------------------
 constexpr int BN1 = 128;
 constexpr int STAGES1 = 6;
@@ -607,15 +609,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // MMAs, of which only two are in flight; the halves' chains are shorter and
 // interleave.
 //
-// 8192 x 8192 x 4096: 239 us, 2300 TFLOP/s, half of the E4M3 instruction rate (the
+// 8192 x 8192 x 4096: 236 us, 2330 TFLOP/s, half of the E4M3 instruction rate (the
 // tensor pipe is active 46% of the time).  A block of a tile takes 1050 cycles
 // where its MMAs take 512 and the same loop with an empty epilogue 720: an
 // epilogue warp waits for 165, has read its columns 440 later and needs the rest
 // for the multiply-adds and a share of the stores, with two warps to a scheduler.
 // More epilogue warps (16: spills, 293 us), 256 x 192 tiles with twelve warps (271
 // us) and single-CTA 128 x 192 tiles (261 us) were slower; one 256-column MMA for
-// both halves took the same time.  With a scale for each of B's rows: 365 us, 1535
-// cycles a block; 2048 x 4096 x 8100 106 us.
+// both halves took the same time.  With a scale for each of B's rows: 366 us, 1535
+// cycles a block (380 us with fp32 results); 2048 x 4096 x 8100 108 us.
 //
 // The block is launched with 168 registers a thread; the first warpgroup
 // (producer, MMA issue, scales) gives up 112 of them and the two epilogue

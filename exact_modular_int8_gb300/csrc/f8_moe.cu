@@ -20,15 +20,15 @@
 // fp32 and enters the second product, scaled the same way, as the sum of two
 // fp16 terms: h to 11 bits and what that leaves out.  Together they are within
 // 2^-23 of the entry or 2^-39 of the row's largest, as fp32 is, for twice that
-// product's MMAs (with the first term alone, 11 bits, 64 tokens take 311 us
+// product's MMAs (with the first term alone, 11 bits, 64 tokens took 311 us
 // instead of 317 and one token 28.7 instead of 30.1).  Each 128-block's sum is
 // scaled in fp32 and added to fp32 sums.
 //
-// 64 tokens through 128 experts of 4096 x 1024 (top 8): 317 us, the weights at
-// the copy rate 237; the two products stream at 6.3 TB/s, and the grid's meetings
-// wait for the slowest SM, 10% behind the median.  One token through 8 of 64
-// experts of 2048 x 1024: 30 us (7.6): router 4, routing 1.5, first product 9,
-// second 5, two meetings of the grid 4 and 1.5, sum 1, launches.
+// 64 tokens through 128 experts of 4096 x 1024 (top 8): 300 to 308 us, the weights
+// at the copy rate 237; the two products stream at 6.3 TB/s, and the grid's
+// meetings wait for the slowest SM, 10% behind the median.  One token through 8 of
+// 64 experts of 2048 x 1024: 30 us (7.6): router 4, routing 1.4, first product 9,
+// second 5, two meetings of the grid 4 and 1.4, sum 1, launches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

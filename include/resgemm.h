@@ -434,7 +434,8 @@ int rg_big_mulmod(const uint64_t* a, int al, const uint64_t* b, int bl, const ui
 /*
  * Quantises X [M][ldx] (M x K entries of x_type RG_TYPE_*).  For each block, a
  * = max |x| (at least 2^-60), scale = a / 448, value = 448 x / a rounded to the
- * nearest E4M3 value, ties to even.  A block holding an inf or NaN gets that
+ * nearest E4M3 value, ties to even.  The quotient is formed in fp32 first (0.875
+ * x, exact for 16-bit entries, over a / 512, correctly rounded).  A block holding an inf or NaN gets that
  * as its scale, and all of it stands for NaN.
  *   RG_F8_ROWS     blocks of 128 along each row: Q [M][ldq], S [M][ceil(K/128)]
  *   RG_F8_COLUMNS  blocks of 128 along each column, stored transposed:
@@ -509,10 +510,11 @@ int linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* sa
  * 128 tile of an expert's matrix: S13 [E][ceil(2I/128)][ceil(H/128)],
  * S2 [E][ceil(H/128)][ceil(I/128)].  All contiguous, starting on 16-byte
  * boundaries; H and I are multiples of 16.  Sums, softmax and the gated
- * product are fp32 (the latter within 2^-23 of an entry or 2^-39 of its row's
- * largest as an operand of the last product); Y is rounded once, and equal
- * calls give equal bits.  An inf or NaN in a token makes that token's whole
- * row NaN.
+ * product are fp32.  As operands of the experts' products a token's entries are
+ * exact down to 2^-28 of its largest and within 2^-39 of that below, those of
+ * the gated product within 2^-23 of themselves or 2^-39 of its largest.  Y is
+ * rounded once, and equal calls give equal bits.  An inf or NaN in a token
+ * makes that token's whole row NaN.
  * ws: moe_layer_f8_ws_bytes() bytes, 256-byte aligned; that function returns 0
  * for invalid sizes.
  * Errors: RG_ERR_RANGE (T > RG_MOE_MAX_TOKENS: use quantize_f8 and
