@@ -17,6 +17,10 @@ Entry points (same names as the C ABI):
   quantize_f8(X, form)           E4M3 values with a scale per 128 entries or per 128 x 128 tile
   scaled_gemm_f8(A, SA, B, SB)   product of two of them
   linear_f8, linear_f8_backward  a linear layer's three products, quantised inside
+  scaled_gemm_act_f8(A, SA, ...) the product with bias, activation and residual in its epilogue
+  linear_act_f8 (and _backward)  a linear layer with these
+  grouped_gemm_f8, grouped_wgrad_f8  products by group of rows (experts)
+  expert_linear_f8 (and _backward)   a linear layer by group of rows
   moe_layer_f8(X, WR, ...)       a mixture-of-experts layer for up to 64 tokens
 Helpers: width_ulps, digest, get_plan, workspace_bytes.
 """
@@ -49,8 +53,11 @@ RG_FLAG_SYNC = 1
 RG_FLAG_HOST = 2
 RG_FLAG_TRANS_B = 4
 RG_FLAG_TILE_B = 8
+RG_FLAG_OFFSETS64 = 16
+RG_FLAG_KEEP_REST = 32
 RG_TYPE_F32, RG_TYPE_F16, RG_TYPE_BF16 = 0, 1, 2
 RG_F8_ROWS, RG_F8_COLUMNS, RG_F8_BOTH, RG_F8_TILES = 0, 1, 2, 3
+RG_ACT_NONE, RG_ACT_RELU, RG_ACT_SILU, RG_ACT_GELU, RG_ACT_GELU_TANH = 0, 1, 2, 3, 4
 RG_OP_I64, RG_OP_LIMBS, RG_OP_ENCLOSE, RG_OP_STAGE, RG_OP_ENCLOSE_F32 = 0, 1, 2, 3, 4
 RG_OP_INTERVAL, RG_OP_INTERVAL_F32 = 5, 6
 RG_PROBE_MMA_S8, RG_PROBE_TCGEN05_F16, RG_PROBE_TCGEN05_E4M3 = 0, 1, 2
@@ -69,7 +76,10 @@ EXPORTED = (
     "rg_solution_free", "rg_rational_reconstruct", "rg_big_gcd", "rg_set_crt_mode", "rg_set_stage_events",
     "rg_probe_mma_rate", "rg_big_mulmod", "quantize_f8", "scaled_gemm_f8",
     "moe_layer_f8", "moe_layer_f8_ws_bytes", "linear_f8", "linear_f8_backward", "linear_f8_saved_bytes",
-    "linear_f8_ws_bytes", "rg_hold_workspace", "rg_stream_capturing",
+    "linear_f8_ws_bytes", "rg_hold_workspace", "rg_stream_capturing", "scaled_gemm_act_f8", "linear_act_f8",
+    "linear_act_f8_backward", "linear_act_f8_saved_bytes", "linear_act_f8_ws_bytes", "quantize_grouped_f8",
+    "grouped_gemm_f8", "grouped_wgrad_f8", "expert_linear_f8", "expert_linear_f8_backward",
+    "expert_linear_f8_saved_bytes", "expert_linear_f8_ws_bytes",
 )
 
 
@@ -188,6 +198,28 @@ def library():
             lib.linear_f8_backward.restype = ci
             for f in ("linear_f8_saved_bytes", "linear_f8_ws_bytes"):
                 getattr(lib, f).argtypes = [i64, i64, i64]
+                getattr(lib, f).restype = sz
+            lib.scaled_gemm_act_f8.argtypes = [vp, i64, vp, vp, i64, vp, vp, ci, ci, vp, i64, vp, vp, ci, i64, i64, i64,
+                                               i64, cu, vp, sz, vp]
+            lib.linear_act_f8.argtypes = [vp, ci, i64, vp, ci, i64, vp, ci, ci, vp, i64, vp, i64, i64, i64, vp, sz, cu,
+                                          vp, sz, vp]
+            lib.linear_act_f8_backward.argtypes = [vp, ci, i64, vp, sz, ci, vp, vp, ci, vp, ci, i64, i64, i64, cu, vp, sz,
+                                                   vp]
+            lib.quantize_grouped_f8.argtypes = [vp, ci, i64, i64, i64, ci, vp, i64, vp, i64, vp, vp, i64, vp, cu, vp]
+            lib.grouped_gemm_f8.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, vp, ci, i64, i64, i64, i64, cu, vp, sz, vp]
+            lib.grouped_wgrad_f8.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, vp, ci, i64, i64, i64, cu, vp, sz, vp]
+            lib.expert_linear_f8.argtypes = [vp, ci, i64, vp, ci, i64, vp, i64, vp, i64, i64, i64, vp, sz, cu, vp, sz, vp]
+            lib.expert_linear_f8_backward.argtypes = [vp, ci, i64, vp, sz, vp, i64, vp, vp, ci, i64, i64, i64, cu, vp, sz,
+                                                      vp]
+            for f in ("scaled_gemm_act_f8", "linear_act_f8", "linear_act_f8_backward", "quantize_grouped_f8",
+                      "grouped_gemm_f8", "grouped_wgrad_f8", "expert_linear_f8", "expert_linear_f8_backward"):
+                getattr(lib, f).restype = ci
+            lib.linear_act_f8_saved_bytes.argtypes = [i64, i64, i64, ci, ci]
+            lib.linear_act_f8_ws_bytes.argtypes = [i64, i64, i64]
+            for f in ("expert_linear_f8_saved_bytes", "expert_linear_f8_ws_bytes"):
+                getattr(lib, f).argtypes = [i64, i64, i64, i64]
+            for f in ("linear_act_f8_saved_bytes", "linear_act_f8_ws_bytes", "expert_linear_f8_saved_bytes",
+                      "expert_linear_f8_ws_bytes"):
                 getattr(lib, f).restype = sz
             lib.moe_layer_f8_ws_bytes.argtypes = [i64, i64, i64, i64, ci]
             lib.moe_layer_f8_ws_bytes.restype = sz
@@ -737,3 +769,6 @@ def rational_reconstruct(x: int, m: int, nbits: int, dbits: int):
 
 # 8-bit block-scaled operators (quantisation, products, linear and expert layers)
 from .f8 import linear_f8, linear_f8_backward, moe_layer_f8, quantize_f8, scaled_gemm_f8  # noqa: E402,F401
+from .f8_act import linear_act_f8, linear_act_f8_backward, scaled_gemm_act_f8  # noqa: E402,F401
+from .f8_experts import (expert_linear_f8, expert_linear_f8_backward, grouped_gemm_f8,  # noqa: E402,F401
+                         grouped_wgrad_f8)

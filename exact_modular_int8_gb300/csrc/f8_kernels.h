@@ -20,9 +20,33 @@ struct QuantArgs {
   uint8_t* QT;
   long long ldqt;
   float* ST;
-  bool vec_x, vec_q, vec_qt;  // set by the launcher: rows start on 16 (8) byte boundaries
+  bool vec_x, vec_q, vec_qt, vec_p;  // set by the launcher: rows start on 16 (8) byte boundaries
+  // tiles: this many matrices, M rows apart
+  long long batch = 1;
+  // columns, both: rows in groups (F8Groups), QT [K][128 blocks], ST [K][blocks]
+  const void* offsets = nullptr;
+  int wide = 0, E = 0;
+  long long blocks = 0;
+  // both: X times the slope of the activation act at P [M][K] (X's type)
+  int act = RG_ACT_NONE;
+  const void* P = nullptr;
+  // both: sums over the rows of each block of 128 rows, [ceil(M/128)][K]
+  float* sums = nullptr;
 };
 cudaError_t launch_quantise_f8(QuantArgs a, int type, int form, cudaStream_t st);
+// out [K] = the sum of `rows` rows of partial sums [rows][K], in a fixed order.
+cudaError_t launch_sum_rows(const float* sums, long long rows, long long K, void* out, int type, cudaStream_t st);
+
+// What happens to a product's sums p before they are stored: p + bias[n] goes to P
+// (C's type and row stride) where that is given, act(p + bias[n]) + R[m][n] to C.
+struct F8Epilogue {
+  const void* bias = nullptr;  // [N]
+  int bias_type = RG_TYPE_F32;
+  int act = RG_ACT_NONE;
+  const void* R = nullptr;  // [M][ldr], C's type
+  long long ldr = 0;
+  void* P = nullptr;
+};
 
 // C [M][N] = sum over 128-blocks kb of sa[m][kb] sb[n][kb] (A_kb B_kb^T).
 // A [M][lda] E4M3, K contiguous.  B [N][ldb] (b_kmajor) or [K][ldb] E4M3.
@@ -39,9 +63,30 @@ struct F8GemmArgs {
   int out_type;  // RG_TYPE_*
   bool b_kmajor, tile_b;
   bool keep_status = false;  // an earlier product of the same call has cleared it
+  const F8Epilogue* ep = nullptr;  // b_kmajor and tile_b only
 };
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, int fault,
                            unsigned long long wait_ns);
+
+// The pair kernel with an epilogue (f8_act.cu); its parameters are those of f8_gemm.cu's.
+const void* pair_act_kernel(int act);
+
+// Products by group, group g holding rows (or, by_blocks, columns along the
+// contraction) offsets[g] .. offsets[g + 1].
+//   rows    C [M][N]: rows of group g times B[g], where B [E][N][ldb] (b_kmajor) or
+//           [E][K][ldb], sb_e scales apart, in tiles
+//   blocks  C [E][M][N]: the sum over group g's blocks of 128 columns of A [M][lda]
+//           and B [N][ldb], which start at block offsets[g] / 128 + g; SA and SB are
+//           [M][blocks], [N][blocks], K = 128 blocks; C's matrices lie without gaps
+struct F8Groups {
+  const void* offsets;  // [E + 1], device
+  bool wide;            // 64-bit
+  long long E;
+  bool zero_rest;  // rows: write 0 to the rows behind the last group
+  bool by_blocks;
+};
+cudaError_t launch_f8_grouped(const F8GemmArgs& a, const F8Groups& g, DevPlan* plan, cudaStream_t st, int fault,
+                              unsigned long long wait_ns);
 
 // The same for M <= kSkinnyRows and a transposed B.
 constexpr int kSkinnyRows = 32;

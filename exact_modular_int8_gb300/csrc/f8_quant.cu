@@ -25,6 +25,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "f8_act.cuh"
 #include "f8_kernels.h"
 
 namespace rg {
@@ -123,6 +124,31 @@ __device__ __forceinline__ uint32_t mag8(const Entries<T>& e) {
   return m;
 }
 
+// Where the entries come from: X itself, or X times the slope of an activation at P.
+template <typename T>
+struct FromX {
+  using E = Entries<T>;
+  using Type = T;
+  // eight entries of a row from column c on, of which `left` exist
+  static __device__ __forceinline__ void load(E& e, const QuantArgs& a, const T* X, long long row, long long c,
+                                              long long left) {
+    load8(e, X + row * a.ldx + c, left, a.vec_x);
+  }
+};
+template <typename T, int ACT>
+struct TimesSlope {
+  using E = Entries<float>;
+  using Type = T;
+  static __device__ __forceinline__ void load(E& e, const QuantArgs& a, const T* X, long long row, long long c,
+                                              long long left) {
+    Entries<T> x, p;
+    load8(x, X + row * a.ldx + c, left, a.vec_x);
+    load8(p, static_cast<const T*>(a.P) + row * a.K + c, left, a.vec_p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e.set(i, x.at(i) * slope(p.at(i), ACT));  // a missing entry: 0
+  }
+};
+
 struct BlockScale {
   float nd, r;  // -a / 512 and the reciprocal of a / 512
 };
@@ -198,12 +224,42 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(QuantArgs a) {
   if (l16 == 0) a.S[row * kb + j] = scale_of(top);
 }
 
+// Slot i of the blocks of 128 rows: the group's, which start at offsets[g] / 128 + g,
+// and behind the last group's those of the rows that belong to none.  Every access
+// stays within the matrix whatever the offsets are; all threads call this.
+struct RowBlock {
+  long long r0, end;
+  bool rest;
+};
+__device__ __forceinline__ RowBlock find_block(const QuantArgs& a, long long i) {
+  auto offset = [&](int g) {
+    return a.wide ? static_cast<const long long*>(a.offsets)[g] : (long long)static_cast<const int*>(a.offsets)[g];
+  };
+  int before = 0;  // groups, with the rest as the last, that start at or before slot i
+  for (int g0 = 0; g0 <= a.E; g0 += blockDim.x) {
+    const int g = g0 + (int)threadIdx.x;
+    before += __syncthreads_count(g <= a.E && offset(min(g, a.E)) / kTile + g <= i);
+  }
+  const int g = max(before - 1, 0);
+  const long long start = offset(g), b = i - (start / kTile + g);
+  RowBlock r{0, 0, g == a.E};
+  if (start >= 0 && start <= a.M && b >= 0 && b <= a.M / kTile) {
+    r.r0 = start + b * kTile;
+    r.end = r.rest ? a.M : min(offset(g + 1), a.M);
+  }
+  return r;
+}
+
 // One 128 x 128 tile per block of 256 threads; a thread holds eight rows of
 // eight columns.  ROWS / COLS: scales along rows and along columns (with both,
-// one read of X gives both results); neither: one scale for the tile.
-template <typename T, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) quantise_tile_kernel(QuantArgs a) {
-  using E = Entries<T>;
+// one read of X gives both results); neither: one scale for the tile.  GROUPED:
+// the blocks along the columns lie in one group of rows each.  SUM: sums over the
+// tile's rows.
+template <typename Src, bool ROWS, bool COLS, bool GROUPED, bool SUM>
+__global__ void __launch_bounds__(256, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 : 4) : 2)
+    quantise_tile_kernel(QuantArgs a) {
+  using E = typename Src::E;
+  using T = typename Src::Type;
   constexpr int kWordsPerRow = kTile / E::kPer;
   __shared__ uint32_t col_mag[COLS ? 16 : 1][kWordsPerRow];  // per 8-row group
   __shared__ __align__(16) float2 col_scale[COLS ? kTile : 1];
@@ -211,15 +267,22 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) quantise_tile_ker
   __shared__ uint32_t warp_mag[8];
   wait_for_predecessor();
   allow_dependents();
-  const long long kb = (a.K + kTile - 1) / kTile, mb = (a.M + kTile - 1) / kTile;
+  const long long kb = (a.K + kTile - 1) / kTile, mb = GROUPED ? a.blocks : (a.M + kTile - 1) / kTile;
   const long long ti = blockIdx.x / kb, tj = blockIdx.x - ti * kb;
   const T* X = static_cast<const T*>(a.X);
+  if constexpr (!ROWS && !COLS) {  // a stack of matrices
+    X += blockIdx.y * a.M * a.ldx;
+    a.Q += blockIdx.y * a.M * a.ldq;
+    a.S += blockIdx.y * mb * kb;
+  }
   const int grp = threadIdx.x >> 4;  // rows 8 grp .. 8 grp + 7 of the tile
   const int l16 = threadIdx.x & 15;  // columns 8 l16 ..
-  const long long r0 = ti * kTile + grp * 8, c0 = tj * kTile + l16 * 8, left = a.K - c0;
+  RowBlock at{ti * kTile, a.M, false};
+  if constexpr (GROUPED) at = find_block(a, ti);
+  const long long r0 = at.r0 + grp * 8, c0 = tj * kTile + l16 * 8, left = a.K - c0;
   E e[8];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) load8(e[r], X + (r0 + r) * a.ldx + c0, r0 + r < a.M ? left : 0, a.vec_x);
+  for (int r = 0; r < 8; ++r) Src::load(e[r], a, X, r0 + r, c0, r0 + r < at.end ? left : 0);
 
   if constexpr (!ROWS && !COLS) {
     uint32_t m = mag8(e[0]);
@@ -239,13 +302,23 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) quantise_tile_ker
     if (threadIdx.x == 0) a.S[ti * kb + tj] = scale_of(top);
     return;
   }
+  if constexpr (SUM) {  // kept where the transposed bytes will be
+    float* part = reinterpret_cast<float*>(t_tile) + grp * kTile + l16 * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v = e[0].at(i);
+#pragma unroll
+      for (int r = 1; r < 8; ++r) v += e[r].at(i);
+      part[i] = v;
+    }
+  }
   if constexpr (COLS) {
 #pragma unroll
     for (int w = 0; w < E::kWords; ++w) {
       uint32_t m = E::mag(e[0].w[w]);
 #pragma unroll
       for (int r = 1; r < 8; ++r) m = E::larger(m, E::mag(e[r].w[w]));
-      col_mag[grp][l16 * E::kWords + w] = m;
+      col_mag[grp][l16 * E::kWords + w] = GROUPED && at.rest ? 0 : m;
     }
   }
   if constexpr (ROWS) {
@@ -267,16 +340,25 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) quantise_tile_ker
     const float top = amax_of(E::top(mine));
     const BlockScale bs = block_scale(top);
     const long long my_row = r0 + (l16 >> 1);
-    if (!(l16 & 1) && my_row < a.M) a.S[my_row * kb + tj] = scale_of(top);
+    if (!(l16 & 1) && my_row < at.end) a.S[my_row * kb + tj] = scale_of(top);
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int src = (threadIdx.x & 16) + 2 * r;
       const BlockScale rs{__shfl_sync(0xFFFFFFFFu, bs.nd, src), __shfl_sync(0xFFFFFFFFu, bs.r, src)};
-      if (r0 + r < a.M)
+      if (r0 + r < at.end)
         store8(a.Q + (r0 + r) * a.ldq + c0, left, a.vec_q, quantise8([&](int i) { return e[r].at(i); }, rs));
     }
   }
   if constexpr (COLS) {
+    if constexpr (GROUPED) {
+      if (ti >= mb) return;  // a slot more for the rest's rows, which are in no column block
+      if (at.rest) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+          for (int w = 0; w < E::kWords; ++w) e[r].w[w] = 0;
+      }
+    }
     __syncthreads();
     if (threadIdx.x < kTile) {
       constexpr int kPer = E::kPer;
@@ -291,6 +373,13 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) quantise_tile_ker
       col_scale[threadIdx.x] = make_float2(bs.nd, bs.r);
       const long long col = tj * kTile + threadIdx.x;
       if (col < a.K) a.ST[col * mb + ti] = scale_of(top);
+      if constexpr (SUM) {
+        const float* part = reinterpret_cast<const float*>(t_tile) + threadIdx.x;
+        float v = part[0];
+#pragma unroll
+        for (int g = 1; g < 16; ++g) v += part[g * kTile];
+        if (col < a.K) a.sums[ti * a.K + col] = v;
+      }
     }
     __syncthreads();
 #pragma unroll
@@ -304,48 +393,100 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) quantise_tile_ker
     }
     __syncthreads();
     const int j = threadIdx.x & 7;  // 16-byte chunk: rows 16 j of the tile
+    const long long limit = GROUPED ? a.blocks * kTile : a.M;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const int c = p * 32 + (threadIdx.x >> 3);
       const long long col = tj * kTile + c, row = ti * kTile + 16 * j;
-      if (col < a.K && row < a.M) {
+      if (col < a.K && row < limit) {
         const uint4 q = *reinterpret_cast<const uint4*>(&t_tile[c * kTile + ((j ^ ((c >> 3) & 7)) * 16)]);
         uint8_t* out = a.QT + col * a.ldqt + row;
-        if (a.vec_qt && a.M - row >= 16) {
+        if (a.vec_qt && limit - row >= 16) {
           *reinterpret_cast<uint4*>(out) = q;
         } else {
           const uint32_t w[4] = {q.x, q.y, q.z, q.w};
           for (int i = 0; i < 16; ++i)
-            if (row + i < a.M) out[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+            if (row + i < limit) out[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
         }
       }
     }
   }
 }
 
+// Eight rows of threads each add every eighth partial sum of 32 columns, then the
+// eight meet in order.
+__global__ void __launch_bounds__(256) sum_rows_kernel(const float* sums, long long rows, long long K, void* out,
+                                                       int type) {
+  __shared__ float part[8][32];
+  wait_for_predecessor();
+  allow_dependents();
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const long long col = (long long)blockIdx.x * 32 + x;
+  float v = 0.0f;
+  if (col < K)
+    for (long long r = y; r < rows; r += 8) v += sums[r * K + col];
+  part[y][x] = v;
+  __syncthreads();
+  if (y == 0 && col < K) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += part[i][x];
+    store_real(out, type, col, v);
+  }
+}
+
+template <typename Src>
+cudaError_t launch_tiles(const QuantArgs& a, int form, dim3 g, cudaStream_t st) {
+  const dim3 b(256);
+  const bool sum = a.sums != nullptr;
+  if (a.offsets)
+    return form == RG_F8_COLUMNS
+               ? launch_dependent(quantise_tile_kernel<Src, false, true, true, false>, g, b, 0, st, a)
+               : launch_dependent(quantise_tile_kernel<Src, true, true, true, false>, g, b, 0, st, a);
+  switch (form) {
+    case RG_F8_ROWS: return launch_dependent(quantise_tile_kernel<Src, true, false, false, false>, g, b, 0, st, a);
+    case RG_F8_COLUMNS: return launch_dependent(quantise_tile_kernel<Src, false, true, false, false>, g, b, 0, st, a);
+    case RG_F8_BOTH:
+      return sum ? launch_dependent(quantise_tile_kernel<Src, true, true, false, true>, g, b, 0, st, a)
+                 : launch_dependent(quantise_tile_kernel<Src, true, true, false, false>, g, b, 0, st, a);
+    default: return launch_dependent(quantise_tile_kernel<Src, false, false, false, false>, g, b, 0, st, a);
+  }
+}
+// With an activation's slope: form both, with the column sums where they are wanted.
+template <typename T, int ACT>
+cudaError_t launch_slope(const QuantArgs& a, dim3 g, cudaStream_t st) {
+  using Src = TimesSlope<T, ACT>;
+  return a.sums ? launch_dependent(quantise_tile_kernel<Src, true, true, false, true>, g, dim3(256), 0, st, a)
+                : launch_dependent(quantise_tile_kernel<Src, true, true, false, false>, g, dim3(256), 0, st, a);
+}
+
 template <typename T>
 cudaError_t launch_t(const QuantArgs& a, int form, cudaStream_t st) {
-  const long long kb = (a.K + kTile - 1) / kTile, mb = (a.M + kTile - 1) / kTile;
+  const long long kb = (a.K + kTile - 1) / kTile;
+  // groups with their rows: a slot more for those behind the last group
+  const long long mb = a.offsets ? a.blocks + (form == RG_F8_BOTH) : (a.M + kTile - 1) / kTile;
   // Along rows: up to 2^15 blocks of 128, or fewer rows than half a tile, go a
   // block to a half-warp, which spreads few blocks over more SMs (512 x 1024:
   // 2.1 us, in tiles 3.0); more go in tiles, where a thread has eight loads on
   // its way (8192 x 4096 bf16: 26 us a block to a half-warp).
   const bool tiles = form != RG_F8_ROWS || (a.M >= 64 && a.M * kb > (1LL << 15));
   const long long blocks = tiles ? mb * kb : (a.M * kb + 15) / 16;
-  if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-  const dim3 g((unsigned)blocks), b(256);
-  if (!tiles) {
-    return launch_dependent(quantise_rows_kernel<T>, g, b, 0, st, a);
-  }
-  switch (form) {
-    case RG_F8_ROWS: return launch_dependent(quantise_tile_kernel<T, true, false>, g, b, 0, st, a);
-    case RG_F8_COLUMNS: return launch_dependent(quantise_tile_kernel<T, false, true>, g, b, 0, st, a);
-    case RG_F8_BOTH: return launch_dependent(quantise_tile_kernel<T, true, true>, g, b, 0, st, a);
-    default: return launch_dependent(quantise_tile_kernel<T, false, false>, g, b, 0, st, a);
+  if (blocks > INT_MAX || a.batch > 65535) return cudaErrorInvalidConfiguration;
+  const dim3 g((unsigned)blocks, (unsigned)a.batch);
+  if (!tiles) return launch_dependent(quantise_rows_kernel<T>, g, dim3(256), 0, st, a);
+  switch (a.act) {
+    case RG_ACT_RELU: return launch_slope<T, RG_ACT_RELU>(a, g, st);
+    case RG_ACT_SILU: return launch_slope<T, RG_ACT_SILU>(a, g, st);
+    case RG_ACT_GELU: return launch_slope<T, RG_ACT_GELU>(a, g, st);
+    case RG_ACT_GELU_TANH: return launch_slope<T, RG_ACT_GELU_TANH>(a, g, st);
+    default: return launch_tiles<FromX<T>>(a, form, g, st);
   }
 }
 
 }  // namespace
+
+cudaError_t launch_sum_rows(const float* sums, long long rows, long long K, void* out, int type, cudaStream_t st) {
+  return launch_dependent(sum_rows_kernel, dim3((unsigned)((K + 31) / 32)), dim3(256), 0, st, sums, rows, K, out, type);
+}
 
 cudaError_t launch_quantise_f8(QuantArgs a, int type, int form, cudaStream_t st) {
   const size_t es = type == RG_TYPE_F32 ? 4 : 2;
@@ -353,6 +494,7 @@ cudaError_t launch_quantise_f8(QuantArgs a, int type, int form, cudaStream_t st)
     return (reinterpret_cast<uintptr_t>(p) % n) == 0 && row_bytes % n == 0;
   };
   a.vec_x = aligned(a.X, a.ldx * (long long)es, 16);
+  a.vec_p = aligned(a.P, a.K * (long long)es, 16);
   a.vec_q = aligned(a.Q, a.ldq, 8);
   a.vec_qt = aligned(a.QT, a.ldqt, 16);
   switch (type) {

@@ -24,6 +24,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "f8_act.cuh"
 #include "f8_kernels.h"
 
 namespace rg {
@@ -44,6 +45,7 @@ struct SkinnyParams {
   int out_type;
   int keep_status;
   DevPlan* plan;
+  F8Epilogue ep;
 };
 
 __device__ __forceinline__ uint32_t h2_of_e4m3x2(uint32_t two) {  // the low 16 bits: two E4M3 values
@@ -91,7 +93,7 @@ struct Shape {
   static constexpr int kSmem = 2 * kRed + kWarps * kRing * kPiece;
 };
 
-template <int NT, int MT, bool TILE_B>
+template <int NT, int MT, bool TILE_B, bool EPI>
 __global__ void __launch_bounds__(kThreads) f8_skinny_kernel(const __grid_constant__ SkinnyParams p) {
   using S = Shape<NT, MT>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -215,6 +217,12 @@ __global__ void __launch_bounds__(kThreads) f8_skinny_kernel(const __grid_consta
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) v += red[(w * MT * 16 + r) * S::kLd + m];
       const long long at = (long long)m * p.ldc + n;
+      if constexpr (EPI) {
+        if (p.ep.bias) v += load_real(p.ep.bias, p.ep.bias_type, n);
+        if (p.ep.P) store_real(p.ep.P, p.out_type, at, v);
+        v = activate(v, p.ep.act);
+        if (p.ep.R) v += load_real(p.ep.R, p.out_type, (long long)m * p.ep.ldr + n);
+      }
       if (p.out_type == RG_TYPE_F32) static_cast<float*>(p.C)[at] = v;
       else if (p.out_type == RG_TYPE_F16) static_cast<__half*>(p.C)[at] = __float2half_rn(v);
       else static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
@@ -224,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) f8_skinny_kernel(const __grid_consta
 }
 
 // The kernel's blocks per SM times the SMs of this device, found once.
-template <int NT, int MT, bool TILE_B>
+template <int NT, int MT, bool TILE_B, bool EPI>
 cudaError_t launch(SkinnyParams p, cudaStream_t st) {
   using S = Shape<NT, MT>;
   static_assert(S::kSmem <= 232448 && S::kPiece % 16 == 0 && S::kRed % 16 == 0, "shared memory");
@@ -236,34 +244,36 @@ cudaError_t launch(SkinnyParams p, cudaStream_t st) {
   int resident = blocks[dev].load(std::memory_order_relaxed);
   if (!resident) {
     int sms = 0, per_sm = 0;
-    e = cudaFuncSetAttribute(f8_skinny_kernel<NT, MT, TILE_B>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    e = cudaFuncSetAttribute(f8_skinny_kernel<NT, MT, TILE_B, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, f8_skinny_kernel<NT, MT, TILE_B>, kThreads, S::kSmem);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, f8_skinny_kernel<NT, MT, TILE_B, EPI>, kThreads, S::kSmem);
     if (e != cudaSuccess) return e;
     resident = sms * std::max(per_sm, 1);
     blocks[dev].store(resident, std::memory_order_relaxed);
   }
   p.tiles = (p.N + 16 * MT - 1) / (16 * MT);
-  return launch_dependent(f8_skinny_kernel<NT, MT, TILE_B>, dim3((unsigned)std::min(p.tiles, resident)),
+  return launch_dependent(f8_skinny_kernel<NT, MT, TILE_B, EPI>, dim3((unsigned)std::min(p.tiles, resident)),
                           dim3(kThreads), S::kSmem, st, p);
 }
 
 template <int NT, int MT>
-cudaError_t launch(const SkinnyParams& p, bool tile_b, cudaStream_t st) {
-  return tile_b ? launch<NT, MT, true>(p, st) : launch<NT, MT, false>(p, st);
+cudaError_t launch(const SkinnyParams& p, bool tile_b, bool epilogue, cudaStream_t st) {
+  if (epilogue) return launch<NT, MT, true, true>(p, st);  // weights: a scale per tile
+  return tile_b ? launch<NT, MT, true, false>(p, st) : launch<NT, MT, false, false>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_f8_skinny(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st) {
   const SkinnyParams p{a.A, a.B, a.SA, a.SB, a.C, a.lda, a.ldb, a.ldc, a.sb_n, (int)a.M, (int)a.N, (int)a.K,
-                       (int)((a.K + 127) / 128), 0, a.out_type, a.keep_status, plan};
+                       (int)((a.K + 127) / 128), 0, a.out_type, a.keep_status, plan,
+                       a.ep ? *a.ep : F8Epilogue{}};
   // with more than eight rows, two row tiles of B share a piece's rows of A
-  if (a.M <= 8) return launch<1, 1>(p, a.tile_b, st);
-  if (a.M <= 16) return launch<2, 2>(p, a.tile_b, st);
-  if (a.M <= 24) return launch<3, 1>(p, a.tile_b, st);
-  return launch<4, 1>(p, a.tile_b, st);
+  if (a.M <= 8) return launch<1, 1>(p, a.tile_b, a.ep != nullptr, st);
+  if (a.M <= 16) return launch<2, 2>(p, a.tile_b, a.ep != nullptr, st);
+  if (a.M <= 24) return launch<3, 1>(p, a.tile_b, a.ep != nullptr, st);
+  return launch<4, 1>(p, a.tile_b, a.ep != nullptr, st);
 }
 
 }  // namespace rg

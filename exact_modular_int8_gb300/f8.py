@@ -21,8 +21,8 @@ import os
 
 import torch
 
-from . import (LIB_PATH, RG_ERR_ARG, RG_ERR_RANGE, RG_F8_BOTH, RG_F8_COLUMNS, RG_F8_ROWS, RG_F8_TILES, RG_FLAG_SYNC,
-               RG_FLAG_TILE_B, RG_FLAG_TRANS_B, RG_TYPE_BF16, RG_TYPE_F16, RG_TYPE_F32, ResGemmError, _check, _output,
+from . import (LIB_PATH, RG_ERR_ARG, RG_ERR_RANGE, RG_F8_BOTH, RG_F8_COLUMNS, RG_F8_ROWS, RG_F8_TILES,
+               RG_FLAG_OFFSETS64, RG_FLAG_SYNC, RG_FLAG_TILE_B, RG_FLAG_TRANS_B, RG_TYPE_BF16, RG_TYPE_F16, RG_TYPE_F32, ResGemmError, _check, _output,
                _ws_cache, capturing, library, workspace)
 
 BLOCK = 128
@@ -83,8 +83,8 @@ class _NoGrad(torch.autograd.Function):
         return call()
 
     @staticmethod
-    def backward(ctx, _):
-        raise NotImplementedError(f"{ctx.where} has no gradient; linear_f8 has one")
+    def backward(ctx, *_):
+        raise NotImplementedError(f"{ctx.where} has no gradient; linear_f8, linear_act_f8 and expert_linear_f8 have one")
 
 
 def _no_grad(where: str, out, call, *tensors):
@@ -152,18 +152,77 @@ def _aligned_rows(q: torch.Tensor):
     return q, ld
 
 
-def quantize_f8(X: torch.Tensor, form: str = "rows", sync: bool = True):
+def _stack_stride(t: torch.Tensor) -> int:
+    """The row stride of a stack [E, R, C] of matrices whose rows are contiguous and that lie without gaps, else 0."""
+    (e, r, c), (s0, s1, s2) = t.shape, t.stride()
+    if s2 != 1 and c > 1:
+        return 0
+    ld = s1 if r > 1 else s0 if e > 1 and r else c or 1
+    return ld if ld >= c and ld and (e <= 1 or s0 == r * ld) else 0
+
+
+def _groups(where: str, offsets: torch.Tensor, E: int):
+    """(offsets, flags) for the library; the values are checked on the device."""
+    if offsets.dim() != 1 or offsets.shape[0] != E + 1 or E < 1 or offsets.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"{where}: offsets [E + 1] int32 or int64 expected")
+    return offsets.contiguous(), RG_FLAG_OFFSETS64 if offsets.dtype == torch.int64 else 0
+
+
+def _quantize_grouped(X, f, offsets, sync):
+    """quantize_f8 of a stack of matrices (offsets None), or of rows in groups."""
+    t = _TYPES.get(X.dtype)
+    stack = offsets is None
+    if t is None or X.dim() != (3 if stack else 2) or (f != RG_F8_TILES if stack else f not in (RG_F8_COLUMNS, RG_F8_BOTH)):
+        raise ValueError("quantize_f8: X [M, K], or with form tiles [E, M, K], float32, float16 or bfloat16 expected, and "
+                         "offsets with form columns or both")
+    dev, flags = X.device, RG_FLAG_SYNC if sync else 0
+    q = s = qt = st = qp = sp = qtp = stp = op = None
+    (M, K), ldq, ldqt = X.shape[-2:], (X.shape[-1] + 15) & ~15, 0
+    if stack:
+        idx, E, ldx = _device_index("quantize_f8", X), X.shape[0], _stack_stride(X)
+        if E == 0:
+            return (torch.empty((0, M, K), dtype=F8, device=dev),
+                    torch.empty((0, _blocks(M), _blocks(K)), dtype=torch.float32, device=dev))
+        if not ldx:
+            X, ldx = X.contiguous(), K
+        q = torch.empty_strided((E, M, K), (M * ldq, ldq, 1), dtype=F8, device=dev)
+        s = torch.empty((E, _blocks(M), _blocks(K)), dtype=torch.float32, device=dev)
+    else:
+        idx, E = _device_index("quantize_f8", X, offsets), offsets.shape[0] - 1 if offsets.dim() == 1 else 0
+        offsets, more = _groups("quantize_f8", offsets, E)
+        flags, op = flags | more, offsets.data_ptr()
+        X, ldx = _rows_of(X)
+        nb = M // BLOCK + E
+        ldqt = BLOCK * nb
+        if f == RG_F8_BOTH:
+            q, s = _empty_rows(M, K, dev), torch.empty((M, _blocks(K)), dtype=torch.float32, device=dev)
+        qt = torch.empty((K, ldqt), dtype=F8, device=dev)
+        st = torch.empty((K, nb), dtype=torch.float32, device=dev)
+        qtp, stp = qt.data_ptr(), st.data_ptr()
+    if q is not None:
+        qp, sp = q.data_ptr(), s.data_ptr()
+    _launch(idx, "quantize_f8", library().quantize_grouped_f8, X.data_ptr(), t, ldx, M, K, f, op, E, qp, ldq, sp, qtp,
+            ldqt, stp, flags)
+    return tuple(r for r in (q, s, qt, st) if r is not None)
+
+
+def quantize_f8(X: torch.Tensor, form: str = "rows", sync: bool = True, offsets: torch.Tensor | None = None):
     """E4M3 values and float32 scales of a float32, float16 or bfloat16 matrix X [M, K].
 
     form "rows":    Q [M, K], S [M, ceil(K/128)]: blocks of 128 along each row
          "columns": Q [K, M], S [K, ceil(M/128)]: the same of X.T
          "both":    (Q, S, Qt, St), the two of them from one read of X
-         "tiles":   Q [M, K], S [ceil(M/128), ceil(K/128)]: 128 x 128 tiles
+         "tiles":   Q [M, K], S [ceil(M/128), ceil(K/128)]: 128 x 128 tiles; of a stack X [E, M, K], each
+                    matrix in tiles of its own, Q [E, M, K], S [E, ceil(M/128), ceil(K/128)]
+    With offsets (f8_experts.py) X's rows are in groups, and the blocks of "columns" and "both" along them lie in one
+    group each: Q [K, 128 NB], S [K, NB], NB = M // 128 + E, with zeros where a block has no row.
     Per block, a = max |x| (at least 2^-60), S = a / 448, Q = 448 x / a to the nearest E4M3 value, ties to
     even; an inf or NaN makes its whole block NaN.  To autograd the results are constants."""
     f = _FORMS.get(form)
     if f is None:
         raise ValueError(f"quantize_f8: form must be one of {', '.join(_FORMS)}")
+    if offsets is not None or X.dim() == 3:
+        return _quantize_grouped(X, f, offsets, sync)
     if X.is_cuda:
         r = _native().quantize(X, f, RG_FLAG_SYNC if sync else 0)
         if r is not None:

@@ -476,6 +476,31 @@ int scaled_gemm_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t
                    size_t ws_bytes, void* stream);
 
 /*
+ * The same product with an epilogue: with p = (A B^T) + bias,
+ *   C = act(p) + R, and P = p where P is given,
+ * for weights B [N][ldb] with a scale per 128 x 128 tile (RG_FLAG_TRANS_B and
+ * RG_FLAG_TILE_B of scaled_gemm_f8, whose kernels and sums these are).
+ *   RG_ACT_RELU       x where x > 0, else 0
+ *   RG_ACT_SILU       x / (1 + exp(-x))
+ *   RG_ACT_GELU       x (1 + erf(x / sqrt 2)) / 2
+ *   RG_ACT_GELU_TANH  x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2
+ * bias [N] is of bias_type, R [M][ldr] and P [M][ldc] of c_type; each may be
+ * null.  All in fp32; C and P are rounded once.  A NaN stays NaN, an infinite p
+ * gives what the formula gives.  R may be C itself (with ldr = ldc); apart from
+ * that C, P and R do not overlap.  K is at least 1.
+ * Errors: as scaled_gemm_f8's.
+ */
+#define RG_ACT_NONE 0
+#define RG_ACT_RELU 1
+#define RG_ACT_SILU 2
+#define RG_ACT_GELU 3
+#define RG_ACT_GELU_TANH 4
+int scaled_gemm_act_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t* B, int64_t ldb, const float* SB,
+                       const void* bias, int bias_type, int act, const void* R, int64_t ldr, void* P, void* C,
+                       int c_type, int64_t ldc, int64_t M, int64_t N, int64_t K, unsigned flags, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/*
  * A linear layer's training step in this format.
  *   forward   Y [M][N] (x_type) = X W^T, X [M][ldx] quantised along K, W [N][ldw]
  *             (w_type) in 128 x 128 tiles
@@ -499,6 +524,102 @@ int linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* sa
                        size_t ws_bytes, void* stream);
 
 /*
+ * A linear layer's training step with bias, activation and residual.
+ *   forward   p = X W^T + bias, Y [M][N] = act(p) + R, in x_type as R [M][ldr] is;
+ *             X and W as for linear_f8
+ *   backward  d = dY * act'(p), dX = d W with d quantised along N, dW = d^T X with
+ *             both quantised along M, dbias = the sum of d's rows; R's gradient is dY
+ * p is kept in x_type (with an activation only), and the slope is taken there; d is
+ * fp32 and is quantised without another rounding.  dY and dX are of x_type.
+ * Without bias pass a null pointer, and dbias null where it is not wanted.  The
+ * backward call takes the forward call's x_type, act and sizes.  Sums over rows
+ * are fp32, in a fixed order.  Sizes of `saved` and ws from the two functions,
+ * which return 0 for sizes or activations the calls refuse (K = 0 among them).
+ * Errors: as linear_f8's.
+ */
+size_t linear_act_f8_saved_bytes(int64_t M, int64_t N, int64_t K, int x_type, int act);
+size_t linear_act_f8_ws_bytes(int64_t M, int64_t N, int64_t K);
+int linear_act_f8(const void* X, int x_type, int64_t ldx, const void* W, int w_type, int64_t ldw, const void* bias,
+                  int bias_type, int act, const void* R, int64_t ldr, void* Y, int64_t M, int64_t N, int64_t K,
+                  void* saved, size_t saved_bytes, unsigned flags, void* ws, size_t ws_bytes, void* stream);
+int linear_act_f8_backward(const void* dY, int x_type, int64_t lddy, const void* saved, size_t saved_bytes, int act,
+                           void* dX, void* dW, int dw_type, void* dbias, int bias_type, int64_t M, int64_t N, int64_t K,
+                           unsigned flags, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products by group: rows sorted by expert, group g holding the rows
+ * offsets[g] <= r < offsets[g + 1], with a weight matrix for each group.
+ * `offsets` [E + 1] is device memory, of 32-bit integers, or of 64-bit ones with
+ * RG_FLAG_OFFSETS64; it starts at 0 and does not fall, groups may be empty, and
+ * rows may follow the last group (a buffer of fixed capacity).  Offsets that do
+ * not, or that end past the rows, give RG_ERR_ARG as the call's device status, and
+ * no result.  1 <= E <= RG_MOE_MAX_EXPERTS.
+ *
+ * Along the rows, blocks of 128 lie in one group each: group g's start at block
+ * offsets[g] / 128 + g and take what its rows need, its last block filled up with
+ * zeros; a matrix of `rows` rows has rows / 128 + E blocks (both quotients
+ * rounded down; that many always suffice), and blocks of no group are zeros.
+ * ------------------------------------------------------------------------ */
+#define RG_FLAG_OFFSETS64 16u
+#define RG_FLAG_KEEP_REST 32u /* grouped_gemm_f8: rows of C behind the last group stay as they are */
+
+/*
+ * quantize_f8 by group.  RG_F8_COLUMNS and RG_F8_BOTH: QT [K][ldqt] with 128
+ * (M / 128 + E) columns and ST [K][M / 128 + E] in blocks as above; Q and S as
+ * quantize_f8 gives them.  RG_F8_TILES: a stack X [E][M][ldx] of matrices, each
+ * in tiles of its own, to Q [E][M][ldq] and S [E][ceil(M/128)][ceil(K/128)];
+ * offsets may be null.  Bad offsets give unspecified values (in bounds), which
+ * the products report.
+ * Errors: RG_ERR_ARG, RG_ERR_CUDA.
+ */
+int quantize_grouped_f8(const void* X, int x_type, int64_t ldx, int64_t M, int64_t K, int form, const void* offsets,
+                        int64_t E, uint8_t* Q, int64_t ldq, float* S, uint8_t* QT, int64_t ldqt, float* ST,
+                        unsigned flags, void* stream);
+
+/*
+ * C [T][ldc]: each row of A [T][lda] times its group's B, [E][K][ldb] or, with
+ * RG_FLAG_TRANS_B, [E][N][ldb], matrices without gaps between them.  SA
+ * [T][ceil(K/128)]; SB per 128 x 128 tile of each matrix, [E][ceil(K/128)]
+ * [ceil(N/128)] or [E][ceil(N/128)][ceil(K/128)].  Sums and rounding as in
+ * scaled_gemm_f8.  Rows behind the last group become 0, or stay as they are
+ * with RG_FLAG_KEEP_REST.  Alignment and ws as for scaled_gemm_f8; K is at least 1.
+ * Errors: RG_ERR_ARG, RG_ERR_WORKSPACE, RG_ERR_CUDA, RG_ERR_TIMEOUT.
+ */
+int grouped_gemm_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t* B, int64_t ldb, const float* SB,
+                    const void* offsets, int64_t E, void* C, int c_type, int64_t ldc, int64_t T, int64_t N, int64_t K,
+                    unsigned flags, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * C [E][M][N] (contiguous): per group, the sum over its rows of A's column times
+ * B's, for operands stored along the rows by group, A [M][lda] with SA [M][blocks]
+ * and B [N][ldb] with SB [N][blocks], 128 * blocks columns (RG_F8_COLUMNS of
+ * quantize_grouped_f8).  A group without rows gives 0.  E * M is at most 2^30.
+ * Errors: RG_ERR_ARG, RG_ERR_WORKSPACE, RG_ERR_CUDA, RG_ERR_TIMEOUT.
+ */
+int grouped_wgrad_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t* B, int64_t ldb, const float* SB,
+                     const void* offsets, int64_t E, void* C, int c_type, int64_t M, int64_t N, int64_t blocks,
+                     unsigned flags, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * An expert layer's training step: linear_f8 by group.
+ *   forward   Y [T][N] (x_type) = X W_g^T, X [T][ldx], W [E][N][ldw] (w_type)
+ *   backward  dX [T][K] (dy_type) = dY W_g, dW [E][N][K] (dw_type): per group dY^T X
+ * Each is what quantize_grouped_f8, quantize_f8, grouped_gemm_f8 and
+ * grouped_wgrad_f8 give one after the other, to the bit.  Rows behind the last
+ * group are 0 in Y and dX.  The backward call takes the forward call's offsets.
+ * Sizes of `saved` and ws from the two functions, which return 0 for what the
+ * calls refuse.  Errors: as grouped_gemm_f8's.
+ */
+size_t expert_linear_f8_saved_bytes(int64_t T, int64_t N, int64_t K, int64_t E);
+size_t expert_linear_f8_ws_bytes(int64_t T, int64_t N, int64_t K, int64_t E);
+int expert_linear_f8(const void* X, int x_type, int64_t ldx, const void* W, int w_type, int64_t ldw,
+                     const void* offsets, int64_t E, void* Y, int64_t T, int64_t N, int64_t K, void* saved,
+                     size_t saved_bytes, unsigned flags, void* ws, size_t ws_bytes, void* stream);
+int expert_linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* saved, size_t saved_bytes,
+                              const void* offsets, int64_t E, void* dX, void* dW, int dw_type, int64_t T, int64_t N,
+                              int64_t K, unsigned flags, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * A whole mixture-of-experts layer for a few tokens (decoding):
  *   p = softmax(X WR^T) over the E experts; each token takes the top_k
  *   largest (equal ones: the lower index), with weights p or, with renorm,
@@ -518,7 +639,7 @@ int linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* sa
  * ws: moe_layer_f8_ws_bytes() bytes, 256-byte aligned; that function returns 0
  * for invalid sizes.
  * Errors: RG_ERR_RANGE (T > RG_MOE_MAX_TOKENS: use quantize_f8 and
- * scaled_gemm_f8 per expert), RG_ERR_ARG, RG_ERR_WORKSPACE, RG_ERR_CUDA,
+ * grouped_gemm_f8), RG_ERR_ARG, RG_ERR_WORKSPACE, RG_ERR_CUDA,
  * RG_ERR_TIMEOUT.
  */
 #define RG_MOE_MAX_TOKENS 64
