@@ -363,7 +363,7 @@ constexpr TileKernel kTileKernels[2][2] = {
 constexpr TileKernel kTileActKernel = f8_gemm_tile_kernel<true, true, true>;
 
 template <bool B_KMAJOR, bool TILE_B>
-constexpr PairKernel kWhole = f8_gemm_pair_kernel<B_KMAJOR, TILE_B, WALK_WHOLE, PLAIN>;
+constexpr PairKernel kWhole = f8_gemm_pair_kernel<B_KMAJOR, TILE_B, WALK_WHOLE, PLAIN, false>;
 constexpr PairKernel kPairKernels[2][2] = {{kWhole<false, false>, kWhole<false, true>},
                                            {kWhole<true, false>, kWhole<true, true>}};
 constexpr int SMEM2_BYTES = pair_smem(WALK_WHOLE, PLAIN);
@@ -384,8 +384,8 @@ cudaError_t f8_device(int dev, F8Device& out) {
         if (e != cudaSuccess) return e;
       }
     cudaError_t set = cudaFuncSetAttribute(kTileActKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM1_BYTES);
-    for (int act = RG_ACT_NONE; act <= RG_ACT_GELU_TANH && set == cudaSuccess; ++act)
-      set = cudaFuncSetAttribute(pair_act_kernel(act), cudaFuncAttributeMaxDynamicSharedMemorySize,
+    for (int i = 0; i < 2 * (RG_ACT_GELU_TANH + 1) && set == cudaSuccess; ++i)
+      set = cudaFuncSetAttribute(pair_act_kernel(i >> 1, i & 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  pair_smem(WALK_WHOLE, SIMPLE_ACT));
     if (set != cudaSuccess) return set;
     int sms = 0;
@@ -498,7 +498,7 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
                                             pair_smem(WALK_WHOLE, a.ep ? SIMPLE_ACT : PLAIN), st, 2, attr);
     CUtensorMap mc = {}, mp = {};
     if (!pair_maps(a, p, dev, &ma, &mc, &mp, a.M)) return cudaErrorInvalidValue;
-    const PairKernel kernel = a.ep ? reinterpret_cast<PairKernel>(const_cast<void*>(pair_act_kernel(a.ep->act)))
+    const PairKernel kernel = a.ep ? reinterpret_cast<PairKernel>(const_cast<void*>(pair_act_kernel(a.ep->act, a.ep->R)))
                                    : kPairKernels[a.b_kmajor][a.tile_b];
     return cudaLaunchKernelEx(&cfg, kernel, ma, mb, mc, mp, p, plan);
   }

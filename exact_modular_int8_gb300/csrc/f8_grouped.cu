@@ -25,12 +25,25 @@ namespace {
 // Persistent, a CTA per SM: a unit is 128 columns of one group's weights times up
 // to 128 of its tokens, over all of K.  The producer runs up to six blocks (of 16
 // KB of weights) ahead, across units, which is what keeps the weights coming.
+//
+// An epilogue warp adds a block's products to its sums while the next block's are
+// read, and the scales reach it multiplied.  (128 tokens to each of 8 groups of
+// 2048 x 4096, operands in L2: SUMS_128 us; ADD_AFTER with each block's read waited for
+// and its two scales multiplied in the loop; without the sums 17.4, which is L2's
+// rate, 11 TB/s.)
 // ---------------------------------------------------------------------------
 constexpr int NTOK = 128;
 constexpr int TOK_BOX = 32;  // tokens per copy
 constexpr int STAGES_N = 6;
 constexpr int STAGE_N_BYTES = 2 * SLAB;
-constexpr int SCALE_N_BYTES = SCALE_BUFS * (int)sizeof(ScaleChunk<NTOK>);
+constexpr int ACCS = 4;  // accumulators: all of tensor memory
+constexpr int SETS = 4;  // of four epilogue warps: every SETS-th 16 tokens each
+constexpr int SUM_WARPS = 4 * SETS;
+constexpr int FEW_THREADS = 128 + 32 * SUM_WARPS;
+struct TokenScales {
+  float s[KC][NTOK + 4];  // token's times the weights'
+};
+constexpr int SCALE_N_BYTES = SCALE_BUFS * (int)sizeof(TokenScales);
 constexpr int SMEM_N_BYTES = 1024 + STAGES_N * STAGE_N_BYTES + SCALE_N_BYTES + 256 + (int)sizeof(GroupTable);
 static_assert(SMEM_N_BYTES <= 232448, "shared memory");
 
@@ -60,19 +73,89 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// An epilogue warp's place in the pipeline.
+struct UnitPipe {
+  uint64_t *done, *tempty, *sfull, *sempty;
+  const TokenScales* scales;
+  uint32_t it, phase;
+  int chunk, st;  // chunks of scales, pipeline stage
+  bool ok;        // the same for all lanes
+};
+
+// One unit's sums of 32 columns from n0 on and PARTS times 16 tokens, every
+// SETS-th 16 from 16 `set` on, and their way to C.
+template <int PARTS>
+__device__ __forceinline__ void sum_unit(const Params& gp, const UnitAt& at, UnitPipe& p, uint32_t lane_addr, int set,
+                                         int n0, int lane, const Ctl& ctl) {
+  constexpr int P = PARTS ? PARTS : 1;
+  uint64_t acc[P][8] = {};
+  for (int kb = 0; kb < at.kb1; ++kb) {
+    const uint32_t b = p.it % ACCS;
+    const int kbi = kb % KC;
+    bool ok = kbi != 0 || wait_bounded(smem_u32(&p.sfull[p.chunk & 1]), (p.chunk >> 1) & 1u, ctl, 46);
+    p.ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded(smem_u32(&p.done[p.st]), p.phase, ctl, 44));
+    if (++p.st == STAGES_N) {
+      p.st = 0;
+      p.phase ^= 1u;
+    }
+    ++p.it;
+    if (!p.ok) return;
+    tc_fence_after();
+    uint32_t r[P][16];
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) tmem_ld16(lane_addr + b * NTOK + 16 * SETS * i, r[i]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[i][j]));
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_relaxed(smem_u32(&p.tempty[b]));
+    const float* s = p.scales[p.chunk & 1].s[kbi] + set * 16;
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(s + 16 * SETS * i + 2 * j);
+        acc[i][j] = fma2(pack2u(r[i][2 * j], r[i][2 * j + 1]), w.x, acc[i][j]);
+        acc[i][j + 1] = fma2(pack2u(r[i][2 * j + 2], r[i][2 * j + 3]), w.y, acc[i][j + 1]);
+      }
+    if (kbi == KC - 1 || kb == at.kb1 - 1) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&p.sempty[p.chunk & 1]));
+      ++p.chunk;
+    }
+  }
+  const int n = n0 + lane;
+  if (n < gp.N) {
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+      const int first = 16 * SETS * i + set * 16, left = at.count - first;
+      const long long out = (long long)(at.m0 + first) * gp.ldc + n;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 f = unpack2(acc[i][j]);
+        if (2 * j < left) store_out(gp.C, out + 2 * j * gp.ldc, gp.out_type, f.x);
+        if (2 * j + 1 < left) store_out(gp.C, out + (2 * j + 1) * gp.ldc, gp.out_type, f.y);
+      }
+    }
+  }
+}
+
 template <bool B_KMAJOR>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(FEW_THREADS, 1)
     f8_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ Params gp, DevPlan* plan) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stage_base = smem;  // weights, then tokens
-  ScaleChunk<NTOK>* scales = reinterpret_cast<ScaleChunk<NTOK>*>(smem + STAGES_N * STAGE_N_BYTES);
+  TokenScales* scales = reinterpret_cast<TokenScales*>(smem + STAGES_N * STAGE_N_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES_N * STAGE_N_BYTES + SCALE_N_BYTES);
   uint64_t* full = bars;
   uint64_t* done = bars + STAGES_N;        // the stage's MMAs are complete
   uint64_t* tempty = bars + 2 * STAGES_N;  // by accumulator
-  uint64_t* sfull = tempty + 2;
+  uint64_t* sfull = tempty + ACCS;
   uint64_t* sempty = sfull + SCALE_BUFS;
   uint64_t* drain = sempty + SCALE_BUFS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -87,10 +170,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&done[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&tempty[b]), EPI_WARPS);
+    for (int b = 0; b < ACCS; ++b) mbar_init(smem_u32(&tempty[b]), SUM_WARPS);
     for (int b = 0; b < SCALE_BUFS; ++b) {
       mbar_init(smem_u32(&sfull[b]), 64);
-      mbar_init(smem_u32(&sempty[b]), EPI_WARPS);
+      mbar_init(smem_u32(&sempty[b]), SUM_WARPS);
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -100,7 +183,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"((uint32_t)(2 * NTOK)));
+                 "r"((uint32_t)(ACCS * NTOK)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
@@ -114,9 +197,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int total = load_groups(gp.gr, tab, NTOK, gp.nt, plan);
   Units units{gp, tab};
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
+  if (warp < 4) {
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
       int stage = 0;
       uint32_t phase = 0;
       bool issued[STAGES_N] = {};
@@ -153,135 +236,83 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (issued[s]) wait_bounded(smem_u32(&full[s]), issued_phase[s], drain_ctl, 0);
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    const uint32_t w_addr = smem_u32(stage_base), x_addr = w_addr + SLAB;
-    const uint64_t wdesc0 = B_KMAJOR ? sw128_desc(w_addr, 16, 1024) : sw128_desc(w_addr, SLAB, 1024);
-    const uint64_t xdesc0 = sw128_desc(x_addr, 16, 1024);
-    constexpr uint32_t w_step = B_KMAJOR ? 2 : 256;  // 32 k: 32 bytes along a row, or 32 rows of 128 bytes
-    int stage = 0;
-    uint32_t phase = 0, it = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const UnitAt at = units.at(t);
-      // the weights are the A operand: M-major where they lie [K][N]
-      const uint32_t idesc = idesc_f8(128, (at.count + 15) & ~15, true) | (B_KMAJOR ? 0u : 1u << 15);
-      for (int kb = 0; kb < at.kb1; ++kb, ++it) {
-        const uint32_t b = it & 1u, aph = (it >> 1) & 1u;
-        ok = wait_both(smem_u32(&tempty[b]), aph ^ 1u, smem_u32(&full[stage]), phase, ctl, 42);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t off = (uint64_t)(stage * (STAGE_N_BYTES >> 4));
-        if (elect_one()) {
+    if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint32_t w_addr = smem_u32(stage_base), x_addr = w_addr + SLAB;
+      const uint64_t wdesc0 = B_KMAJOR ? sw128_desc(w_addr, 16, 1024) : sw128_desc(w_addr, SLAB, 1024);
+      const uint64_t xdesc0 = sw128_desc(x_addr, 16, 1024);
+      constexpr uint32_t w_step = B_KMAJOR ? 2 : 256;  // 32 k: 32 bytes along a row, or 32 rows of 128 bytes
+      int stage = 0;
+      uint32_t phase = 0, it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const UnitAt at = units.at(t);
+        // the weights are the A operand: M-major where they lie [K][N]
+        const uint32_t idesc = idesc_f8(128, (at.count + 15) & ~15, true) | (B_KMAJOR ? 0u : 1u << 15);
+        for (int kb = 0; kb < at.kb1; ++kb, ++it) {
+          const uint32_t b = it % ACCS, aph = (it / ACCS) & 1u;
+          ok = wait_both(smem_u32(&tempty[b]), aph ^ 1u, smem_u32(&full[stage]), phase, ctl, 42);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t off = (uint64_t)(stage * (STAGE_N_BYTES >> 4));
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            umma_f8(tmem_base + b * NTOK, wdesc0 + off + (uint64_t)(w_step * kk), xdesc0 + off + (uint64_t)(2 * kk),
-                    idesc, kk > 0);
-          if (!(gp.fault == 1 && it == 0)) umma_commit(smem_u32(&done[stage]));
+            for (int kk = 0; kk < BK / 32; ++kk)
+              umma_f8(tmem_base + b * NTOK, wdesc0 + off + (uint64_t)(w_step * kk), xdesc0 + off + (uint64_t)(2 * kk),
+                      idesc, kk > 0);
+            if (!(gp.fault == 1 && it == 0)) umma_commit(smem_u32(&done[stage]));
+          }
+          __syncwarp();
+          if (++stage == STAGES_N) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
+      }
+      if (!ok && it > 0) {  // all issued MMAs must finish before the memory is freed
+        Ctl drain_ctl = ctl;
+        volatile int never = 0;
+        drain_ctl.abort = &never;
+        if (elect_one()) umma_commit(smem_u32(drain));
         __syncwarp();
-        if (++stage == STAGES_N) {
-          stage = 0;
-          phase ^= 1u;
+        wait_bounded(smem_u32(drain), 0, drain_ctl, 0);
+      }
+    }
+    if (warp >= 2) {
+      // ---------------------------------------------------------- scales
+      const int tid = threadIdx.x - 64, kbi = tid & (KC - 1);
+      int c = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const UnitAt at = units.at(t);
+        const float* SB = gp.SB + at.g * gp.sb_e + at.n0 / 128 * gp.sb_n;
+        for (int kb0 = 0; kb0 < at.kb1; kb0 += KC, ++c) {
+          const int b = c & 1, kb = min(kb0 + kbi, at.kb1 - 1);
+          ok = wait_bounded(smem_u32(&sempty[b]), ((c >> 1) & 1u) ^ 1u, ctl, 45);
+          if (!ok) break;
+          const float sb = SB[kb * gp.sb_k];
+          const float* sa = gp.SA + (long long)at.m0 * gp.sa_ld + kb;
+#pragma unroll 4
+          for (int r = tid >> 3; r < at.count; r += 8) scales[b].s[kbi][r] = sa[r * gp.sa_ld] * sb;
+          mbar_arrive(smem_u32(&sfull[b]));
         }
       }
     }
-    if (!ok && it > 0) {  // all issued MMAs must finish before the memory is freed
-      Ctl drain_ctl = ctl;
-      volatile int never = 0;
-      drain_ctl.abort = &never;
-      if (elect_one()) umma_commit(smem_u32(drain));
-      __syncwarp();
-      wait_bounded(smem_u32(drain), 0, drain_ctl, 0);
-    }
-  } else if (warp < 4) {
-    // ------------------------------------------------------------ scales
-    const int tid = threadIdx.x - 64, kbi = tid & (KC - 1);
-    int c = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const UnitAt at = units.at(t);
-      const float* SB = gp.SB + at.g * gp.sb_e + at.n0 / 128 * gp.sb_n;
-      for (int kb0 = 0; kb0 < at.kb1; kb0 += KC, ++c) {
-        const int b = c & 1, kb = min(kb0 + kbi, at.kb1 - 1);
-        ok = wait_bounded(smem_u32(&sempty[b]), ((c >> 1) & 1u) ^ 1u, ctl, 45);
-        if (!ok) break;
-        for (int r = tid >> 3; r < at.count; r += 8)
-          cp_async4(smem_u32(&scales[b].a[kbi][r]), gp.SA + (long long)(at.m0 + r) * gp.sa_ld + kb);
-        if (tid < KC) cp_async4(smem_u32(&scales[b].b[kbi][0]), SB + kb * gp.sb_k);
-        cp_async_arrive(smem_u32(&sfull[b]));
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ------------------------------------------------------------ epilogue
     const int q4 = warp & 3;           // tensor-memory lane quarter this warp may access
-    const int odd = (warp - 4) >> 2;  // every other 16 tokens, from these on
-    constexpr int PARTS = NTOK / 32;
-    const uint32_t lane_addr = tmem_base + ((uint32_t)(q4 * 32) << 16) + odd * 16;
-    uint32_t it = 0, phase = 0;
-    int chunk = 0, st = 0;  // pipeline stage
-    bool ok = true;
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+    const int set = (warp - 4) >> 2;
+    static_assert(NTOK == 2 * 16 * SETS, "up to two parts to a warp");
+    const uint32_t lane_addr = tmem_base + ((uint32_t)(q4 * 32) << 16) + set * 16;
+    UnitPipe pipe{full + STAGES_N, tempty, sfull, sempty, scales, 0, 0, 0, 0, true};
+    for (int t = blockIdx.x; t < total && pipe.ok; t += gridDim.x) {
       const UnitAt at = units.at(t);
-      const int mine = (at.count - odd * 16 + 31) / 32;  // 16-token parts with a token
-      uint64_t acc[PARTS][8] = {};
-      for (int kb = 0; kb < at.kb1; ++kb, ++it) {
-        const uint32_t b = it & 1u;
-        const int kbi = kb % KC;
-        const ScaleChunk<NTOK>& sc = scales[chunk & 1];
-        ok = kbi != 0 || wait_bounded(smem_u32(&sfull[chunk & 1]), (chunk >> 1) & 1u, ctl, 46);
-        ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded(smem_u32(&done[st]), phase, ctl, 44));
-        if (++st == STAGES_N) {
-          st = 0;
-          phase ^= 1u;
-        }
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t r[PARTS][16];
-#pragma unroll
-        for (int i = 0; i < PARTS; ++i)
-          if (i < mine) tmem_ld16(lane_addr + b * NTOK + 32 * i, r[i]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < PARTS; ++i)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(r[i][j]));
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_relaxed(smem_u32(&tempty[b]));
-        // the scales' product first, as the pair kernel forms it
-        const uint64_t sb = pack2(sc.b[kbi][0], sc.b[kbi][0]);
-#pragma unroll
-        for (int i = 0; i < PARTS; ++i)
-          if (i < mine) {
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              const ulonglong2 sa = *reinterpret_cast<const ulonglong2*>(&sc.a[kbi][32 * i + odd * 16 + 2 * j]);
-              acc[i][j] = fma2(pack2u(r[i][2 * j], r[i][2 * j + 1]), mul2(sa.x, sb), acc[i][j]);
-              acc[i][j + 1] = fma2(pack2u(r[i][2 * j + 2], r[i][2 * j + 3]), mul2(sa.y, sb), acc[i][j + 1]);
-            }
-          }
-        if (kbi == KC - 1 || kb == at.kb1 - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sempty[chunk & 1]));
-          ++chunk;
-        }
-      }
-      const int n = at.n0 + q4 * 32 + lane;
-      if (ok && n < gp.N) {
-#pragma unroll
-        for (int i = 0; i < PARTS; ++i)
-          if (i < mine) {
-            const int first = 32 * i + odd * 16, left = at.count - first;
-            const long long out = (long long)(at.m0 + first) * gp.ldc + n;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float2 f = unpack2(acc[i][j]);
-              if (2 * j < left) store_out(gp.C, out + 2 * j * gp.ldc, gp.out_type, f.x);
-              if (2 * j + 1 < left) store_out(gp.C, out + (2 * j + 1) * gp.ldc, gp.out_type, f.y);
-            }
-          }
+      const int n0 = at.n0 + q4 * 32;
+      // 16-token parts with a token: an instance for each number, whose loops are unrolled
+      switch ((at.count - set * 16 + 16 * SETS - 1) / (16 * SETS)) {
+        case 0: sum_unit<0>(gp, at, pipe, lane_addr, set, n0, lane, ctl); break;
+        case 1: sum_unit<1>(gp, at, pipe, lane_addr, set, n0, lane, ctl); break;
+        default: sum_unit<2>(gp, at, pipe, lane_addr, set, n0, lane, ctl); break;
       }
     }
   }
@@ -292,7 +323,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
-                 "r"((uint32_t)(2 * NTOK)));
+                 "r"((uint32_t)(ACCS * NTOK)));
   }
 }
 
@@ -301,9 +332,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // ---------------------------------------------------------------------------
 using FewKernel = void (*)(const CUtensorMap, const CUtensorMap, const Params, DevPlan*);
 constexpr FewKernel kFewKernels[2] = {f8_few_kernel<false>, f8_few_kernel<true>};
-constexpr PairKernel kRowsKernels[2] = {f8_gemm_pair_kernel<false, true, WALK_ROWS, PLAIN>,
-                                        f8_gemm_pair_kernel<true, true, WALK_ROWS, PLAIN>};
-constexpr PairKernel kBlocksKernel = f8_gemm_pair_kernel<true, false, WALK_BLOCKS, PLAIN>;
+constexpr PairKernel kRowsKernels[2] = {f8_gemm_pair_kernel<false, true, WALK_ROWS, PLAIN, false>,
+                                        f8_gemm_pair_kernel<true, true, WALK_ROWS, PLAIN, false>};
+constexpr PairKernel kBlocksKernel = f8_gemm_pair_kernel<true, false, WALK_BLOCKS, PLAIN, false>;
 
 struct GroupedDevice {
   int sms = 0, max_pairs = 0;
@@ -395,7 +426,7 @@ cudaError_t launch_f8_grouped(const F8GemmArgs& a, const F8Groups& g, DevPlan* p
       return cudaErrorInvalidValue;
     const long long units = (a.M / NTOK + groups) * p.nt;
     return launch_dependent(kFewKernels[a.b_kmajor], dim3((unsigned)std::min<long long>(units, gd.sms)),
-                            dim3(NUM_THREADS), SMEM_N_BYTES, st, ma, mb, p, plan);
+                            dim3(FEW_THREADS), SMEM_N_BYTES, st, ma, mb, p, plan);
   }
   p.nt = (int)((a.N + BN2 - 1) / BN2);
   long long tiles = (a.M / 256 + groups) * p.nt;

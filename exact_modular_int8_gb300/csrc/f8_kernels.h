@@ -69,7 +69,7 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
                            unsigned long long wait_ns);
 
 // The pair kernel with an epilogue (f8_act.cu); its parameters are those of f8_gemm.cu's.
-const void* pair_act_kernel(int act);
+const void* pair_act_kernel(int act, bool residual);
 
 // Products by group, group g holding rows (or, by_blocks, columns along the
 // contraction) offsets[g] .. offsets[g + 1].

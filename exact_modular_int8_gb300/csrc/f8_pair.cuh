@@ -36,6 +36,7 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int BN2 = 256;
 constexpr int STAGES2 = 5;
+constexpr int STAGES2_RES = 4;  // with a residual, whose rings take a stage's place
 constexpr int STAGE2_BYTES = 2 * SLAB;
 constexpr int HALF_SLAB = SLAB / 2;  // a CTA's 64 columns of one half
 constexpr int PAIR_COLS = BN2 * 4 / EPI_WARPS;  // columns per epilogue warp
@@ -44,6 +45,8 @@ constexpr int OUT_WARP = 2 * OUT_BUF;
 constexpr int SCALE2_BYTES = SCALE_BUFS * (int)sizeof(ScaleChunk<BN2>);
 constexpr int SMEM2_BASE = 1024 + STAGES2 * STAGE2_BYTES + EPI_WARPS * OUT_WARP + SCALE2_BYTES + 256;
 constexpr int BIAS_BYTES = EPI_WARPS * PAIR_COLS * 4;
+constexpr int RES_BYTES = EPI_WARPS * OUT_WARP;  // two buffers like a warp's for its results
+static_assert(RES_BYTES <= STAGE2_BYTES, "in the place of a stage");
 
 // What the tiles cover.
 constexpr int WALK_WHOLE = 0;  // one matrix
@@ -225,57 +228,69 @@ __device__ __forceinline__ void store_rows(const Params& gp, const CUtensorMap* 
   }
 }
 
-// 64 bytes of this lane's row of the residual from column cc on, as loaded.
+// 64 bytes of each of a warp's rows of the residual, from column cc on, on their way
+// to a buffer laid out like the ones for results.  Where its rows do not start on
+// 16-byte boundaries, or end within these columns, wait_residual fetches them.
 template <int ES>
-__device__ __forceinline__ void load_residual(const Params& gp, uint4 (&r)[4], int row, bool live, int cc) {
-  constexpr int COLS = 64 / ES;
-  const uint8_t* p = static_cast<const uint8_t*>(gp.ep.R) + ((long long)row * gp.ep.ldr + cc) * ES;
-  if (live && gp.vec_r && cc + COLS <= gp.N) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = reinterpret_cast<const uint4*>(p)[i];  // not __ldg: it may be C
-  } else {
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = 0;
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < COLS; ++i)
-        if (cc + i < gp.N) {
-          if constexpr (ES == 4) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-          else w[i >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  }
+__device__ __forceinline__ bool residual_async(const Params& gp, int cc) {
+  return gp.vec_r && cc + 64 / ES <= gp.N;
 }
 template <int ES>
-__device__ __forceinline__ float2 residual_pair(const uint4 (&r)[4], int j, int type) {  // columns 2 j, 2 j + 1
-  const uint32_t w[16] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w,
-                          r[2].x, r[2].y, r[2].z, r[2].w, r[3].x, r[3].y, r[3].z, r[3].w};
+__device__ __forceinline__ void start_residual(const Params& gp, uint8_t* buf, int row0, int rows, int cc, int lane) {
+  if (residual_async<ES>(gp, cc)) {
+    const uint8_t* p = static_cast<const uint8_t*>(gp.ep.R) + ((long long)row0 * gp.ep.ldr + cc) * ES + 16 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      if (r < rows)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(buf) + r * 64 +
+                                                                       (((lane & 3) ^ ((r >> 1) & 3)) << 4)),
+                     "l"(p + r * gp.ep.ldr * ES)
+                     : "memory");
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int ES>
+__device__ __forceinline__ void wait_residual(const Params& gp, uint8_t* buf, int row0, int rows, int cc, int lane) {
+  asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the next chunk's
+  if (!residual_async<ES>(gp, cc)) {
+    const int cols = min(64 / ES, gp.N - cc);
+    const uint8_t* p = static_cast<const uint8_t*>(gp.ep.R) + ((long long)row0 * gp.ep.ldr + cc) * ES;
+    for (int r = 0; r < rows; ++r)
+      for (int j = lane; j < cols; j += 32) {
+        uint8_t* dst = buf + r * 64 + (((j * ES >> 4) ^ ((r >> 1) & 3)) << 4) + (j * ES & 15);
+        if constexpr (ES == 4)
+          *reinterpret_cast<uint32_t*>(dst) = reinterpret_cast<const uint32_t*>(p + r * gp.ep.ldr * ES)[j];
+        else
+          *reinterpret_cast<uint16_t*>(dst) = reinterpret_cast<const uint16_t*>(p + r * gp.ep.ldr * ES)[j];
+      }
+  }
+  __syncwarp();
+}
+template <int ES>
+__device__ __forceinline__ float2 residual_pair(const uint4& r, int j, int type) {  // columns 2 j, 2 j + 1 of 16 bytes
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
   if constexpr (ES == 4) return make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
   else if (type == RG_TYPE_F16) return __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
   else return make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
 }
 
 // The same with an epilogue: sums + bias, stored where they are wanted before the
-// activation, then the activation and the residual.  The residual's rows are
-// on their way to L2 since the tile began (prefetch_residual) and read 64 bytes a
-// lane ahead, each lane its own row: whole sectors, though not whole lines.
-template <int ES, int ACT>
+// activation, then the activation and the residual.  The residual comes 64 bytes
+// of each row at a time through a ring of two buffers, the first two of them since
+// the tile began (start_residual there).
+template <int ES, int ACT, bool RES>
 __device__ __forceinline__ void store_rows_act(const Params& gp, const CUtensorMap* tmC, const CUtensorMap* tmP,
-                                               Sums<PAIR_COLS, true>& sums, const float* bias, uint8_t* stage, int row0,
-                                               int rows, int col0, int lane) {
-  constexpr int COLS = 64 / ES, CHUNKS = PAIR_COLS / COLS;
-  const bool relu = ACT == SIMPLE_ACT && gp.ep.act == RG_ACT_RELU, live = lane < rows;
-  uint4 res[2][4];
-  if (gp.ep.R) load_residual<ES>(gp, res[0], row0 + lane, live, col0);
+                                               Sums<PAIR_COLS, true>& sums, const float* bias, uint8_t* stage,
+                                               uint8_t* ring, int row0, int rows, int col0, int lane) {
+  constexpr int COLS = 64 / ES, CHUNKS = PAIR_COLS / COLS, PER = 8 / ES;  // pairs of columns in 16 bytes
+  const bool relu = ACT == SIMPLE_ACT && gp.ep.act == RG_ACT_RELU;
   int n = 0;  // stores
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
     uint64_t* acc = sums.acc[0] + c * (COLS / 2);
     const int cc = col0 + c * COLS;
-    if (gp.ep.R && c + 1 < CHUNKS) load_residual<ES>(gp, res[(c + 1) & 1], row0 + lane, live, cc + COLS);
 #pragma unroll
     for (int j = 0; j < COLS / 2; j += 2) {
       const float4 b = *reinterpret_cast<const float4*>(bias + c * COLS + 2 * j);
@@ -289,20 +304,32 @@ __device__ __forceinline__ void store_rows_act(const Params& gp, const CUtensorM
       stage_row<ES>(buf, acc, gp.out_type, lane);
       store_chunk<ES>(tmP, gp.vec_c, gp.ep.P, gp.ldc, gp.vec_c, buf, row0, rows, cc, gp.N, lane);
     }
+    uint8_t* in = ring + (c & 1) * OUT_BUF;
+    if constexpr (RES) wait_residual<ES>(gp, in, row0, rows, cc, lane);
 #pragma unroll
-    for (int j = 0; j < COLS / 2; ++j) {
-      float2 f = unpack2(acc[j]);
-      if constexpr (ACT == SIMPLE_ACT) {
-        if (relu) f = make_float2(activate<RG_ACT_RELU>(f.x), activate<RG_ACT_RELU>(f.y));
-      } else {
-        f = make_float2(activate<ACT>(f.x), activate<ACT>(f.y));
+    for (int i = 0; i < 4; ++i) {
+      uint4 res = make_uint4(0, 0, 0, 0);
+      if constexpr (RES) res = *reinterpret_cast<const uint4*>(in + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        float2 f = unpack2(acc[i * PER + j]);
+        if constexpr (ACT == SIMPLE_ACT) {
+          if (relu) f = make_float2(activate<RG_ACT_RELU>(f.x), activate<RG_ACT_RELU>(f.y));
+        } else {
+          f = make_float2(activate<ACT>(f.x), activate<ACT>(f.y));
+        }
+        if constexpr (RES) {
+          const float2 r = residual_pair<ES>(res, j, gp.out_type);
+          f.x += r.x;
+          f.y += r.y;
+        }
+        acc[i * PER + j] = pack2(f.x, f.y);
       }
-      if (gp.ep.R) {
-        const float2 r = residual_pair<ES>(res[c & 1], j, gp.out_type);
-        f.x += r.x;
-        f.y += r.y;
-      }
-      acc[j] = pack2(f.x, f.y);
+    }
+    if constexpr (RES) {
+      __syncwarp();
+      if (c + 2 < CHUNKS) start_residual<ES>(gp, in, row0, rows, cc + 2 * COLS, lane);
+      else asm volatile("cp.async.commit_group;" ::: "memory");
     }
     buffer_free(gp.vec_c, lane);
     uint8_t* buf = stage + (n++ & 1) * OUT_BUF;
@@ -310,34 +337,29 @@ __device__ __forceinline__ void store_rows_act(const Params& gp, const CUtensorM
     store_chunk<ES>(tmC, gp.vec_c, gp.C, gp.ldc, gp.vec_c, buf, row0, rows, cc, gp.N, lane);
   }
 }
-// The residual of this warp's rows and columns to L2, a row to a lane.
-__device__ __forceinline__ void prefetch_residual(const Params& gp, int row, int col0, int es) {
-  if (row >= gp.M || col0 >= gp.N) return;
-  const uint8_t* p = static_cast<const uint8_t*>(gp.ep.R) + ((long long)row * gp.ep.ldr + col0) * es;
-  const int bytes = min(PAIR_COLS, gp.N - col0) * es;
-  for (int i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
-}
 
-template <bool B_KMAJOR, bool TILE_B, int WALK, int ACT>
+template <bool B_KMAJOR, bool TILE_B, int WALK, int ACT, bool RES>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     f8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmP,
                         const __grid_constant__ Params gp, DevPlan* plan) {
-  static_assert(ACT == PLAIN || (TILE_B && WALK == WALK_WHOLE), "an epilogue has a bias for each column");
+  static_assert(ACT == PLAIN ? !RES : TILE_B && WALK == WALK_WHOLE, "an epilogue has a row to a lane");
+  constexpr int STAGES = RES ? STAGES2_RES : STAGES2;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t rank = cluster_rank();
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stage_base = smem;
   uint8_t* out_base = smem + STAGES2 * STAGE2_BYTES;
+  uint8_t* ring_base = smem + STAGES2_RES * STAGE2_BYTES;  // RES
   ScaleChunk<BN2>* scales = reinterpret_cast<ScaleChunk<BN2>*>(out_base + EPI_WARPS * OUT_WARP);
   uint64_t* bars = reinterpret_cast<uint64_t*>(out_base + EPI_WARPS * OUT_WARP + SCALE2_BYTES);
   uint8_t* more = reinterpret_cast<uint8_t*>(bars) + 256;
   GroupTable& tab = *reinterpret_cast<GroupTable*>(more);   // WALK_ROWS, WALK_BLOCKS
   float* bias_base = reinterpret_cast<float*>(more);        // epilogues
   uint64_t* full = bars;
-  uint64_t* done = bars + STAGES2;         // by half * STAGES2 + stage: the half's MMAs of the stage are complete
-  uint64_t* tempty = bars + 3 * STAGES2;  // by half * 2 + accumulator
+  uint64_t* done = bars + STAGES;         // by half * STAGES + stage: the half's MMAs of the stage are complete
+  uint64_t* tempty = bars + 3 * STAGES;  // by half * 2 + accumulator
   uint64_t* sfull = tempty + 4;
   uint64_t* sempty = sfull + SCALE_BUFS;
   uint64_t* drain = sempty + SCALE_BUFS;  // by half
@@ -348,10 +370,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   Ctl ctl{abort_flag, &plan->status, &plan->timeout_where, gp.wait_ns};
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES2; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&done[s]), 1);
-      mbar_init(smem_u32(&done[STAGES2 + s]), 1);
+      mbar_init(smem_u32(&done[STAGES + s]), 1);
     }
     for (int b = 0; b < 4; ++b) mbar_init(smem_u32(&tempty[b]), EPI_WARPS);  // the half's warps of both CTAs
     for (int b = 0; b < SCALE_BUFS; ++b) {
@@ -394,7 +416,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const TileAt at = walk.at(t);
         for (int kb = at.kb0; kb < at.kb1; ++kb) {
           if (!wait_bounded(smem_u32(&done[stage]), phase ^ 1u, ctl, 31) ||
-              !wait_bounded(smem_u32(&done[STAGES2 + stage]), phase ^ 1u, ctl, 31)) {
+              !wait_bounded(smem_u32(&done[STAGES + stage]), phase ^ 1u, ctl, 31)) {
             ok = false;
             break;
           }
@@ -415,7 +437,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               else tma_load_2d_pair(b_dst, &tmB, fb, n0, kb * BK);
             }
           }
-          if (++stage == STAGES2) {
+          if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
@@ -448,10 +470,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < BK / 32; ++kk)
               umma_f8_pair(d, adesc0 + off + (uint64_t)(2 * kk), bdesc0 + off + (uint64_t)(b_step * kk), idesc, kk > 0);
-            if (!(gp.fault == 1 && it == 0)) umma_commit_pair(smem_u32(&done[half * STAGES2 + stage]));
+            if (!(gp.fault == 1 && it == 0)) umma_commit_pair(smem_u32(&done[half * STAGES + stage]));
           }
           __syncwarp();
-          if (++stage == STAGES2) {
+          if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
@@ -504,6 +526,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // a group's last tile: warps without a row of it leave the sums alone
       const bool mine = WALK != WALK_ROWS || row0 < at.m_end;
       float* bias = bias_base + ew * PAIR_COLS;
+      uint8_t* ring = ring_base + ew * OUT_WARP;
       if constexpr (ACT != PLAIN) {
 #pragma unroll
         for (int j = 0; j < PAIR_COLS; j += 32) {
@@ -511,7 +534,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           bias[j + lane] = gp.ep.bias && n < gp.N ? load_real(gp.ep.bias, gp.ep.bias_type, n) : 0.0f;
         }
         __syncwarp();
-        if (gp.ep.R) prefetch_residual(gp, row0 + lane, col0, gp.out_type == RG_TYPE_F32 ? 4 : 2);
+        if constexpr (RES) {
+          const int rows = min(32, at.m_end - row0), es = gp.out_type == RG_TYPE_F32 ? 4 : 2;
+          for (int c = 0; c < 2; ++c) {
+            uint8_t* buf = ring + c * OUT_BUF;
+            if (es == 4) start_residual<4>(gp, buf, row0, rows, col0 + c * 16, lane);
+            else start_residual<2>(gp, buf, row0, rows, col0 + c * 32, lane);
+          }
+        }
       }
       using Acc = Sums<PAIR_COLS, TILE_B>;
       Acc sums = {};
@@ -520,8 +550,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int kbi = (kb - at.kb0) % KC;
         const ScaleChunk<BN2>& sc = scales[chunk & 1];
         ok = kbi != 0 || wait_bounded(smem_u32(&sfull[chunk & 1]), (chunk >> 1) & 1u, ctl, 36);
-        ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded(smem_u32(&done[half * STAGES2 + st]), phase, ctl, 34));
-        if (++st == STAGES2) {
+        ok = __all_sync(0xFFFFFFFFu, ok && wait_bounded(smem_u32(&done[half * STAGES + st]), phase, ctl, 34));
+        if (++st == STAGES) {
           st = 0;
           phase ^= 1u;
         }
@@ -552,10 +582,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (ok && row0 < at.m_end && col0 < gp.N) {
         const int rows = min(32, at.m_end - row0);
         if constexpr (ACT != PLAIN) {
+          // nothing that is computed from these before the blocks' loop, where no register is free
+          int r0 = row0, c0 = col0, l = lane;
+          asm volatile("" : "+r"(r0), "+r"(c0), "+r"(l));
           if (gp.out_type == RG_TYPE_F32)
-            store_rows_act<4, ACT>(gp, &tmC, &tmP, sums, bias, stage, row0, rows, col0, lane);
+            store_rows_act<4, ACT, RES>(gp, &tmC, &tmP, sums, bias, stage, ring, r0, rows, c0, l);
           else
-            store_rows_act<2, ACT>(gp, &tmC, &tmP, sums, bias, stage, row0, rows, col0, lane);
+            store_rows_act<2, ACT, RES>(gp, &tmC, &tmP, sums, bias, stage, ring, r0, rows, c0, l);
         } else {
           const int c_row0 = row0 + (WALK == WALK_BLOCKS ? at.g * gp.M : 0);
           if (gp.out_type == RG_TYPE_F32) store_rows<4, TILE_B, WALK>(gp, &tmC, sums, stage, c_row0, rows, col0, lane);
@@ -563,6 +596,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
     }
+    if constexpr (RES) asm volatile("cp.async.wait_all;" ::: "memory");
     bulk_wait0();
   }
 

@@ -45,9 +45,12 @@ def _native():
         loader.exec_module(m)
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
         entries = (lib.quantize_f8, lib.scaled_gemm_f8, lib.linear_f8, lib.linear_f8_backward,
-                   lib.linear_f8_saved_bytes, lib.linear_f8_ws_bytes, lib.rg_stream_capturing)
+                   lib.linear_f8_saved_bytes, lib.linear_f8_ws_bytes, lib.rg_stream_capturing, lib.scaled_gemm_act_f8,
+                   lib.linear_act_f8, lib.linear_act_f8_backward, lib.linear_act_f8_saved_bytes,
+                   lib.linear_act_f8_ws_bytes, lib.grouped_gemm_f8, lib.grouped_wgrad_f8, lib.expert_linear_f8,
+                   lib.expert_linear_f8_backward, lib.expert_linear_f8_saved_bytes, lib.expert_linear_f8_ws_bytes)
         m.setup(tuple(address(f) for f in entries), (torch.float32, torch.float16, torch.bfloat16), F8, torch.uint8,
-                torch.empty, torch.empty_strided, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache,
+                (torch.int32, torch.int64), torch.empty, torch.empty_strided, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache,
                 _check)
         _call = m
     return _call

@@ -15,7 +15,7 @@ import torch
 
 from . import (RG_ACT_GELU, RG_ACT_GELU_TANH, RG_ACT_NONE, RG_ACT_RELU, RG_ACT_SILU, RG_ERR_ARG, RG_FLAG_SYNC,
                ResGemmError, _output, library)
-from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _device_index, _launch, _no_grad, _rows_of,
+from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _device_index, _launch, _native, _no_grad, _rows_of,
                  _scratch)
 
 _ACTS = {None: RG_ACT_NONE, "relu": RG_ACT_RELU, "silu": RG_ACT_SILU, "gelu": RG_ACT_GELU,
@@ -53,6 +53,12 @@ def _there(*ts):
     return [t for t in ts if t is not None]
 
 
+def _differentiable(A, B, C, D, bias, residual) -> bool:
+    return torch.is_grad_enabled() and (
+        A.requires_grad or B.requires_grad or C.requires_grad or D.requires_grad
+        or (bias is not None and bias.requires_grad) or (residual is not None and residual.requires_grad))
+
+
 def scaled_gemm_act_f8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torch.Tensor,
                        bias: torch.Tensor | None = None, act: str | None = None,
                        residual: torch.Tensor | None = None, pre: bool = False,
@@ -64,12 +70,16 @@ def scaled_gemm_act_f8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: t
     x 128 tile; K at least 1.  bias [N] in float32, float16 or bfloat16; residual [M, N] in out_dtype, which C and P
     are rounded to once.  out may be the residual itself, which it then replaces.  No gradient (linear_act_f8 has
     one): a backward pass through C raises."""
-    if torch.is_grad_enabled() and any(t.requires_grad for t in _there(A, SA, B, SB, bias, residual)):
+    if _differentiable(A, SA, B, SB, bias, residual):
         return _no_grad("scaled_gemm_act_f8", out,
                         lambda: scaled_gemm_act_f8(A, SA, B, SB, bias, act, residual, pre, out_dtype, sync, None, ws),
                         *_there(A, SA, B, SB, bias, residual))
     where = "scaled_gemm_act_f8"
     a = _act(where, act)
+    if out is None and ws is None and A.is_cuda:
+        r = _native().act(A, SA, B, SB, bias, a, residual, pre, out_dtype, RG_FLAG_SYNC if sync else 0)
+        if r is not None:
+            return r
     if A.dim() != 2 or B.dim() != 2 or A.dtype != F8 or B.dtype != F8 or A.shape[1] != B.shape[1] or not A.shape[1]:
         raise ValueError(f"{where}: A [M, K] and B [N, K] float8_e4m3fn expected")
     (M, K), N = A.shape, B.shape[0]
@@ -128,11 +138,16 @@ def linear_act_f8(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = 
     dtype, which residual [M, N] has too; bias [N].  `saved` is what linear_act_f8_backward needs: with an
     activation also X W^T + bias in X's dtype, where the activation's slope is taken.  Where an argument requires a
     gradient autograd calls linear_act_f8_backward for Y."""
-    if torch.is_grad_enabled() and any(t.requires_grad for t in _there(X, W, bias, residual)):
+    if _differentiable(X, W, X, W, bias, residual):
         saved = []
         return _LinearActGrad.apply(X, W, bias, residual, act, sync, ws, saved), tuple(saved)
     where = "linear_act_f8"
     a = _act(where, act)
+    if ws is None and X.is_cuda:
+        r = _native().linear_act(X, W, bias, a, residual, RG_FLAG_SYNC if sync else 0)
+        if r is not None:
+            Y, kept, M, N, K = r
+            return Y, (kept, M, N, K, act, X.dtype, None if bias is None else bias.dtype)
     tx, tw = _TYPES.get(X.dtype), _TYPES.get(W.dtype)
     if tx is None or tw is None or X.dim() != 2 or W.dim() != 2 or X.shape[1] != W.shape[1] or not X.shape[1]:
         raise ValueError(f"{where}: X [M, K] and W [N, K] float32, float16 or bfloat16 expected")
@@ -161,8 +176,12 @@ def linear_act_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype:
     t, tw = _TYPES.get(dY.dtype), _TYPES.get(dw_dtype)
     if dY.dtype != dtype or tw is None or dY.shape != (M, N):
         raise ValueError(f"{where}: dY with the output's shape and dtype expected")
-    idx = _device_index(where, dY, kept)
     a = _act(where, act)
+    if ws is None and dY.is_cuda:
+        r = _native().linear_act_backward(dY, kept, M, N, K, a, bias_dtype, dw_dtype, RG_FLAG_SYNC if sync else 0)
+        if r is not None:
+            return r
+    idx = _device_index(where, dY, kept)
     need = _linear_act_bytes(M, N, K, t, a)[1]
     dY, lddy = _rows_of(dY)
     dX = torch.empty((M, K), dtype=dtype, device=dY.device)

@@ -17,8 +17,8 @@ import torch
 
 from . import (RG_ERR_ARG, RG_FLAG_KEEP_REST, RG_FLAG_OFFSETS64, RG_FLAG_SYNC, RG_FLAG_TRANS_B, ResGemmError, _output,
                library)
-from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _device_index, _groups, _launch, _no_grad, _rows_of,
-                 _scratch, _stack_stride)
+from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _device_index, _groups, _launch, _native, _no_grad,
+                 _rows_of, _scratch, _stack_stride)
 
 
 def _aligned_stack(q: torch.Tensor):
@@ -50,6 +50,10 @@ def grouped_gemm_f8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: torc
     if torch.is_grad_enabled() and (A.requires_grad or SA.requires_grad or B.requires_grad or SB.requires_grad):
         return _no_grad(where, out, lambda: grouped_gemm_f8(A, SA, B, SB, offsets, out_dtype, transb, sync, None, ws),
                         A, SA, B, SB)
+    if out is None and ws is None and A.is_cuda:
+        C = _native().rows(A, SA, B, SB, offsets, out_dtype, transb, RG_FLAG_SYNC if sync else 0)
+        if C is not None:
+            return C
     if A.dim() != 2 or B.dim() != 3 or A.dtype != F8 or B.dtype != F8 or not A.shape[1]:
         raise ValueError(f"{where}: A [T, K] and B [E, K, N] (transb: [E, N, K]) float8_e4m3fn expected")
     T, K = A.shape
@@ -88,6 +92,10 @@ def grouped_wgrad_f8(A: torch.Tensor, SA: torch.Tensor, B: torch.Tensor, SB: tor
     if torch.is_grad_enabled() and (A.requires_grad or SA.requires_grad or B.requires_grad or SB.requires_grad):
         return _no_grad(where, out, lambda: grouped_wgrad_f8(A, SA, B, SB, offsets, out_dtype, sync, None, ws),
                         A, SA, B, SB)
+    if out is None and ws is None and A.is_cuda:
+        C = _native().sums(A, SA, B, SB, offsets, out_dtype, RG_FLAG_SYNC if sync else 0)
+        if C is not None:
+            return C
     if A.dim() != 2 or B.dim() != 2 or A.dtype != F8 or B.dtype != F8 or A.shape[1] != B.shape[1] or \
             A.shape[1] % 128:
         raise ValueError(f"{where}: A [M, 128 NB] and B [N, 128 NB] float8_e4m3fn expected")
@@ -150,6 +158,10 @@ def expert_linear_f8(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, sy
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
         saved = []
         return _ExpertGrad.apply(X, W, offsets, sync, ws, saved), tuple(saved)
+    if X.is_cuda and ws is None:
+        r = _native().expert(X, W, offsets, RG_FLAG_SYNC if sync else 0)
+        if r is not None:
+            return r
     where = "expert_linear_f8"
     tx, tw = _TYPES.get(X.dtype), _TYPES.get(W.dtype)
     if tx is None or tw is None or X.dim() != 2 or W.dim() != 3 or X.shape[1] != W.shape[2] or not X.shape[1]:
@@ -177,6 +189,10 @@ def expert_linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dty
     dtype, 0 behind the last group, and dW [E, N, K] = dY^T X over each group's rows, both quantised along them, in
     dw_dtype."""
     kept, offsets, T, N, K, E = saved
+    if dY.is_cuda and ws is None:
+        r = _native().expert_backward(dY, kept, offsets, T, N, K, E, dw_dtype, RG_FLAG_SYNC if sync else 0)
+        if r is not None:
+            return r
     where = "expert_linear_f8_backward"
     t, tw = _TYPES.get(dY.dtype), _TYPES.get(dw_dtype)
     if t is None or tw is None or dY.shape != (T, N):
