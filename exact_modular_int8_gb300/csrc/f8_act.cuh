@@ -6,9 +6,15 @@
 //   gelu_tanh(x) = x (1 + tanh u) / 2          s + 2 u' x s (1 - s)
 //                = x s, s = 1 / (1 + exp(-2 u)), u = sqrt(2 / pi) (x + 0.044715 x^3)
 //
-// tanh enters as the logistic function, which loses nothing where 1 + tanh u is
-// small.  1 + erf loses there: gelu is off by up to |x| 2^-23 in absolute terms.
-// NaN stays NaN; an infinity gives what the formula gives.
+// A few operations each, since a tile's epilogue and the quantisation of a gradient
+// are bound by their instructions and the code of an activation stands 128 times in
+// the pair kernel.  tanh enters as the logistic function, which loses nothing where 1
+// + tanh u is small.  Exponentials and reciprocals are the hardware's approximations
+// (2^-22 and 2^-23 of themselves; an exponential another |argument| 2^-24 for the
+// rounding of its argument, where it hardly counts).  erf is Abramowitz and
+// Stegun's 7.1.26, off by 1.5 10^-7, with its exp(-x^2 / 2) shared by the slope; gelu
+// is so off by up to |x| 2^-22 in absolute terms.  NaN stays NaN; an infinity gives
+// what the formula gives.
 #pragma once
 #include <cstdint>
 
@@ -20,18 +26,44 @@
 namespace rg {
 namespace {
 
-// The quotient to 2 ulp; 0 for a denominator above 2^126, where these quotients are below 2^-100 |x|.
-__device__ __forceinline__ float logistic_times(float x, float e) { return __fdividef(x, 1.0f + e); }
-
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kSqrt2OverPi = 0.7978845608028654f;
+
+// 1 / (1 + 2^a)
+__device__ __forceinline__ float logistic2(float a) { return rcp_fast(1.0f + exp2_fast(a)); }
+// gelu_tanh's 1 / (1 + exp(-2 u)), and u' over sqrt(2 / pi)
+__device__ __forceinline__ float tanh_logistic(float x, float x2) {
+  return logistic2(x * fmaf(x2, -2.0f * kLog2E * kSqrt2OverPi * 0.044715f, -2.0f * kLog2E * kSqrt2OverPi));
+}
+
+// (1 + erf(x / sqrt 2)) / 2, given e = exp(-x^2 / 2).
+__device__ __forceinline__ float normal_cdf(float x, float e) {
+  const float t = rcp_fast(fmaf(fabsf(x), 0.3275911f * 0.7071067811865476f, 1.0f));
+  float q = fmaf(t, 0.5f * 1.061405429f, -0.5f * 1.453152027f);
+  q = fmaf(q, t, 0.5f * 1.421413741f);
+  q = fmaf(q, t, -0.5f * 0.284496736f);
+  q = fmaf(q, t, 0.5f * 0.254829592f);
+  // (a choice of the sign by comparison spilled registers in the pair kernel's epilogue)
+  return 0.5f + copysignf(fmaf(-q * t, e, 0.5f), x);
+}
+__device__ __forceinline__ float exp_half_square(float x) { return exp2_fast(x * (-0.5f * kLog2E * x)); }
 
 template <int ACT>
 __device__ __forceinline__ float activate(float x) {
   if constexpr (ACT == RG_ACT_RELU) return x <= 0.0f ? 0.0f : x;
-  if constexpr (ACT == RG_ACT_SILU) return logistic_times(x, expf(-x));
-  if constexpr (ACT == RG_ACT_GELU) return 0.5f * x * (1.0f + erff(x * 0.7071067811865476f));
-  if constexpr (ACT == RG_ACT_GELU_TANH)
-    return logistic_times(x, expf(-2.0f * kSqrt2OverPi * fmaf(0.044715f * x * x, x, x)));
+  if constexpr (ACT == RG_ACT_SILU) return x * logistic2(-kLog2E * x);
+  if constexpr (ACT == RG_ACT_GELU) return x * normal_cdf(x, exp_half_square(x));
+  if constexpr (ACT == RG_ACT_GELU_TANH) return x * tanh_logistic(x, x * x);
   return x;
 }
 __device__ __forceinline__ float activate(float x, int act) {
@@ -44,23 +76,24 @@ __device__ __forceinline__ float activate(float x, int act) {
   }
 }
 
-__device__ __forceinline__ float slope(float x, int act) {
-  switch (act) {
-    case RG_ACT_RELU: return x <= 0.0f ? 0.0f : x > 0.0f ? 1.0f : x;
-    case RG_ACT_SILU: {
-      const float s = logistic_times(1.0f, expf(-x));
-      return s * fmaf(x, 1.0f - s, 1.0f);
-    }
-    case RG_ACT_GELU:
-      return fmaf(x * 0.3989422804014327f, expf(-0.5f * x * x), 0.5f + 0.5f * erff(x * 0.7071067811865476f));
-    case RG_ACT_GELU_TANH: {
-      // beyond 30 s is 0 or 1 and the second term 0, which x^2 overflowing would hide
-      const float v = x > 30.0f ? 30.0f : x < -30.0f ? -30.0f : x, q = 0.044715f * v * v;
-      const float s = logistic_times(1.0f, expf(-2.0f * kSqrt2OverPi * fmaf(q, v, v)));
-      return fmaf(2.0f * kSqrt2OverPi * fmaf(3.0f, q, 1.0f) * v, s * (1.0f - s), s);
-    }
-    default: return 1.0f;
+template <int ACT>
+__device__ __forceinline__ float slope(float x) {
+  if constexpr (ACT == RG_ACT_RELU) return x <= 0.0f ? 0.0f : x > 0.0f ? 1.0f : x;
+  if constexpr (ACT == RG_ACT_SILU) {
+    const float s = logistic2(-kLog2E * x);
+    return s * fmaf(x, 1.0f - s, 1.0f);
   }
+  if constexpr (ACT == RG_ACT_GELU) {
+    const float e = exp_half_square(x);
+    return fmaf(x * 0.3989422804014327f, e, normal_cdf(x, e));
+  }
+  if constexpr (ACT == RG_ACT_GELU_TANH) {
+    // beyond 30 s is 0 or 1 and the second term 0, which x^2 overflowing would hide
+    const float v = x > 30.0f ? 30.0f : x < -30.0f ? -30.0f : x, v2 = v * v;
+    const float s = tanh_logistic(v, v2);
+    return fmaf(v * fmaf(v2, 6.0f * kSqrt2OverPi * 0.044715f, 2.0f * kSqrt2OverPi), s * (1.0f - s), s);
+  }
+  return 1.0f;
 }
 
 __device__ __forceinline__ float load_real(const void* p, int type, long long at) {

@@ -65,33 +65,81 @@ __device__ __forceinline__ void store4(const Params& gp, void* C, long long out,
   }
 }
 
-// Four entries of row m from column n on (c of the tile) through the epilogue to C.
-__device__ __forceinline__ void finish4(const Params& gp, int m, int n, int c, int cols, float4 v) {
-  const long long out = (long long)m * gp.ldc + n;
-  const int left = cols - c;
-  float e[4] = {v.x, v.y, v.z, v.w};
-  if (gp.ep.bias) {
+// What the epilogue needs of the parameters, by value.
+struct Finish {
+  void *C, *P;
+  int out_type, act, vec;
+  float4 bias;
+};
+__device__ __forceinline__ float entry(const uint4& w, int type, int q) {  // of four, as loaded
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  if (type == RG_TYPE_F32) return __uint_as_float(v[q]);
+  const uint32_t h = v[q >> 1] >> (16 * (q & 1));
+  return type == RG_TYPE_F16 ? __half2float(__ushort_as_half((unsigned short)h)) : __uint_as_float(h << 16);
+}
+__device__ __forceinline__ void put4(void* p, long long at, int type, int vec, int left, const float (&e)[4]) {
+  if (vec && left >= 4) {
+    if (type == RG_TYPE_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(e[0], e[1], e[2], e[3]);
+    } else {
+      uint2 w;
+      if (type == RG_TYPE_F16) {
+        const __half2 a = __floats2half2_rn(e[0], e[1]), b = __floats2half2_rn(e[2], e[3]);
+        w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(e[0], e[1]), b = __floats2bfloat162_rn(e[2], e[3]);
+        w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) = w;
+    }
+  } else {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (q < left) e[q] += load_real(gp.ep.bias, gp.ep.bias_type, n + q);
+      if (q < left) store_real(p, type, at + q, e[q]);
   }
-  if (gp.ep.P) store4(gp, gp.ep.P, out, c, cols, make_float4(e[0], e[1], e[2], e[3]));
+}
+// Four entries of a row, `left` of them in the matrix, through the epilogue; res: the
+// residual's.  Not inlined: a warp's rows share its code, whose fetching is what a
+// small product would wait for (512 x 1024 x 1024 with a bias: INLINED us, 5.9
+// without an epilogue).
+__device__ __noinline__ void finish4(Finish f, long long out, int left, float4 v, uint4 res) {
+  float e[4] = {v.x + f.bias.x, v.y + f.bias.y, v.z + f.bias.z, v.w + f.bias.w};
+  if (f.P) put4(f.P, out, f.out_type, f.vec, left, e);
+  switch (f.act) {
+    case RG_ACT_RELU:
+      for (float& x : e) x = activate<RG_ACT_RELU>(x);
+      break;
+    case RG_ACT_SILU:
+      for (float& x : e) x = activate<RG_ACT_SILU>(x);
+      break;
+    case RG_ACT_GELU:
+      for (float& x : e) x = activate<RG_ACT_GELU>(x);
+      break;
+    case RG_ACT_GELU_TANH:
+      for (float& x : e) x = activate<RG_ACT_GELU_TANH>(x);
+      break;
+  }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) e[q] = activate(e[q], gp.ep.act);
-  if (gp.ep.R) {
-    const long long in = (long long)m * gp.ep.ldr + n;
-    if (gp.vec_r && left >= 4 && gp.out_type != RG_TYPE_F32) {
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(gp.ep.R) + in);
-      const uint16_t h[4] = {(uint16_t)w.x, (uint16_t)(w.x >> 16), (uint16_t)w.y, (uint16_t)(w.y >> 16)};
+  for (int q = 0; q < 4; ++q) e[q] += entry(res, f.out_type, q);
+  put4(f.C, out, f.out_type, f.vec, left, e);
+}
+// The residual's four entries from `at` on, as entry() takes them; zeros without one.
+__device__ __forceinline__ uint4 load_residual4(const Params& gp, long long at, int left) {
+  uint4 w = make_uint4(0, 0, 0, 0);
+  if (!gp.ep.R) return w;
+  if (gp.vec_r && left >= 4) {
+    if (gp.out_type == RG_TYPE_F32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(gp.ep.R) + at);
+    const uint2 h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(gp.ep.R) + at);
+    return make_uint4(h.x, h.y, 0, 0);
+  }
+  uint32_t v[4] = {};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) e[q] += load_real(h, gp.out_type, q);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < left) e[q] += load_real(gp.ep.R, gp.out_type, in + q);
+  for (int q = 0; q < 4; ++q)
+    if (q < left) {
+      if (gp.out_type == RG_TYPE_F32) v[q] = static_cast<const uint32_t*>(gp.ep.R)[at + q];
+      else v[q >> 1] |= (uint32_t)static_cast<const uint16_t*>(gp.ep.R)[at + q] << (16 * (q & 1));
     }
-  }
-  store4(gp, gp.C, out, c, cols, make_float4(e[0], e[1], e[2], e[3]));
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
 // Rows rank, rank + S, ... of the tile: the slices' sums in rank order.  A warp
@@ -105,9 +153,29 @@ __device__ __forceinline__ void join_slices(const Params& gp, uint32_t part, int
   constexpr int WARPS = NUM_THREADS / 32, ROWS = (128 / S + WARPS - 1) / WARPS, R = S == 1 ? (ROWS + 1) / 2 : ROWS;
   const int rows = min(128, gp.M - tm * 128), cols = min(BN1, gp.N - tn * BN1);
   const int c = 4 * lane;  // this lane's columns
+  Finish f = {};
+  if constexpr (EPI) {
+    f = Finish{gp.C, gp.ep.P, gp.out_type, gp.ep.act, gp.vec_c, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+    if (gp.ep.bias) {
+      float* b = &f.bias.x;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c + q < cols) b[q] = load_real(gp.ep.bias, gp.ep.bias_type, tn * BN1 + c + q);
+    }
+  }
 #pragma unroll
   for (int i0 = 0; i0 < ROWS; i0 += R) {
     float4 v[S][R];
+    uint4 res[EPI ? R : 1];
+    if constexpr (EPI) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int r = rank + S * (warp + WARPS * (i0 + i));
+        res[i] = make_uint4(0, 0, 0, 0);
+        if (live && r < rows && c < cols)
+          res[i] = load_residual4(gp, (long long)(tm * 128 + r) * gp.ep.ldr + tn * BN1 + c, cols - c);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < S; ++k)
 #pragma unroll
@@ -134,8 +202,9 @@ __device__ __forceinline__ void join_slices(const Params& gp, uint32_t part, int
     for (int i = 0; i < R; ++i) {
       const int r = rank + S * (warp + WARPS * (i0 + i));
       if (live && r < rows && c < cols) {
-        if constexpr (EPI) finish4(gp, tm * 128 + r, tn * BN1 + c, c, cols, v[0][i]);
-        else store4(gp, gp.C, (long long)(tm * 128 + r) * gp.ldc + (long long)tn * BN1 + c, c, cols, v[0][i]);
+        const long long out = (long long)(tm * 128 + r) * gp.ldc + (long long)tn * BN1 + c;
+        if constexpr (EPI) finish4(f, out, cols - c, v[0][i], res[i]);
+        else store4(gp, gp.C, out, c, cols, v[0][i]);
       }
     }
   }
@@ -281,6 +350,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ------------------------------------------------------------ epilogue
+    if constexpr (EPI) {  // the tile's residual to L2
+      const int row = tm * 128 + (threadIdx.x >> 1) - 64, n0 = tn * BN1, es = gp.out_type == RG_TYPE_F32 ? 4 : 2;
+      const int bytes = min(BN1, gp.N - n0) * es;
+      if (gp.ep.R && row < gp.M)
+        for (int i = 128 * (threadIdx.x & 1); i < bytes; i += 256)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(gp.ep.R) +
+                                                         ((long long)row * gp.ep.ldr + n0) * es + i));
+    }
     const int q4 = warp & 3;  // tensor-memory lane quarter this warp may access
     constexpr int WC = BN1 * 4 / EPI_WARPS;  // columns per warp
     const int col0 = ((warp - 4) >> 2) * WC;

@@ -36,7 +36,7 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int BN2 = 256;
 constexpr int STAGES2 = 5;
-constexpr int STAGES2_RES = 4;  // with a residual, whose rings take a stage's place
+constexpr int STAGES2_RING = 4;  // where a ring of two more buffers to a warp takes a stage's place
 constexpr int STAGE2_BYTES = 2 * SLAB;
 constexpr int HALF_SLAB = SLAB / 2;  // a CTA's 64 columns of one half
 constexpr int PAIR_COLS = BN2 * 4 / EPI_WARPS;  // columns per epilogue warp
@@ -44,7 +44,10 @@ constexpr int OUT_BUF = 32 * 64;  // 64 bytes of each of a warp's rows
 constexpr int OUT_WARP = 2 * OUT_BUF;
 constexpr int SCALE2_BYTES = SCALE_BUFS * (int)sizeof(ScaleChunk<BN2>);
 constexpr int SMEM2_BASE = 1024 + STAGES2 * STAGE2_BYTES + EPI_WARPS * OUT_WARP + SCALE2_BYTES + 256;
-constexpr int BIAS_BYTES = EPI_WARPS * PAIR_COLS * 4;
+// Biases of three tiles: the scales' warp, which fetches them, may be two tiles
+// ahead of the warps that still store one.
+constexpr int BIAS_BUFS = 3;
+constexpr int BIAS_BYTES = BIAS_BUFS * BN2 * 4;
 constexpr int RES_BYTES = EPI_WARPS * OUT_WARP;  // two buffers like a warp's for its results
 static_assert(RES_BYTES <= STAGE2_BYTES, "in the place of a stage");
 
@@ -154,10 +157,11 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* tm, bool tma, voi
   }
   __syncwarp();
 }
-// The staging buffer that the last store but one used has been read.
+// Of BUFS staging buffers the one whose turn it is has been read by its last store.
+template <int BUFS = 2>
 __device__ __forceinline__ void buffer_free(bool tma, int lane) {
   if (tma) {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(BUFS - 1) : "memory");
     __syncwarp();
   }
 }
@@ -194,12 +198,14 @@ __device__ __forceinline__ void stage_row(uint8_t* buf, const uint64_t* acc, int
 }
 
 // This warp's 32 rows x 128 columns of sums to C through two alternating staging
-// buffers.  c_row0: row0 in C, whose matrices may lie one behind the other.
+// buffers, or four where little is summed for much that is stored (sums over
+// groups: 32 of 2048 x 2048 over 16384 rows BUFS4 us, with two buffers 211).  c_row0:
+// row0 in C, whose matrices may lie one behind the other.
 template <int ES, bool TILE_B, int WALK>
 __device__ __forceinline__ void store_rows(const Params& gp, const CUtensorMap* tmC,
-                                           const Sums<PAIR_COLS, TILE_B>& sums, uint8_t* stage, int c_row0, int rows,
-                                           int col0, int lane) {
-  constexpr int COLS = 64 / ES;
+                                           const Sums<PAIR_COLS, TILE_B>& sums, uint8_t* stage, uint8_t* ring,
+                                           int c_row0, int rows, int col0, int lane) {
+  constexpr int COLS = 64 / ES, BUFS = WALK == WALK_BLOCKS ? 4 : 2;
   // a whole matrix's last rows are cut by the TMA store too
   const bool tma = gp.vec_c && (WALK == WALK_WHOLE || rows == 32);
   if (WALK != WALK_WHOLE && gp.vec_c && !tma) {  // the last tile's stores have read both buffers
@@ -208,8 +214,8 @@ __device__ __forceinline__ void store_rows(const Params& gp, const CUtensorMap* 
   }
 #pragma unroll
   for (int c = 0; c < PAIR_COLS / COLS; ++c) {
-    uint8_t* buf = stage + (c & 1) * OUT_BUF;
-    buffer_free(tma, lane);
+    uint8_t* buf = (c & (BUFS - 2) ? ring : stage) + (c & 1) * OUT_BUF;
+    buffer_free<BUFS>(tma, lane);
     if constexpr (TILE_B) {
       stage_row<ES>(buf, sums.acc[0] + c * (COLS / 2), gp.out_type, lane);
     } else {
@@ -293,10 +299,9 @@ __device__ __forceinline__ void store_rows_act(const Params& gp, const CUtensorM
     const int cc = col0 + c * COLS;
 #pragma unroll
     for (int j = 0; j < COLS / 2; j += 2) {
-      const float4 b = *reinterpret_cast<const float4*>(bias + c * COLS + 2 * j);
-      const float2 f = unpack2(acc[j]), h = unpack2(acc[j + 1]);
-      acc[j] = pack2(f.x + b.x, f.y + b.y);
-      acc[j + 1] = pack2(h.x + b.z, h.y + b.w);
+      const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(bias + c * COLS + 2 * j);
+      acc[j] = add2(acc[j], b.x);
+      acc[j + 1] = add2(acc[j + 1], b.y);
     }
     if (gp.ep.P) {
       buffer_free(gp.vec_c, lane);
@@ -312,18 +317,17 @@ __device__ __forceinline__ void store_rows_act(const Params& gp, const CUtensorM
       if constexpr (RES) res = *reinterpret_cast<const uint4*>(in + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
-        float2 f = unpack2(acc[i * PER + j]);
+        uint64_t& a = acc[i * PER + j];
+        const float2 f = unpack2(a);
         if constexpr (ACT == SIMPLE_ACT) {
-          if (relu) f = make_float2(activate<RG_ACT_RELU>(f.x), activate<RG_ACT_RELU>(f.y));
+          if (relu) a = pack2(activate<RG_ACT_RELU>(f.x), activate<RG_ACT_RELU>(f.y));
         } else {
-          f = make_float2(activate<ACT>(f.x), activate<ACT>(f.y));
+          a = pack2(activate<ACT>(f.x), activate<ACT>(f.y));
         }
         if constexpr (RES) {
           const float2 r = residual_pair<ES>(res, j, gp.out_type);
-          f.x += r.x;
-          f.y += r.y;
+          a = add2(a, pack2(r.x, r.y));
         }
-        acc[i * PER + j] = pack2(f.x, f.y);
       }
     }
     if constexpr (RES) {
@@ -344,14 +348,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmP,
                         const __grid_constant__ Params gp, DevPlan* plan) {
   static_assert(ACT == PLAIN ? !RES : TILE_B && WALK == WALK_WHOLE, "an epilogue has a row to a lane");
-  constexpr int STAGES = RES ? STAGES2_RES : STAGES2;
+  constexpr int STAGES = RES || WALK == WALK_BLOCKS ? STAGES2_RING : STAGES2;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t rank = cluster_rank();
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stage_base = smem;
   uint8_t* out_base = smem + STAGES2 * STAGE2_BYTES;
-  uint8_t* ring_base = smem + STAGES2_RES * STAGE2_BYTES;  // RES
+  uint8_t* ring_base = smem + STAGES2_RING * STAGE2_BYTES;  // RES, WALK_BLOCKS
   ScaleChunk<BN2>* scales = reinterpret_cast<ScaleChunk<BN2>*>(out_base + EPI_WARPS * OUT_WARP);
   uint64_t* bars = reinterpret_cast<uint64_t*>(out_base + EPI_WARPS * OUT_WARP + SCALE2_BYTES);
   uint8_t* more = reinterpret_cast<uint8_t*>(bars) + 256;
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int b = 0; b < 4; ++b) mbar_init(smem_u32(&tempty[b]), EPI_WARPS);  // the half's warps of both CTAs
     for (int b = 0; b < SCALE_BUFS; ++b) {
-      mbar_init(smem_u32(&sfull[b]), 32);
+      mbar_init(smem_u32(&sfull[b]), ACT == PLAIN ? 32 : 33);  // 33: the bias
       mbar_init(smem_u32(&sempty[b]), EPI_WARPS);
     }
     for (int h = 0; h < 2; ++h) mbar_init(smem_u32(&drain[h]), 1);
@@ -493,6 +497,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int c = 0;
       bool ok = true;
       Walk<WALK> walk{gp, tab};
+      int slot = 0;  // of the biases
       for (int t = cid; t < total && ok; t += ncl) {
         const TileAt at = walk.at(t);
         const float* SB = WALK == WALK_ROWS ? gp.SB + at.g * gp.sb_e : gp.SB;
@@ -501,6 +506,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = wait_bounded(smem_u32(&sempty[b]), ((c >> 1) & 1u) ^ 1u, ctl, 35);
           if (!ok) break;
           load_scales<BN2, TILE_B, 32>(gp, SB, scales[b], at.m0 + (int)rank * 128, at.n0, kb, at.kb1, lane);
+          if constexpr (ACT != PLAIN) {
+            if (kb == at.kb0) {
+              float* bias = bias_base + slot * BN2;
+              for (int j = lane; j < BN2; j += 32)
+                bias[j] = gp.ep.bias && at.n0 + j < gp.N ? load_real(gp.ep.bias, gp.ep.bias_type, at.n0 + j) : 0.0f;
+              slot = slot + 1 == BIAS_BUFS ? 0 : slot + 1;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sfull[b]));
+          }
           cp_async_arrive(smem_u32(&sfull[b]));
         }
       }
@@ -520,27 +535,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int chunk = 0, st = 0;  // pipeline stage
     bool ok = true;
     Walk<WALK> walk{gp, tab};
+    int slot = 0;  // of the biases
     for (int t = cid; t < total && ok; t += ncl) {
       const TileAt at = walk.at(t);
       const int row0 = at.m0 + (int)rank * 128 + q4 * 32, col0 = at.n0 + col;
       // a group's last tile: warps without a row of it leave the sums alone
       const bool mine = WALK != WALK_ROWS || row0 < at.m_end;
-      float* bias = bias_base + ew * PAIR_COLS;
       uint8_t* ring = ring_base + ew * OUT_WARP;
-      if constexpr (ACT != PLAIN) {
-#pragma unroll
-        for (int j = 0; j < PAIR_COLS; j += 32) {
-          const int n = col0 + j + lane;
-          bias[j + lane] = gp.ep.bias && n < gp.N ? load_real(gp.ep.bias, gp.ep.bias_type, n) : 0.0f;
+      if constexpr (RES) {
+        const int rows = min(32, at.m_end - row0), es = gp.out_type == RG_TYPE_F32 ? 4 : 2;
+        for (int c = 0; c < 2; ++c) {
+          uint8_t* buf = ring + c * OUT_BUF;
+          if (es == 4) start_residual<4>(gp, buf, row0, rows, col0 + c * 16, lane);
+          else start_residual<2>(gp, buf, row0, rows, col0 + c * 32, lane);
         }
-        __syncwarp();
-        if constexpr (RES) {
-          const int rows = min(32, at.m_end - row0), es = gp.out_type == RG_TYPE_F32 ? 4 : 2;
-          for (int c = 0; c < 2; ++c) {
-            uint8_t* buf = ring + c * OUT_BUF;
-            if (es == 4) start_residual<4>(gp, buf, row0, rows, col0 + c * 16, lane);
-            else start_residual<2>(gp, buf, row0, rows, col0 + c * 32, lane);
-          }
+        // the rest of the warp's rows, as far as L2
+        if (lane < rows && col0 < gp.N) {
+          const uint8_t* p = static_cast<const uint8_t*>(gp.ep.R) + ((long long)(row0 + lane) * gp.ep.ldr + col0) * es;
+          const int bytes = min(PAIR_COLS, gp.N - col0) * es;
+          for (int i = 128; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
         }
       }
       using Acc = Sums<PAIR_COLS, TILE_B>;
@@ -579,22 +592,36 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ++chunk;
         }
       }
-      if (ok && row0 < at.m_end && col0 < gp.N) {
+      if constexpr (WALK == WALK_BLOCKS) {
+        // found again: kept over the blocks' loop, where no register is free, they spilled
+        int u = t;
+        asm volatile("" : "+r"(u));
+        const TileAt at2 = walk.at(u);
+        const int row = at2.m0 + (int)rank * 128 + q4 * 32, n0 = at2.n0 + col;
+        if (ok && row < gp.M && n0 < gp.N) {
+          const int rows = min(32, gp.M - row), c_row = row + at2.g * gp.M;
+          if (gp.out_type == RG_TYPE_F32) store_rows<4, TILE_B, WALK>(gp, &tmC, sums, stage, ring, c_row, rows, n0, lane);
+          else store_rows<2, TILE_B, WALK>(gp, &tmC, sums, stage, ring, c_row, rows, n0, lane);
+        }
+      } else if (ok && row0 < at.m_end && col0 < gp.N) {
         const int rows = min(32, at.m_end - row0);
         if constexpr (ACT != PLAIN) {
-          // nothing that is computed from these before the blocks' loop, where no register is free
+          // nothing that is computed from these before the blocks' loop
           int r0 = row0, c0 = col0, l = lane;
           asm volatile("" : "+r"(r0), "+r"(c0), "+r"(l));
+          const float* bias = bias_base + slot * BN2 + (ew >> 2) * PAIR_COLS;
           if (gp.out_type == RG_TYPE_F32)
             store_rows_act<4, ACT, RES>(gp, &tmC, &tmP, sums, bias, stage, ring, r0, rows, c0, l);
           else
             store_rows_act<2, ACT, RES>(gp, &tmC, &tmP, sums, bias, stage, ring, r0, rows, c0, l);
         } else {
-          const int c_row0 = row0 + (WALK == WALK_BLOCKS ? at.g * gp.M : 0);
-          if (gp.out_type == RG_TYPE_F32) store_rows<4, TILE_B, WALK>(gp, &tmC, sums, stage, c_row0, rows, col0, lane);
-          else store_rows<2, TILE_B, WALK>(gp, &tmC, sums, stage, c_row0, rows, col0, lane);
+          if (gp.out_type == RG_TYPE_F32)
+            store_rows<4, TILE_B, WALK>(gp, &tmC, sums, stage, ring, row0, rows, col0, lane);
+          else
+            store_rows<2, TILE_B, WALK>(gp, &tmC, sums, stage, ring, row0, rows, col0, lane);
         }
       }
+      if constexpr (ACT != PLAIN) slot = slot + 1 == BIAS_BUFS ? 0 : slot + 1;
     }
     if constexpr (RES) asm volatile("cp.async.wait_all;" ::: "memory");
     bulk_wait0();

@@ -129,23 +129,28 @@ template <typename T>
 struct FromX {
   using E = Entries<T>;
   using Type = T;
+  static constexpr int kRows = 8;  // rows of a tile to a thread
   // eight entries of a row from column c on, of which `left` exist
   static __device__ __forceinline__ void load(E& e, const QuantArgs& a, const T* X, long long row, long long c,
                                               long long left) {
     load8(e, X + row * a.ldx + c, left, a.vec_x);
   }
 };
+// Half the rows to a thread: the products are fp32 and the slopes take their time, so
+// that twice the warps are worth more (8192 x 4096 bf16 with gelu: SLOPE4 us, SLOPE8 with
+// eight rows; the bytes at the copy rate: 30).
 template <typename T, int ACT>
 struct TimesSlope {
   using E = Entries<float>;
   using Type = T;
+  static constexpr int kRows = 4;
   static __device__ __forceinline__ void load(E& e, const QuantArgs& a, const T* X, long long row, long long c,
                                               long long left) {
     Entries<T> x, p;
     load8(x, X + row * a.ldx + c, left, a.vec_x);
     load8(p, static_cast<const T*>(a.P) + row * a.K + c, left, a.vec_p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e.set(i, x.at(i) * slope(p.at(i), ACT));  // a missing entry: 0
+    for (int i = 0; i < 8; ++i) e.set(i, x.at(i) * slope<ACT>(p.at(i)));  // a missing entry: 0
   }
 };
 
@@ -251,20 +256,21 @@ __device__ __forceinline__ RowBlock find_block(const QuantArgs& a, long long i) 
 }
 
 // One 128 x 128 tile per block of 256 threads; a thread holds eight rows of
-// eight columns.  ROWS / COLS: scales along rows and along columns (with both,
+// eight columns (or 512 threads and four rows).  ROWS / COLS: scales along rows and along columns (with both,
 // one read of X gives both results); neither: one scale for the tile.  GROUPED:
 // the blocks along the columns lie in one group of rows each.  SUM: sums over the
 // tile's rows.
 template <typename Src, bool ROWS, bool COLS, bool GROUPED, bool SUM>
-__global__ void __launch_bounds__(256, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 : 4) : 2)
+__global__ void __launch_bounds__(16 * kTile / Src::kRows, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 : 4) : 2)
     quantise_tile_kernel(QuantArgs a) {
+  constexpr int R = Src::kRows, GRPS = kTile / R;  // rows of a thread, groups of them
   using E = typename Src::E;
   using T = typename Src::Type;
   constexpr int kWordsPerRow = kTile / E::kPer;
-  __shared__ uint32_t col_mag[COLS ? 16 : 1][kWordsPerRow];  // per 8-row group
+  __shared__ uint32_t col_mag[COLS ? GRPS : 1][kWordsPerRow];  // per group of rows
   __shared__ __align__(16) float2 col_scale[COLS ? kTile : 1];
   __shared__ __align__(16) uint8_t t_tile[COLS ? kTile * kTile : 16];  // transposed bytes, 16-byte chunks swizzled
-  __shared__ uint32_t warp_mag[8];
+  __shared__ uint32_t warp_mag[GRPS / 2];
   wait_for_predecessor();
   allow_dependents();
   const long long kb = (a.K + kTile - 1) / kTile, mb = GROUPED ? a.blocks : (a.M + kTile - 1) / kTile;
@@ -275,28 +281,28 @@ __global__ void __launch_bounds__(256, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 
     a.Q += blockIdx.y * a.M * a.ldq;
     a.S += blockIdx.y * mb * kb;
   }
-  const int grp = threadIdx.x >> 4;  // rows 8 grp .. 8 grp + 7 of the tile
+  const int grp = threadIdx.x >> 4;  // rows R grp .. R grp + R - 1 of the tile
   const int l16 = threadIdx.x & 15;  // columns 8 l16 ..
   RowBlock at{ti * kTile, a.M, false};
   if constexpr (GROUPED) at = find_block(a, ti);
-  const long long r0 = at.r0 + grp * 8, c0 = tj * kTile + l16 * 8, left = a.K - c0;
-  E e[8];
+  const long long r0 = at.r0 + grp * R, c0 = tj * kTile + l16 * 8, left = a.K - c0;
+  E e[R];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) Src::load(e[r], a, X, r0 + r, c0, r0 + r < at.end ? left : 0);
+  for (int r = 0; r < R; ++r) Src::load(e[r], a, X, r0 + r, c0, r0 + r < at.end ? left : 0);
 
   if constexpr (!ROWS && !COLS) {
     uint32_t m = mag8(e[0]);
 #pragma unroll
-    for (int r = 1; r < 8; ++r) m = E::larger(m, mag8(e[r]));
+    for (int r = 1; r < R; ++r) m = E::larger(m, mag8(e[r]));
     m = __reduce_max_sync(0xFFFFFFFFu, E::top(m));
     if ((threadIdx.x & 31) == 0) warp_mag[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = max(m, warp_mag[w]);
+    for (int w = 0; w < GRPS / 2; ++w) m = max(m, warp_mag[w]);
     const float top = amax_of(m);
     const BlockScale bs = block_scale(top);
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
+    for (int r = 0; r < R; ++r)
       if (r0 + r < a.M)
         store8(a.Q + (r0 + r) * a.ldq + c0, left, a.vec_q, quantise8([&](int i) { return e[r].at(i); }, bs));
     if (threadIdx.x == 0) a.S[ti * kb + tj] = scale_of(top);
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(256, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 
     for (int i = 0; i < 8; ++i) {
       float v = e[0].at(i);
 #pragma unroll
-      for (int r = 1; r < 8; ++r) v += e[r].at(i);
+      for (int r = 1; r < R; ++r) v += e[r].at(i);
       part[i] = v;
     }
   }
@@ -317,18 +323,19 @@ __global__ void __launch_bounds__(256, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 
     for (int w = 0; w < E::kWords; ++w) {
       uint32_t m = E::mag(e[0].w[w]);
 #pragma unroll
-      for (int r = 1; r < 8; ++r) m = E::larger(m, E::mag(e[r].w[w]));
+      for (int r = 1; r < R; ++r) m = E::larger(m, E::mag(e[r].w[w]));
       col_mag[grp][l16 * E::kWords + w] = GROUPED && at.rest ? 0 : m;
     }
   }
   if constexpr (ROWS) {
-    // The eight rows' maxima over 16 lanes: each step halves the rows a lane
-    // holds, so that lane l ends up with row l / 2's, and makes its scale.
-    uint32_t m[8];
+    // The rows' maxima over 16 lanes: each step halves the rows a lane holds, so
+    // that lane l ends up with row l R / 16's, and makes its scale.
+    constexpr int SPAN = 16 / R;
+    uint32_t m[R];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) m[r] = mag8(e[r]);
+    for (int r = 0; r < R; ++r) m[r] = mag8(e[r]);
 #pragma unroll
-    for (int n = 4, bit = 8; n; n >>= 1, bit >>= 1) {
+    for (int n = R / 2, bit = 8; n; n >>= 1, bit >>= 1) {
       const bool up = l16 & bit;
 #pragma unroll
       for (int r = 0; r < n; ++r) {
@@ -336,14 +343,16 @@ __global__ void __launch_bounds__(256, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 
         m[r] = E::larger(up ? m[r + n] : m[r], other);
       }
     }
-    const uint32_t mine = E::larger(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], 1));
+    uint32_t mine = m[0];
+#pragma unroll
+    for (int bit = SPAN / 2; bit; bit >>= 1) mine = E::larger(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, bit));
     const float top = amax_of(E::top(mine));
     const BlockScale bs = block_scale(top);
-    const long long my_row = r0 + (l16 >> 1);
-    if (!(l16 & 1) && my_row < at.end) a.S[my_row * kb + tj] = scale_of(top);
+    const long long my_row = r0 + l16 / SPAN;
+    if (l16 % SPAN == 0 && my_row < at.end) a.S[my_row * kb + tj] = scale_of(top);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int src = (threadIdx.x & 16) + 2 * r;
+    for (int r = 0; r < R; ++r) {
+      const int src = (threadIdx.x & 16) + SPAN * r;
       const BlockScale rs{__shfl_sync(0xFFFFFFFFu, bs.nd, src), __shfl_sync(0xFFFFFFFFu, bs.r, src)};
       if (r0 + r < at.end)
         store8(a.Q + (r0 + r) * a.ldq + c0, left, a.vec_q, quantise8([&](int i) { return e[r].at(i); }, rs));
@@ -354,7 +363,7 @@ __global__ void __launch_bounds__(256, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 
       if (ti >= mb) return;  // a slot more for the rest's rows, which are in no column block
       if (at.rest) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int w = 0; w < E::kWords; ++w) e[r].w[w] = 0;
       }
@@ -365,7 +374,7 @@ __global__ void __launch_bounds__(256, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 
       const int w = threadIdx.x / kPer;
       uint32_t m = col_mag[0][w];
 #pragma unroll
-      for (int g = 1; g < 16; ++g) m = E::larger(m, col_mag[g][w]);
+      for (int g = 1; g < GRPS; ++g) m = E::larger(m, col_mag[g][w]);
       // this column's of the word's entries
       if constexpr (kPer == 2) m = threadIdx.x & 1 ? m & 0xFFFF0000u : m << 16;
       const float top = amax_of(E::top(m));
@@ -377,7 +386,7 @@ __global__ void __launch_bounds__(256, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 
         const float* part = reinterpret_cast<const float*>(t_tile) + threadIdx.x;
         float v = part[0];
 #pragma unroll
-        for (int g = 1; g < 16; ++g) v += part[g * kTile];
+        for (int g = 1; g < GRPS; ++g) v += part[g * kTile];
         if (col < a.K) a.sums[ti * a.K + col] = v;
       }
     }
@@ -386,17 +395,24 @@ __global__ void __launch_bounds__(256, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 
     for (int i = 0; i < 8; ++i) {
       const int c = l16 * 8 + i;
       const float2 cs = col_scale[c];
-      // column c's 128 bytes are a row of t_tile; this thread's 8 bytes are half of its 16-byte chunk grp / 2
-      const int chunk = (grp >> 1) ^ (l16 & 7);
-      *reinterpret_cast<uint2*>(&t_tile[c * kTile + chunk * 16 + (grp & 1) * 8]) =
-          quantise8([&](int r) { return e[r].at(i); }, BlockScale{cs.x, cs.y});
+      // column c's 128 bytes are a row of t_tile; this thread's R bytes lie in its 16-byte chunk grp R / 16
+      const int chunk = (grp * R >> 4) ^ (l16 & 7);
+      uint8_t* dst = &t_tile[c * kTile + chunk * 16 + (grp * R & 15)];
+      const BlockScale bs{cs.x, cs.y};
+      if constexpr (R == 8) {
+        *reinterpret_cast<uint2*>(dst) = quantise8([&](int r) { return e[r].at(i); }, bs);
+      } else {
+        const uint64_t nd = pair(bs.nd, bs.nd), rr = pair(bs.r, bs.r);
+        *reinterpret_cast<uint32_t*>(dst) =
+            quantise2(e[0].at(i), e[1].at(i), nd, rr) | (quantise2(e[2].at(i), e[3].at(i), nd, rr) << 16);
+      }
     }
     __syncthreads();
     const int j = threadIdx.x & 7;  // 16-byte chunk: rows 16 j of the tile
     const long long limit = GROUPED ? a.blocks * kTile : a.M;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int c = p * 32 + (threadIdx.x >> 3);
+    for (int p = 0; p < R / 2; ++p) {
+      const int c = p * 2 * GRPS + (threadIdx.x >> 3);
       const long long col = tj * kTile + c, row = ti * kTile + 16 * j;
       if (col < a.K && row < limit) {
         const uint4 q = *reinterpret_cast<const uint4*>(&t_tile[c * kTile + ((j ^ ((c >> 3) & 7)) * 16)]);
@@ -455,8 +471,9 @@ cudaError_t launch_tiles(const QuantArgs& a, int form, dim3 g, cudaStream_t st) 
 template <typename T, int ACT>
 cudaError_t launch_slope(const QuantArgs& a, dim3 g, cudaStream_t st) {
   using Src = TimesSlope<T, ACT>;
-  return a.sums ? launch_dependent(quantise_tile_kernel<Src, true, true, false, true>, g, dim3(256), 0, st, a)
-                : launch_dependent(quantise_tile_kernel<Src, true, true, false, false>, g, dim3(256), 0, st, a);
+  const dim3 b(16 * kTile / Src::kRows);
+  return a.sums ? launch_dependent(quantise_tile_kernel<Src, true, true, false, true>, g, b, 0, st, a)
+                : launch_dependent(quantise_tile_kernel<Src, true, true, false, false>, g, b, 0, st, a);
 }
 
 template <typename T>
