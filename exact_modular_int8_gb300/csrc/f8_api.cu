@@ -330,7 +330,11 @@ int linear_act_f8(const void* X, int x_type, int64_t ldx, const void* W, int w_t
   Carver c{static_cast<uint8_t*>(ws) + kCallBlockBytes};
   const Quantised x = carve(c, M, K, M);
   int rc = quantise(quant_args(X, ldx, M, K, x, xt), x_type, RG_F8_BOTH, st);
-  if (!rc) rc = quantise(quant_args(W, ldw, N, K, w, Quantised{}), w_type, RG_F8_TILES, st);
+  if (!rc) {  // beside X's quantisation
+    QuantArgs q = quant_args(W, ldw, N, K, w, Quantised{});
+    q.late = M > 0;
+    rc = quantise(q, w_type, RG_F8_TILES, st);
+  }
   if (!rc) {
     const F8Epilogue ep{bias, bias_type, act, R, ldr, v.p};
     F8GemmArgs a = gemm_args(x.q, x.ld, x.s, w.q, w.ld, w.s, Y, x_type, N, M, N, K, true, true);
@@ -365,10 +369,17 @@ int linear_act_f8_backward(const void* dY, int x_type, int64_t lddy, const void*
   if (!rc && dbias && N &&
       launch_sum_rows(q.sums, M ? blocks128(M) : 0, N, dbias, bias_type, st) != cudaSuccess)
     rc = RG_ERR_CUDA;
-  if (!rc) rc = product(gemm_args(d.q, d.ld, d.s, w.q, w.ld, w.s, dX, x_type, K, M, K, N, false, true), plan, st);
+  // The sums of rows and the two products read what the quantisation wrote, and
+  // nothing of each other's.
+  if (!rc) {
+    F8GemmArgs a = gemm_args(d.q, d.ld, d.s, w.q, w.ld, w.s, dX, x_type, K, M, K, N, false, true);
+    a.late = M && N && dbias;
+    rc = product(a, plan, st);
+  }
   if (!rc) {
     F8GemmArgs a = gemm_args(dt.q, dt.ld, dt.s, xt.q, xt.ld, xt.s, dW, dw_type, K, N, K, M, true, false);
     a.keep_status = true;
+    a.late = M && N;
     rc = product(a, plan, st);
   }
   return rc ? rc : finish_call(ws, st, flags);
@@ -467,7 +478,11 @@ int expert_linear_f8(const void* X, int x_type, int64_t ldx, const void* W, int 
   Carver c{static_cast<uint8_t*>(ws) + kCallBlockBytes};
   const Quantised x = carve(c, T, K, T);
   int rc = quantise_groups(quant_args(X, ldx, T, K, x, v.xt), x_type, RG_F8_BOTH, offsets, E, flags, st);
-  if (!rc) rc = quantise_stack(quant_args(W, ldw, N, K, v.w, Quantised{}), w_type, E, st);
+  if (!rc) {  // beside X's quantisation
+    QuantArgs q = quant_args(W, ldw, N, K, v.w, Quantised{});
+    q.late = true;
+    rc = quantise_stack(q, w_type, E, st);
+  }
   if (!rc)
     rc = grouped(gemm_args(x.q, x.ld, x.s, v.w.q, v.w.ld, v.w.s, Y, x_type, N, T, N, K, true, true),
                  groups(offsets, E, flags & ~RG_FLAG_KEEP_REST, false), static_cast<DevPlan*>(ws), st);
@@ -503,6 +518,7 @@ int expert_linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const v
   if (!rc) {  // dW [E][N][K]: per group dY^T X
     F8GemmArgs a = blocks_args(dt, v.xt, dW, dw_type, N, K, group_blocks(T, E));
     a.keep_status = true;
+    a.late = T && N;  // beside dX, which it does not read
     rc = grouped(a, groups(offsets, E, flags, true), plan, st);
   }
   return rc ? rc : finish_call(ws, st, flags);

@@ -123,6 +123,16 @@ __device__ __noinline__ void finish4(Finish f, long long out, int left, float4 v
   for (int q = 0; q < 4; ++q) e[q] += entry(res, f.out_type, q);
   put4(f.C, out, f.out_type, f.vec, left, e);
 }
+__device__ __forceinline__ Finish make_finish(const Params& gp, int n, int left) {
+  Finish f = {gp.C, gp.ep.P, gp.out_type, gp.ep.act, gp.vec_c, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  if (gp.ep.bias) {
+    if (left > 0) f.bias.x = load_real(gp.ep.bias, gp.ep.bias_type, n);
+    if (left > 1) f.bias.y = load_real(gp.ep.bias, gp.ep.bias_type, n + 1);
+    if (left > 2) f.bias.z = load_real(gp.ep.bias, gp.ep.bias_type, n + 2);
+    if (left > 3) f.bias.w = load_real(gp.ep.bias, gp.ep.bias_type, n + 3);
+  }
+  return f;
+}
 // The residual's four entries from `at` on, as entry() takes them; zeros without one.
 __device__ __forceinline__ uint4 load_residual4(const Params& gp, long long at, int left) {
   uint4 w = make_uint4(0, 0, 0, 0);
@@ -149,20 +159,10 @@ __device__ __forceinline__ uint4 load_residual4(const Params& gp, long long at, 
 // before their stores to C.
 template <int S, bool EPI>
 __device__ __forceinline__ void join_slices(const Params& gp, uint32_t part, int rank, int tm, int tn, int warp, int lane,
-                                            bool live) {
+                                            bool live, const Finish& f) {
   constexpr int WARPS = NUM_THREADS / 32, ROWS = (128 / S + WARPS - 1) / WARPS, R = S == 1 ? (ROWS + 1) / 2 : ROWS;
   const int rows = min(128, gp.M - tm * 128), cols = min(BN1, gp.N - tn * BN1);
   const int c = 4 * lane;  // this lane's columns
-  Finish f = {};
-  if constexpr (EPI) {
-    f = Finish{gp.C, gp.ep.P, gp.out_type, gp.ep.act, gp.vec_c, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-    if (gp.ep.bias) {
-      float* b = &f.bias.x;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (c + q < cols) b[q] = load_real(gp.ep.bias, gp.ep.bias_type, tn * BN1 + c + q);
-    }
-  }
 #pragma unroll
   for (int i0 = 0; i0 < ROWS; i0 += R) {
     float4 v[S][R];
@@ -263,9 +263,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   // the set-up above overlaps the predecessor's tail
-  wait_for_predecessor();
+  if (!gp.late) wait_for_predecessor();
+  if (threadIdx.x == 0) clear_status(gp, plan);  // before a late one that keeps it can start
   allow_dependents();
-  if (threadIdx.x == 0) clear_status(gp, plan);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -414,6 +414,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 
   __syncwarp();
+  Finish f = {};
+  if constexpr (EPI) f = make_finish(gp, tn * BN1 + 4 * lane, gp.N - tn * BN1 - 4 * lane);  // under way as the CTAs meet
+  if (gp.late) wait_for_predecessor();
   tc_fence_before();
   if (S > 1) cluster_sync();
   else __syncthreads();
@@ -424,10 +427,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   const bool live = !*abort_flag;
   const uint32_t part = smem_u32(stage_base);
-  if (S == 1) join_slices<1, EPI>(gp, part, rank, tm, tn, warp, lane, live);
-  else if (S == 2) join_slices<2, EPI>(gp, part, rank, tm, tn, warp, lane, live);
-  else if (S == 4) join_slices<4, EPI>(gp, part, rank, tm, tn, warp, lane, live);
-  else join_slices<8, EPI>(gp, part, rank, tm, tn, warp, lane, live);
+  if (S == 1) join_slices<1, EPI>(gp, part, rank, tm, tn, warp, lane, live, f);
+  else if (S == 2) join_slices<2, EPI>(gp, part, rank, tm, tn, warp, lane, live, f);
+  else if (S == 4) join_slices<4, EPI>(gp, part, rank, tm, tn, warp, lane, live, f);
+  else join_slices<8, EPI>(gp, part, rank, tm, tn, warp, lane, live, f);
 }
 
 // ---------------------------------------------------------------------------
@@ -548,6 +551,7 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
   p.vec_c = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc * es % 16 == 0;
   p.fault = fault;
   p.keep_status = a.keep_status;
+  p.late = a.late;
   p.wait_ns = wait_ns;
   if (a.ep) {
     p.ep = *a.ep;

@@ -191,9 +191,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   // the set-up above overlaps the predecessor's tail
-  wait_for_predecessor();
+  if (!gp.late) wait_for_predecessor();
+  if (threadIdx.x == 0) clear_status(gp, plan);  // before a late one that keeps it can start
   allow_dependents();
-  if (threadIdx.x == 0) clear_status(gp, plan);
   const int total = load_groups(gp.gr, tab, NTOK, gp.nt, plan);
   Units units{gp, tab};
 
@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   }
 
   __syncwarp();
+  if (gp.late) wait_for_predecessor();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -374,7 +375,7 @@ cudaError_t grouped_device(int dev, GroupedDevice& out) {
 }
 
 // Rows to a group, on average, up to which the kernel for few is the faster one.
-constexpr long long kFewRows = 128;
+constexpr long long kFewRows = 112;
 
 }  // namespace
 
@@ -404,6 +405,7 @@ cudaError_t launch_f8_grouped(const F8GemmArgs& a, const F8Groups& g, DevPlan* p
   p.vec_c = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc * es % 16 == 0;
   p.fault = fault;
   p.keep_status = a.keep_status;
+  p.late = a.late;
   p.wait_ns = wait_ns;
   p.gr = Groups{g.offsets, g.wide, (int)g.E, g.by_blocks ? p.KB : p.M, g.zero_rest};
   const bool few = !g.by_blocks && (variant == 1 || (variant == 0 && a.M <= kFewRows * g.E));

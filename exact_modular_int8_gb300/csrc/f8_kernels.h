@@ -32,6 +32,7 @@ struct QuantArgs {
   const void* P = nullptr;
   // both: sums over the rows of each block of 128 rows, [ceil(M/128)][K]
   float* sums = nullptr;
+  bool late = false;  // tiles: see F8GemmArgs
 };
 cudaError_t launch_quantise_f8(QuantArgs a, int type, int form, cudaStream_t st);
 // out [K] = the sum of `rows` rows of partial sums [rows][K], in a fixed order.
@@ -64,6 +65,12 @@ struct F8GemmArgs {
   bool b_kmajor, tile_b;
   bool keep_status = false;  // an earlier product of the same call has cleared it
   const F8Epilogue* ep = nullptr;  // b_kmajor and tile_b only
+  // Reads nothing that the kernel before it in the stream writes, nor writes what
+  // that reads, so that the two may run at the same time: it waits for that kernel
+  // as it ends, not as it starts.  What the kernels further back wrote is there: the
+  // one before has waited for them before it let this one start, or is late itself
+  // and was let by one that had.  (A call's first kernel is never late.)
+  bool late = false;
 };
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, int fault,
                            unsigned long long wait_ns);

@@ -401,9 +401,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   // the set-up above overlaps the predecessor's tail
-  wait_for_predecessor();
+  if (!gp.late) wait_for_predecessor();
+  if (threadIdx.x == 0) clear_status(gp, plan);  // before a late one that keeps it can start
   allow_dependents();
-  if (threadIdx.x == 0) clear_status(gp, plan);
   int total = gp.mt * gp.nt;
   if constexpr (WALK == WALK_ROWS) total = load_groups(gp.gr, tab, 256, gp.nt, plan);
   if constexpr (WALK == WALK_BLOCKS) total *= load_groups(gp.gr, tab, 0, 0, plan) * gp.gr.E;
@@ -628,6 +628,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 
   __syncwarp();  // whole warps again before the abort check and the barriers below
+  if (gp.late) wait_for_predecessor();
   if (*abort_flag) {
     // an aborted role may leave copies in flight that signal either CTA:
     // give them time to land before the pair leaves

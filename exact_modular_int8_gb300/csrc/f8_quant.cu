@@ -271,12 +271,13 @@ __global__ void __launch_bounds__(16 * kTile / Src::kRows, Src::E::kPer == 2 && 
   __shared__ __align__(16) float2 col_scale[COLS ? kTile : 1];
   __shared__ __align__(16) uint8_t t_tile[COLS ? kTile * kTile : 16];  // transposed bytes, 16-byte chunks swizzled
   __shared__ uint32_t warp_mag[GRPS / 2];
-  wait_for_predecessor();
+  constexpr bool TILES = !ROWS && !COLS;
+  if (!TILES || !a.late) wait_for_predecessor();
   allow_dependents();
   const long long kb = (a.K + kTile - 1) / kTile, mb = GROUPED ? a.blocks : (a.M + kTile - 1) / kTile;
   const long long ti = blockIdx.x / kb, tj = blockIdx.x - ti * kb;
   const T* X = static_cast<const T*>(a.X);
-  if constexpr (!ROWS && !COLS) {  // a stack of matrices
+  if constexpr (TILES) {  // a stack of matrices
     X += blockIdx.y * a.M * a.ldx;
     a.Q += blockIdx.y * a.M * a.ldq;
     a.S += blockIdx.y * mb * kb;
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(16 * kTile / Src::kRows, Src::E::kPer == 2 && 
 #pragma unroll
   for (int r = 0; r < R; ++r) Src::load(e[r], a, X, r0 + r, c0, r0 + r < at.end ? left : 0);
 
-  if constexpr (!ROWS && !COLS) {
+  if constexpr (TILES) {
     uint32_t m = mag8(e[0]);
 #pragma unroll
     for (int r = 1; r < R; ++r) m = E::larger(m, mag8(e[r]));
@@ -306,6 +307,7 @@ __global__ void __launch_bounds__(16 * kTile / Src::kRows, Src::E::kPer == 2 && 
       if (r0 + r < a.M)
         store8(a.Q + (r0 + r) * a.ldq + c0, left, a.vec_q, quantise8([&](int i) { return e[r].at(i); }, bs));
     if (threadIdx.x == 0) a.S[ti * kb + tj] = scale_of(top);
+    if (a.late) wait_for_predecessor();
     return;
   }
   if constexpr (SUM) {  // kept where the transposed bytes will be

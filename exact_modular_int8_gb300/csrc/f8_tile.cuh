@@ -48,6 +48,7 @@ struct Params {
   int vec_c;  // rows of C start on 16-byte boundaries
   int fault;
   int keep_status;
+  int late;
   unsigned long long wait_ns;
   F8Epilogue ep;
   int vec_r;  // rows of the residual start on 16-byte boundaries
