@@ -365,15 +365,18 @@ int linear_act_f8_backward(const void* dY, int x_type, int64_t lddy, const void*
   q.act = act;
   q.P = v.p;
   q.sums = dbias ? reinterpret_cast<float*>(c.take((size_t)blocks128(M) * N * 4)) : nullptr;
+  q.out = dbias;
+  q.out_type = bias_type;
   int rc = quantise(q, x_type, RG_F8_BOTH, st);
-  if (!rc && dbias && N &&
+  const bool sum = dbias && N && (!M || blocks128(M) > kSumCluster);
+  if (!rc && sum &&
       launch_sum_rows(q.sums, M ? blocks128(M) : 0, N, dbias, bias_type, st) != cudaSuccess)
     rc = RG_ERR_CUDA;
   // The sums of rows and the two products read what the quantisation wrote, and
   // nothing of each other's.
   if (!rc) {
     F8GemmArgs a = gemm_args(d.q, d.ld, d.s, w.q, w.ld, w.s, dX, x_type, K, M, K, N, false, true);
-    a.late = M && N && dbias;
+    a.late = M && N && sum;
     rc = product(a, plan, st);
   }
   if (!rc) {

@@ -292,8 +292,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
           if (!ok) break;
           const float sb = SB[kb * gp.sb_k];
           const float* sa = gp.SA + (long long)at.m0 * gp.sa_ld + kb;
-#pragma unroll 4
-          for (int r = tid >> 3; r < at.count; r += 8) scales[b].s[kbi][r] = sa[r * gp.sa_ld] * sb;
+          float v[NTOK / 8];  // all under way before the first is stored
+#pragma unroll
+          for (int i = 0; i < NTOK / 8; ++i) {
+            const int r = (tid >> 3) + 8 * i;
+            v[i] = r < at.count ? __ldg(sa + r * gp.sa_ld) : 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < NTOK / 8; ++i)
+            if ((tid >> 3) + 8 * i < at.count) scales[b].s[kbi][(tid >> 3) + 8 * i] = v[i] * sb;
           mbar_arrive(smem_u32(&sfull[b]));
         }
       }
@@ -374,8 +381,25 @@ cudaError_t grouped_device(int dev, GroupedDevice& out) {
   return cudaSuccess;
 }
 
-// Rows to a group, on average, up to which the kernel for few is the faster one.
-constexpr long long kFewRows = 112;
+// Which kernel, by the time that each would take: waves of its tiles, of which half
+// a one is lost to each group (but a group has at least one), times what a tile
+// takes.  The few-row kernel's blocks take 0.28 us with a token and 0.44 with 128, the
+// pairs' 0.53, and a tile 0.8 and 2.5 more.  Measured, us, few-row kernel first (groups
+// of uneven sizes; E x N x K, rows to a group on average):
+//   64 x 2048 x 4096  8: 88 / 137   64: 115 / 139   96: 142 / 154   128: 158 / 156
+//                     256: 276 / 212   1024: 922 / 575
+//   16 x 1544 x 2056  312: 49 / 38;   16 x 1024 x 1024  250: 14.6 / 16.3
+//   8 x 1024 x 1024   128: 9.2 / 9.8
+bool few_rows_to_a_group(long long T, long long E, long long N, long long KB, int sms, int pairs) {
+  const long long G = std::min(E, T);
+  auto tiles = [&](long long rows, long long cols) {
+    return std::max(G, T / rows + G / 2) * ((N + cols - 1) / cols);
+  };
+  const double waves_few = (double)((tiles(NTOK, 128) + sms - 1) / sms);
+  const double waves_pair = (double)((tiles(256, BN2) + pairs - 1) / pairs);
+  const double tokens = std::min(1.0, (double)T / (double)(G * NTOK));
+  return waves_few * ((0.28 + 0.16 * tokens) * (double)KB + 0.8) < waves_pair * (0.53 * (double)KB + 2.5);
+}
 
 }  // namespace
 
@@ -408,7 +432,8 @@ cudaError_t launch_f8_grouped(const F8GemmArgs& a, const F8Groups& g, DevPlan* p
   p.late = a.late;
   p.wait_ns = wait_ns;
   p.gr = Groups{g.offsets, g.wide, (int)g.E, g.by_blocks ? p.KB : p.M, g.zero_rest};
-  const bool few = !g.by_blocks && (variant == 1 || (variant == 0 && a.M <= kFewRows * g.E));
+  const bool few = !g.by_blocks && (variant == 1 || (variant == 0 && few_rows_to_a_group(a.M, g.E, a.N, p.KB, gd.sms,
+                                                                                         gd.max_pairs)));
   // groups that can have a row, and the rows behind them
   const long long groups = std::min(g.E, a.M) + 1;
   cudaLaunchAttribute attr[2];

@@ -30,10 +30,14 @@ struct QuantArgs {
   // both: X times the slope of the activation act at P [M][K] (X's type)
   int act = RG_ACT_NONE;
   const void* P = nullptr;
-  // both: sums over the rows of each block of 128 rows, [ceil(M/128)][K]
+  // both: sums over the rows, [K] in out_type to `out` where kSumCluster blocks of 128
+  // rows hold them all, else over each such block's, [ceil(M/128)][K], to `sums`
   float* sums = nullptr;
+  void* out = nullptr;
+  int out_type = RG_TYPE_F32;
   bool late = false;  // tiles: see F8GemmArgs
 };
+constexpr int kSumCluster = 8;
 cudaError_t launch_quantise_f8(QuantArgs a, int type, int form, cudaStream_t st);
 // out [K] = the sum of `rows` rows of partial sums [rows][K], in a fixed order.
 cudaError_t launch_sum_rows(const float* sums, long long rows, long long K, void* out, int type, cudaStream_t st);

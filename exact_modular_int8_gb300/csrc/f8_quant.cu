@@ -259,9 +259,10 @@ __device__ __forceinline__ RowBlock find_block(const QuantArgs& a, long long i) 
 // eight columns (or 512 threads and four rows).  ROWS / COLS: scales along rows and along columns (with both,
 // one read of X gives both results); neither: one scale for the tile.  GROUPED:
 // the blocks along the columns lie in one group of rows each.  SUM: sums over the
-// tile's rows.
+// tile's rows, or with a.out over all rows: the blocks of a column of tiles are then
+// a cluster, whose sums meet in the first's shared memory.
 template <typename Src, bool ROWS, bool COLS, bool GROUPED, bool SUM>
-__global__ void __launch_bounds__(16 * kTile / Src::kRows, Src::E::kPer == 2 && !SUM ? (GROUPED ? 3 : 4) : 2)
+__global__ void __launch_bounds__(16 * kTile / Src::kRows, Src::E::kPer == 2 && !SUM ? (GROUPED && ROWS ? 3 : 4) : 2)
     quantise_tile_kernel(QuantArgs a) {
   constexpr int R = Src::kRows, GRPS = kTile / R;  // rows of a thread, groups of them
   using E = typename Src::E;
@@ -271,11 +272,18 @@ __global__ void __launch_bounds__(16 * kTile / Src::kRows, Src::E::kPer == 2 && 
   __shared__ __align__(16) float2 col_scale[COLS ? kTile : 1];
   __shared__ __align__(16) uint8_t t_tile[COLS ? kTile * kTile : 16];  // transposed bytes, 16-byte chunks swizzled
   __shared__ uint32_t warp_mag[GRPS / 2];
+  __shared__ float col_sum[SUM ? kTile : 1];
   constexpr bool TILES = !ROWS && !COLS;
   if (!TILES || !a.late) wait_for_predecessor();
   allow_dependents();
   const long long kb = (a.K + kTile - 1) / kTile, mb = GROUPED ? a.blocks : (a.M + kTile - 1) / kTile;
-  const long long ti = blockIdx.x / kb, tj = blockIdx.x - ti * kb;
+  long long ti = blockIdx.x / kb, tj = blockIdx.x - ti * kb;
+  if constexpr (SUM) {
+    if (a.out) {  // down the columns
+      tj = blockIdx.x / mb;
+      ti = blockIdx.x - tj * mb;
+    }
+  }
   const T* X = static_cast<const T*>(a.X);
   if constexpr (TILES) {  // a stack of matrices
     X += blockIdx.y * a.M * a.ldx;
@@ -389,7 +397,8 @@ __global__ void __launch_bounds__(16 * kTile / Src::kRows, Src::E::kPer == 2 && 
         float v = part[0];
 #pragma unroll
         for (int g = 1; g < GRPS; ++g) v += part[g * kTile];
-        if (col < a.K) a.sums[ti * a.K + col] = v;
+        if (a.out) col_sum[threadIdx.x] = v;
+        else if (col < a.K) a.sums[ti * a.K + col] = v;
       }
     }
     __syncthreads();
@@ -428,6 +437,27 @@ __global__ void __launch_bounds__(16 * kTile / Src::kRows, Src::E::kPer == 2 && 
         }
       }
     }
+    if constexpr (SUM) {
+      if (a.out) {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        const long long col = tj * kTile + threadIdx.x;
+        if (ti == 0 && threadIdx.x < kTile && col < a.K) {
+          const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&col_sum[threadIdx.x]);
+          float v = col_sum[threadIdx.x];
+          for (int r = 1; r < (int)mb; ++r) {
+            uint32_t at;
+            float w;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(r));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(at) : "memory");
+            v += w;
+          }
+          store_real(a.out, a.out_type, col, v);
+        }
+        __syncwarp();  // none leaves while its sums are read
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+      }
+    }
   }
 }
 
@@ -452,10 +482,33 @@ __global__ void __launch_bounds__(256) sum_rows_kernel(const float* sums, long l
   }
 }
 
+// A kernel with column sums: in clusters down the columns where one holds them all.
+template <typename Src>
+cudaError_t launch_sums(QuantArgs a, dim3 g, dim3 b, cudaStream_t st) {
+  const auto kernel = quantise_tile_kernel<Src, true, true, false, true>;
+  const long long mb = (a.M + kTile - 1) / kTile;
+  if (!a.out || mb > kSumCluster) {
+    a.out = nullptr;
+    return launch_dependent(kernel, g, b, 0, st, a);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = g;
+  cfg.blockDim = b;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)mb;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <typename Src>
 cudaError_t launch_tiles(const QuantArgs& a, int form, dim3 g, cudaStream_t st) {
   const dim3 b(256);
-  const bool sum = a.sums != nullptr;
   if (a.offsets)
     return form == RG_F8_COLUMNS
                ? launch_dependent(quantise_tile_kernel<Src, false, true, true, false>, g, b, 0, st, a)
@@ -464,8 +517,8 @@ cudaError_t launch_tiles(const QuantArgs& a, int form, dim3 g, cudaStream_t st) 
     case RG_F8_ROWS: return launch_dependent(quantise_tile_kernel<Src, true, false, false, false>, g, b, 0, st, a);
     case RG_F8_COLUMNS: return launch_dependent(quantise_tile_kernel<Src, false, true, false, false>, g, b, 0, st, a);
     case RG_F8_BOTH:
-      return sum ? launch_dependent(quantise_tile_kernel<Src, true, true, false, true>, g, b, 0, st, a)
-                 : launch_dependent(quantise_tile_kernel<Src, true, true, false, false>, g, b, 0, st, a);
+      return a.sums ? launch_sums<Src>(a, g, b, st)
+                    : launch_dependent(quantise_tile_kernel<Src, true, true, false, false>, g, b, 0, st, a);
     default: return launch_dependent(quantise_tile_kernel<Src, false, false, false, false>, g, b, 0, st, a);
   }
 }
@@ -474,7 +527,7 @@ template <typename T, int ACT>
 cudaError_t launch_slope(const QuantArgs& a, dim3 g, cudaStream_t st) {
   using Src = TimesSlope<T, ACT>;
   const dim3 b(16 * kTile / Src::kRows);
-  return a.sums ? launch_dependent(quantise_tile_kernel<Src, true, true, false, true>, g, b, 0, st, a)
+  return a.sums ? launch_sums<Src>(a, g, b, st)
                 : launch_dependent(quantise_tile_kernel<Src, true, true, false, false>, g, b, 0, st, a);
 }
 

@@ -43,6 +43,8 @@ typedef int (*expert_fn)(const void*, int, int64_t, const void*, int, int64_t, c
                          int64_t, int64_t, void*, size_t, unsigned, void*, size_t, void*);
 typedef int (*expert_backward_fn)(const void*, int, int64_t, const void*, size_t, const void*, int64_t, void*, void*, int,
                                   int64_t, int64_t, int64_t, unsigned, void*, size_t, void*);
+typedef int (*quantize_grouped_fn)(const void*, int, int64_t, int64_t, int64_t, int, const void*, int64_t, uint8_t*,
+                                   int64_t, float*, uint8_t*, int64_t, float*, unsigned, void*);
 typedef size_t (*expert_bytes_fn)(int64_t, int64_t, int64_t, int64_t);
 typedef int (*capturing_fn)(void*);
 
@@ -59,6 +61,7 @@ static rows_fn lib_rows;
 static sums_fn lib_sums;
 static expert_fn lib_expert;
 static expert_backward_fn lib_expert_backward;
+static quantize_grouped_fn lib_quantize_grouped;
 static expert_bytes_fn lib_expert_saved_bytes, lib_expert_ws_bytes;
 static capturing_fn lib_capturing;
 static PyObject *types[3], *f8_type, *byte_type; /* torch dtypes by RG_TYPE_*, E4M3, uint8 */
@@ -651,6 +654,41 @@ static PyObject* rows(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return finish(rc, "grouped_gemm_f8", C);
 }
 
+/* quantize_grouped(X, form, offsets, flags) -> (QT, ST) or (Q, S, QT, ST); None to decline */
+static PyObject* quantize_grouped(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  if (n != 4) return decline();
+  const long form = PyLong_AsLong(a[1]);
+  unsigned flags = (unsigned)PyLong_AsUnsignedLong(a[3]);
+  int64_t dev, E = -1;
+  void *stream, *off;
+  matrix x;
+  if (PyErr_Occurred() || !place(a[0], &dev, &stream)) return decline();
+  const int t = real_of(a[0], -1, &x);
+  if (t < 0 || !offsets_of(a[2], dev, &E, &off, &flags)) return decline();
+  PyObject* device = PyObject_GetAttr(a[0], s_device);
+  if (!device) return decline();
+  quantised d = {0}, c = {0};
+  const int direct = form == RG_F8_BOTH;
+  int ok = !direct || new_quantised(x.m, x.k, x.m, device, &d);
+  ok = ok && new_quantised(x.k, 128 * (x.m / 128 + E), x.k, device, &c);
+  Py_DECREF(device);
+  PyObject* r = NULL;
+  if (ok) {
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = lib_quantize_grouped(x.p, t, x.ld, x.m, x.k, (int)form, off, E, d.qp, d.ld, d.sp, c.qp, c.ld, c.sp, flags, stream);
+    Py_END_ALLOW_THREADS
+    r = direct ? PyTuple_Pack(4, d.q, d.s, c.q, c.s) : PyTuple_Pack(2, c.q, c.s);
+    if (r) r = finish(rc, "quantize_f8", r);
+  }
+  Py_XDECREF(d.q);
+  Py_XDECREF(d.s);
+  Py_XDECREF(c.q);
+  Py_XDECREF(c.s);
+  return r;
+}
+
 /* A new stack [e][m][k]. */
 static PyObject* new_stack(int64_t e, int64_t m, int64_t k, PyObject* type, PyObject* device) {
   return new_tensor(Py_BuildValue("(LLL)", (long long)e, (long long)m, (long long)k), type, device);
@@ -777,11 +815,11 @@ static PyObject* expert_backward(PyObject* self, PyObject* const* a, Py_ssize_t 
   return r ? finish(rc, "expert_linear_f8_backward", r) : NULL;
 }
 
-/* setup((eighteen addresses), (f32, f16, bf16), f8, uint8, (int32, int64), empty, empty_strided, raw_stream,
+/* setup((nineteen addresses), (f32, f16, bf16), f8, uint8, (int32, int64), empty, empty_strided, raw_stream,
  * current_device, workspaces, raise) */
 static PyObject* setup(PyObject* self, PyObject* args) {
   (void)self;
-  enum { kEntries = 18 };
+  enum { kEntries = 19 };
   uintptr_t f[kEntries];
   PyObject *t0, *t1, *t2, *addresses;
   if (!PyArg_ParseTuple(args, "O!(OOO)OO(OO)OOOOOO", &PyTuple_Type, &addresses, &t0, &t1, &t2, &f8_type, &byte_type,
@@ -812,6 +850,7 @@ static PyObject* setup(PyObject* self, PyObject* args) {
   lib_expert_backward = (expert_backward_fn)f[15];
   lib_expert_saved_bytes = (expert_bytes_fn)f[16];
   lib_expert_ws_bytes = (expert_bytes_fn)f[17];
+  lib_quantize_grouped = (quantize_grouped_fn)f[18];
   types[RG_TYPE_F32] = t0;
   types[RG_TYPE_F16] = t1;
   types[RG_TYPE_BF16] = t2;
@@ -839,6 +878,7 @@ static PyMethodDef methods[] = {{"setup", setup, METH_VARARGS, NULL},
                                 {"linear_act", (PyCFunction)(void (*)(void))linear_act, METH_FASTCALL, NULL},
                                 {"linear_act_backward", (PyCFunction)(void (*)(void))linear_act_backward, METH_FASTCALL,
                                  NULL},
+                                {"quantize_grouped", (PyCFunction)(void (*)(void))quantize_grouped, METH_FASTCALL, NULL},
                                 {"rows", (PyCFunction)(void (*)(void))rows, METH_FASTCALL, NULL},
                                 {"sums", (PyCFunction)(void (*)(void))sums, METH_FASTCALL, NULL},
                                 {"expert", (PyCFunction)(void (*)(void))expert, METH_FASTCALL, NULL},

@@ -48,7 +48,8 @@ def _native():
                    lib.linear_f8_saved_bytes, lib.linear_f8_ws_bytes, lib.rg_stream_capturing, lib.scaled_gemm_act_f8,
                    lib.linear_act_f8, lib.linear_act_f8_backward, lib.linear_act_f8_saved_bytes,
                    lib.linear_act_f8_ws_bytes, lib.grouped_gemm_f8, lib.grouped_wgrad_f8, lib.expert_linear_f8,
-                   lib.expert_linear_f8_backward, lib.expert_linear_f8_saved_bytes, lib.expert_linear_f8_ws_bytes)
+                   lib.expert_linear_f8_backward, lib.expert_linear_f8_saved_bytes, lib.expert_linear_f8_ws_bytes,
+                   lib.quantize_grouped_f8)
         m.setup(tuple(address(f) for f in entries), (torch.float32, torch.float16, torch.bfloat16), F8, torch.uint8,
                 (torch.int32, torch.int64), torch.empty, torch.empty_strided, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache,
                 _check)
@@ -173,6 +174,10 @@ def _groups(where: str, offsets: torch.Tensor, E: int):
 
 def _quantize_grouped(X, f, offsets, sync):
     """quantize_f8 of a stack of matrices (offsets None), or of rows in groups."""
+    if offsets is not None and X.is_cuda and f in (RG_F8_COLUMNS, RG_F8_BOTH):
+        r = _native().quantize_grouped(X, f, offsets, RG_FLAG_SYNC if sync else 0)
+        if r is not None:
+            return r
     t = _TYPES.get(X.dtype)
     stack = offsets is None
     if t is None or X.dim() != (3 if stack else 2) or (f != RG_F8_TILES if stack else f not in (RG_F8_COLUMNS, RG_F8_BOTH)):
