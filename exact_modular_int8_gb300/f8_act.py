@@ -15,8 +15,8 @@ import torch
 
 from . import (RG_ACT_GELU, RG_ACT_GELU_TANH, RG_ACT_NONE, RG_ACT_RELU, RG_ACT_SILU, RG_ERR_ARG, RG_FLAG_SYNC,
                ResGemmError, _output, library)
-from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _device_index, _launch, _native, _no_grad, _rows_of,
-                 _scratch)
+from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _device_index, _join_graph, _launch, _native, _no_grad,
+                 _rows_of, _scratch)
 
 _ACTS = {None: RG_ACT_NONE, "relu": RG_ACT_RELU, "silu": RG_ACT_SILU, "gelu": RG_ACT_GELU,
          "gelu_tanh": RG_ACT_GELU_TANH}
@@ -140,6 +140,7 @@ def linear_act_f8(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = 
     gradient autograd calls linear_act_f8_backward for Y."""
     if _differentiable(X, W, X, W, bias, residual):
         saved = []
+        nodes = _join_graph("linear_act_f8", X, W, bias, residual)  # noqa: F841 (kept until the call has been made)
         return _LinearActGrad.apply(X, W, bias, residual, act, sync, ws, saved), tuple(saved)
     where = "linear_act_f8"
     a = _act(where, act)
