@@ -26,11 +26,14 @@ namespace {
 // to 128 of its tokens, over all of K.  The producer runs up to six blocks (of 16
 // KB of weights) ahead, across units, which is what keeps the weights coming.
 //
-// An epilogue warp adds a block's products to its sums while the next block's are
-// read, and the scales reach it multiplied.  (128 tokens to each of 8 groups of
-// 2048 x 4096, operands in L2: SUMS_128 us; ADD_AFTER with each block's read waited for
-// and its two scales multiplied in the loop; without the sums 17.4, which is L2's
-// rate, 11 TB/s.)
+// Sixteen epilogue warps with an instance of their loop for each number of 16-token
+// parts, and scales that reach them multiplied.  8 groups of 2048 x 4096, operands in
+// L2, 1 and 128 tokens to a group: 14.3 and 20.9 us, of which each block of k takes
+// 0.31 and 0.44; with an empty epilogue 11.7 and 17.4, which is L2's rate of 11 TB/s.
+// Eight warps took 13.7 and 23.1, with parts skipped at run time and the scales
+// multiplied in the loop 15.5 and 26.5 (parts that are not there still cost their
+// moves), two blocks to a barrier 16.1 and 30.5.  64 groups of 2048 x 2048 from memory,
+// 1 token each: 45.4 us, 5.9 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int NTOK = 128;
 constexpr int TOK_BOX = 32;  // tokens per copy

@@ -28,7 +28,16 @@ namespace {
 // More epilogue warps (16: spills, 293 us), 256 x 192 tiles with twelve warps (271
 // us) and single-CTA 128 x 192 tiles (261 us) were slower; one 256-column MMA for
 // both halves took the same time.  With a scale for each of B's rows: 366 us, 1535
-// cycles a block (380 us with fp32 results); 2048 x 4096 x 8100 108 us.
+// cycles a block (380 us with fp32 results); 2048 x 4096 x 8100 108 us.  (16 warps whose
+// registers hold, 56 and 104 of them, 64 columns each: 271 us; with a scale for each
+// of B's rows, where tensor memory gives fragments 250 bytes a cycle, 360 us.)
+//
+// With an epilogue, 8192 x 8192 x 2048 bf16 (135 us without): a bias 145 us, silu 164,
+// gelu 176, residual 173, values before the activation 160, gelu with all of these 226.
+// The epilogue warps do it while no sums are made, so its instructions and waits
+// count whole: biases come through the scales' warp (fetched by the epilogue warps:
+// 152 us), activations are 5 to 13 operations (gelu by erff: 214), the residual comes
+// through a ring (loads by the lanes spilled in the blocks' loop: 323).
 //
 // The block is launched with 168 registers a thread; the first warpgroup
 // (producer, MMA issue, scales) gives up 112 of them and the two epilogue
@@ -36,7 +45,7 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int BN2 = 256;
 constexpr int STAGES2 = 5;
-constexpr int STAGES2_RING = 4;  // where a ring of two more buffers to a warp takes a stage's place
+constexpr int STAGES2_RING = 4;  // with a residual, whose rings take a stage's place
 constexpr int STAGE2_BYTES = 2 * SLAB;
 constexpr int HALF_SLAB = SLAB / 2;  // a CTA's 64 columns of one half
 constexpr int PAIR_COLS = BN2 * 4 / EPI_WARPS;  // columns per epilogue warp
@@ -157,11 +166,10 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* tm, bool tma, voi
   }
   __syncwarp();
 }
-// Of BUFS staging buffers the one whose turn it is has been read by its last store.
-template <int BUFS = 2>
+// The staging buffer that the last store but one used has been read.
 __device__ __forceinline__ void buffer_free(bool tma, int lane) {
   if (tma) {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(BUFS - 1) : "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
     __syncwarp();
   }
 }
@@ -198,14 +206,14 @@ __device__ __forceinline__ void stage_row(uint8_t* buf, const uint64_t* acc, int
 }
 
 // This warp's 32 rows x 128 columns of sums to C through two alternating staging
-// buffers, or four where little is summed for much that is stored (sums over
-// groups: 32 of 2048 x 2048 over 16384 rows BUFS4 us, with two buffers 211).  c_row0:
-// row0 in C, whose matrices may lie one behind the other.
+// buffers.  c_row0: row0 in C, whose matrices may lie one behind the other.  (Four
+// buffers in a stage's place were worth 1% where little is summed for much that is
+// stored, in sums over groups.)
 template <int ES, bool TILE_B, int WALK>
 __device__ __forceinline__ void store_rows(const Params& gp, const CUtensorMap* tmC,
-                                           const Sums<PAIR_COLS, TILE_B>& sums, uint8_t* stage, uint8_t* ring,
-                                           int c_row0, int rows, int col0, int lane) {
-  constexpr int COLS = 64 / ES, BUFS = WALK == WALK_BLOCKS ? 4 : 2;
+                                           const Sums<PAIR_COLS, TILE_B>& sums, uint8_t* stage, int c_row0, int rows,
+                                           int col0, int lane) {
+  constexpr int COLS = 64 / ES;
   // a whole matrix's last rows are cut by the TMA store too
   const bool tma = gp.vec_c && (WALK == WALK_WHOLE || rows == 32);
   if (WALK != WALK_WHOLE && gp.vec_c && !tma) {  // the last tile's stores have read both buffers
@@ -214,8 +222,8 @@ __device__ __forceinline__ void store_rows(const Params& gp, const CUtensorMap* 
   }
 #pragma unroll
   for (int c = 0; c < PAIR_COLS / COLS; ++c) {
-    uint8_t* buf = (c & (BUFS - 2) ? ring : stage) + (c & 1) * OUT_BUF;
-    buffer_free<BUFS>(tma, lane);
+    uint8_t* buf = stage + (c & 1) * OUT_BUF;
+    buffer_free(tma, lane);
     if constexpr (TILE_B) {
       stage_row<ES>(buf, sums.acc[0] + c * (COLS / 2), gp.out_type, lane);
     } else {
@@ -348,14 +356,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmP,
                         const __grid_constant__ Params gp, DevPlan* plan) {
   static_assert(ACT == PLAIN ? !RES : TILE_B && WALK == WALK_WHOLE, "an epilogue has a row to a lane");
-  constexpr int STAGES = RES || WALK == WALK_BLOCKS ? STAGES2_RING : STAGES2;
+  constexpr int STAGES = RES ? STAGES2_RING : STAGES2;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t rank = cluster_rank();
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stage_base = smem;
   uint8_t* out_base = smem + STAGES2 * STAGE2_BYTES;
-  uint8_t* ring_base = smem + STAGES2_RING * STAGE2_BYTES;  // RES, WALK_BLOCKS
+  uint8_t* ring_base = smem + STAGES2_RING * STAGE2_BYTES;  // RES
   ScaleChunk<BN2>* scales = reinterpret_cast<ScaleChunk<BN2>*>(out_base + EPI_WARPS * OUT_WARP);
   uint64_t* bars = reinterpret_cast<uint64_t*>(out_base + EPI_WARPS * OUT_WARP + SCALE2_BYTES);
   uint8_t* more = reinterpret_cast<uint8_t*>(bars) + 256;
@@ -600,8 +608,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int row = at2.m0 + (int)rank * 128 + q4 * 32, n0 = at2.n0 + col;
         if (ok && row < gp.M && n0 < gp.N) {
           const int rows = min(32, gp.M - row), c_row = row + at2.g * gp.M;
-          if (gp.out_type == RG_TYPE_F32) store_rows<4, TILE_B, WALK>(gp, &tmC, sums, stage, ring, c_row, rows, n0, lane);
-          else store_rows<2, TILE_B, WALK>(gp, &tmC, sums, stage, ring, c_row, rows, n0, lane);
+          if (gp.out_type == RG_TYPE_F32) store_rows<4, TILE_B, WALK>(gp, &tmC, sums, stage, c_row, rows, n0, lane);
+          else store_rows<2, TILE_B, WALK>(gp, &tmC, sums, stage, c_row, rows, n0, lane);
         }
       } else if (ok && row0 < at.m_end && col0 < gp.N) {
         const int rows = min(32, at.m_end - row0);
@@ -616,9 +624,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             store_rows_act<2, ACT, RES>(gp, &tmC, &tmP, sums, bias, stage, ring, r0, rows, c0, l);
         } else {
           if (gp.out_type == RG_TYPE_F32)
-            store_rows<4, TILE_B, WALK>(gp, &tmC, sums, stage, ring, row0, rows, col0, lane);
+            store_rows<4, TILE_B, WALK>(gp, &tmC, sums, stage, row0, rows, col0, lane);
           else
-            store_rows<2, TILE_B, WALK>(gp, &tmC, sums, stage, ring, row0, rows, col0, lane);
+            store_rows<2, TILE_B, WALK>(gp, &tmC, sums, stage, row0, rows, col0, lane);
         }
       }
       if constexpr (ACT != PLAIN) slot = slot + 1 == BIAS_BUFS ? 0 : slot + 1;

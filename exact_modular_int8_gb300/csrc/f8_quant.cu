@@ -137,8 +137,8 @@ struct FromX {
   }
 };
 // Half the rows to a thread: the products are fp32 and the slopes take their time, so
-// that twice the warps are worth more (8192 x 4096 bf16 with gelu: SLOPE4 us, SLOPE8 with
-// eight rows; the bytes at the copy rate: 30).
+// that twice the warps are worth more (8192 x 4096 bf16 with gelu: 50 us, 62 with eight
+// rows; the bytes at the copy rate: 30).
 template <typename T, int ACT>
 struct TimesSlope {
   using E = Entries<float>;

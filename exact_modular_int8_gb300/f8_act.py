@@ -18,6 +18,7 @@ from . import (RG_ACT_GELU, RG_ACT_GELU_TANH, RG_ACT_NONE, RG_ACT_RELU, RG_ACT_S
 from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _device_index, _join_graph, _launch, _native, _no_grad,
                  _rows_of, _scratch)
 
+_grad_enabled = torch.is_grad_enabled
 _ACTS = {None: RG_ACT_NONE, "relu": RG_ACT_RELU, "silu": RG_ACT_SILU, "gelu": RG_ACT_GELU,
          "gelu_tanh": RG_ACT_GELU_TANH}
 
@@ -54,7 +55,7 @@ def _there(*ts):
 
 
 def _differentiable(A, B, C, D, bias, residual) -> bool:
-    return torch.is_grad_enabled() and (
+    return _grad_enabled() and (
         A.requires_grad or B.requires_grad or C.requires_grad or D.requires_grad
         or (bias is not None and bias.requires_grad) or (residual is not None and residual.requires_grad))
 
