@@ -41,42 +41,7 @@ constexpr int SCALE1_BYTES = SCALE_BUFS * (int)sizeof(ScaleChunk<BN1>);
 constexpr int SMEM1_BYTES = 1024 + STAGES1 * STAGE1_BYTES + SCALE1_BYTES + 256;
 static_assert(SMEM1_BYTES <= 232448, "shared memory");
 
-// Four neighbouring entries of a row of C (or what is laid out like it) from column c of the tile on.
-__device__ __forceinline__ void store4(const Params& gp, void* C, long long out, int c, int cols, float4 v) {
-  if (gp.vec_c && c + 4 <= cols) {
-    if (gp.out_type == RG_TYPE_F32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(C) + out) = v;
-    } else {
-      uint2 w;
-      if (gp.out_type == RG_TYPE_F16) {
-        const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
-        w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-      } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-        w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-      }
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(C) + out) = w;
-    }
-  } else {
-    const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (c + q < cols) store_out(C, out + q, gp.out_type, e[q]);
-  }
-}
-
-// What the epilogue needs of the parameters, by value.
-struct Finish {
-  void *C, *P;
-  int out_type, act, vec;
-  float4 bias;
-};
-__device__ __forceinline__ float entry(const uint4& w, int type, int q) {  // of four, as loaded
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-  if (type == RG_TYPE_F32) return __uint_as_float(v[q]);
-  const uint32_t h = v[q >> 1] >> (16 * (q & 1));
-  return type == RG_TYPE_F16 ? __half2float(__ushort_as_half((unsigned short)h)) : __uint_as_float(h << 16);
-}
+// Four neighbouring entries of a row, `left` of them in the matrix; vec: rows start on 16-byte boundaries.
 __device__ __forceinline__ void put4(void* p, long long at, int type, int vec, int left, const float (&e)[4]) {
   if (vec && left >= 4) {
     if (type == RG_TYPE_F32) {
@@ -97,6 +62,18 @@ __device__ __forceinline__ void put4(void* p, long long at, int type, int vec, i
     for (int q = 0; q < 4; ++q)
       if (q < left) store_real(p, type, at + q, e[q]);
   }
+}
+// What the epilogue needs of the parameters, by value.
+struct Finish {
+  void *C, *P;
+  int out_type, act, vec;
+  float4 bias;
+};
+__device__ __forceinline__ float entry(const uint4& w, int type, int q) {  // of four, as loaded
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  if (type == RG_TYPE_F32) return __uint_as_float(v[q]);
+  const uint32_t h = v[q >> 1] >> (16 * (q & 1));
+  return type == RG_TYPE_F16 ? __half2float(__ushort_as_half((unsigned short)h)) : __uint_as_float(h << 16);
 }
 // Four entries of a row, `left` of them in the matrix, through the epilogue; res: the
 // residual's.  Not inlined: a warp's rows share its code, whose fetching is what a
@@ -204,7 +181,7 @@ __device__ __forceinline__ void join_slices(const Params& gp, uint32_t part, int
       if (live && r < rows && c < cols) {
         const long long out = (long long)(tm * 128 + r) * gp.ldc + (long long)tn * BN1 + c;
         if constexpr (EPI) finish4(f, out, cols - c, v[0][i], res[i]);
-        else store4(gp, gp.C, out, c, cols, v[0][i]);
+        else put4(gp.C, out, gp.out_type, gp.vec_c, cols - c, {v[0][i].x, v[0][i].y, v[0][i].z, v[0][i].w});
       }
     }
   }

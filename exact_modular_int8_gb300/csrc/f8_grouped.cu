@@ -139,8 +139,8 @@ __device__ __forceinline__ void sum_unit(const Params& gp, const UnitAt& at, Uni
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float2 f = unpack2(acc[i][j]);
-        if (2 * j < left) store_out(gp.C, out + 2 * j * gp.ldc, gp.out_type, f.x);
-        if (2 * j + 1 < left) store_out(gp.C, out + (2 * j + 1) * gp.ldc, gp.out_type, f.y);
+        if (2 * j < left) store_real(gp.C, gp.out_type, out + 2 * j * gp.ldc, f.x);
+        if (2 * j + 1 < left) store_real(gp.C, gp.out_type, out + (2 * j + 1) * gp.ldc, f.y);
       }
     }
   }
@@ -329,6 +329,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 
   __syncwarp();
   if (gp.late) wait_for_predecessor();
+  if (*abort_flag) {  // products that no role has waited for: give them time to end
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 200000ull) {
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

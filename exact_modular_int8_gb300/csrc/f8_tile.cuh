@@ -165,12 +165,6 @@ __device__ __forceinline__ void load_scales(const Params& gp, const float* SB, S
   }
 }
 
-__device__ __forceinline__ void store_out(void* C, long long at, int type, float v) {
-  if (type == RG_TYPE_F32) static_cast<float*>(C)[at] = v;
-  else if (type == RG_TYPE_F16) static_cast<__half*>(C)[at] = __float2half_rn(v);
-  else static_cast<__nv_bfloat16*>(C)[at] = __float2bfloat16_rn(v);
-}
-
 // Pairs of fp32 (fma.rn.f32x2: two multiply-adds per instruction).
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t d;

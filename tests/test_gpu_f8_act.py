@@ -354,3 +354,22 @@ def test_timeout_is_reported(rg, variant):  # noqa: F811
         lib.rg_inject_fault(0)
         lib.rg_set_wait_limit_ns(old)
     assert torch.equal(rg.scaled_gemm_act_f8(*args, bias=b, act="silu"), good)
+
+
+def test_product_of_many_entries(rg):  # noqa: F811
+    """Results, residual and values before the activation whose entries pass 2^31."""
+    m, n = 70000, 32768
+    A, a = random_f8(m, 16, 1)
+    B, b = random_f8(n, 16, 2)
+    SA, sa = random_scales((m, 1), 3)
+    SB, sb = random_scales((n // 128, 1), 4)
+    r = torch.zeros((m, n), dtype=torch.bfloat16, device="cuda")
+    r[::7] = 1.0
+    C, P = rg.scaled_gemm_act_f8(A, SA, B, SB, act="relu", residual=r, pre=True)
+    bv = b * np.repeat(sb, 128, 0)
+    for row in (0, 7, 65535, 65536, 69993, 69999):
+        av = a[row] * sa[row]
+        ref, e = bv @ av, 145 * 2.0**-23 * (np.abs(bv) @ np.abs(av))
+        within(P[row], ref, e + U[torch.bfloat16] * np.abs(ref))
+        y = np.maximum(ref, 0) + (row % 7 == 0)
+        within(C[row], y, e + 2.0**-24 * np.abs(y) + U[torch.bfloat16] * (np.abs(y) + e))

@@ -429,3 +429,38 @@ def test_timeout_is_reported(rg, variant):  # noqa: F811
         lib.rg_inject_fault(0)
         lib.rg_set_wait_limit_ns(old)
     assert torch.equal(rg.grouped_gemm_f8(A, SA, B, SB, offsets_of([200, 100]), torch.float32, True), good)
+
+
+# ---------------------------------------------------------------------------
+# results of more than 2^31 entries
+# ---------------------------------------------------------------------------
+
+
+def test_rows_of_many_entries(rg, variant):  # noqa: F811
+    """The last rows of a result whose entries pass 2^31, and the rows behind the last group."""
+    t, n, counts = 70000, 32768, [30000, 39990]
+    A, a = random_f8(t, 16, 1)
+    B, b = stack_f8(2, n, 16, 2)
+    SA, sa = random_scales((t, 1), 3)
+    SB, sb = random_scales((2, n // 128, 1), 4)
+    C = rg.grouped_gemm_f8(A, SA, B, SB, offsets_of(counts), torch.bfloat16, True)
+    rows = np.r_[0:3, 29998:30003, 65530:65540, 69980:69990]
+    for r in rows:
+        g = int(r >= 30000)
+        bv = b[g] * np.repeat(sb[g], 128, 0)
+        av = a[r] * sa[r]
+        close(C[r], bv @ av, np.abs(bv) @ np.abs(av), 1)
+    assert (C[69990:] == 0).all()
+
+
+def test_sums_of_many_entries(rg):  # noqa: F811
+    m, counts = 8192, [3] * 40
+    x = normal((120, m), 1, 1.0, torch.bfloat16).cuda()
+    off = offsets_of(counts)
+    A, SA = rg.quantize_f8(x, "columns", offsets=off)
+    C = rg.grouped_wgrad_f8(A, SA, A, SA, off, out_dtype=torch.bfloat16)
+    av = A.double().cpu().numpy() * spread(SA.double().cpu().numpy(), 1, 128, A.shape)
+    for g in (0, 31, 32, 39):
+        at = slice(128 * starts(counts)[g], 128 * starts(counts)[g] + 3)
+        for r in (0, 4095, 8191):
+            close(C[g, r], av[:, at] @ av[r, at], np.abs(av[:, at]) @ np.abs(av[r, at]), 1)
