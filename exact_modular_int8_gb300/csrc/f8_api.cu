@@ -190,7 +190,7 @@ int quantize_f8(const void* X, int x_type, int64_t ldx, int64_t M, int64_t K, in
       return RG_ERR_ARG;
     const long long tiles = form == RG_F8_ROWS ? (M * blocks128(K) + 15) / 16 : blocks128(M) * blocks128(K);
     if (tiles > INT_MAX) return RG_ERR_ARG;
-    const int rc = quantise(QuantArgs{X, ldx, M, K, Q, ldq, S, QT, ldqt, ST, false, false, false, false}, x_type, form, st);
+    const int rc = quantise(QuantArgs{X, ldx, M, K, Q, ldq, S, QT, ldqt, ST}, x_type, form, st);
     if (rc) return rc;
   }
   if ((flags & RG_FLAG_SYNC) && cudaStreamSynchronize(st) != cudaSuccess) return RG_ERR_CUDA;
@@ -243,10 +243,10 @@ int linear_f8(const void* X, int x_type, int64_t ldx, const void* W, int w_type,
   const Saved v = carve_saved(static_cast<uint8_t*>(saved), M, N, K);
   Carver c{static_cast<uint8_t*>(ws) + kCallBlockBytes};
   const Quantised x = carve(c, M, K, M);
-  int rc = quantise(QuantArgs{X, ldx, M, K, x.q, x.ld, x.s, v.xt.q, v.xt.ld, v.xt.s, false, false, false, false}, x_type,
+  int rc = quantise(QuantArgs{X, ldx, M, K, x.q, x.ld, x.s, v.xt.q, v.xt.ld, v.xt.s}, x_type,
                     RG_F8_BOTH, st);
   if (!rc)
-    rc = quantise(QuantArgs{W, ldw, N, K, v.w.q, v.w.ld, v.w.s, nullptr, 0, nullptr, false, false, false, false}, w_type,
+    rc = quantise(QuantArgs{W, ldw, N, K, v.w.q, v.w.ld, v.w.s, nullptr, 0, nullptr}, w_type,
                   RG_F8_TILES, st);
   if (!rc)
     rc = product(gemm_args(x.q, x.ld, x.s, v.w.q, v.w.ld, v.w.s, Y, x_type, N, M, N, K, true, true),
@@ -268,7 +268,7 @@ int linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* sa
   DevPlan* plan = static_cast<DevPlan*>(ws);
   Carver c{static_cast<uint8_t*>(ws) + kCallBlockBytes};
   const Quantised d = carve(c, M, N, M), dt = carve(c, N, M, N);
-  int rc = quantise(QuantArgs{dY, lddy, M, N, d.q, d.ld, d.s, dt.q, dt.ld, dt.s, false, false, false, false}, dy_type,
+  int rc = quantise(QuantArgs{dY, lddy, M, N, d.q, d.ld, d.s, dt.q, dt.ld, dt.s}, dy_type,
                     RG_F8_BOTH, st);
   if (!rc)  // dX [M][K] = dY [M][N] W [N][K]
     rc = product(gemm_args(d.q, d.ld, d.s, v.w.q, v.w.ld, v.w.s, dX, dy_type, K, M, K, N, false, true), plan, st);

@@ -14,6 +14,7 @@
 // memory and MMA issue, the rest of the first four copy the scales to shared
 // memory, warps 4..11 epilogue.  Every wait is bounded as in the residue
 // product.
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <mutex>
@@ -41,7 +42,7 @@ constexpr int SCALE1_BYTES = SCALE_BUFS * (int)sizeof(ScaleChunk<BN1>);
 constexpr int SMEM1_BYTES = 1024 + STAGES1 * STAGE1_BYTES + SCALE1_BYTES + 256;
 static_assert(SMEM1_BYTES <= 232448, "shared memory");
 
-// Four neighbouring entries of a row, `left` of them in the matrix; vec: rows start on 16-byte boundaries.
+// Four neighbouring entries of a row, `left` of them in the matrix; vec: they lie on a boundary of their size.
 __device__ __forceinline__ void put4(void* p, long long at, int type, int vec, int left, const float (&e)[4]) {
   if (vec && left >= 4) {
     if (type == RG_TYPE_F32) {
@@ -63,6 +64,8 @@ __device__ __forceinline__ void put4(void* p, long long at, int type, int vec, i
       if (q < left) store_real(p, type, at + q, e[q]);
   }
 }
+__device__ __forceinline__ int four_at_once(int unit, int type) { return unit >= (type == RG_TYPE_F32 ? 16 : 8); }
+
 // What the epilogue needs of the parameters, by value.
 struct Finish {
   void *C, *P;
@@ -101,7 +104,7 @@ __device__ __noinline__ void finish4(Finish f, long long out, int left, float4 v
   put4(f.C, out, f.out_type, f.vec, left, e);
 }
 __device__ __forceinline__ Finish make_finish(const Params& gp, int n, int left) {
-  Finish f = {gp.C, gp.ep.P, gp.out_type, gp.ep.act, gp.vec_c, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  Finish f = {gp.C, gp.ep.P, gp.out_type, gp.ep.act, four_at_once(gp.unit_c, gp.out_type), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   if (gp.ep.bias) {
     if (left > 0) f.bias.x = load_real(gp.ep.bias, gp.ep.bias_type, n);
     if (left > 1) f.bias.y = load_real(gp.ep.bias, gp.ep.bias_type, n + 1);
@@ -114,7 +117,7 @@ __device__ __forceinline__ Finish make_finish(const Params& gp, int n, int left)
 __device__ __forceinline__ uint4 load_residual4(const Params& gp, long long at, int left) {
   uint4 w = make_uint4(0, 0, 0, 0);
   if (!gp.ep.R) return w;
-  if (gp.vec_r && left >= 4) {
+  if (four_at_once(gp.unit_r, gp.out_type) && left >= 4) {
     if (gp.out_type == RG_TYPE_F32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(gp.ep.R) + at);
     const uint2 h = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(gp.ep.R) + at);
     return make_uint4(h.x, h.y, 0, 0);
@@ -181,7 +184,8 @@ __device__ __forceinline__ void join_slices(const Params& gp, uint32_t part, int
       if (live && r < rows && c < cols) {
         const long long out = (long long)(tm * 128 + r) * gp.ldc + (long long)tn * BN1 + c;
         if constexpr (EPI) finish4(f, out, cols - c, v[0][i], res[i]);
-        else put4(gp.C, out, gp.out_type, gp.vec_c, cols - c, {v[0][i].x, v[0][i].y, v[0][i].z, v[0][i].w});
+        else put4(gp.C, out, gp.out_type, four_at_once(gp.unit_c, gp.out_type), cols - c,
+                   {v[0][i].x, v[0][i].y, v[0][i].z, v[0][i].w});
       }
     }
   }
@@ -420,7 +424,7 @@ constexpr TileKernel kTileKernels[2][2] = {
 constexpr TileKernel kTileActKernel = f8_gemm_tile_kernel<true, true, true>;
 
 template <bool B_KMAJOR, bool TILE_B>
-constexpr PairKernel kWhole = f8_gemm_pair_kernel<B_KMAJOR, TILE_B, WALK_WHOLE, PLAIN, false>;
+constexpr PairKernel kWhole = f8_gemm_pair_kernel<B_KMAJOR, TILE_B, WALK_WHOLE, PLAIN, false, false>;
 constexpr PairKernel kPairKernels[2][2] = {{kWhole<false, false>, kWhole<false, true>},
                                            {kWhole<true, false>, kWhole<true, true>}};
 constexpr int SMEM2_BYTES = pair_smem(WALK_WHOLE, PLAIN);
@@ -441,9 +445,9 @@ cudaError_t f8_device(int dev, F8Device& out) {
         if (e != cudaSuccess) return e;
       }
     cudaError_t set = cudaFuncSetAttribute(kTileActKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM1_BYTES);
-    for (int i = 0; i < 2 * (RG_ACT_GELU_TANH + 1) && set == cudaSuccess; ++i)
-      set = cudaFuncSetAttribute(pair_act_kernel(i >> 1, i & 1), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 pair_smem(WALK_WHOLE, SIMPLE_ACT));
+    for (int i = 0; i < 4 * (RG_ACT_GELU_TANH + 1) && set == cudaSuccess; ++i)
+      set = cudaFuncSetAttribute((i & 2 ? pair_act_ragged_kernel : pair_act_kernel)(i >> 2, i & 1),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, pair_smem(WALK_WHOLE, SIMPLE_ACT));
     if (set != cudaSuccess) return set;
     int sms = 0;
     cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -525,15 +529,15 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
   p.nt = (int)((a.N + BN1 - 1) / BN1);
   p.out_type = a.out_type;
   const int es = a.out_type == RG_TYPE_F32 ? 4 : 2;
-  p.vec_c = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc * es % 16 == 0;
+  p.unit_c = row_unit(a.C, a.ldc * es);
   p.fault = fault;
   p.keep_status = a.keep_status;
   p.late = a.late;
   p.wait_ns = wait_ns;
   if (a.ep) {
     p.ep = *a.ep;
-    p.vec_c = p.vec_c && reinterpret_cast<uintptr_t>(a.ep->P) % 16 == 0;
-    p.vec_r = reinterpret_cast<uintptr_t>(a.ep->R) % 16 == 0 && a.ep->ldr * es % 16 == 0;
+    p.unit_c = std::min(p.unit_c, row_unit(a.ep->P, a.ldc * es));
+    p.unit_r = row_unit(a.ep->R, a.ep->ldr * es);
   }
   cudaLaunchAttribute attr[2];
   const long long tiles2 = ((a.M + 255) / 256) * ((a.N + BN2 - 1) / BN2);
@@ -556,8 +560,12 @@ cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, 
                                             pair_smem(WALK_WHOLE, a.ep ? SIMPLE_ACT : PLAIN), st, 2, attr);
     CUtensorMap mc = {}, mp = {};
     if (!pair_maps(a, p, dev, &ma, &mc, &mp, a.M)) return cudaErrorInvalidValue;
-    const PairKernel kernel = a.ep ? reinterpret_cast<PairKernel>(const_cast<void*>(pair_act_kernel(a.ep->act, a.ep->R)))
-                                   : kPairKernels[a.b_kmajor][a.tile_b];
+    PairKernel kernel = kPairKernels[a.b_kmajor][a.tile_b];
+    if (a.ep) {
+      const bool ragged = p.unit_c < 16 || (p.ep.R && (p.unit_r < 16 || a.N * es % 16 != 0));
+      const void* act = (ragged ? pair_act_ragged_kernel : pair_act_kernel)(a.ep->act, a.ep->R);
+      kernel = reinterpret_cast<PairKernel>(const_cast<void*>(act));
+    }
     return cudaLaunchKernelEx(&cfg, kernel, ma, mb, mc, mp, p, plan);
   }
   if (!make_map_2d(&ma, dev, a.A, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.lda, BK, 128)) return cudaErrorInvalidValue;

@@ -348,9 +348,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 // ---------------------------------------------------------------------------
 using FewKernel = void (*)(const CUtensorMap, const CUtensorMap, const Params, DevPlan*);
 constexpr FewKernel kFewKernels[2] = {f8_few_kernel<false>, f8_few_kernel<true>};
-constexpr PairKernel kRowsKernels[2] = {f8_gemm_pair_kernel<false, true, WALK_ROWS, PLAIN, false>,
-                                        f8_gemm_pair_kernel<true, true, WALK_ROWS, PLAIN, false>};
-constexpr PairKernel kBlocksKernel = f8_gemm_pair_kernel<true, false, WALK_BLOCKS, PLAIN, false>;
+constexpr PairKernel kRowsKernels[2] = {f8_gemm_pair_kernel<false, true, WALK_ROWS, PLAIN, false, false>,
+                                        f8_gemm_pair_kernel<true, true, WALK_ROWS, PLAIN, false, false>};
+constexpr PairKernel kBlocksKernel = f8_gemm_pair_kernel<true, false, WALK_BLOCKS, PLAIN, false, false>;
 
 struct GroupedDevice {
   int sms = 0, max_pairs = 0;
@@ -434,7 +434,7 @@ cudaError_t launch_f8_grouped(const F8GemmArgs& a, const F8Groups& g, DevPlan* p
   p.sb_k = a.sb_k;
   p.sb_e = (long long)p.KB * ((a.N + 127) / 128);
   p.out_type = a.out_type;
-  p.vec_c = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc * es % 16 == 0;
+  p.unit_c = row_unit(a.C, a.ldc * es);
   p.fault = fault;
   p.keep_status = a.keep_status;
   p.late = a.late;

@@ -20,7 +20,8 @@ struct QuantArgs {
   uint8_t* QT;
   long long ldqt;
   float* ST;
-  bool vec_x, vec_q, vec_qt, vec_p;  // set by the launcher: rows start on 16 (8) byte boundaries
+  int unit_x, unit_p;     // set by the launcher: rows start on boundaries of 16, 8, 4 or 2 bytes
+  bool vec_q, vec_qt;     // and on 8 and 16
   // tiles: this many matrices, M rows apart
   long long batch = 1;
   // columns, both: rows in groups (F8Groups), QT [K][128 blocks], ST [K][blocks]
@@ -79,8 +80,9 @@ struct F8GemmArgs {
 cudaError_t launch_f8_gemm(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st, int fault,
                            unsigned long long wait_ns);
 
-// The pair kernel with an epilogue (f8_act.cu); its parameters are those of f8_gemm.cu's.
+// The pair kernel with an epilogue (f8_act.cu, f8_act_ragged.cu); its parameters are those of f8_gemm.cu's.
 const void* pair_act_kernel(int act, bool residual);
+const void* pair_act_ragged_kernel(int act, bool residual);
 
 // Products by group, group g holding rows (or, by_blocks, columns along the
 // contraction) offsets[g] .. offsets[g + 1].

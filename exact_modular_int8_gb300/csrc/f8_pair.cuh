@@ -121,12 +121,37 @@ struct Walk {
   }
 };
 
-// 64 bytes of each of a warp's rows leave its staging buffer (16-byte chunks
-// swizzled as the TMA's 64-byte mode has them) for columns cc.. of D.  Where D's
-// rows start on 16-byte boundaries and all 32 rows are the tile's, a TMA store
-// takes them away and cuts them to the matrix; else the warp writes them.
+// Byte `at` of row r's 64 in a staging buffer, whose 16-byte chunks are swizzled as
+// the TMA's 64-byte mode has them.
+__device__ __forceinline__ uint32_t staged(int r, int at) {
+  return r * 64 + (((at >> 4) ^ ((r >> 1) & 3)) << 4) + (at & 15);
+}
+// The largest unit (up to `unit`) of which `bytes` is a multiple.
+__device__ __forceinline__ int unit_of(int unit, int bytes) {
+  while (bytes & (unit - 1)) unit >>= 1;
+  return unit;
+}
+// Rows of `bytes` (up to 64) from a staging buffer to memory, `pitch` bytes apart, a
+// unit to a lane: neighbouring lanes write neighbouring units.
+template <typename Unit>
+__device__ __forceinline__ void store_units(uint8_t* out, long long pitch, const uint8_t* buf, int rows, int bytes,
+                                            int lane) {
+  constexpr int PER = 64 / sizeof(Unit);  // lanes to a row
+  const int at = (lane % PER) * (int)sizeof(Unit);
+  if (at < bytes) {
+#pragma unroll 4
+    for (int r = lane / PER; r < rows; r += 32 / PER)
+      *reinterpret_cast<Unit*>(out + r * pitch + at) = *reinterpret_cast<const Unit*>(buf + staged(r, at));
+  }
+}
+// 64 bytes of each of a warp's rows leave its staging buffer for columns cc.. of D.
+// Where D's rows start on 16-byte boundaries and all 32 rows are the tile's, a TMA
+// store takes them away and cuts them to the matrix; else the warp writes them, in
+// the largest units that fit (8192 x 4096 x 2048 bf16: 65 us; of 4092 columns 75, 4094
+// 79, 4095 90.  Entry by entry, two to a lane: 91 each.  The unit found anew at each
+// row, in a quarter of the code: 86, 109 and 143).
 template <int ES>
-__device__ __forceinline__ void store_chunk(const CUtensorMap* tm, bool tma, void* D, long long ldd, bool vec,
+__device__ __forceinline__ void store_chunk(const CUtensorMap* tm, bool tma, void* D, long long ldd, int unit,
                                             const uint8_t* buf, int row0, int rows, int cc, int N, int lane) {
   constexpr int COLS = 64 / ES;
   if (tma) {
@@ -143,26 +168,15 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* tm, bool tma, voi
     return;
   }
   __syncwarp();
-  const int cols = min(COLS, N - cc);
-  uint8_t* out = static_cast<uint8_t*>(D) + ((long long)row0 * ldd + cc) * ES;
-  if (vec && cols == COLS) {  // 16 bytes at a time, a row to four lanes
-#pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 8) {
-      const int r = r0 + (lane >> 2), i = lane & 3;
-      if (r < rows)
-        *reinterpret_cast<uint4*>(out + (long long)r * ldd * ES + 16 * i) =
-            *reinterpret_cast<const uint4*>(buf + r * 64 + ((i ^ ((r >> 1) & 3)) << 4));
-    }
-  } else {
-    for (int r = 0; r < rows; ++r)
-      for (int j = lane; j < cols; j += 32) {
-        const int at = j * ES;
-        const uint8_t* src = buf + r * 64 + (((at >> 4) ^ ((r >> 1) & 3)) << 4) + (at & 15);
-        if constexpr (ES == 4)
-          reinterpret_cast<uint32_t*>(out + (long long)r * ldd * ES)[j] = *reinterpret_cast<const uint32_t*>(src);
-        else
-          reinterpret_cast<uint16_t*>(out + (long long)r * ldd * ES)[j] = *reinterpret_cast<const uint16_t*>(src);
-      }
+  const int bytes = min(COLS, N - cc) * ES;
+  if (bytes > 0) {
+    uint8_t* out = static_cast<uint8_t*>(D) + ((long long)row0 * ldd + cc) * ES;
+    const long long pitch = ldd * ES;
+    const int u = unit_of(unit, bytes);
+    if (u == 16) store_units<uint4>(out, pitch, buf, rows, bytes, lane);
+    else if (u == 8) store_units<uint2>(out, pitch, buf, rows, bytes, lane);
+    else if (u == 4) store_units<uint32_t>(out, pitch, buf, rows, bytes, lane);
+    else store_units<uint16_t>(out, pitch, buf, rows, bytes, lane);
   }
   __syncwarp();
 }
@@ -201,7 +215,7 @@ __device__ __forceinline__ void stage_row(uint8_t* buf, const uint64_t* acc, int
       for (int j = 0; j < 4; ++j) p[j] = packed<ES>(unpack2(acc[4 * i + j]), type);
       w = make_uint4(p[0], p[1], p[2], p[3]);
     }
-    *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) = w;
+    *reinterpret_cast<uint4*>(buf + staged(lane, 16 * i)) = w;
   }
 }
 
@@ -215,8 +229,8 @@ __device__ __forceinline__ void store_rows(const Params& gp, const CUtensorMap* 
                                            int col0, int lane) {
   constexpr int COLS = 64 / ES;
   // a whole matrix's last rows are cut by the TMA store too
-  const bool tma = gp.vec_c && (WALK == WALK_WHOLE || rows == 32);
-  if (WALK != WALK_WHOLE && gp.vec_c && !tma) {  // the last tile's stores have read both buffers
+  const bool tma = gp.unit_c == 16 && (WALK == WALK_WHOLE || rows == 32);
+  if (WALK != WALK_WHOLE && gp.unit_c == 16 && !tma) {  // the last tile's stores have read both buffers
     if (lane == 0) bulk_wait_read0();
     __syncwarp();
   }
@@ -233,52 +247,64 @@ __device__ __forceinline__ void store_rows(const Params& gp, const CUtensorMap* 
 #pragma unroll
         for (int j = 0; j < COLS / 8; ++j) {
           const int at = (8 * j + 2 * (lane & 3)) * ES;  // byte within the row's 64
-          stage_pair<ES>(buf + r * 64 + (((at >> 4) ^ ((r >> 1) & 3)) << 4) + (at & 15),
-                         unpack2(sums.acc[i][c * (COLS / 8) + j]), gp.out_type);
+          stage_pair<ES>(buf + staged(r, at), unpack2(sums.acc[i][c * (COLS / 8) + j]), gp.out_type);
         }
       }
     }
-    store_chunk<ES>(tmC, tma, gp.C, gp.ldc, gp.vec_c, buf, c_row0, rows, col0 + c * COLS, gp.N, lane);
+    store_chunk<ES>(tmC, tma, gp.C, gp.ldc, gp.unit_c, buf, c_row0, rows, col0 + c * COLS, gp.N, lane);
   }
 }
 
 // 64 bytes of each of a warp's rows of the residual, from column cc on, on their way
-// to a buffer laid out like the ones for results.  Where its rows do not start on
-// 16-byte boundaries, or end within these columns, wait_residual fetches them.
-template <int ES>
-__device__ __forceinline__ bool residual_async(const Params& gp, int cc) {
-  return gp.vec_r && cc + 64 / ES <= gp.N;
-}
-template <int ES>
-__device__ __forceinline__ void start_residual(const Params& gp, uint8_t* buf, int row0, int rows, int cc, int lane) {
-  if (residual_async<ES>(gp, cc)) {
-    const uint8_t* p = static_cast<const uint8_t*>(gp.ep.R) + ((long long)row0 * gp.ep.ldr + cc) * ES + 16 * (lane & 3);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2);
-      if (r < rows)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(buf) + r * 64 +
-                                                                       (((lane & 3) ^ ((r >> 1) & 3)) << 4)),
-                     "l"(p + r * gp.ep.ldr * ES)
-                     : "memory");
+// to a buffer laid out like the ones for results, in the largest units that fit;
+// units of two bytes, which no asynchronous copy takes, wait_residual fetches (8192 x
+// 4096 x 2048 bf16: 81 us; of 4094 columns 157, 4095 215; each read where it is added: 477, 487).
+template <typename Unit>
+__device__ __forceinline__ void copy_units(uint32_t buf, const uint8_t* in, long long pitch, int rows, int bytes,
+                                           int lane) {
+  constexpr int PER = 64 / sizeof(Unit);  // lanes to a row
+  const int at = (lane % PER) * (int)sizeof(Unit);
+  if (at < bytes) {
+#pragma unroll 4
+    for (int r = lane / PER; r < rows; r += 32 / PER) {
+      const uint32_t dst = buf + staged(r, at);
+      const uint8_t* src = in + r * pitch + at;
+      if constexpr (sizeof(Unit) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"((int)sizeof(Unit)) : "memory");
     }
+  }
+}
+template <int ES, bool RAGGED>
+__device__ __forceinline__ void start_residual(const Params& gp, uint8_t* buf, int row0, int rows, int cc, int lane) {
+  const int bytes = min(64 / ES, gp.N - cc) * ES;
+  if (bytes > 0) {
+    const uint8_t* in = static_cast<const uint8_t*>(gp.ep.R) + ((long long)row0 * gp.ep.ldr + cc) * ES;
+    const long long pitch = gp.ep.ldr * ES;
+    const int u = RAGGED ? unit_of(gp.unit_r, bytes) : 16;
+    if (u == 16) copy_units<uint4>(smem_u32(buf), in, pitch, rows, bytes, lane);
+    else if (u == 8) copy_units<uint2>(smem_u32(buf), in, pitch, rows, bytes, lane);
+    else if (u == 4) copy_units<uint32_t>(smem_u32(buf), in, pitch, rows, bytes, lane);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
-template <int ES>
+template <int ES, bool RAGGED>
 __device__ __forceinline__ void wait_residual(const Params& gp, uint8_t* buf, int row0, int rows, int cc, int lane) {
   asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the next chunk's
-  if (!residual_async<ES>(gp, cc)) {
-    const int cols = min(64 / ES, gp.N - cc);
-    const uint8_t* p = static_cast<const uint8_t*>(gp.ep.R) + ((long long)row0 * gp.ep.ldr + cc) * ES;
-    for (int r = 0; r < rows; ++r)
-      for (int j = lane; j < cols; j += 32) {
-        uint8_t* dst = buf + r * 64 + (((j * ES >> 4) ^ ((r >> 1) & 3)) << 4) + (j * ES & 15);
-        if constexpr (ES == 4)
-          *reinterpret_cast<uint32_t*>(dst) = reinterpret_cast<const uint32_t*>(p + r * gp.ep.ldr * ES)[j];
-        else
-          *reinterpret_cast<uint16_t*>(dst) = reinterpret_cast<const uint16_t*>(p + r * gp.ep.ldr * ES)[j];
+  if constexpr (RAGGED && ES == 2) {
+    const int cols = min(32, gp.N - cc);
+    if (cols > 0 && unit_of(gp.unit_r, cols * 2) == 2) {
+      const uint16_t* in = static_cast<const uint16_t*>(gp.ep.R) + (long long)row0 * gp.ep.ldr + cc + lane;
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += 8) {  // eight rows under way at a time
+        uint16_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r0 + i < rows && lane < cols ? in[(r0 + i) * gp.ep.ldr] : (uint16_t)0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint16_t*>(buf + staged(r0 + i, 2 * lane)) = v[i];
       }
+    }
   }
   __syncwarp();
 }
@@ -294,12 +320,13 @@ __device__ __forceinline__ float2 residual_pair(const uint4& r, int j, int type)
 // activation, then the activation and the residual.  The residual comes 64 bytes
 // of each row at a time through a ring of two buffers, the first two of them since
 // the tile began (start_residual there).
-template <int ES, int ACT, bool RES>
+template <int ES, int ACT, bool RES, bool RAGGED>
 __device__ __forceinline__ void store_rows_act(const Params& gp, const CUtensorMap* tmC, const CUtensorMap* tmP,
                                                Sums<PAIR_COLS, true>& sums, const float* bias, uint8_t* stage,
                                                uint8_t* ring, int row0, int rows, int col0, int lane) {
   constexpr int COLS = 64 / ES, CHUNKS = PAIR_COLS / COLS, PER = 8 / ES;  // pairs of columns in 16 bytes
   const bool relu = ACT == SIMPLE_ACT && gp.ep.act == RG_ACT_RELU;
+  const bool tma = !RAGGED || gp.unit_c == 16;
   int n = 0;  // stores
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
@@ -312,17 +339,17 @@ __device__ __forceinline__ void store_rows_act(const Params& gp, const CUtensorM
       acc[j + 1] = add2(acc[j + 1], b.y);
     }
     if (gp.ep.P) {
-      buffer_free(gp.vec_c, lane);
+      buffer_free(tma, lane);
       uint8_t* buf = stage + (n++ & 1) * OUT_BUF;
       stage_row<ES>(buf, acc, gp.out_type, lane);
-      store_chunk<ES>(tmP, gp.vec_c, gp.ep.P, gp.ldc, gp.vec_c, buf, row0, rows, cc, gp.N, lane);
+      store_chunk<ES>(tmP, tma, gp.ep.P, gp.ldc, gp.unit_c, buf, row0, rows, cc, gp.N, lane);
     }
     uint8_t* in = ring + (c & 1) * OUT_BUF;
-    if constexpr (RES) wait_residual<ES>(gp, in, row0, rows, cc, lane);
+    if constexpr (RES) wait_residual<ES, RAGGED>(gp, in, row0, rows, cc, lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint4 res = make_uint4(0, 0, 0, 0);
-      if constexpr (RES) res = *reinterpret_cast<const uint4*>(in + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+      if constexpr (RES) res = *reinterpret_cast<const uint4*>(in + staged(lane, 16 * i));
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         uint64_t& a = acc[i * PER + j];
@@ -340,22 +367,26 @@ __device__ __forceinline__ void store_rows_act(const Params& gp, const CUtensorM
     }
     if constexpr (RES) {
       __syncwarp();
-      if (c + 2 < CHUNKS) start_residual<ES>(gp, in, row0, rows, cc + 2 * COLS, lane);
+      if (c + 2 < CHUNKS) start_residual<ES, RAGGED>(gp, in, row0, rows, cc + 2 * COLS, lane);
       else asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    buffer_free(gp.vec_c, lane);
+    buffer_free(tma, lane);
     uint8_t* buf = stage + (n++ & 1) * OUT_BUF;
     stage_row<ES>(buf, acc, gp.out_type, lane);
-    store_chunk<ES>(tmC, gp.vec_c, gp.C, gp.ldc, gp.vec_c, buf, row0, rows, cc, gp.N, lane);
+    store_chunk<ES>(tmC, tma, gp.C, gp.ldc, gp.unit_c, buf, row0, rows, cc, gp.N, lane);
   }
 }
 
-template <bool B_KMAJOR, bool TILE_B, int WALK, int ACT, bool RES>
+// RAGGED, with an epilogue: rows of C or of the residual that start or end off a
+// 16-byte boundary.  Instances of their own: the same code in the others takes
+// registers of the sums (8192 x 4096 x 2048 bf16 with a bias 71 -> 94 us, with a residual 81 -> 117).
+template <bool B_KMAJOR, bool TILE_B, int WALK, int ACT, bool RES, bool RAGGED>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     f8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmP,
                         const __grid_constant__ Params gp, DevPlan* plan) {
   static_assert(ACT == PLAIN ? !RES : TILE_B && WALK == WALK_WHOLE, "an epilogue has a row to a lane");
+  static_assert(ACT != PLAIN || !RAGGED, "found out as it runs");
   constexpr int STAGES = RES ? STAGES2_RING : STAGES2;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t rank = cluster_rank();
@@ -554,14 +585,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int rows = min(32, at.m_end - row0), es = gp.out_type == RG_TYPE_F32 ? 4 : 2;
         for (int c = 0; c < 2; ++c) {
           uint8_t* buf = ring + c * OUT_BUF;
-          if (es == 4) start_residual<4>(gp, buf, row0, rows, col0 + c * 16, lane);
-          else start_residual<2>(gp, buf, row0, rows, col0 + c * 32, lane);
+          if (es == 4) start_residual<4, RAGGED>(gp, buf, row0, rows, col0 + c * 16, lane);
+          else start_residual<2, RAGGED>(gp, buf, row0, rows, col0 + c * 32, lane);
         }
         // the rest of the warp's rows, as far as L2
         if (lane < rows && col0 < gp.N) {
           const uint8_t* p = static_cast<const uint8_t*>(gp.ep.R) + ((long long)(row0 + lane) * gp.ep.ldr + col0) * es;
           const int bytes = min(PAIR_COLS, gp.N - col0) * es;
-          for (int i = 128; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+          for (int i = RAGGED ? 0 : 128; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
         }
       }
       using Acc = Sums<PAIR_COLS, TILE_B>;
@@ -619,9 +650,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           asm volatile("" : "+r"(r0), "+r"(c0), "+r"(l));
           const float* bias = bias_base + slot * BN2 + (ew >> 2) * PAIR_COLS;
           if (gp.out_type == RG_TYPE_F32)
-            store_rows_act<4, ACT, RES>(gp, &tmC, &tmP, sums, bias, stage, ring, r0, rows, c0, l);
+            store_rows_act<4, ACT, RES, RAGGED>(gp, &tmC, &tmP, sums, bias, stage, ring, r0, rows, c0, l);
           else
-            store_rows_act<2, ACT, RES>(gp, &tmC, &tmP, sums, bias, stage, ring, r0, rows, c0, l);
+            store_rows_act<2, ACT, RES, RAGGED>(gp, &tmC, &tmP, sums, bias, stage, ring, r0, rows, c0, l);
         } else {
           if (gp.out_type == RG_TYPE_F32)
             store_rows<4, TILE_B, WALK>(gp, &tmC, sums, stage, row0, rows, col0, lane);
@@ -657,6 +688,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 using PairKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const Params,
                             DevPlan*);
 
+template <bool RAGGED>
+const void* pair_act_instance(int act, bool residual) {
+  auto pick = [residual](PairKernel with, PairKernel without) {
+    return reinterpret_cast<const void*>(residual ? with : without);
+  };
+#define RG_PAIR_ACT(ACT) \
+  pick(f8_gemm_pair_kernel<true, true, WALK_WHOLE, ACT, true, RAGGED>, \
+       f8_gemm_pair_kernel<true, true, WALK_WHOLE, ACT, false, RAGGED>)
+  switch (act) {
+    case RG_ACT_SILU: return RG_PAIR_ACT(RG_ACT_SILU);
+    case RG_ACT_GELU: return RG_PAIR_ACT(RG_ACT_GELU);
+    case RG_ACT_GELU_TANH: return RG_PAIR_ACT(RG_ACT_GELU_TANH);
+    default: return RG_PAIR_ACT(SIMPLE_ACT);
+  }
+#undef RG_PAIR_ACT
+}
+
 // The maps of A, of C and of what an epilogue stores before the activation.
 bool pair_maps(const F8GemmArgs& a, const Params& p, int dev, CUtensorMap* ma, CUtensorMap* mc, CUtensorMap* mp,
                long long c_rows) {
@@ -667,7 +715,7 @@ bool pair_maps(const F8GemmArgs& a, const Params& p, int dev, CUtensorMap* ma, C
                        CU_TENSOR_MAP_SWIZZLE_64B, type);
   };
   return make_map_2d(ma, dev, a.A, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.lda, BK, 128) &&
-         (!p.vec_c || (out_map(mc, a.C) && (!p.ep.P || out_map(mp, p.ep.P))));
+         (p.unit_c != 16 || (out_map(mc, a.C) && (!p.ep.P || out_map(mp, p.ep.P))));
 }
 
 }  // namespace

@@ -47,6 +47,10 @@ struct Entries {
     const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
     w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
   }
+  __device__ __forceinline__ void load_words(const T* p) {  // from a 4-byte boundary
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  }
   __device__ __forceinline__ void set(int i, T v) {
     uint16_t h;
     memcpy(&h, &v, 2);
@@ -96,6 +100,10 @@ struct Entries<float> {
     w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
     w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
   }
+  __device__ __forceinline__ void load_words(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  }
   __device__ __forceinline__ void set(int i, float v) { w[i] = __float_as_uint(v); }
   static __device__ __forceinline__ uint32_t mag(uint32_t a) { return a & 0x7FFFFFFFu; }
   static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
@@ -103,11 +111,15 @@ struct Entries<float> {
   static __device__ __forceinline__ uint32_t top(uint32_t m) { return m; }
 };
 
-// Eight entries from p, of which `left` exist; missing ones read as 0.
+// Eight entries from p, of which `left` exist; missing ones read as 0.  unit: all rows
+// start on boundaries of so many bytes.  (8192 rows of bf16: 4096 columns 17.7 us, 4094
+// 24.4, entry by entry 34; of 4095 columns 35, shifted out of the words around them no less.)
 template <typename T>
-__device__ __forceinline__ void load8(Entries<T>& e, const T* p, long long left, bool vec) {
-  if (vec && left >= 8) {
+__device__ __forceinline__ void load8(Entries<T>& e, const T* p, long long left, int unit) {
+  if (unit == 16 && left >= 8) {
     e.load(p);
+  } else if (unit >= 4 && left >= 8) {
+    e.load_words(p);
   } else {
 #pragma unroll
     for (int i = 0; i < Entries<T>::kWords; ++i) e.w[i] = 0;
@@ -133,7 +145,7 @@ struct FromX {
   // eight entries of a row from column c on, of which `left` exist
   static __device__ __forceinline__ void load(E& e, const QuantArgs& a, const T* X, long long row, long long c,
                                               long long left) {
-    load8(e, X + row * a.ldx + c, left, a.vec_x);
+    load8(e, X + row * a.ldx + c, left, a.unit_x);
   }
 };
 // Half the rows to a thread: the products are fp32 and the slopes take their time, so
@@ -147,8 +159,8 @@ struct TimesSlope {
   static __device__ __forceinline__ void load(E& e, const QuantArgs& a, const T* X, long long row, long long c,
                                               long long left) {
     Entries<T> x, p;
-    load8(x, X + row * a.ldx + c, left, a.vec_x);
-    load8(p, static_cast<const T*>(a.P) + row * a.K + c, left, a.vec_p);
+    load8(x, X + row * a.ldx + c, left, a.unit_x);
+    load8(p, static_cast<const T*>(a.P) + row * a.K + c, left, a.unit_p);
 #pragma unroll
     for (int i = 0; i < 8; ++i) e.set(i, x.at(i) * slope<ACT>(p.at(i)));  // a missing entry: 0
   }
@@ -219,7 +231,7 @@ __global__ void __launch_bounds__(256) quantise_rows_kernel(QuantArgs a) {
   const bool live = b < total;
   const long long row = live ? b / kb : 0, j = live ? b - row * kb : 0, c = j * kTile + l16 * 8;
   E e;
-  load8(e, X + row * a.ldx + c, live ? a.K - c : 0, a.vec_x);
+  load8(e, X + row * a.ldx + c, live ? a.K - c : 0, a.unit_x);
   uint32_t m = mag8(e);
 #pragma unroll
   for (int o = 8; o; o >>= 1) m = E::larger(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -565,8 +577,12 @@ cudaError_t launch_quantise_f8(QuantArgs a, int type, int form, cudaStream_t st)
   auto aligned = [](const void* p, long long row_bytes, unsigned n) {
     return (reinterpret_cast<uintptr_t>(p) % n) == 0 && row_bytes % n == 0;
   };
-  a.vec_x = aligned(a.X, a.ldx * (long long)es, 16);
-  a.vec_p = aligned(a.P, a.K * (long long)es, 16);
+  auto unit = [](const void* p, long long row_bytes) {
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | (uintptr_t)row_bytes;
+    return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
+  };
+  a.unit_x = unit(a.X, a.ldx * (long long)es);
+  a.unit_p = unit(a.P, a.K * (long long)es);
   a.vec_q = aligned(a.Q, a.ldq, 8);
   a.vec_qt = aligned(a.QT, a.ldqt, 16);
   switch (type) {
