@@ -32,8 +32,8 @@ namespace {
 // registers hold, 56 and 104 of them, 64 columns each: 271 us; with a scale for each
 // of B's rows, where tensor memory gives fragments 250 bytes a cycle, 360 us.)
 //
-// With an epilogue, 8192 x 8192 x 2048 bf16 (135 us without): a bias 145 us, silu 164,
-// gelu 176, residual 173, values before the activation 160, gelu with all of these 226.
+// With an epilogue, 8192 x 8192 x 2048 bf16 (133 us without): a bias 141 us, silu 159,
+// gelu 172, residual 164, values before the activation 154, gelu with all of these 211.
 // The epilogue warps do it while no sums are made, so its instructions and waits
 // count whole: biases come through the scales' warp (fetched by the epilogue warps:
 // 152 us), activations are 5 to 13 operations (gelu by erff: 214), the residual comes
@@ -144,13 +144,27 @@ __device__ __forceinline__ void store_units(uint8_t* out, long long pitch, const
       *reinterpret_cast<Unit*>(out + r * pitch + at) = *reinterpret_cast<const Unit*>(buf + staged(r, at));
   }
 }
+__device__ __forceinline__ void store_units(uint8_t* out, long long pitch, const uint8_t* buf, int rows, int bytes,
+                                            int u, int lane) {
+  if (u == 16) store_units<uint4>(out, pitch, buf, rows, bytes, lane);
+  else if (u == 8) store_units<uint2>(out, pitch, buf, rows, bytes, lane);
+  else if (u == 4) store_units<uint32_t>(out, pitch, buf, rows, bytes, lane);
+  else store_units<uint16_t>(out, pitch, buf, rows, bytes, lane);
+}
+// The same as a call, for the kernels with an epilogue, whose unrolled loops over
+// columns would hold many copies (8192 x 4092 x 2048 with a bias 108 us, 85 called; in
+// the kernels without, calls cost 5 to 10%).
+__device__ __noinline__ void store_ragged(uint8_t* out, long long pitch, const uint8_t* buf, int rows, int bytes,
+                                          int u, int lane) {
+  store_units(out, pitch, buf, rows, bytes, u, lane);
+}
 // 64 bytes of each of a warp's rows leave its staging buffer for columns cc.. of D.
 // Where D's rows start on 16-byte boundaries and all 32 rows are the tile's, a TMA
 // store takes them away and cuts them to the matrix; else the warp writes them, in
 // the largest units that fit (8192 x 4096 x 2048 bf16: 65 us; of 4092 columns 75, 4094
 // 79, 4095 90.  Entry by entry, two to a lane: 91 each.  The unit found anew at each
-// row, in a quarter of the code: 86, 109 and 143).
-template <int ES>
+// row: 86, 109 and 143).
+template <int ES, bool CALL = false>
 __device__ __forceinline__ void store_chunk(const CUtensorMap* tm, bool tma, void* D, long long ldd, int unit,
                                             const uint8_t* buf, int row0, int rows, int cc, int N, int lane) {
   constexpr int COLS = 64 / ES;
@@ -173,10 +187,8 @@ __device__ __forceinline__ void store_chunk(const CUtensorMap* tm, bool tma, voi
     uint8_t* out = static_cast<uint8_t*>(D) + ((long long)row0 * ldd + cc) * ES;
     const long long pitch = ldd * ES;
     const int u = unit_of(unit, bytes);
-    if (u == 16) store_units<uint4>(out, pitch, buf, rows, bytes, lane);
-    else if (u == 8) store_units<uint2>(out, pitch, buf, rows, bytes, lane);
-    else if (u == 4) store_units<uint32_t>(out, pitch, buf, rows, bytes, lane);
-    else store_units<uint16_t>(out, pitch, buf, rows, bytes, lane);
+    if constexpr (CALL) store_ragged(out, pitch, buf, rows, bytes, u, lane);
+    else store_units(out, pitch, buf, rows, bytes, u, lane);
   }
   __syncwarp();
 }
@@ -258,7 +270,7 @@ __device__ __forceinline__ void store_rows(const Params& gp, const CUtensorMap* 
 // 64 bytes of each of a warp's rows of the residual, from column cc on, on their way
 // to a buffer laid out like the ones for results, in the largest units that fit;
 // units of two bytes, which no asynchronous copy takes, wait_residual fetches (8192 x
-// 4096 x 2048 bf16: 81 us; of 4094 columns 157, 4095 215; each read where it is added: 477, 487).
+// 4096 x 2048 bf16: 81 us; of 4094 columns 121, 4095 156; each read where it is added: 477, 487).
 template <typename Unit>
 __device__ __forceinline__ void copy_units(uint32_t buf, const uint8_t* in, long long pitch, int rows, int bytes,
                                            int lane) {
@@ -276,16 +288,31 @@ __device__ __forceinline__ void copy_units(uint32_t buf, const uint8_t* in, long
     }
   }
 }
+__device__ __noinline__ void copy_ragged(uint32_t buf, const uint8_t* in, long long pitch, int rows, int bytes, int u,
+                                         int lane) {
+  if (u == 16) copy_units<uint4>(buf, in, pitch, rows, bytes, lane);
+  else if (u == 8) copy_units<uint2>(buf, in, pitch, rows, bytes, lane);
+  else if (u == 4) copy_units<uint32_t>(buf, in, pitch, rows, bytes, lane);
+}
+// A lane to a column of two bytes, eight rows under way at a time.
+__device__ __noinline__ void fetch_ragged(uint8_t* buf, const uint16_t* in, long long ld, int rows, int cols, int lane) {
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    uint16_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = r0 + i < rows && lane < cols ? in[(r0 + i) * ld] : (uint16_t)0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint16_t*>(buf + staged(r0 + i, 2 * lane)) = v[i];
+  }
+}
 template <int ES, bool RAGGED>
 __device__ __forceinline__ void start_residual(const Params& gp, uint8_t* buf, int row0, int rows, int cc, int lane) {
   const int bytes = min(64 / ES, gp.N - cc) * ES;
   if (bytes > 0) {
     const uint8_t* in = static_cast<const uint8_t*>(gp.ep.R) + ((long long)row0 * gp.ep.ldr + cc) * ES;
     const long long pitch = gp.ep.ldr * ES;
-    const int u = RAGGED ? unit_of(gp.unit_r, bytes) : 16;
-    if (u == 16) copy_units<uint4>(smem_u32(buf), in, pitch, rows, bytes, lane);
-    else if (u == 8) copy_units<uint2>(smem_u32(buf), in, pitch, rows, bytes, lane);
-    else if (u == 4) copy_units<uint32_t>(smem_u32(buf), in, pitch, rows, bytes, lane);
+    if constexpr (RAGGED) copy_ragged(smem_u32(buf), in, pitch, rows, bytes, unit_of(gp.unit_r, bytes), lane);
+    else copy_units<uint4>(smem_u32(buf), in, pitch, rows, bytes, lane);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -296,14 +323,7 @@ __device__ __forceinline__ void wait_residual(const Params& gp, uint8_t* buf, in
     const int cols = min(32, gp.N - cc);
     if (cols > 0 && unit_of(gp.unit_r, cols * 2) == 2) {
       const uint16_t* in = static_cast<const uint16_t*>(gp.ep.R) + (long long)row0 * gp.ep.ldr + cc + lane;
-#pragma unroll
-      for (int r0 = 0; r0 < 32; r0 += 8) {  // eight rows under way at a time
-        uint16_t v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = r0 + i < rows && lane < cols ? in[(r0 + i) * gp.ep.ldr] : (uint16_t)0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint16_t*>(buf + staged(r0 + i, 2 * lane)) = v[i];
-      }
+      fetch_ragged(buf, in, gp.ep.ldr, rows, cols, lane);
     }
   }
   __syncwarp();
@@ -342,7 +362,7 @@ __device__ __forceinline__ void store_rows_act(const Params& gp, const CUtensorM
       buffer_free(tma, lane);
       uint8_t* buf = stage + (n++ & 1) * OUT_BUF;
       stage_row<ES>(buf, acc, gp.out_type, lane);
-      store_chunk<ES>(tmP, tma, gp.ep.P, gp.ldc, gp.unit_c, buf, row0, rows, cc, gp.N, lane);
+      store_chunk<ES, RAGGED>(tmP, tma, gp.ep.P, gp.ldc, gp.unit_c, buf, row0, rows, cc, gp.N, lane);
     }
     uint8_t* in = ring + (c & 1) * OUT_BUF;
     if constexpr (RES) wait_residual<ES, RAGGED>(gp, in, row0, rows, cc, lane);
@@ -373,13 +393,14 @@ __device__ __forceinline__ void store_rows_act(const Params& gp, const CUtensorM
     buffer_free(tma, lane);
     uint8_t* buf = stage + (n++ & 1) * OUT_BUF;
     stage_row<ES>(buf, acc, gp.out_type, lane);
-    store_chunk<ES>(tmC, tma, gp.C, gp.ldc, gp.unit_c, buf, row0, rows, cc, gp.N, lane);
+    store_chunk<ES, RAGGED>(tmC, tma, gp.C, gp.ldc, gp.unit_c, buf, row0, rows, cc, gp.N, lane);
   }
 }
 
 // RAGGED, with an epilogue: rows of C or of the residual that start or end off a
-// 16-byte boundary.  Instances of their own: the same code in the others takes
-// registers of the sums (8192 x 4096 x 2048 bf16 with a bias 71 -> 94 us, with a residual 81 -> 117).
+// 16-byte boundary.  Instances of their own: those that can do both took 74 us for 8192
+// x 4096 x 2048 bf16 with a bias, 90 with a residual, 112 with these, silu and stored
+// values; without the other path 71, 81 and 96.
 template <bool B_KMAJOR, bool TILE_B, int WALK, int ACT, bool RES, bool RAGGED>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     f8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
