@@ -155,6 +155,39 @@ def test_product_strides_alignment_and_out(rg, m):  # noqa: F811
         assert torch.equal(again, want)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [512, 508, 506, 505, 490, 264])
+def test_product_on_every_boundary(rg, variant, n, dtype):  # noqa: F811
+    """Results and a residual whose rows start 0, 1, 2, 4 entries off 16-byte boundaries: bits as on them, and nothing
+    written beside the result."""
+    m, k = 300, 520
+    (A, SA, B, SB), _, _ = operands(m, 512, k, 3)
+    bias, r = normal((512,), 4, 0.5, dtype).cuda(), normal((m, 512), 5, 1.0, dtype).cuda()
+    want, first = rg.scaled_gemm_act_f8(A, SA, B, SB, bias, "gelu", r, True, dtype)
+    product = rg.scaled_gemm_f8(A, SA, B, SB, dtype, True)
+    B = B[:n].contiguous()
+    SB = SB[: blocks(n)].contiguous()
+    wide = torch.empty((m, n + 8 + 8 - n % 8), dtype=dtype, device="cuda")
+    for off in (0, 1, 2, 4):
+        res = wide[:, off : off + n]
+        res.copy_(r[:, :n])
+        buf = torch.full((m * n + 16,), 7.0, dtype=dtype, device="cuda")
+        out = buf[off : off + m * n].view(m, n)
+        for bound in (res, res.contiguous()):
+            _, p = rg.scaled_gemm_act_f8(A, SA, B, SB, bias[:n], "gelu", bound, True, out=out, out_dtype=dtype)
+            assert torch.equal(out, want[:, :n]) and torch.equal(p, first[:, :n])
+            assert (buf[:off] == 7).all() and (buf[off + m * n :] == 7).all()
+            buf[off : off + m * n] = 7
+        own = buf[off : off + m * n].view(m, n)
+        own.copy_(r[:, :n])  # in the residual's place
+        rg.scaled_gemm_act_f8(A, SA, B, SB, bias[:n], "gelu", own, out=own, out_dtype=dtype)
+        assert torch.equal(own, want[:, :n])
+        assert (buf[:off] == 7).all() and (buf[off + m * n :] == 7).all()
+        rg.scaled_gemm_f8(A, SA, B, SB, dtype, True, out=own)
+        assert torch.equal(own, product[:, :n])
+        assert (buf[:off] == 7).all() and (buf[off + m * n :] == 7).all()
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_special_values(rg, variant, act, m):  # noqa: F811

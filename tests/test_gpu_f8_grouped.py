@@ -134,6 +134,35 @@ def test_rows_strides_and_alignment(rg, variant):  # noqa: F811
     assert torch.equal(rg.grouped_gemm_f8(A, SA, B, SB, off, torch.float32, True, out=odd), C)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [256, 252, 250, 249])
+def test_products_on_every_boundary(rg, variant, n, dtype):  # noqa: F811
+    """By rows and summed over them, results 0, 1, 2, 4 entries off 16-byte boundaries: bits as on them, and rows behind
+    the last group and memory beside the result left alone."""
+    counts, m = [3, 130, 0, 300], 136
+    off = offsets_of(counts)
+    T, E = sum(counts) + 5, len(counts)
+    A, SA, B, SB, C = check_rows(rg, counts, 256, 384, True, dtype, seed=9)
+    XA, XS = rg.quantize_f8(torch.randn((T, m), device="cuda"), "columns", offsets=off)
+    Y = torch.randn((T, 256), device="cuda")
+    YB, YS = rg.quantize_f8(Y, "columns", offsets=off)
+    want = rg.grouped_wgrad_f8(XA, XS, YB, YS, off, out_dtype=dtype)
+    B, SB = B[:, :n].contiguous(), SB[:, : -(-n // 128)].contiguous()
+    YB, YS = YB[:n], YS[:n]
+    rows = C.shape[0]
+    for shift in (0, 1, 2, 4):
+        buf = torch.full((rows * n + 16,), 7.0, dtype=dtype, device="cuda")
+        out = buf[shift : shift + rows * n].view(rows, n)
+        rg.grouped_gemm_f8(A, SA, B, SB, off, dtype, True, out=out)
+        assert torch.equal(out[: sum(counts)], C[: sum(counts), :n])
+        assert (out[sum(counts) :] == 7).all() and (buf[:shift] == 7).all() and (buf[shift + rows * n :] == 7).all()
+        buf = torch.full((E * m * n + 16,), 7.0, dtype=dtype, device="cuda")
+        out = buf[shift : shift + E * m * n].view(E, m, n)
+        rg.grouped_wgrad_f8(XA, XS, YB, YS, off, out=out, out_dtype=dtype)
+        assert torch.equal(out, want[:, :, :n])
+        assert (buf[:shift] == 7).all() and (buf[shift + E * m * n :] == 7).all()
+
+
 @pytest.mark.parametrize("bad", [[1, 3, 9], [0, 5, 4], [0, 3, 11], [0, -1, 9], [0, 2**40, 9], [0, 3, 2**31 + 3],
                                  [-5, 0, 9]])
 def test_bad_offsets_are_reported(rg, variant, bad):  # noqa: F811

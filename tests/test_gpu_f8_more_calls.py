@@ -276,3 +276,25 @@ def test_offsets_on_another_type_or_layout(rg):  # noqa: F811
         assert torch.equal(rg.expert_linear_f8(x, w, o)[0], want)
         y, saved = rg.expert_linear_f8(x, w, o)
         assert all(torch.isfinite(t).all() for t in rg.expert_linear_f8_backward(y, saved))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("k", [512, 508, 510, 505, 260, 9])
+def test_quantise_on_every_boundary(rg, k, dtype):  # noqa: F811
+    """Rows 0, 1, 2, 4 entries off 16-byte boundaries: what the same rows on them give."""
+    m = 300
+    x = normal((m, k), 5, 1.0, dtype).cuda()
+    even = torch.zeros((m, 520), dtype=dtype, device="cuda")[:, :k]
+    even.copy_(x)
+    offsets = torch.tensor([0, 100, 100, 290], device="cuda")
+    calls = [(form, off) for form in ("rows", "columns", "both") for off in (None, offsets)
+             if not (form == "rows" and off is not None)] + [("tiles", None)]
+    for form, off in calls:
+        want = rg.quantize_f8(even, form, offsets=off)
+        for shift in (0, 1, 2, 4):
+            for width in (k, k + 16 - k % 8):
+                buf = torch.full((m * width + 8,), float("nan"), dtype=dtype, device="cuda")
+                odd = buf[shift : shift + m * width].view(m, width)[:, :k]
+                odd.copy_(x)
+                for a, b in zip(rg.quantize_f8(odd, form, offsets=off), want):
+                    assert torch.equal(a.float(), b.float())
