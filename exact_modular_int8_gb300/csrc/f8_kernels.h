@@ -8,6 +8,12 @@
 
 namespace rg {
 
+// The largest of 16, 8, 4 and 2 bytes on whose boundaries all rows start.
+inline int row_unit(const void* p, long long row_bytes) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | (uintptr_t)row_bytes;
+  return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
+}
+
 // X [M][K] (row stride ldx, in entries) to E4M3: Q [M][ldq] with S
 // [M][ceil(K/128)] (rows) or [ceil(M/128)][ceil(K/128)] (tiles), and / or its
 // transpose QT [K][ldqt] with ST [K][ceil(M/128)] (columns).

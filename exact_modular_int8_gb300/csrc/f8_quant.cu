@@ -577,12 +577,8 @@ cudaError_t launch_quantise_f8(QuantArgs a, int type, int form, cudaStream_t st)
   auto aligned = [](const void* p, long long row_bytes, unsigned n) {
     return (reinterpret_cast<uintptr_t>(p) % n) == 0 && row_bytes % n == 0;
   };
-  auto unit = [](const void* p, long long row_bytes) {
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | (uintptr_t)row_bytes;
-    return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
-  };
-  a.unit_x = unit(a.X, a.ldx * (long long)es);
-  a.unit_p = unit(a.P, a.K * (long long)es);
+  a.unit_x = row_unit(a.X, a.ldx * (long long)es);
+  a.unit_p = row_unit(a.P, a.K * (long long)es);
   a.vec_q = aligned(a.Q, a.ldq, 8);
   a.vec_qt = aligned(a.QT, a.ldqt, 16);
   switch (type) {

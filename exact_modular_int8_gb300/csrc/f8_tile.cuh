@@ -364,12 +364,6 @@ __device__ __forceinline__ int load_groups(const Groups& gr, GroupTable& tab, in
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-// The largest of 16, 8, 4 and 2 bytes on whose boundaries all rows start.
-int row_unit(const void* p, long long row_bytes) {
-  const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | (uintptr_t)row_bytes;
-  return bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
-}
-
 // The encoder is a driver function: it needs a current context, which a host
 // thread has only after a runtime call that makes one, and a product in a new
 // thread comes here before any other.  It is made where the encoder has failed
