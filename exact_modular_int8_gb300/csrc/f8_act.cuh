@@ -14,7 +14,7 @@
 // rounding of its argument, where it hardly counts).  erf is Abramowitz and
 // Stegun's 7.1.26, off by 1.5 10^-7, with its exp(-x^2 / 2) shared by the slope; gelu
 // is so off by up to |x| 2^-22 in absolute terms.  NaN stays NaN; an infinity gives
-// what the formula gives.
+// what the formula gives, and to a slope its limit (0 or 1).
 #pragma once
 #include <cstdint>
 
@@ -76,20 +76,28 @@ __device__ __forceinline__ float activate(float x, int act) {
   }
 }
 
+// x held to [-top, top]; a NaN stays one.
+__device__ __forceinline__ float held(float x, float top) { return x > top ? top : x < -top ? -top : x; }
+
+// Far out a slope is 0 or 1, and the product of x with what is 0 there exactly is
+// taken at a finite x: an infinity is an ordinary value here, since what is kept for
+// the slope is rounded to 16 bits (fp16: beyond 65504).
 template <int ACT>
 __device__ __forceinline__ float slope(float x) {
   if constexpr (ACT == RG_ACT_RELU) return x <= 0.0f ? 0.0f : x > 0.0f ? 1.0f : x;
   if constexpr (ACT == RG_ACT_SILU) {
-    const float s = logistic2(-kLog2E * x);
-    return s * fmaf(x, 1.0f - s, 1.0f);
+    // beyond 128: 1 + exp(x) overflows and s is 0, or exp(-x) is below 2^-126 and s is 1
+    const float v = held(x, 128.0f), s = logistic2(-kLog2E * v);
+    return s * fmaf(v, 1.0f - s, 1.0f);
   }
   if constexpr (ACT == RG_ACT_GELU) {
-    const float e = exp_half_square(x);
-    return fmaf(x * 0.3989422804014327f, e, normal_cdf(x, e));
+    // beyond 16 e is 0: exp(-128) is below 2^-126
+    const float v = held(x, 16.0f), e = exp_half_square(v);
+    return fmaf(v * 0.3989422804014327f, e, normal_cdf(v, e));
   }
   if constexpr (ACT == RG_ACT_GELU_TANH) {
     // beyond 30 s is 0 or 1 and the second term 0, which x^2 overflowing would hide
-    const float v = x > 30.0f ? 30.0f : x < -30.0f ? -30.0f : x, v2 = v * v;
+    const float v = held(x, 30.0f), v2 = v * v;
     const float s = tanh_logistic(v, v2);
     return fmaf(v * fmaf(v2, 6.0f * kSqrt2OverPi * 0.044715f, 2.0f * kSqrt2OverPi), s * (1.0f - s), s);
   }

@@ -529,8 +529,9 @@ int linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* sa
  *             X and W as for linear_f8
  *   backward  d = dY * act'(p), dX = d W with d quantised along N, dW = d^T X with
  *             both quantised along M, dbias = the sum of d's rows; R's gradient is dY
- * p is kept in x_type (with an activation only), and the slope is taken there; d is
- * fp32 and is quantised without another rounding.  dY and dX are of x_type.
+ * p is kept in x_type (with an activation only), and the slope is taken there: at an
+ * infinite p (fp16: one beyond 65504) it is its limit, 0 or 1.  d is fp32 and is
+ * quantised without another rounding.  dY and dX are of x_type.
  * Without bias pass a null pointer, and dbias null where it is not wanted.  The
  * backward call takes the forward call's x_type, act and sizes.  Sums over rows
  * are fp32, in a fixed order.  Sizes of `saved` and ws from the two functions,
