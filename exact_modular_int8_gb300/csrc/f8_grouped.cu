@@ -195,8 +195,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   // the set-up above overlaps the predecessor's tail
   if (!gp.late) wait_for_predecessor();
-  if (threadIdx.x == 0) clear_status(gp, plan);  // before a late one that keeps it can start
-  allow_dependents();
+  start_status(gp, plan);
   const int total = load_groups(gp.gr, tab, NTOK, gp.nt, plan);
   Units units{gp, tab};
 

@@ -462,8 +462,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   // the set-up above overlaps the predecessor's tail
   if (!gp.late) wait_for_predecessor();
-  if (threadIdx.x == 0) clear_status(gp, plan);  // before a late one that keeps it can start
-  allow_dependents();
+  start_status(gp, plan);
   int total = gp.mt * gp.nt;
   if constexpr (WALK == WALK_ROWS) total = load_groups(gp.gr, tab, 256, gp.nt, plan);
   if constexpr (WALK == WALK_BLOCKS) total *= load_groups(gp.gr, tab, 0, 0, plan) * gp.gr.E;

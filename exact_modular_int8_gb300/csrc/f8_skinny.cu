@@ -99,10 +99,15 @@ __global__ void __launch_bounds__(kThreads) f8_skinny_kernel(const __grid_consta
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   wait_for_predecessor();
-  allow_dependents();
-  if (blockIdx.x == 0 && threadIdx.x == 0 && !p.keep_status) {  // no wait here that could fail
-    p.plan->status = 0;
-    p.plan->timeout_where = 0;
+  if (blockIdx.x == 0 && !p.keep_status) {  // no wait here that could fail; a late product that keeps it starts after this
+    if (threadIdx.x == 0) {
+      p.plan->status = 0;
+      p.plan->timeout_where = 0;
+      __threadfence();
+      allow_dependents();
+    }
+  } else {
+    allow_dependents();
   }
   const uint32_t ring = su32(smem) + 2 * S::kRed + warp * S::kRing * S::kPiece;
 

@@ -65,11 +65,19 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t adesc, uint64_t bde
 
 // The call's status, in place of a memset before the kernel: by the grid's first
 // thread as it starts, a time limit (which no wait can have used up yet) before
-// any CTA could write to it.
-__device__ __forceinline__ void clear_status(const Params& gp, DevPlan* plan) {
+// any CTA could write to it.  Then the next kernel may start.  A late one that keeps
+// the status has to find it cleared, and one thread that lets it start counts for its
+// block: in the first block that is the clearing thread, once its stores are visible.
+__device__ __forceinline__ void start_status(const Params& gp, DevPlan* plan) {
   if (blockIdx.x == 0 && !gp.keep_status) {
-    plan->status = 0;
-    plan->timeout_where = 0;
+    if (threadIdx.x == 0) {
+      plan->status = 0;
+      plan->timeout_where = 0;
+      __threadfence();
+      allow_dependents();
+    }
+  } else {
+    allow_dependents();
   }
 }
 

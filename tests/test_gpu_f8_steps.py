@@ -35,3 +35,17 @@ def test_slopes_of_infinite_values(rg, dtype, big, act):  # noqa: F811
         gone = torch.ones(n, dtype=torch.bool)[::5]
         gone[[i for i in range(len(gone)) if (5 * i) % 7 == 2]] = False  # overwritten by +big
         assert (got[2][::5][gone] == 0).all()
+
+
+def test_status_of_two_products_at_once(rg):  # noqa: F811
+    """The weight gradient's kernel may run beside the input gradient's, whose first block clears the status for both:
+    what either reports stays."""
+    x, w, dy = normal((40, 128), 1, 1.0, bf).cuda(), normal((2, 96, 128), 2, 0.1).cuda(), normal((40, 96), 3, 1.0, bf).cuda()
+    off = torch.tensor([0, 10, 40], dtype=torch.int32, device="cuda")
+    ws = torch.empty(rg.library().expert_linear_f8_ws_bytes(40, 96, 128, 2), dtype=torch.uint8, device="cuda")
+    _, (kept, _, *rest) = rg.expert_linear_f8(x, w, off, ws=ws)
+    bad = torch.tensor([0, 50, 40], dtype=torch.int32, device="cuda")
+    for i in range(100):
+        at, code = (bad, rg.RG_ERR_ARG) if i % 3 else (off, rg.RG_OK)
+        rg.expert_linear_f8_backward(dy, (kept, at, *rest), sync=False, ws=ws)
+        assert rg.status(ws) == code
