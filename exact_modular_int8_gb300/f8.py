@@ -61,22 +61,30 @@ _call = None
 
 
 _STREAM = "resgemm_stream"
+_AccumulateGrad = torch._C._functions.AccumulateGrad
 
 
-def _join_graph(where: str, *tensors):
-    """To be called before a differentiable call, its result kept until that has been made: a leaf's gradient is
-    accumulated on the stream where the first graph that holds the leaf was made, so that a backward pass captured on
-    another one, while a graph from outside the capture lives, would break the capture off (or the process, where
-    nothing catches it).  Refused here."""
-    captured = torch._C._cuda_isCurrentStreamCapturing()
+def _note_stream(*tensors):
+    """To be called before a differentiable call, its result kept until that has been made: notes at each leaf's
+    accumulation node the stream on which these layers first met it, for _check_capture."""
     nodes = [torch.autograd.graph.get_gradient_edge(t).node for t in tensors
              if t is not None and t.requires_grad and t.is_leaf and t.is_cuda]
     for n in nodes:  # a node lives as long as the graphs that hold its leaf
-        stream = torch._C._cuda_getCurrentRawStream(n.variable.get_device())
-        if n.metadata.setdefault(_STREAM, stream) != stream and captured:
-            raise RuntimeError(f"{where}: a graph made on another stream holds a tensor of this captured call and would "
-                               "accumulate its gradient there: free that graph before the capture")
+        n.metadata.setdefault(_STREAM, torch._C._cuda_getCurrentRawStream(n.variable.get_device()))
     return nodes
+
+
+def _check_capture(where: str, ctx):
+    """To be called as a backward pass starts: a leaf's gradient is accumulated on the stream where the first graph
+    that holds the leaf was made.  Another one takes part in a capture, but the default stream cannot: it would break
+    the capture off (or the process, where nothing catches it).  Refused here where that graph is one of these layers';
+    one of other operators on the leaf itself is not known."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        for n, _ in ctx.next_functions:
+            if isinstance(n, _AccumulateGrad) and n.metadata.get(_STREAM) == 0:
+                raise RuntimeError(f"{where}: a graph made on the default stream holds a tensor of this captured call and "
+                                   "would accumulate its gradient there: free that graph before the capture, or make it "
+                                   "on another stream")
 
 
 class _LinearGrad(torch.autograd.Function):
@@ -93,6 +101,7 @@ class _LinearGrad(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
+        _check_capture("linear_f8", ctx)
         return (*linear_f8_backward(dY, (*ctx.saved_tensors, *ctx.sizes), *ctx.call), None, None, None)
 
 
@@ -349,7 +358,7 @@ def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True, ws: torch.Ten
     linear_f8_backward for Y, with W's gradient in W's dtype."""
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
         saved = []
-        nodes = _join_graph("linear_f8", X, W)  # noqa: F841 (kept until the call has been made)
+        nodes = _note_stream(X, W)  # noqa: F841 (kept until the call has been made)
         return _LinearGrad.apply(X, W, sync, ws, saved), tuple(saved)
     if X.is_cuda and ws is None:
         r = _native().linear(X, W, RG_FLAG_SYNC if sync else 0)

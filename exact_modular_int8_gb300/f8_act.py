@@ -15,8 +15,8 @@ import torch
 
 from . import (RG_ACT_GELU, RG_ACT_GELU_TANH, RG_ACT_NONE, RG_ACT_RELU, RG_ACT_SILU, RG_ERR_ARG, RG_FLAG_SYNC,
                ResGemmError, _output, library)
-from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _device_index, _join_graph, _launch, _native, _no_grad,
-                 _rows_of, _scratch)
+from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _check_capture, _device_index, _launch, _native, _no_grad,
+                 _note_stream, _rows_of, _scratch)
 
 _grad_enabled = torch.is_grad_enabled
 _ACTS = {None: RG_ACT_NONE, "relu": RG_ACT_RELU, "silu": RG_ACT_SILU, "gelu": RG_ACT_GELU,
@@ -129,6 +129,7 @@ class _LinearActGrad(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
+        _check_capture("linear_act_f8", ctx)
         dX, dW, dbias = linear_act_f8_backward(dY, (*ctx.saved_tensors, *ctx.rest), *ctx.call)
         return dX, dW, dbias, dY if ctx.needs_input_grad[3] else None, None, None, None, None
 
@@ -141,7 +142,7 @@ def linear_act_f8(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = 
     gradient autograd calls linear_act_f8_backward for Y."""
     if _differentiable(X, W, X, W, bias, residual):
         saved = []
-        nodes = _join_graph("linear_act_f8", X, W, bias, residual)  # noqa: F841 (kept until the call has been made)
+        nodes = _note_stream(X, W, bias, residual)  # noqa: F841 (kept until the call has been made)
         return _LinearActGrad.apply(X, W, bias, residual, act, sync, ws, saved), tuple(saved)
     where = "linear_act_f8"
     a = _act(where, act)

@@ -17,8 +17,8 @@ import torch
 
 from . import (RG_ERR_ARG, RG_FLAG_KEEP_REST, RG_FLAG_OFFSETS64, RG_FLAG_SYNC, RG_FLAG_TRANS_B, ResGemmError, _output,
                library)
-from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _device_index, _groups, _join_graph, _launch, _native,
-                 _no_grad, _rows_of, _scratch, _stack_stride)
+from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _check_capture, _device_index, _groups, _launch, _native,
+                 _no_grad, _note_stream, _rows_of, _scratch, _stack_stride)
 
 
 def _aligned_stack(q: torch.Tensor):
@@ -146,6 +146,7 @@ class _ExpertGrad(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
+        _check_capture("expert_linear_f8", ctx)
         return (*expert_linear_f8_backward(dY, (*ctx.saved_tensors, *ctx.sizes), *ctx.call), None, None, None, None)
 
 
@@ -157,7 +158,7 @@ def expert_linear_f8(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, sy
     expert_linear_f8_backward for Y, with W's gradient in W's dtype."""
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
         saved = []
-        nodes = _join_graph("expert_linear_f8", X, W)  # noqa: F841 (kept until the call has been made)
+        nodes = _note_stream(X, W)  # noqa: F841 (kept until the call has been made)
         return _ExpertGrad.apply(X, W, offsets, sync, ws, saved), tuple(saved)
     if X.is_cuda and ws is None:
         r = _native().expert(X, W, offsets, RG_FLAG_SYNC if sync else 0)

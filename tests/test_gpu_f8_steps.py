@@ -49,3 +49,90 @@ def test_status_of_two_products_at_once(rg):  # noqa: F811
         at, code = (bad, rg.RG_ERR_ARG) if i % 3 else (off, rg.RG_OK)
         rg.expert_linear_f8_backward(dy, (kept, at, *rest), sync=False, ws=ws)
         assert rg.status(ws) == code
+
+
+def layers(rg, seed):  # noqa: F811
+    """Leaves, and a loss of them through each of the layers."""
+    w1, b1, w2, w3, we = (normal(s, seed + i, 0.1, d).cuda().requires_grad_() for i, (s, d) in enumerate(
+        [((200, 128), f32), ((200,), bf), ((128, 200), f32), ((96, 128), bf), ((3, 64, 96), f32)]))
+    x, off = normal((70, 128), seed + 9, 1.0, bf).cuda(), torch.tensor([0, 20, 20, 70], device="cuda")
+
+    def out():
+        h, _ = rg.linear_act_f8(x, w1, bias=b1, act="silu", sync=False)
+        y, _ = rg.linear_act_f8(h, w2, residual=x, sync=False)
+        z, _ = rg.linear_f8(y, w3, sync=False)
+        return rg.expert_linear_f8(z, we, off, sync=False)[0]
+
+    return (w1, b1, w2, w3, we), out
+
+
+def test_capture_beside_a_living_graph_of_a_side_stream(rg):  # noqa: F811
+    """Warm-up on a side stream, whose last output and loss stay variables, then the capture on a stream of its own."""
+    leaves, out = layers(rg, 1)
+    want = torch.autograd.grad(out().float().square().mean(), leaves)
+    side, own = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            for t in leaves:
+                t.grad = None
+            y = out()
+            loss = y.float().square().mean()
+            loss.backward()
+    torch.cuda.synchronize()
+    for t in leaves:
+        t.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=own):
+        out().float().square().mean().backward()
+    for t in leaves:
+        t.grad.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.isfinite(loss.detach()) and all(torch.equal(t.grad, g) for t, g in zip(leaves, want))
+
+
+def test_captured_forward_pass_with_gradients_enabled(rg):  # noqa: F811
+    """Nothing is accumulated: a living graph of the default stream is no reason to refuse it."""
+    _, out = layers(rg, 20)
+    alive = out()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        y = out()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert y.requires_grad and torch.equal(y, alive)
+
+
+@pytest.mark.parametrize("on_default", [False, True])
+def test_capture_with_a_node_that_is_held_for_good(rg, on_default):  # noqa: F811
+    """As data-parallel wrappers hold them: the stream on which the layers first met the leaf decides."""
+    leaves, out = layers(rg, 40)
+    want = torch.autograd.grad(out().float().square().mean(), leaves)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(torch.cuda.default_stream() if on_default else side):
+        held = [torch.autograd.graph.get_gradient_edge(t).node for t in leaves]
+        out().float().square().mean().backward()
+    torch.cuda.synchronize()
+    for t in leaves:
+        t.grad = None
+
+    def capture():
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out().float().square().mean().backward()
+        return graph
+
+    if on_default:
+        for _ in range(2):
+            with pytest.raises(RuntimeError, match="default stream"):
+                capture()
+        torch.cuda.synchronize()
+        del held
+    graph = capture()
+    for t in leaves:
+        t.grad.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(t.grad, g) for t, g in zip(leaves, want))
