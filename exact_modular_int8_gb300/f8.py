@@ -64,14 +64,16 @@ _STREAM = "resgemm_stream"
 _AccumulateGrad = torch._C._functions.AccumulateGrad
 
 
-def _note_stream(*tensors):
-    """To be called before a differentiable call, its result kept until that has been made: notes at each leaf's
-    accumulation node the stream on which these layers first met it, for _check_capture."""
-    nodes = [torch.autograd.graph.get_gradient_edge(t).node for t in tensors
-             if t is not None and t.requires_grad and t.is_leaf and t.is_cuda]
-    for n in nodes:  # a node lives as long as the graphs that hold its leaf
-        n.metadata.setdefault(_STREAM, torch._C._cuda_getCurrentRawStream(n.variable.get_device()))
-    return nodes
+def _note_stream(Y):
+    """A differentiable call's result, after noting at each leaf's accumulation node the stream on which these layers
+    first met it, for _check_capture.  (Read off the result: 3 us of linear_f8's 35 on the host; by way of the leaves, 25.)"""
+    stream = None
+    for n, _ in Y.grad_fn.next_functions:
+        if isinstance(n, _AccumulateGrad) and Y.is_cuda:  # lives as long as the graphs that hold its leaf
+            if stream is None:
+                stream = torch._C._cuda_getCurrentRawStream(Y.get_device())
+            n.metadata.setdefault(_STREAM, stream)
+    return Y
 
 
 def _check_capture(where: str, ctx):
@@ -358,8 +360,7 @@ def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True, ws: torch.Ten
     linear_f8_backward for Y, with W's gradient in W's dtype."""
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
         saved = []
-        nodes = _note_stream(X, W)  # noqa: F841 (kept until the call has been made)
-        return _LinearGrad.apply(X, W, sync, ws, saved), tuple(saved)
+        return _note_stream(_LinearGrad.apply(X, W, sync, ws, saved)), tuple(saved)
     if X.is_cuda and ws is None:
         r = _native().linear(X, W, RG_FLAG_SYNC if sync else 0)
         if r is not None:

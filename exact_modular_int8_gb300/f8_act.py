@@ -142,8 +142,7 @@ def linear_act_f8(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = 
     gradient autograd calls linear_act_f8_backward for Y."""
     if _differentiable(X, W, X, W, bias, residual):
         saved = []
-        nodes = _note_stream(X, W, bias, residual)  # noqa: F841 (kept until the call has been made)
-        return _LinearActGrad.apply(X, W, bias, residual, act, sync, ws, saved), tuple(saved)
+        return _note_stream(_LinearActGrad.apply(X, W, bias, residual, act, sync, ws, saved)), tuple(saved)
     where = "linear_act_f8"
     a = _act(where, act)
     if ws is None and X.is_cuda:

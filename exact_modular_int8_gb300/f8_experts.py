@@ -158,8 +158,7 @@ def expert_linear_f8(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, sy
     expert_linear_f8_backward for Y, with W's gradient in W's dtype."""
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
         saved = []
-        nodes = _note_stream(X, W)  # noqa: F841 (kept until the call has been made)
-        return _ExpertGrad.apply(X, W, offsets, sync, ws, saved), tuple(saved)
+        return _note_stream(_ExpertGrad.apply(X, W, offsets, sync, ws, saved)), tuple(saved)
     if X.is_cuda and ws is None:
         r = _native().expert(X, W, offsets, RG_FLAG_SYNC if sync else 0)
         if r is not None:
