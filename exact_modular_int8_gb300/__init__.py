@@ -55,6 +55,8 @@ RG_FLAG_TRANS_B = 4
 RG_FLAG_TILE_B = 8
 RG_FLAG_OFFSETS64 = 16
 RG_FLAG_KEEP_REST = 32
+RG_FLAG_NO_DX = 64
+RG_FLAG_NO_DW = 128
 RG_TYPE_F32, RG_TYPE_F16, RG_TYPE_BF16 = 0, 1, 2
 RG_F8_ROWS, RG_F8_COLUMNS, RG_F8_BOTH, RG_F8_TILES = 0, 1, 2, 3
 RG_ACT_NONE, RG_ACT_RELU, RG_ACT_SILU, RG_ACT_GELU, RG_ACT_GELU_TANH = 0, 1, 2, 3, 4

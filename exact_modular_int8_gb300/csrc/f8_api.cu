@@ -24,12 +24,16 @@ bool good_moe(long long T, long long H, long long I, long long E, long long top_
          top_k <= E && top_k <= RG_MOE_MAX_TOP_K;
 }
 
+int reset_status(DevPlan* plan, cudaStream_t st) {
+  return cudaMemsetAsync(plan, 0, sizeof(DevPlan), st) == cudaSuccess ? RG_OK : RG_ERR_CUDA;
+}
+
 // C = A B (an empty sum where K is 0) for operands that have been checked;
 // the kernels clear the status themselves.
 int product(const F8GemmArgs& a, DevPlan* plan, cudaStream_t st) {
   const size_t es = a.out_type == RG_TYPE_F32 ? 4 : 2;
   if (!(a.M && a.N && a.K)) {  // (with an epilogue K is at least 1)
-    if (!a.keep_status && cudaMemsetAsync(plan, 0, sizeof(DevPlan), st) != cudaSuccess) return RG_ERR_CUDA;
+    if (!a.keep_status && reset_status(plan, st)) return RG_ERR_CUDA;
     if (a.M && a.N && cudaMemset2DAsync(a.C, (size_t)a.ldc * es, 0, (size_t)a.N * es, (size_t)a.M, st) != cudaSuccess)
       return RG_ERR_CUDA;
     return RG_OK;
@@ -92,6 +96,14 @@ bool good_linear(long long M, long long N, long long K) {
          blocks128(N) * blocks128(K) <= INT_MAX / 8;
 }
 
+// The gradients that a backward call computes, and the form in which they need the
+// output's: along its rows for the input's, along its columns for the weights'.
+struct Wanted {
+  bool dx, dw;
+  explicit Wanted(unsigned flags) : dx(!(flags & RG_FLAG_NO_DX)), dw(!(flags & RG_FLAG_NO_DW)) {}
+  int form() const { return dx && dw ? RG_F8_BOTH : dx ? RG_F8_ROWS : RG_F8_COLUMNS; }
+};
+
 bool good_act(int act) { return act >= RG_ACT_NONE && act <= RG_ACT_GELU_TANH; }
 size_t type_bytes(int t) { return t == RG_TYPE_F32 ? 4 : 2; }
 
@@ -147,10 +159,7 @@ F8Groups groups(const void* offsets, long long E, unsigned flags, bool by_blocks
   return F8Groups{offsets, (flags & RG_FLAG_OFFSETS64) != 0, E, (flags & RG_FLAG_KEEP_REST) == 0, by_blocks};
 }
 int grouped(const F8GemmArgs& a, const F8Groups& g, DevPlan* plan, cudaStream_t st) {
-  if (!(a.M && a.N)) {
-    if (!a.keep_status && cudaMemsetAsync(plan, 0, sizeof(DevPlan), st) != cudaSuccess) return RG_ERR_CUDA;
-    return RG_OK;
-  }
+  if (!(a.M && a.N)) return a.keep_status ? RG_OK : reset_status(plan, st);
   return launch_f8_grouped(a, g, plan, st, take_fault(), wait_limit_ns()) == cudaSuccess ? RG_OK : RG_ERR_CUDA;
 }
 // Rows in groups: also the blocks along the columns.
@@ -261,20 +270,24 @@ int linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* sa
       !good_type(dy_type) || !good_type(dw_type) || !good_linear(M, N, K))
     return RG_ERR_ARG;
   if (ws_bytes < linear_f8_ws_bytes(M, N, K) || saved_bytes < linear_f8_saved_bytes(M, N, K)) return RG_ERR_WORKSPACE;
-  if ((M && N && (!dY || lddy < N)) || (M && K && !dX) || (N && K && !dW)) return RG_ERR_ARG;
+  const Wanted want(flags);
+  if ((M && N && (!dY || lddy < N)) || (want.dx && M && K && !dX) || (want.dw && N && K && !dW)) return RG_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const WorkspaceTurn turn(ws);
   const Saved v = carve_saved(static_cast<uint8_t*>(const_cast<void*>(saved)), M, N, K);
   DevPlan* plan = static_cast<DevPlan*>(ws);
   Carver c{static_cast<uint8_t*>(ws) + kCallBlockBytes};
   const Quantised d = carve(c, M, N, M), dt = carve(c, N, M, N);
-  int rc = quantise(QuantArgs{dY, lddy, M, N, d.q, d.ld, d.s, dt.q, dt.ld, dt.s}, dy_type,
-                    RG_F8_BOTH, st);
-  if (!rc)  // dX [M][K] = dY [M][N] W [N][K]
+  if (!want.dx && !want.dw) {
+    const int rc = reset_status(plan, st);
+    return rc ? rc : finish_call(ws, st, flags);
+  }
+  int rc = quantise(quant_args(dY, lddy, M, N, d, dt), dy_type, want.form(), st);
+  if (!rc && want.dx)  // dX [M][K] = dY [M][N] W [N][K]
     rc = product(gemm_args(d.q, d.ld, d.s, v.w.q, v.w.ld, v.w.s, dX, dy_type, K, M, K, N, false, true), plan, st);
-  if (!rc) {  // dW [N][K] = dY^T [N][M] (X^T [K][M])^T
+  if (!rc && want.dw) {  // dW [N][K] = dY^T [N][M] (X^T [K][M])^T
     F8GemmArgs a = gemm_args(dt.q, dt.ld, dt.s, v.xt.q, v.xt.ld, v.xt.s, dW, dw_type, K, N, K, M, true, false);
-    a.keep_status = true;
+    a.keep_status = want.dx;
     rc = product(a, plan, st);
   }
   return rc ? rc : finish_call(ws, st, flags);
@@ -353,7 +366,8 @@ int linear_act_f8_backward(const void* dY, int x_type, int64_t lddy, const void*
     return RG_ERR_ARG;
   if (ws_bytes < linear_act_f8_ws_bytes(M, N, K) || saved_bytes < linear_act_f8_saved_bytes(M, N, K, x_type, act))
     return RG_ERR_WORKSPACE;
-  if ((M && N && (!dY || lddy < N)) || (M && !dX) || (N && !dW)) return RG_ERR_ARG;
+  const Wanted want(flags);
+  if ((M && N && (!dY || lddy < N)) || (want.dx && M && !dX) || (want.dw && N && !dW)) return RG_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const WorkspaceTurn turn(ws);
   const SavedAct v = carve_saved_act(static_cast<uint8_t*>(const_cast<void*>(saved)), M, N, K, x_type, act);
@@ -361,30 +375,36 @@ int linear_act_f8_backward(const void* dY, int x_type, int64_t lddy, const void*
   DevPlan* plan = static_cast<DevPlan*>(ws);
   Carver c{static_cast<uint8_t*>(ws) + kCallBlockBytes};
   const Quantised d = carve(c, M, N, M), dt = carve(c, N, M, N);
+  if (!want.dx && !want.dw && !dbias) {
+    const int rc = reset_status(plan, st);
+    return rc ? rc : finish_call(ws, st, flags);
+  }
   QuantArgs q = quant_args(dY, lddy, M, N, d, dt);
   q.act = act;
   q.P = v.p;
   q.sums = dbias ? reinterpret_cast<float*>(c.take((size_t)blocks128(M) * N * 4)) : nullptr;
   q.out = dbias;
   q.out_type = bias_type;
-  int rc = quantise(q, x_type, RG_F8_BOTH, st);
+  // with a slope or sums there is one form
+  int rc = quantise(q, x_type, act == RG_ACT_NONE && !dbias ? want.form() : RG_F8_BOTH, st);
   const bool sum = dbias && N && (!M || blocks128(M) > kSumCluster);
   if (!rc && sum &&
       launch_sum_rows(q.sums, M ? blocks128(M) : 0, N, dbias, bias_type, st) != cudaSuccess)
     rc = RG_ERR_CUDA;
   // The sums of rows and the two products read what the quantisation wrote, and
   // nothing of each other's.
-  if (!rc) {
+  if (!rc && want.dx) {
     F8GemmArgs a = gemm_args(d.q, d.ld, d.s, w.q, w.ld, w.s, dX, x_type, K, M, K, N, false, true);
     a.late = M && N && sum;
     rc = product(a, plan, st);
   }
-  if (!rc) {
+  if (!rc && want.dw) {
     F8GemmArgs a = gemm_args(dt.q, dt.ld, dt.s, xt.q, xt.ld, xt.s, dW, dw_type, K, N, K, M, true, false);
-    a.keep_status = true;
-    a.late = M && N;
+    a.keep_status = want.dx;
+    a.late = M && N && (sum || want.dx);
     rc = product(a, plan, st);
   }
+  if (!rc && !want.dx && !want.dw) rc = reset_status(plan, st);
   return rc ? rc : finish_call(ws, st, flags);
 }
 
@@ -501,27 +521,34 @@ int expert_linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const v
     return RG_ERR_ARG;
   if (ws_bytes < expert_linear_f8_ws_bytes(T, N, K, E) || saved_bytes < expert_linear_f8_saved_bytes(T, N, K, E))
     return RG_ERR_WORKSPACE;
-  if ((T && N && (!dY || lddy < N)) || (T && !dX) || (N && !dW)) return RG_ERR_ARG;
+  const Wanted want(flags);
+  if ((T && N && (!dY || lddy < N)) || (want.dx && T && !dX) || (want.dw && N && !dW)) return RG_ERR_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const WorkspaceTurn turn(ws);
   const SavedExperts v = carve_saved_experts(static_cast<uint8_t*>(const_cast<void*>(saved)), T, N, K, E);
   DevPlan* plan = static_cast<DevPlan*>(ws);
   Carver c{static_cast<uint8_t*>(ws) + kCallBlockBytes};
   const Quantised d = carve(c, T, N, T), dt = carve(c, N, 128 * group_blocks(T, E), N);
-  int rc = quantise_groups(quant_args(dY, lddy, T, N, d, dt), dy_type, RG_F8_BOTH, offsets, E, flags, st);
-  if (!rc) {  // dX [T][K] = dY [T][N] W_g [N][K]; nothing to sum without N
+  if (!want.dx && !want.dw) {
+    const int rc = reset_status(plan, st);
+    return rc ? rc : finish_call(ws, st, flags);
+  }
+  const QuantArgs q = quant_args(dY, lddy, T, N, d, dt);
+  int rc = want.dw ? quantise_groups(q, dy_type, want.form(), offsets, E, flags, st)
+                   : quantise(q, dy_type, RG_F8_ROWS, st);  // blocks along the rows' entries know no groups
+  if (!rc && want.dx) {  // dX [T][K] = dY [T][N] W_g [N][K]; nothing to sum without N
     if (N) {
       rc = grouped(gemm_args(d.q, d.ld, d.s, v.w.q, v.w.ld, v.w.s, dX, dy_type, K, T, K, N, false, true),
                    groups(offsets, E, flags & ~RG_FLAG_KEEP_REST, false), plan, st);
-    } else if (cudaMemsetAsync(plan, 0, sizeof(DevPlan), st) != cudaSuccess ||
+    } else if (reset_status(plan, st) ||
                (T && cudaMemsetAsync(dX, 0, (size_t)T * K * type_bytes(dy_type), st) != cudaSuccess)) {
       rc = RG_ERR_CUDA;
     }
   }
-  if (!rc) {  // dW [E][N][K]: per group dY^T X
+  if (!rc && want.dw) {  // dW [E][N][K]: per group dY^T X
     F8GemmArgs a = blocks_args(dt, v.xt, dW, dw_type, N, K, group_blocks(T, E));
-    a.keep_status = true;
-    a.late = T && N;  // beside dX, which it does not read
+    a.keep_status = want.dx;
+    a.late = want.dx && T && N;  // beside dX, which it does not read
     rc = grouped(a, groups(offsets, E, flags, true), plan, st);
   }
   return rc ? rc : finish_call(ws, st, flags);

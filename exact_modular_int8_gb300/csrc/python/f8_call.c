@@ -216,7 +216,11 @@ static PyObject* new_tensor(PyObject* size, PyObject* type, PyObject* device) {
 static PyObject* new_matrix(int64_t m, int64_t k, PyObject* type, PyObject* device) {
   return new_tensor(pair_of(m, k), type, device);
 }
-static void* data_of(PyObject* t) { return (void*)(uintptr_t)call_int(t, s_data_ptr); }
+static void* data_of(PyObject* t) { return t == Py_None ? NULL : (void*)(uintptr_t)call_int(t, s_data_ptr); }
+/* A gradient [m][k], or None where it is not wanted (`no`). */
+static PyObject* new_gradient(unsigned no, int64_t m, int64_t k, PyObject* type, PyObject* device) {
+  return no ? Py_NewRef(Py_None) : new_matrix(m, k, type, device);
+}
 
 /* The stream's cached workspace, at least `need` bytes; none under capture into a graph, whose calls have their own.
  * The tensor is held until after the call (a new reference): while the call runs without the interpreter's lock,
@@ -414,7 +418,7 @@ static PyObject* linear(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return r ? finish(rc, "linear_f8", r) : NULL;
 }
 
-/* backward(dY, saved, M, N, K, dw_dtype, flags) -> (dX, dW); None to decline */
+/* backward(dY, saved, M, N, K, dw_dtype, flags) -> (dX, dW), None for those not wanted; None to decline */
 static PyObject* backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   if (n != 7) return decline();
@@ -437,8 +441,8 @@ static PyObject* backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Py_DECREF(device);
     return decline();
   }
-  PyObject* dX = new_matrix(M, K, types[t], device);
-  PyObject* dW = dX ? new_matrix(N, K, types[tw], device) : NULL;
+  PyObject* dX = new_gradient(flags & RG_FLAG_NO_DX, M, K, types[t], device);
+  PyObject* dW = dX ? new_gradient(flags & RG_FLAG_NO_DW, N, K, types[tw], device) : NULL;
   Py_DECREF(device);
   if (!dW) {
     Py_XDECREF(dX);
@@ -567,8 +571,8 @@ static PyObject* linear_act(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return r ? finish(rc, "linear_act_f8", r) : NULL;
 }
 
-/* linear_act_backward(dY, saved, M, N, K, act, bias dtype or None, dw_dtype, flags) -> (dX, dW, dbias or None); None to
- * decline.  The caller has compared dY's dtype. */
+/* linear_act_backward(dY, saved, M, N, K, act, bias dtype or None, dw_dtype, flags) -> (dX, dW, dbias), None for those not
+ * wanted; None to decline.  The caller has compared dY's dtype. */
 static PyObject* linear_act_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   if (n != 9) return decline();
@@ -590,8 +594,8 @@ static PyObject* linear_act_backward(PyObject* self, PyObject* const* a, Py_ssiz
     Py_DECREF(device);
     return decline();
   }
-  PyObject* dX = new_matrix(M, K, types[t], device);
-  PyObject* dW = dX ? new_matrix(N, K, types[tw], device) : NULL;
+  PyObject* dX = new_gradient(flags & RG_FLAG_NO_DX, M, K, types[t], device);
+  PyObject* dW = dX ? new_gradient(flags & RG_FLAG_NO_DW, N, K, types[tw], device) : NULL;
   PyObject* db = a[6] == Py_None ? Py_NewRef(Py_None) : dW ? new_tensor(PyLong_FromLongLong(N), a[6], device) : NULL;
   Py_DECREF(device);
   if (!dW || !db) {
@@ -601,7 +605,7 @@ static PyObject* linear_act_backward(PyObject* self, PyObject* const* a, Py_ssiz
     Py_DECREF(ws.tensor);
     return NULL;
   }
-  void *dx = data_of(dX), *dw = data_of(dW), *dbp = db == Py_None ? NULL : data_of(db);
+  void *dx = data_of(dX), *dw = data_of(dW), *dbp = data_of(db);
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = lib_linear_act_backward(dY.p, t, dY.ld, s, (size_t)kept_bytes, kind, dx, dw, tw, dbp, tb, M, N, K, flags, ws.p,
@@ -771,7 +775,8 @@ static PyObject* expert(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return r ? finish(rc, "expert_linear_f8", r) : NULL;
 }
 
-/* expert_backward(dY, saved, offsets, T, N, K, E, dw_dtype, flags) -> (dX, dW); None to decline */
+/* expert_backward(dY, saved, offsets, T, N, K, E, dw_dtype, flags) -> (dX, dW), None for those not wanted; None to
+ * decline */
 static PyObject* expert_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   if (n != 9) return decline();
@@ -796,8 +801,8 @@ static PyObject* expert_backward(PyObject* self, PyObject* const* a, Py_ssize_t 
     Py_DECREF(device);
     return decline();
   }
-  PyObject* dX = new_matrix(T, K, types[t], device);
-  PyObject* dW = dX ? new_stack(E, N, K, types[tw], device) : NULL;
+  PyObject* dX = new_gradient(flags & RG_FLAG_NO_DX, T, K, types[t], device);
+  PyObject* dW = !dX ? NULL : flags & RG_FLAG_NO_DW ? Py_NewRef(Py_None) : new_stack(E, N, K, types[tw], device);
   Py_DECREF(device);
   if (!dW) {
     Py_XDECREF(dX);

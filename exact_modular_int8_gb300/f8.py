@@ -21,9 +21,9 @@ import os
 
 import torch
 
-from . import (LIB_PATH, RG_ERR_ARG, RG_ERR_RANGE, RG_F8_BOTH, RG_F8_COLUMNS, RG_F8_ROWS, RG_F8_TILES,
-               RG_FLAG_OFFSETS64, RG_FLAG_SYNC, RG_FLAG_TILE_B, RG_FLAG_TRANS_B, RG_TYPE_BF16, RG_TYPE_F16, RG_TYPE_F32, ResGemmError, _check, _output,
-               _ws_cache, capturing, library, workspace)
+from . import (LIB_PATH, RG_ERR_ARG, RG_ERR_RANGE, RG_F8_BOTH, RG_F8_COLUMNS, RG_F8_ROWS, RG_F8_TILES, RG_FLAG_NO_DW,
+               RG_FLAG_NO_DX, RG_FLAG_OFFSETS64, RG_FLAG_SYNC, RG_FLAG_TILE_B, RG_FLAG_TRANS_B, RG_TYPE_BF16, RG_TYPE_F16,
+               RG_TYPE_F32, ResGemmError, _check, _output, _ws_cache, capturing, library, workspace)
 
 BLOCK = 128
 F8 = torch.float8_e4m3fn
@@ -51,8 +51,8 @@ def _native():
                    lib.expert_linear_f8_backward, lib.expert_linear_f8_saved_bytes, lib.expert_linear_f8_ws_bytes,
                    lib.quantize_grouped_f8)
         m.setup(tuple(address(f) for f in entries), (torch.float32, torch.float16, torch.bfloat16), F8, torch.uint8,
-                (torch.int32, torch.int64), torch.empty, torch.empty_strided, torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, _ws_cache,
-                _check)
+                (torch.int32, torch.int64), torch.empty, torch.empty_strided, torch._C._cuda_getCurrentRawStream,
+                torch._C._cuda_getDevice, _ws_cache, _check)
         _call = m
     return _call
 
@@ -66,7 +66,8 @@ _AccumulateGrad = torch._C._functions.AccumulateGrad
 
 def _note_stream(Y):
     """A differentiable call's result, after noting at each leaf's accumulation node the stream on which these layers
-    first met it, for _check_capture.  (Read off the result: 3 us of linear_f8's 35 on the host; by way of the leaves, 25.)"""
+    first met it, for _check_capture.  (Read off the result: 3 us of linear_f8's 35 on the host; by way of the leaves
+    25.)"""
     stream = None
     for n, _ in Y.grad_fn.next_functions:
         if isinstance(n, _AccumulateGrad) and Y.is_cuda:  # lives as long as the graphs that hold its leaf
@@ -84,9 +85,9 @@ def _check_capture(where: str, ctx):
     if torch._C._cuda_isCurrentStreamCapturing():
         for n, _ in ctx.next_functions:
             if isinstance(n, _AccumulateGrad) and n.metadata.get(_STREAM) == 0:
-                raise RuntimeError(f"{where}: a graph made on the default stream holds a tensor of this captured call and "
-                                   "would accumulate its gradient there: free that graph before the capture, or make it "
-                                   "on another stream")
+                raise RuntimeError(f"{where}: a graph made on the default stream holds a tensor of this captured call "
+                                   "and would accumulate its gradient there: free that graph before the capture, or "
+                                   "make it on another stream")
 
 
 class _LinearGrad(torch.autograd.Function):
@@ -104,7 +105,8 @@ class _LinearGrad(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
         _check_capture("linear_f8", ctx)
-        return (*linear_f8_backward(dY, (*ctx.saved_tensors, *ctx.sizes), *ctx.call), None, None, None)
+        return (*linear_f8_backward(dY, (*ctx.saved_tensors, *ctx.sizes), *ctx.call, *ctx.needs_input_grad[:2]), None,
+                None, None)
 
 
 class _NoGrad(torch.autograd.Function):
@@ -382,13 +384,23 @@ def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True, ws: torch.Ten
     return Y, (kept, M, N, K)
 
 
+def _backward_flags(sync: bool, dx: bool, dw: bool) -> int:
+    return (RG_FLAG_SYNC if sync else 0) | (0 if dx else RG_FLAG_NO_DX) | (0 if dw else RG_FLAG_NO_DW)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 def linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: torch.dtype = torch.float32,
-                       ws: torch.Tensor | None = None):
+                       ws: torch.Tensor | None = None, dx: bool = True, dw: bool = True):
     """(dX, dW) of linear_f8 for the output's gradient dY [M, N]: dX = dY W with dY quantised along N, in dY's
-    dtype, and dW = dY^T X with both quantised along M, in dw_dtype."""
+    dtype, and dW = dY^T X with both quantised along M, in dw_dtype.  With dx or dw false that gradient is not computed,
+    and None."""
     kept, M, N, K = saved
+    flags = _backward_flags(sync, dx, dw)
     if dY.is_cuda and ws is None:
-        r = _native().backward(dY, kept, M, N, K, dw_dtype, RG_FLAG_SYNC if sync else 0)
+        r = _native().backward(dY, kept, M, N, K, dw_dtype, flags)
         if r is not None:
             return r
     t, tw = _TYPES.get(dY.dtype), _TYPES.get(dw_dtype)
@@ -397,12 +409,11 @@ def linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: tor
     idx = _device_index("linear_f8_backward", dY, kept)
     need = _linear_bytes(M, N, K)[1]
     dY, lddy = _rows_of(dY)
-    dX = torch.empty((M, K), dtype=dY.dtype, device=dY.device)
-    dW = torch.empty((N, K), dtype=dw_dtype, device=dY.device)
+    dX = torch.empty((M, K), dtype=dY.dtype, device=dY.device) if dx else None
+    dW = torch.empty((N, K), dtype=dw_dtype, device=dY.device) if dw else None
     w = ws if ws is not None else _scratch(need, idx)
     _launch(idx, "linear_f8_backward", library().linear_f8_backward, dY.data_ptr(), t, lddy, kept.data_ptr(),
-            kept.numel(), dX.data_ptr(), dW.data_ptr(), tw, M, N, K, RG_FLAG_SYNC if sync else 0, w.data_ptr(),
-            w.numel())
+            kept.numel(), _ptr(dX), _ptr(dW), tw, M, N, K, flags, w.data_ptr(), w.numel())
     return dX, dW
 
 

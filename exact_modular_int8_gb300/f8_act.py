@@ -15,8 +15,8 @@ import torch
 
 from . import (RG_ACT_GELU, RG_ACT_GELU_TANH, RG_ACT_NONE, RG_ACT_RELU, RG_ACT_SILU, RG_ERR_ARG, RG_FLAG_SYNC,
                ResGemmError, _output, library)
-from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _check_capture, _device_index, _launch, _native, _no_grad,
-                 _note_stream, _rows_of, _scratch)
+from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _backward_flags, _blocks, _check_capture, _device_index, _launch,
+                 _native, _no_grad, _note_stream, _ptr, _rows_of, _scratch)
 
 _grad_enabled = torch.is_grad_enabled
 _ACTS = {None: RG_ACT_NONE, "relu": RG_ACT_RELU, "silu": RG_ACT_SILU, "gelu": RG_ACT_GELU,
@@ -44,10 +44,6 @@ def _beside(where: str, M: int, N: int, bias, residual, dtype):
             raise ValueError(f"{where}: residual {(M, N)} of the output's dtype expected")
         residual, ldr = _rows_of(residual)
     return bias, tb, residual, ldr
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def _there(*ts):
@@ -130,8 +126,9 @@ class _LinearActGrad(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
         _check_capture("linear_act_f8", ctx)
-        dX, dW, dbias = linear_act_f8_backward(dY, (*ctx.saved_tensors, *ctx.rest), *ctx.call)
-        return dX, dW, dbias, dY if ctx.needs_input_grad[3] else None, None, None, None, None
+        *needs, residual = ctx.needs_input_grad[:4]
+        grads = linear_act_f8_backward(dY, (*ctx.saved_tensors, *ctx.rest), *ctx.call, *needs) if any(needs) else (None,) * 3
+        return *grads, dY if residual else None, None, None, None, None
 
 
 def linear_act_f8(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str | None = None,
@@ -169,28 +166,31 @@ def linear_act_f8(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = 
 
 
 def linear_act_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: torch.dtype = torch.float32,
-                           ws: torch.Tensor | None = None):
+                           ws: torch.Tensor | None = None, dx: bool = True, dw: bool = True, db: bool = True):
     """(dX, dW, dbias) of linear_act_f8 for the output's gradient dY [M, N], in the output's dtype: with d = dY times
     the activation's slope (float32), dX = d W and dW = d^T X, with d quantised along N and along M, dX in dY's dtype,
-    dW in dw_dtype, and dbias = the sum of d's rows in bias's dtype (None without a bias).  The residual's gradient is dY."""
+    dW in dw_dtype, and dbias = the sum of d's rows in bias's dtype (None without a bias).  The residual's gradient is
+    dY.  With dx, dw or db false that gradient is not computed, and None."""
     kept, M, N, K, act, dtype, bias_dtype = saved
     where = "linear_act_f8_backward"
     t, tw = _TYPES.get(dY.dtype), _TYPES.get(dw_dtype)
     if dY.dtype != dtype or tw is None or dY.shape != (M, N):
         raise ValueError(f"{where}: dY with the output's shape and dtype expected")
     a = _act(where, act)
+    if not db:
+        bias_dtype = None
+    flags = _backward_flags(sync, dx, dw)
     if ws is None and dY.is_cuda:
-        r = _native().linear_act_backward(dY, kept, M, N, K, a, bias_dtype, dw_dtype, RG_FLAG_SYNC if sync else 0)
+        r = _native().linear_act_backward(dY, kept, M, N, K, a, bias_dtype, dw_dtype, flags)
         if r is not None:
             return r
     idx = _device_index(where, dY, kept)
     need = _linear_act_bytes(M, N, K, t, a)[1]
     dY, lddy = _rows_of(dY)
-    dX = torch.empty((M, K), dtype=dtype, device=dY.device)
-    dW = torch.empty((N, K), dtype=dw_dtype, device=dY.device)
+    dX = torch.empty((M, K), dtype=dtype, device=dY.device) if dx else None
+    dW = torch.empty((N, K), dtype=dw_dtype, device=dY.device) if dw else None
     dbias = None if bias_dtype is None else torch.empty(N, dtype=bias_dtype, device=dY.device)
     w = ws if ws is not None else _scratch(need, idx)
     _launch(idx, where, library().linear_act_f8_backward, dY.data_ptr(), t, lddy, kept.data_ptr(), kept.numel(), a,
-            dX.data_ptr(), dW.data_ptr(), tw, _ptr(dbias), _TYPES.get(bias_dtype, 0), M, N, K,
-            RG_FLAG_SYNC if sync else 0, w.data_ptr(), w.numel())
+            _ptr(dX), _ptr(dW), tw, _ptr(dbias), _TYPES.get(bias_dtype, 0), M, N, K, flags, w.data_ptr(), w.numel())
     return dX, dW, dbias

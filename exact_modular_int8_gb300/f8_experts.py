@@ -17,8 +17,8 @@ import torch
 
 from . import (RG_ERR_ARG, RG_FLAG_KEEP_REST, RG_FLAG_OFFSETS64, RG_FLAG_SYNC, RG_FLAG_TRANS_B, ResGemmError, _output,
                library)
-from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _blocks, _check_capture, _device_index, _groups, _launch, _native,
-                 _no_grad, _note_stream, _rows_of, _scratch, _stack_stride)
+from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _backward_flags, _blocks, _check_capture, _device_index, _groups,
+                 _launch, _native, _no_grad, _note_stream, _ptr, _rows_of, _scratch, _stack_stride)
 
 
 def _aligned_stack(q: torch.Tensor):
@@ -147,7 +147,8 @@ class _ExpertGrad(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
         _check_capture("expert_linear_f8", ctx)
-        return (*expert_linear_f8_backward(dY, (*ctx.saved_tensors, *ctx.sizes), *ctx.call), None, None, None, None)
+        return (*expert_linear_f8_backward(dY, (*ctx.saved_tensors, *ctx.sizes), *ctx.call, *ctx.needs_input_grad[:2]),
+                None, None, None, None)
 
 
 def expert_linear_f8(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, sync: bool = True,
@@ -185,13 +186,14 @@ def expert_linear_f8(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, sy
 
 
 def expert_linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: torch.dtype = torch.float32,
-                              ws: torch.Tensor | None = None):
+                              ws: torch.Tensor | None = None, dx: bool = True, dw: bool = True):
     """(dX, dW) of expert_linear_f8 for the output's gradient dY [T, N]: dX = dY W[g] with dY quantised along N, in dY's
     dtype, 0 behind the last group, and dW [E, N, K] = dY^T X over each group's rows, both quantised along them, in
-    dw_dtype."""
+    dw_dtype.  With dx or dw false that gradient is not computed, and None."""
     kept, offsets, T, N, K, E = saved
+    flags = _backward_flags(sync, dx, dw)
     if dY.is_cuda and ws is None:
-        r = _native().expert_backward(dY, kept, offsets, T, N, K, E, dw_dtype, RG_FLAG_SYNC if sync else 0)
+        r = _native().expert_backward(dY, kept, offsets, T, N, K, E, dw_dtype, flags)
         if r is not None:
             return r
     where = "expert_linear_f8_backward"
@@ -199,13 +201,12 @@ def expert_linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dty
     if t is None or tw is None or dY.shape != (T, N):
         raise ValueError(f"{where}: dY with the output's shape, float32, float16 or bfloat16, expected")
     idx = _device_index(where, dY, kept, offsets)
-    offsets, flags = _groups(where, offsets, E)
+    offsets, wide = _groups(where, offsets, E)
     need = _expert_bytes(T, N, K, E)[1]
     dY, lddy = _rows_of(dY)
-    dX = torch.empty((T, K), dtype=dY.dtype, device=dY.device)
-    dW = torch.empty((E, N, K), dtype=dw_dtype, device=dY.device)
+    dX = torch.empty((T, K), dtype=dY.dtype, device=dY.device) if dx else None
+    dW = torch.empty((E, N, K), dtype=dw_dtype, device=dY.device) if dw else None
     w = ws if ws is not None else _scratch(need, idx)
     _launch(idx, where, library().expert_linear_f8_backward, dY.data_ptr(), t, lddy, kept.data_ptr(), kept.numel(),
-            offsets.data_ptr(), E, dX.data_ptr(), dW.data_ptr(), tw, T, N, K, flags | (RG_FLAG_SYNC if sync else 0),
-            w.data_ptr(), w.numel())
+            offsets.data_ptr(), E, _ptr(dX), _ptr(dW), tw, T, N, K, flags | wide, w.data_ptr(), w.numel())
     return dX, dW

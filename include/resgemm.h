@@ -519,6 +519,8 @@ size_t linear_f8_ws_bytes(int64_t M, int64_t N, int64_t K);
 int linear_f8(const void* X, int x_type, int64_t ldx, const void* W, int w_type, int64_t ldw, void* Y, int64_t M,
               int64_t N, int64_t K, void* saved, size_t saved_bytes, unsigned flags, void* ws, size_t ws_bytes,
               void* stream);
+#define RG_FLAG_NO_DX 64u  /* backward calls: the input's gradient is not wanted, dX is not looked at */
+#define RG_FLAG_NO_DW 128u /* nor the weights' and dW */
 int linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const void* saved, size_t saved_bytes, void* dX,
                        void* dW, int dw_type, int64_t M, int64_t N, int64_t K, unsigned flags, void* ws,
                        size_t ws_bytes, void* stream);

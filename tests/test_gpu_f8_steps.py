@@ -151,3 +151,71 @@ def test_differentiable_calls_read_the_nodes_off_their_results(rg, monkeypatch):
     assert all(t.grad is None for t in leaves)
     y.float().square().mean().backward()
     assert all(torch.isfinite(t.grad).all() for t in leaves)
+
+
+@pytest.mark.parametrize("m", [70, 1100])
+@pytest.mark.parametrize("act", [None, "relu", "gelu"])
+def test_gradients_that_are_not_wanted(rg, act, m):  # noqa: F811
+    """Each subset of the gradients is that part of all of them, by the native and by the general call path."""
+    x, w, b, dy = layer_inputs(m, 136, 264, bf)
+    _, saved = rg.linear_act_f8(x, w, bias=b, act=act)
+    grads = rg.linear_act_f8_backward(dy, saved)
+    ws = torch.empty(rg.library().linear_act_f8_ws_bytes(m, 136, 264), dtype=torch.uint8, device="cuda")
+    for n in range(8):
+        need = (bool(n & 1), bool(n & 2), bool(n & 4))
+        for kw in ({}, {"ws": ws}):
+            got = rg.linear_act_f8_backward(dy, saved, dx=need[0], dw=need[1], db=need[2], **kw)
+            for g, want, wanted in zip(got, grads, need):
+                assert torch.equal(g, want) if wanted else g is None
+    _, saved = rg.linear_act_f8(x, w, act=act)  # without a bias
+    dx, dw, _ = rg.linear_act_f8_backward(dy, saved)
+    assert torch.equal(rg.linear_act_f8_backward(dy, saved, dw=False)[0], dx)
+    assert torch.equal(rg.linear_act_f8_backward(dy, saved, dx=False)[1], dw)
+    if act is None:
+        _, saved = rg.linear_f8(x, w)
+        ws = torch.empty(rg.library().linear_f8_ws_bytes(m, 136, 264), dtype=torch.uint8, device="cuda")
+        for kw in ({}, {"ws": ws}):
+            assert torch.equal(rg.linear_f8_backward(dy, saved, dw=False, **kw)[0], dx)
+            assert torch.equal(rg.linear_f8_backward(dy, saved, dx=False, **kw)[1], dw)
+            assert rg.linear_f8_backward(dy, saved, dx=False, dw=False, **kw) == (None, None)
+
+
+@pytest.mark.parametrize("counts", [(3, 0, 70, 50), (300, 0, 0, 257), (0, 0, 0, 0)])
+def test_expert_gradients_that_are_not_wanted(rg, counts):  # noqa: F811
+    t = sum(counts) + 5
+    x, w, dy = normal((t, 200), 1, 1.0, bf).cuda(), normal((4, 96, 200), 2, 0.1).cuda(), normal((t, 96), 3, 1.0, bf).cuda()
+    off = torch.tensor([0, *torch.tensor(counts).cumsum(0).tolist()], dtype=torch.int32, device="cuda")
+    _, saved = rg.expert_linear_f8(x, w, off)
+    dx, dw = rg.expert_linear_f8_backward(dy, saved)
+    ws = torch.empty(rg.library().expert_linear_f8_ws_bytes(t, 96, 200, 4), dtype=torch.uint8, device="cuda")
+    for kw in ({}, {"ws": ws}):
+        got = rg.expert_linear_f8_backward(dy, saved, dw=False, **kw)
+        assert torch.equal(got[0], dx) and got[1] is None
+        got = rg.expert_linear_f8_backward(dy, saved, dx=False, **kw)
+        assert got[0] is None and torch.equal(got[1], dw)
+        assert rg.expert_linear_f8_backward(dy, saved, dx=False, dw=False, **kw) == (None, None)
+    kept, _, *rest = saved
+    bad = torch.tensor([0, 5, 4, 4, 4], dtype=torch.int32, device="cuda")
+    for kw in ({"dx": False}, {"dw": False}):  # each product reports
+        with pytest.raises(rg.ResGemmError) as err:
+            rg.expert_linear_f8_backward(dy, (kept, bad, *rest), **kw)
+        assert err.value.code == rg.RG_ERR_ARG
+
+
+def test_frozen_weights_take_no_memory(rg):  # noqa: F811
+    """No gradient of frozen weights is made and dropped."""
+    x, dy = normal((64, 1024), 1, 1.0, bf).cuda().requires_grad_(), normal((64, 1024), 2, 1.0, bf).cuda()
+    we, w = torch.randn((8, 1024, 1024), device="cuda"), torch.randn((1024, 1024), device="cuda")
+    r = normal((64, 1024), 3, 1.0, bf).cuda().requires_grad_()
+    off = torch.arange(0, 65, 8, device="cuda")
+    for call, most in ((lambda: rg.expert_linear_f8(x, we, off)[0], we.numel()), (lambda: rg.linear_f8(x, w)[0], w.numel()),
+                       (lambda: rg.linear_act_f8(x, w, act="silu")[0], w.numel()),
+                       (lambda: rg.linear_act_f8(x.detach(), w, residual=r)[0], x.numel())):
+        for _ in range(2):  # the workspace first
+            y = call()
+            torch.cuda.synchronize()
+            before = torch.cuda.memory_allocated()
+            torch.cuda.reset_peak_memory_stats()
+            y.backward(dy)
+            assert torch.cuda.max_memory_allocated() - before < max(most, 1 << 20)
+            x.grad = r.grad = None
