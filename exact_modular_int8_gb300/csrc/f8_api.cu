@@ -136,6 +136,7 @@ bool good_expert_linear(long long T, long long N, long long K, long long E) {
          E * K <= kMaxDim;
 }
 struct SavedExperts {
+  long long* offsets;  // [E + 1]
   Quantised xt, w;
   size_t bytes;
 };
@@ -150,6 +151,7 @@ Quantised carve_stack(Carver& c, long long count, long long rows, long long cols
 SavedExperts carve_saved_experts(uint8_t* base, long long T, long long N, long long K, long long E) {
   Carver c{base};
   SavedExperts v;
+  v.offsets = reinterpret_cast<long long*>(c.take((size_t)(E + 1) * 8));
   v.xt = carve(c, K, 128 * group_blocks(T, E), K);
   v.w = carve_stack(c, E, N, K);
   v.bytes = c.off;
@@ -500,7 +502,9 @@ int expert_linear_f8(const void* X, int x_type, int64_t ldx, const void* W, int 
   const SavedExperts v = carve_saved_experts(static_cast<uint8_t*>(saved), T, N, K, E);
   Carver c{static_cast<uint8_t*>(ws) + kCallBlockBytes};
   const Quantised x = carve(c, T, K, T);
-  int rc = quantise_groups(quant_args(X, ldx, T, K, x, v.xt), x_type, RG_F8_BOTH, offsets, E, flags, st);
+  QuantArgs qx = quant_args(X, ldx, T, K, x, v.xt);
+  qx.kept_offsets = v.offsets;
+  int rc = quantise_groups(qx, x_type, RG_F8_BOTH, offsets, E, flags, st);
   if (!rc) {  // beside X's quantisation
     QuantArgs q = quant_args(W, ldw, N, K, v.w, Quantised{});
     q.late = true;

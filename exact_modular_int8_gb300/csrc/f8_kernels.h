@@ -33,6 +33,7 @@ struct QuantArgs {
   // columns, both: rows in groups (F8Groups), QT [K][128 blocks], ST [K][blocks]
   const void* offsets = nullptr;
   int wide = 0, E = 0;
+  long long* kept_offsets = nullptr;  // a copy of them, [E + 1]
   long long blocks = 0;
   // both: X times the slope of the activation act at P [M][K] (X's type)
   int act = RG_ACT_NONE;

@@ -252,6 +252,8 @@ __device__ __forceinline__ RowBlock find_block(const QuantArgs& a, long long i) 
   auto offset = [&](int g) {
     return a.wide ? static_cast<const long long*>(a.offsets)[g] : (long long)static_cast<const int*>(a.offsets)[g];
   };
+  if (a.kept_offsets && blockIdx.x == 0)
+    for (int g = (int)threadIdx.x; g <= a.E; g += (int)blockDim.x) a.kept_offsets[g] = offset(g);
   int before = 0;  // groups, with the rest as the last, that start at or before slot i
   for (int g0 = 0; g0 <= a.E; g0 += blockDim.x) {
     const int g = g0 + (int)threadIdx.x;

@@ -735,7 +735,7 @@ static PyObject* sums(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return finish(rc, "grouped_wgrad_f8", C);
 }
 
-/* expert(X, W, offsets, flags) -> (Y, (saved, offsets, T, N, K, E)); None to decline */
+/* expert(X, W, offsets, flags) -> (Y, (saved, None, T, N, K, E)); None to decline */
 static PyObject* expert(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   if (n != 4) return decline();
@@ -771,12 +771,12 @@ static PyObject* expert(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   rc = lib_expert(X.p, tx, X.ld, W.p, tw, W.ld, off, E, y, T, N, K, s, kept_bytes, flags, ws.p, (size_t)ws.bytes, stream);
   Py_END_ALLOW_THREADS
   Py_DECREF(ws.tensor);
-  PyObject* r = Py_BuildValue("(N(NOLLLL))", Y, kept, a[2], (long long)T, (long long)N, (long long)K, (long long)E);
+  PyObject* r = Py_BuildValue("(N(NOLLLL))", Y, kept, Py_None, (long long)T, (long long)N, (long long)K, (long long)E);
   return r ? finish(rc, "expert_linear_f8", r) : NULL;
 }
 
 /* expert_backward(dY, saved, offsets, T, N, K, E, dw_dtype, flags) -> (dX, dW), None for those not wanted; None to
- * decline */
+ * decline.  offsets may be None: the copy with which `saved` begins. */
 static PyObject* expert_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   if (n != 9) return decline();
@@ -788,11 +788,15 @@ static PyObject* expert_backward(PyObject* self, PyObject* const* a, Py_ssize_t 
   matrix dY;
   if (PyErr_Occurred() || tw == 3 || !place(a[0], &dev, &stream)) return decline();
   const int t = real_of(a[0], -1, &dY);
-  if (t < 0 || dY.m != T || dY.k != N || E < 1 || call_int(a[1], s_get_device) != dev ||
-      !offsets_of(a[2], dev, &E, &off, &flags))
-    return decline();
+  if (t < 0 || dY.m != T || dY.k != N || E < 1 || call_int(a[1], s_get_device) != dev) return decline();
   const int64_t kept_bytes = call_int(a[1], s_numel);
   void* s = data_of(a[1]);
+  if (a[2] == Py_None) {
+    off = s;
+    flags |= RG_FLAG_OFFSETS64;
+  } else if (!offsets_of(a[2], dev, &E, &off, &flags)) {
+    return decline();
+  }
   const size_t need = lib_expert_ws_bytes(T, N, K, E);
   PyObject* device = PyErr_Occurred() || !need ? NULL : PyObject_GetAttr(a[0], s_device);
   if (!device) return decline();

@@ -137,17 +137,17 @@ class _ExpertGrad(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, X, W, offsets, sync, ws, saved):
-        Y, (kept, at, *ctx.sizes) = expert_linear_f8(X, W, offsets, sync, ws)
-        ctx.save_for_backward(kept, at)
+        Y, (kept, *ctx.rest) = expert_linear_f8(X, W, offsets, sync, ws)
+        ctx.save_for_backward(kept, offsets)  # offsets: so that autograd notices where they change
         ctx.call = sync, W.dtype, ws
-        saved.extend((kept, at, *ctx.sizes))
+        saved.extend((kept, *ctx.rest))
         return Y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
         _check_capture("expert_linear_f8", ctx)
-        return (*expert_linear_f8_backward(dY, (*ctx.saved_tensors, *ctx.sizes), *ctx.call, *ctx.needs_input_grad[:2]),
+        return (*expert_linear_f8_backward(dY, (ctx.saved_tensors[0], *ctx.rest), *ctx.call, *ctx.needs_input_grad[:2]),
                 None, None, None, None)
 
 
@@ -155,8 +155,9 @@ def expert_linear_f8(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, sy
                      ws: torch.Tensor | None = None):
     """(Y, saved): linear_f8 by group: Y [T, N] = X W[g]^T for each group's rows of X [T, K], weights W [E, N, K], in X's
     dtype (both float32, float16 or bfloat16); rows behind the last group are 0.  `saved` is what
-    expert_linear_f8_backward needs, the offsets among it.  Where X or W requires a gradient autograd calls
-    expert_linear_f8_backward for Y, with W's gradient in W's dtype."""
+    expert_linear_f8_backward needs, a copy of the offsets among it: the caller's own may be rewritten for another call
+    in between (not under autograd, whose backward pass refuses tensors that have changed).  Where X or W requires a
+    gradient autograd calls expert_linear_f8_backward for Y, with W's gradient in W's dtype."""
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
         saved = []
         return _note_stream(_ExpertGrad.apply(X, W, offsets, sync, ws, saved)), tuple(saved)
@@ -182,7 +183,7 @@ def expert_linear_f8(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, sy
     _launch(idx, where, library().expert_linear_f8, X.data_ptr(), tx, ldx, W.data_ptr(), tw, ldw, offsets.data_ptr(), E,
             Y.data_ptr(), T, N, K, kept.data_ptr(), nsaved, flags | (RG_FLAG_SYNC if sync else 0), w.data_ptr(),
             w.numel())
-    return Y, (kept, offsets, T, N, K, E)
+    return Y, (kept, None, T, N, K, E)  # None: the copy of the offsets with which the buffer begins
 
 
 def expert_linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dtype: torch.dtype = torch.float32,
@@ -200,8 +201,10 @@ def expert_linear_f8_backward(dY: torch.Tensor, saved, sync: bool = True, dw_dty
     t, tw = _TYPES.get(dY.dtype), _TYPES.get(dw_dtype)
     if t is None or tw is None or dY.shape != (T, N):
         raise ValueError(f"{where}: dY with the output's shape, float32, float16 or bfloat16, expected")
-    idx = _device_index(where, dY, kept, offsets)
-    offsets, wide = _groups(where, offsets, E)
+    if offsets is None:
+        idx, offsets, wide = _device_index(where, dY, kept), kept, RG_FLAG_OFFSETS64
+    else:
+        idx, (offsets, wide) = _device_index(where, dY, kept, offsets), _groups(where, offsets, E)
     need = _expert_bytes(T, N, K, E)[1]
     dY, lddy = _rows_of(dY)
     dX = torch.empty((T, K), dtype=dY.dtype, device=dY.device) if dx else None

@@ -609,7 +609,9 @@ int grouped_wgrad_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8
  *   backward  dX [T][K] (dy_type) = dY W_g, dW [E][N][K] (dw_type): per group dY^T X
  * Each is what quantize_grouped_f8, quantize_f8, grouped_gemm_f8 and
  * grouped_wgrad_f8 give one after the other, to the bit.  Rows behind the last
- * group are 0 in Y and dX.  The backward call takes the forward call's offsets.
+ * group are 0 in Y and dX.  The backward call takes the forward call's offsets, as
+ * they were then: `saved` begins with a copy, [E + 1] 64-bit integers, which may be
+ * given as its `offsets` (with RG_FLAG_OFFSETS64) where the caller's own change.
  * Sizes of `saved` and ws from the two functions, which return 0 for what the
  * calls refuse.  Errors: as grouped_gemm_f8's.
  */

@@ -219,3 +219,38 @@ def test_frozen_weights_take_no_memory(rg):  # noqa: F811
             y.backward(dy)
             assert torch.cuda.max_memory_allocated() - before < max(most, 1 << 20)
             x.grad = r.grad = None
+
+
+@pytest.mark.parametrize("kind", [torch.int32, torch.int64])
+@pytest.mark.parametrize("general", [False, True])
+def test_offsets_are_rewritten_between_the_passes(rg, general, kind):  # noqa: F811
+    """One buffer of offsets for several micro-batches: each backward call uses those of its forward call."""
+    first, second = (torch.tensor(o, dtype=kind, device="cuda") for o in ([0, 20, 20, 70], [0, 0, 65, 70]))
+    w = normal((3, 96, 200), 9, 0.1).cuda()
+    ws = torch.empty(rg.library().expert_linear_f8_ws_bytes(70, 96, 200, 3), dtype=torch.uint8, device="cuda")
+    kw = {"ws": ws} if general else {}
+    batches = [(normal((70, 200), i, 1.0, bf).cuda(), normal((70, 96), i + 1, 1.0, bf).cuda()) for i in (1, 3)]
+    want = []
+    for (x, dy), off in zip(batches, (first, second)):
+        y, saved = rg.expert_linear_f8(x, w, off, **kw)
+        want.append((y, *rg.expert_linear_f8_backward(dy, saved, **kw)))
+    buf = first.clone()
+    kept = []
+    for (x, _), off, outs in zip(batches, (first, second), want):
+        buf.copy_(off)
+        y, saved = rg.expert_linear_f8(x, w, buf, sync=False, **kw)
+        assert torch.equal(y, outs[0])
+        kept.append(saved)
+    for (_, dy), saved, outs in reversed(list(zip(batches, kept, want))):
+        assert all(torch.equal(a, b) for a, b in zip(rg.expert_linear_f8_backward(dy, saved, **kw), outs[1:]))
+
+
+def test_offsets_are_kept_without_rows_or_columns(rg):  # noqa: F811
+    """512 groups, and calls that multiply nothing: the copy of the offsets is there all the same."""
+    for t, n, e in ((0, 30, 2), (5, 0, 3), (700, 16, 512)):
+        off = (torch.arange(e + 1, device="cuda") * t // e).int()
+        x, w = normal((t, 40), 1, 1.0, bf).cuda(), torch.ones((e, n, 40), device="cuda")
+        y, saved = rg.expert_linear_f8(x, w, off)
+        want = rg.expert_linear_f8_backward(y, saved)
+        off.fill_(7)
+        assert all(torch.equal(a, b) for a, b in zip(rg.expert_linear_f8_backward(y, saved), want))
