@@ -8,6 +8,7 @@ import torch
 from gpu_util import rg  # noqa: F401
 from test_gpu_f8 import normal
 from test_gpu_f8_act import ACTS, layer_inputs
+from test_gpu_f8_act import test_layer_gradients as check_layer_gradients
 
 pytestmark = pytest.mark.gpu
 bf, f16, f32 = torch.bfloat16, torch.float16, torch.float32
@@ -254,3 +255,11 @@ def test_offsets_are_kept_without_rows_or_columns(rg):  # noqa: F811
         want = rg.expert_linear_f8_backward(y, saved)
         off.fill_(7)
         assert all(torch.equal(a, b) for a, b in zip(rg.expert_linear_f8_backward(y, saved), want))
+
+
+@pytest.mark.parametrize("act", [None, "relu", "silu", "gelu"])
+@pytest.mark.parametrize("m,dtype", [(897, f16), (1000, bf), (1024, bf), (1024, f32), (1025, bf), (1025, f16)])
+def test_sums_on_both_sides_of_a_cluster(rg, m, dtype, act):  # noqa: F811
+    """Up to 1024 rows, eight blocks of 128, the bias's gradient is summed within a cluster, beyond by a kernel of its
+    own, beside which the input gradient's product runs."""
+    check_layer_gradients(rg, m, 264, 136, dtype, act)
