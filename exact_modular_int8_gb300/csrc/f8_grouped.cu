@@ -391,7 +391,10 @@ cudaError_t grouped_device(int dev, GroupedDevice& out) {
 // Which kernel, by the time that each would take: waves of its tiles, of which half
 // a one is lost to each group (but a group has at least one), times what a tile
 // takes.  The few-row kernel's blocks take 0.28 us with a token and 0.44 with 128, the
-// pairs' 0.53, and a tile 0.8 and 2.5 more.  Measured, us, few-row kernel first (groups
+// pairs' 0.53, and a tile 0.8 and 2.5 more.  (Alone a block with a token takes 0.31, as
+// above; either value chooses alike in every row below.)  T is all rows of A, those
+// behind the last group among them, since the offsets are on the device: a few rows in
+// a buffer with room for many go to the pairs.  Measured, us, few-row kernel first (groups
 // of uneven sizes; E x N x K, rows to a group on average):
 //   64 x 2048 x 4096  8: 88 / 137   64: 115 / 139   96: 142 / 154   128: 158 / 156
 //                     256: 276 / 212   1024: 922 / 575

@@ -4,7 +4,8 @@ are made).
 offsets [E + 1] (int32 or int64, on the device) says where each group's rows start: group g holds rows offsets[g] to
 offsets[g + 1] - 1, from offsets[0] = 0 on.  Groups may be empty, and rows may follow the last one.  Nothing here
 reads the offsets on the host: ones that fall, or end past the rows, are a device-side error (ResGemmError, with
-sync=False from status()).
+sync=False from status()).  The kernel of a product is therefore chosen by all rows of the buffer, and spare ones are
+quantised with the others: a buffer not far above what a call holds costs least.
 
 Along the rows, blocks of 128 lie in one group each: group g's start at block offsets[g] // 128 + g, its last one is
 filled up with zeros, and a matrix of T rows has T // 128 + E blocks.  quantize_f8 with offsets lays them out.

@@ -556,7 +556,7 @@ int linear_act_f8_backward(const void* dY, int x_type, int64_t lddy, const void*
  * RG_FLAG_OFFSETS64; it starts at 0 and does not fall, groups may be empty, and
  * rows may follow the last group (a buffer of fixed capacity).  Offsets that do
  * not, or that end past the rows, give RG_ERR_ARG as the call's device status, and
- * no result.  1 <= E <= RG_MOE_MAX_EXPERTS.
+ * no result; a call with an empty result does not check them.  1 <= E <= RG_MOE_MAX_EXPERTS.
  *
  * Along the rows, blocks of 128 lie in one group each: group g's start at block
  * offsets[g] / 128 + g and take what its rows need, its last block filled up with
