@@ -3,12 +3,13 @@
 Every translation unit under csrc/ (.cu, and host-only .cpp) is compiled in parallel and linked into
 ``_build/libresgemm.so`` next to this file.  A unit is rebuilt when it, a
 header it includes, or this script is newer than its object file.
-csrc/python/f8_call.c, the binding's native call path, becomes the extension
-module ``_build/f8_call.so``.
+csrc/python/f8_call.c, the binding's native call path, and f8_grad.cpp, which reads
+torch's autograd nodes, become the extension modules ``_build/f8_call.so`` and ``f8_grad.so``.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -22,7 +23,10 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libresgemm.so")
 CALL_SRC = os.path.join(CSRC, "python", "f8_call.c")
 CALL_LIB = os.path.join(BUILD, "f8_call.so")
+GRAD_SRC = os.path.join(CSRC, "python", "f8_grad.cpp")
+GRAD_LIB = os.path.join(BUILD, "f8_grad.so")
 CC = os.environ.get("CC", "gcc")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -41,16 +45,27 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _build_call():
-    """The Python extension module of csrc/python (no CUDA in it)."""
-    if not _stale(CALL_LIB, [CALL_SRC, os.path.join(ROOT, "include", "resgemm.h"), os.path.abspath(__file__)]):
+def _build_module(src, lib, command, *options):
+    """A Python extension module of csrc/python (no CUDA in it)."""
+    if not _stale(lib, [src, os.path.join(ROOT, "include", "resgemm.h"), os.path.abspath(__file__)]):
         return
-    tmp = CALL_LIB + f".tmp{os.getpid()}"
-    cmd = [CC, "-O2", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_paths()["include"], CALL_SRC, "-o", tmp]
+    tmp = lib + f".tmp{os.getpid()}"
+    cmd = [*command, "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_paths()["include"], src, "-o", tmp, *options]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{CC} failed for {CALL_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALL_LIB)
+        raise RuntimeError(f"{command[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, lib)
+
+
+def _build_call():
+    _build_module(CALL_SRC, CALL_LIB, [CC, "-O2"])
+
+
+def _build_grad():
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    lib = os.path.join(torch, "lib")
+    _build_module(GRAD_SRC, GRAD_LIB, [CXX, "-O1", "-std=c++20"], "-isystem", os.path.join(torch, "include"), "-L", lib,
+                  "-lc10", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}")
 
 
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -71,9 +86,10 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         return obj, r.stdout + r.stderr
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(sources), os.cpu_count() or 1))) as ex:
-        call = ex.submit(_build_call)
+        modules = [ex.submit(f) for f in (_build_call, _build_grad)]
         results = list(ex.map(compile_one, sources))
-        call.result()
+        for m in modules:
+            m.result()
     objs = [o for o, _ in results]
     if verbose or ptxas_info:
         for _, log in results:

@@ -32,17 +32,22 @@ _FORMS = {"rows": RG_F8_ROWS, "columns": RG_F8_COLUMNS, "both": RG_F8_BOTH, "til
 _WS_BYTES = 4096
 
 
+def _extension(name: str):
+    """An extension module beside the library (csrc/python)."""
+    path = os.path.join(os.path.dirname(LIB_PATH), f"{name}.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python -m exact_modular_int8_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, path, loader=loader))
+    loader.exec_module(m)
+    return m
+
+
 def _native():
     """The native call path (csrc/python/f8_call.c), set up once."""
     global _call
     if _call is None:
-        lib = library()
-        path = os.path.join(os.path.dirname(LIB_PATH), "f8_call.so")
-        if not os.path.exists(path):
-            raise ImportError(f"{path} is missing: build it with `python -m exact_modular_int8_gb300.build`")
-        loader = importlib.machinery.ExtensionFileLoader("f8_call", path)
-        m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("f8_call", path, loader=loader))
-        loader.exec_module(m)
+        lib, m = library(), _extension("f8_call")
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
         entries = (lib.quantize_f8, lib.scaled_gemm_f8, lib.linear_f8, lib.linear_f8_backward,
                    lib.linear_f8_saved_bytes, lib.linear_f8_ws_bytes, lib.rg_stream_capturing, lib.scaled_gemm_act_f8,
@@ -60,31 +65,18 @@ def _native():
 _call = None
 
 
-_STREAM = "resgemm_stream"
-_AccumulateGrad = torch._C._functions.AccumulateGrad
-
-
-def _note_stream(Y):
-    """A differentiable call's result, after noting at each leaf's accumulation node the stream on which these layers
-    first met it, for _check_capture.  (Read off the result: 3 us of linear_f8's 35 on the host; by way of the leaves
-    25.)"""
-    stream = None
-    for n, _ in Y.grad_fn.next_functions:
-        if isinstance(n, _AccumulateGrad) and Y.is_cuda:  # lives as long as the graphs that hold its leaf
-            if stream is None:
-                stream = torch._C._cuda_getCurrentRawStream(Y.get_device())
-            n.metadata.setdefault(_STREAM, stream)
-    return Y
+@functools.lru_cache(maxsize=None)
+def _on_default_stream():
+    return _extension("f8_grad").on_default_stream
 
 
 def _check_capture(where: str, ctx):
     """To be called as a backward pass starts: a leaf's gradient is accumulated on the stream where the first graph
     that holds the leaf was made.  Another one takes part in a capture, but the default stream cannot: it would break
-    the capture off (or the process, where nothing catches it).  Refused here where that graph is one of these layers';
-    one of other operators on the leaf itself is not known."""
+    the capture off (or the process, where nothing catches it).  Refused here."""
     if torch._C._cuda_isCurrentStreamCapturing():
         for n, _ in ctx.next_functions:
-            if isinstance(n, _AccumulateGrad) and n.metadata.get(_STREAM) == 0:
+            if isinstance(n, torch._C._functions.AccumulateGrad) and _on_default_stream()(n):
                 raise RuntimeError(f"{where}: a graph made on the default stream holds a tensor of this captured call "
                                    "and would accumulate its gradient there: free that graph before the capture, or "
                                    "make it on another stream")
@@ -362,7 +354,7 @@ def linear_f8(X: torch.Tensor, W: torch.Tensor, sync: bool = True, ws: torch.Ten
     linear_f8_backward for Y, with W's gradient in W's dtype."""
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
         saved = []
-        return _note_stream(_LinearGrad.apply(X, W, sync, ws, saved)), tuple(saved)
+        return _LinearGrad.apply(X, W, sync, ws, saved), tuple(saved)
     if X.is_cuda and ws is None:
         r = _native().linear(X, W, RG_FLAG_SYNC if sync else 0)
         if r is not None:

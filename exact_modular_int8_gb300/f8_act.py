@@ -16,7 +16,7 @@ import torch
 from . import (RG_ACT_GELU, RG_ACT_GELU_TANH, RG_ACT_NONE, RG_ACT_RELU, RG_ACT_SILU, RG_ERR_ARG, RG_FLAG_SYNC,
                ResGemmError, _output, library)
 from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _backward_flags, _blocks, _check_capture, _device_index, _launch,
-                 _native, _no_grad, _note_stream, _ptr, _rows_of, _scratch)
+                 _native, _no_grad, _ptr, _rows_of, _scratch)
 
 _grad_enabled = torch.is_grad_enabled
 _ACTS = {None: RG_ACT_NONE, "relu": RG_ACT_RELU, "silu": RG_ACT_SILU, "gelu": RG_ACT_GELU,
@@ -139,7 +139,7 @@ def linear_act_f8(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = 
     gradient autograd calls linear_act_f8_backward for Y."""
     if _differentiable(X, W, X, W, bias, residual):
         saved = []
-        return _note_stream(_LinearActGrad.apply(X, W, bias, residual, act, sync, ws, saved)), tuple(saved)
+        return _LinearActGrad.apply(X, W, bias, residual, act, sync, ws, saved), tuple(saved)
     where = "linear_act_f8"
     a = _act(where, act)
     if ws is None and X.is_cuda:

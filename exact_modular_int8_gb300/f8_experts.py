@@ -19,7 +19,7 @@ import torch
 from . import (RG_ERR_ARG, RG_FLAG_KEEP_REST, RG_FLAG_OFFSETS64, RG_FLAG_SYNC, RG_FLAG_TRANS_B, ResGemmError, _output,
                library)
 from .f8 import (_TYPES, _WS_BYTES, F8, _aligned_rows, _backward_flags, _blocks, _check_capture, _device_index, _groups,
-                 _launch, _native, _no_grad, _note_stream, _ptr, _rows_of, _scratch, _stack_stride)
+                 _launch, _native, _no_grad, _ptr, _rows_of, _scratch, _stack_stride)
 
 
 def _aligned_stack(q: torch.Tensor):
@@ -161,7 +161,7 @@ def expert_linear_f8(X: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, sy
     gradient autograd calls expert_linear_f8_backward for Y, with W's gradient in W's dtype."""
     if torch.is_grad_enabled() and (X.requires_grad or W.requires_grad):
         saved = []
-        return _note_stream(_ExpertGrad.apply(X, W, offsets, sync, ws, saved)), tuple(saved)
+        return _ExpertGrad.apply(X, W, offsets, sync, ws, saved), tuple(saved)
     if X.is_cuda and ws is None:
         r = _native().expert(X, W, offsets, RG_FLAG_SYNC if sync else 0)
         if r is not None:

@@ -263,3 +263,40 @@ def test_sums_on_both_sides_of_a_cluster(rg, m, dtype, act):  # noqa: F811
     """Up to 1024 rows, eight blocks of 128, the bias's gradient is summed within a cluster, beyond by a kernel of its
     own, beside which the input gradient's product runs."""
     check_layer_gradients(rg, m, 264, 136, dtype, act)
+
+
+def test_capture_while_another_operators_graph_lives(rg):  # noqa: F811
+    """Whoever's graph was the first to hold the leaf: made on the default stream it is refused before anything would be
+    accumulated there, on a side stream it takes part, whatever ran on the default stream since."""
+    w = normal((96, 128), 1, 0.1).cuda().requires_grad_()
+    x, dy = normal((70, 128), 2, 1.0, bf).cuda(), normal((70, 96), 3, 1.0, bf).cuda()
+    step = lambda: rg.linear_f8(x, w, sync=False)[0].backward(dy)  # noqa: E731
+    own, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def capture():
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=own):
+            w.grad = None
+            step()
+        return graph
+
+    step()
+    want = w.grad.clone()
+    alive = (2 * w).sum()
+    with pytest.raises(RuntimeError, match="default stream"):
+        capture()
+    torch.cuda.synchronize()
+    assert torch.isfinite(alive)
+    del alive
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        alive = (2 * w).sum()
+    torch.cuda.current_stream().wait_stream(side)
+    w.grad = None
+    step()
+    torch.cuda.synchronize()
+    graph = capture()
+    w.grad.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.isfinite(alive) and torch.equal(w.grad, want)
