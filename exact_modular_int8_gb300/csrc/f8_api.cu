@@ -157,8 +157,8 @@ SavedExperts carve_saved_experts(uint8_t* base, long long T, long long N, long l
   v.bytes = c.off;
   return v;
 }
-F8Groups groups(const void* offsets, long long E, unsigned flags, bool by_blocks) {
-  return F8Groups{offsets, (flags & RG_FLAG_OFFSETS64) != 0, E, (flags & RG_FLAG_KEEP_REST) == 0, by_blocks};
+F8Groups groups(const void* offsets, long long E, unsigned flags, bool by_blocks, long long rows) {
+  return F8Groups{offsets, (flags & RG_FLAG_OFFSETS64) != 0, E, (flags & RG_FLAG_KEEP_REST) == 0, by_blocks, rows};
 }
 int grouped(const F8GemmArgs& a, const F8Groups& g, DevPlan* plan, cudaStream_t st) {
   if (!(a.M && a.N)) return a.keep_status ? RG_OK : reset_status(plan, st);
@@ -449,7 +449,7 @@ int grouped_gemm_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const WorkspaceTurn turn(ws);
   const int rc = grouped(gemm_args(A, lda, SA, B, ldb, SB, C, c_type, ldc, T, N, K, transb, true),
-                         groups(offsets, E, flags, false), static_cast<DevPlan*>(ws), st);
+                         groups(offsets, E, flags, false, T), static_cast<DevPlan*>(ws), st);
   return rc ? rc : finish_call(ws, st, flags);
 }
 
@@ -469,8 +469,9 @@ int grouped_wgrad_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8
   const WorkspaceTurn turn(ws);
   const Quantised a{const_cast<uint8_t*>(A), const_cast<float*>(SA), lda};
   const Quantised b{const_cast<uint8_t*>(B), const_cast<float*>(SB), ldb};
-  const int rc = grouped(blocks_args(a, b, C, c_type, M, N, blocks), groups(offsets, E, flags, true),
-                         static_cast<DevPlan*>(ws), st);
+  // the most rows that take so many blocks
+  const F8Groups g = groups(offsets, E, flags, true, 128 * (blocks - E) + 127);
+  const int rc = grouped(blocks_args(a, b, C, c_type, M, N, blocks), g, static_cast<DevPlan*>(ws), st);
   return rc ? rc : finish_call(ws, st, flags);
 }
 
@@ -512,7 +513,7 @@ int expert_linear_f8(const void* X, int x_type, int64_t ldx, const void* W, int 
   }
   if (!rc)
     rc = grouped(gemm_args(x.q, x.ld, x.s, v.w.q, v.w.ld, v.w.s, Y, x_type, N, T, N, K, true, true),
-                 groups(offsets, E, flags & ~RG_FLAG_KEEP_REST, false), static_cast<DevPlan*>(ws), st);
+                 groups(offsets, E, flags & ~RG_FLAG_KEEP_REST, false, T), static_cast<DevPlan*>(ws), st);
   return rc ? rc : finish_call(ws, st, flags);
 }
 
@@ -543,7 +544,7 @@ int expert_linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const v
   if (!rc && want.dx) {  // dX [T][K] = dY [T][N] W_g [N][K]; nothing to sum without N
     if (N) {
       rc = grouped(gemm_args(d.q, d.ld, d.s, v.w.q, v.w.ld, v.w.s, dX, dy_type, K, T, K, N, false, true),
-                   groups(offsets, E, flags & ~RG_FLAG_KEEP_REST, false), plan, st);
+                   groups(offsets, E, flags & ~RG_FLAG_KEEP_REST, false, T), plan, st);
     } else if (reset_status(plan, st) ||
                (T && cudaMemsetAsync(dX, 0, (size_t)T * K * type_bytes(dy_type), st) != cudaSuccess)) {
       rc = RG_ERR_CUDA;
@@ -553,7 +554,7 @@ int expert_linear_f8_backward(const void* dY, int dy_type, int64_t lddy, const v
     F8GemmArgs a = blocks_args(dt, v.xt, dW, dw_type, N, K, group_blocks(T, E));
     a.keep_status = want.dx;
     a.late = want.dx && T && N;  // beside dX, which it does not read
-    rc = grouped(a, groups(offsets, E, flags, true), plan, st);
+    rc = grouped(a, groups(offsets, E, flags, true, T), plan, st);
   }
   return rc ? rc : finish_call(ws, st, flags);
 }

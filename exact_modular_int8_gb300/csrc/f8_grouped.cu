@@ -441,7 +441,7 @@ cudaError_t launch_f8_grouped(const F8GemmArgs& a, const F8Groups& g, DevPlan* p
   p.keep_status = a.keep_status;
   p.late = a.late;
   p.wait_ns = wait_ns;
-  p.gr = Groups{g.offsets, g.wide, (int)g.E, g.by_blocks ? p.KB : p.M, g.zero_rest};
+  p.gr = Groups{g.offsets, g.wide, (int)g.E, (int)g.rows, g.zero_rest};
   const bool few = !g.by_blocks && (variant == 1 || (variant == 0 && few_rows_to_a_group(a.M, g.E, a.N, p.KB, gd.sms,
                                                                                          gd.max_pairs)));
   // groups that can have a row, and the rows behind them

@@ -104,6 +104,7 @@ struct F8Groups {
   long long E;
   bool zero_rest;  // rows: write 0 to the rows behind the last group
   bool by_blocks;
+  long long rows;  // offsets end here at the latest
 };
 cudaError_t launch_f8_grouped(const F8GemmArgs& a, const F8Groups& g, DevPlan* plan, cudaStream_t st, int fault,
                               unsigned long long wait_ns);

@@ -32,7 +32,7 @@ struct Groups {
   const void* offsets;  // [E + 1]
   int wide;             // 64-bit offsets
   int E;
-  int limit;      // rows of A; along the contraction: blocks of 128
+  int limit;      // rows
   int zero_rest;  // write 0 to the rows behind the last group
 };
 constexpr int kMaxGroups = RG_MOE_MAX_EXPERTS;
@@ -337,7 +337,7 @@ __device__ __forceinline__ int load_groups(const Groups& gr, GroupTable& tab, in
   for (int i = threadIdx.x; i <= gr.E; i += blockDim.x) {
     const int v = offset_at(gr, i, ok);
     ok = ok && (i ? offset_at(gr, i - 1, ok) <= v : v == 0);
-    if (i == gr.E) ok = ok && (tile_rows ? v <= gr.limit : first_block(v, gr.E) <= gr.limit);
+    if (i == gr.E) ok = ok && v <= gr.limit;
     tab.rows[i] = v;
   }
   if (threadIdx.x == 0) tab.rows[gr.E + 1] = gr.limit;

@@ -597,6 +597,8 @@ int grouped_gemm_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_
  * B's, for operands stored along the rows by group, A [M][lda] with SA [M][blocks]
  * and B [N][ldb] with SB [N][blocks], 128 * blocks columns (RG_F8_COLUMNS of
  * quantize_grouped_f8).  A group without rows gives 0.  E * M is at most 2^30.
+ * The rows are known by their blocks alone: offsets that end past 128 (blocks - E)
+ * + 127 are refused.
  * Errors: RG_ERR_ARG, RG_ERR_WORKSPACE, RG_ERR_CUDA, RG_ERR_TIMEOUT.
  */
 int grouped_wgrad_f8(const uint8_t* A, int64_t lda, const float* SA, const uint8_t* B, int64_t ldb, const float* SB,

@@ -300,3 +300,46 @@ def test_capture_while_another_operators_graph_lives(rg):  # noqa: F811
     graph.replay()
     torch.cuda.synchronize()
     assert torch.isfinite(alive) and torch.equal(w.grad, want)
+
+
+def test_weight_gradients_alone_report_offsets_past_the_rows(rg):  # noqa: F811
+    """Within the last block of 128 rows too, which the blocks alone do not show."""
+    x, w, dy = normal((7, 50), 1, 1.0, bf).cuda(), normal((2, 40, 50), 2, 0.1).cuda(), normal((7, 40), 3, 1.0, bf).cuda()
+    off = torch.tensor([0, 3, 7], device="cuda")
+    _, (kept, _, *rest) = rg.expert_linear_f8(x, w, off)
+    want = rg.expert_linear_f8_backward(dy, (kept, off, *rest), dx=False)[1]
+    for end in (8, 100, 127, 128, 1000):
+        for bad in (torch.tensor([0, 3, end], device="cuda"), torch.tensor([0, end, end], device="cuda").int()):
+            with pytest.raises(rg.ResGemmError) as err:
+                rg.expert_linear_f8_backward(dy, (kept, bad, *rest), dx=False)
+            assert err.value.code == rg.RG_ERR_ARG
+    assert torch.equal(rg.expert_linear_f8_backward(dy, (kept, off, *rest), dx=False)[1], want)
+
+
+def test_graphed_callable(rg):  # noqa: F811
+    """torch.cuda.make_graphed_callables: forward and backward pass captured one after the other."""
+    class Layer(torch.nn.Module):
+        def __init__(self):
+            super().__init__()
+            self.w1, self.w2 = (torch.nn.Parameter(normal((128, 128), i, 0.1).cuda()) for i in (1, 2))
+            self.b = torch.nn.Parameter(normal((128,), 3, 0.1).cuda())
+
+        def forward(self, x):
+            h, _ = rg.linear_act_f8(x, self.w1, bias=self.b, act="gelu", sync=False)
+            return rg.linear_f8(h, self.w2, sync=False)[0]
+
+    layer = Layer()
+    xs = [normal((70, 128), 10 + i, 1.0, bf).cuda().requires_grad_() for i in range(3)]
+    dy = normal((70, 128), 20, 1.0, bf).cuda()
+    want = []
+    for x in xs:
+        y = layer(x)
+        want.append((y.detach(), *torch.autograd.grad(y, (x, *layer.parameters()), dy)))
+        del y
+    torch.cuda.synchronize()
+    graphed = torch.cuda.make_graphed_callables(layer, (xs[0].detach().clone().requires_grad_(),))
+    for x, outs in zip(xs, want):
+        y = graphed(x)
+        got = (y.detach(), *torch.autograd.grad(y, (x, *layer.parameters()), dy))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, outs))
